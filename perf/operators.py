@@ -279,7 +279,7 @@ def _kv_cache(case, s):
     import layout_driven_movement_gb300 as lm
     p, h, d = case["page"], case["heads"], case["dim"]
     page = lm.Layout.make([p, h, d], [h * d, d, 1] if case["order"] == "nhd"
-                          else [d, p * d, 1])
+                          else [d, p * d, 1], [1, 1, 1])
     store = None if case["store"] == "same" else case["store"]
     plan = lm.KVPlan(page, DTYPES[case["dtype"]], store)
     return lm.KVCache(plan, s["k_pages"], s["v_pages"], s["k_scale"],
