@@ -45,6 +45,8 @@ typedef struct lm_layout lm_layout; /* opaque, freed by lm_layout_destroy */
 typedef struct lm_plan lm_plan;     /* opaque, freed by lm_plan_destroy   */
 typedef struct lm_tv_plan lm_tv_plan; /* opaque, freed by lm_tv_plan_destroy */
 typedef struct lm_exchange lm_exchange; /* opaque, lm_exchange_destroy       */
+typedef struct lm_rope_plan lm_rope_plan; /* opaque, lm_rope_plan_destroy     */
+typedef struct lm_kv_plan lm_kv_plan; /* opaque, freed by lm_kv_plan_destroy */
 
 typedef enum lm_status {
   LM_OK = 0,
@@ -62,7 +64,10 @@ typedef enum lm_status {
   LM_E_TIMEOUT = -9,           /* a bounded device wait gave up (see
                                   lm_device_status)                           */
   LM_E_NOMEM = -10,            /* host allocation failed                      */
-  LM_E_BUFFER = -11            /* a text output buffer is too small           */
+  LM_E_BUFFER = -11,           /* a text output buffer is too small           */
+  LM_E_RANGE = -12             /* a position, slot or page number on the
+                                  device was out of range (see
+                                  lm_device_status)                           */
 } lm_status;
 
 /* ---------------------------------------------------------------------------
@@ -554,6 +559,213 @@ int lm_tv_copy(const lm_tv_plan* plan, const void* src_dev,
 
 void lm_tv_plan_destroy(lm_tv_plan* plan);
 
+/* ---------------------------------------------------------------------------
+ * The paged key-value cache: rotary positions, write, read back, attention
+ *
+ * A serving program keeps every token's keys and values in pages: a page is a
+ * static layout of (tokens, heads, dim), and which page holds which tokens of
+ * which sequence is data, a page table on the device -- the one mode of the
+ * cache's layout that no shape:stride pair can express.  The calls below move
+ * rows between dense tensors and such pages and attend over the pages where
+ * they are.  (The pages name attention as a consumer of such layouts,
+ * "CUTLASS Layout可视化" §4.2 and "CUTE布局代数" §3.1; they define none of
+ * it.)
+ *
+ * Conventions of this section, besides those above:
+ *  - Nothing here allocates; every buffer is the caller's.  Only the calls
+ *    that take a cuda_stream enqueue work.
+ *  - Arithmetic is in 32 bits whatever the types, each result rounded once.
+ *  - Numbers that only the device holds (positions, slots, page numbers,
+ *    lengths) are checked there: one out of range reads and writes nothing
+ *    out of bounds, has the effect given with its call, and is recorded for
+ *    lm_device_status (LM_E_RANGE).
+ * ------------------------------------------------------------------------- */
+
+/* Element types of dense tensors. */
+typedef enum lm_elem { LM_BF16 = 1, LM_F16 = 2, LM_F32 = 3 } lm_elem;
+
+/* How a cache holds a row (the dim elements of one token and head).
+ *  SAME  the elements themselves.
+ *  E4M3  8-bit floats (4 exponent bits, 3 mantissa bits, largest magnitude
+ *        448) under one 32-bit scale per row, the smallest power of two
+ *        2^e, e >= -126, with max|x| / 2^e <= 448: x / 2^e is exact, so each
+ *        element is rounded once (to nearest, ties to even), and never
+ *        clipped.
+ *  INT8  whole numbers rint(x * (127 / max|x|)), ties to even, under the
+ *        scale max|x| / 127 (at least 2^-126).
+ * A row of zeros has scale 1.  A row with an infinity or a NaN is held as
+ * zeros under the scale NaN, so that whatever is computed from it is NaN. */
+typedef enum lm_kv_store {
+  LM_KV_SAME = 0,
+  LM_KV_E4M3 = 1,
+  LM_KV_INT8 = 2
+} lm_kv_store;
+
+/* A dense tensor of rows on the device: row (t, h) is dim contiguous
+ * elements at data + t * token_stride + h * head_stride.  capacity: elements
+ * from data to the end of the buffer.  Strides may be any >= 0 for inputs;
+ * an output's rows must not overlap. */
+typedef struct lm_rows {
+  void* data;
+  int64_t capacity;
+  int64_t token_stride;
+  int64_t head_stride;
+} lm_rows;
+
+/* A cache's buffers: the first element of page 0's keys and values (16-byte
+ * aligned; the two may lie interleaved in one buffer) with the elements from
+ * there to the end of each, the scales of an E4M3 or INT8 cache (one per
+ * page, head and token, in that order, tokens fastest; ignored for SAME),
+ * and the number of pages. */
+typedef struct lm_kv_cache {
+  void* k;
+  void* v;
+  int64_t k_capacity;
+  int64_t v_capacity;
+  float* k_scale;
+  float* v_scale;
+  int64_t scale_capacity;
+  int64_t pages;
+} lm_kv_cache;
+
+/* Rotary positions.  Pair i of a row's first rotary_dim elements -- elements
+ * (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved -- turns by the
+ * angle position * f_i: (a, b) becomes (a cos - b sin, b cos + a sin).  The
+ * rest of the row passes through.  f_i = base^(-2i / rotary_dim), scaled for
+ * contexts longer than the trained one:
+ *   NONE    f_i
+ *   LINEAR  f_i / factor
+ *   NTK     base replaced by base * factor^(rotary_dim / (rotary_dim - 2))
+ *   YARN    (1 - g) f_i / factor + g f_i, where g rises linearly from 0 to
+ *           1 as the turns of pair i over original_positions go from
+ *           beta_slow to beta_fast; cos and sin are multiplied by
+ *           0.1 ln(factor) + 1 (Peng et al., "YaRN: Efficient Context Window
+ *           Extension of Large Language Models", 2023). */
+typedef enum lm_rope_scaling {
+  LM_ROPE_NONE = 0,
+  LM_ROPE_LINEAR = 1,
+  LM_ROPE_NTK = 2,
+  LM_ROPE_YARN = 3
+} lm_rope_scaling;
+
+/* Errors: LM_E_INVALID (NULL out, head_dim outside 2..1024, rotary_dim odd
+ * or outside 2..head_dim, base <= 1 or not finite, factor < 1 or not finite,
+ * an unknown scaling, NTK with rotary_dim 2, YARN with original_positions < 1
+ * or beta_fast <= beta_slow or a beta that is negative or not finite). */
+int lm_rope_plan_create(int head_dim, int rotary_dim, int interleaved,
+                        double base, int scaling, double factor,
+                        int64_t original_positions, double beta_fast,
+                        double beta_slow, lm_rope_plan** out);
+
+/* The rotary_dim / 2 scaled frequencies f_i and the factor of cos and sin
+ * (either pointer may be NULL).  Errors: LM_E_INVALID, LM_E_BUFFER (cap <
+ * rotary_dim / 2). */
+int lm_rope_plan_frequencies(const lm_rope_plan* plan, double* freqs, int cap,
+                             double* amplitude);
+
+/* Enqueue the table of positions 0..rows-1: row p holds rotary_dim / 2
+ * cosines, then as many sines, computed in 64 bits and rounded once to 32.
+ * capacity counts floats.  Errors: LM_E_INVALID (NULL, rows < 0),
+ * LM_E_CAPACITY, LM_E_CUDA. */
+int lm_rope_table(const lm_rope_plan* plan, float* table, int64_t rows,
+                  int64_t capacity, void* cuda_stream);
+
+/* Enqueue out[t, h] = x[t, h] turned by positions[t] for every token and
+ * head.  elem: lm_elem of both.  positions: tokens 32- or 64-bit integers
+ * (position_bytes 4 or 8).  inverse != 0 turns back by the same angles: with
+ * amplitude 1 that undoes the call, and in any case it is its gradient
+ * (x := d/d out, out := d/d x).  out may be x itself, with the same strides
+ * (in place); otherwise the two must not overlap.  A position outside
+ * [0, table_rows) makes the rotated part of its token's rows NaN.
+ * Errors: LM_E_INVALID (NULL, elem, tokens or heads < 0, position_bytes,
+ * misaligned pointers, negative strides, an output whose rows overlap),
+ * LM_E_CAPACITY, LM_E_OVERLAP, LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_rope(const lm_rope_plan* plan, int elem, const lm_rows* x,
+            const lm_rows* out, int64_t tokens, int heads,
+            const void* positions, int position_bytes, const float* table,
+            int64_t table_rows, int inverse, void* cuda_stream);
+
+void lm_rope_plan_destroy(lm_rope_plan* plan);
+
+/* Plan a cache.  page: a layout of three plain modes (tokens, heads, dim),
+ * dim with unit stride; page_stride: elements between pages (0: the page's
+ * cosize rounded up to 16 bytes).  elem: LM_BF16 or LM_F16, the type of the
+ * dense keys, values, queries and outputs.  The head and token strides and
+ * page_stride are multiples of 16 bytes as the cache holds them; dim is a
+ * multiple of 16 bytes' worth of elements, at most 256.
+ * Errors: LM_E_INVALID (NULL, elem, store, not three plain modes, an empty
+ * page, dim, page_stride smaller than the page), LM_E_NOT_REPRESENTABLE (a
+ * swizzled page, dim not of unit stride, strides or dim not multiples of 16
+ * bytes), LM_E_NOT_INJECTIVE, LM_E_OVERFLOW. */
+int lm_kv_plan_create(const lm_layout* page, int64_t page_stride, int elem,
+                      int store, lm_kv_plan** out);
+
+/* JSON description of a plan (same buffer rules as lm_plan_describe). */
+int lm_kv_plan_describe(const lm_kv_plan* plan, char* buf, size_t cap);
+
+/* Enqueue the write of tokens' rows into the cache: k[t, h] and v[t, h] go
+ * to token slots[t] % P of page slots[t] / P, P tokens a page, held as the
+ * plan's store says.  A negative slot skips its token; one past the last
+ * page is out of range and skipped too.  The slots of a call are distinct.
+ * With rope (NULL: none), keys are first turned as lm_rope turns them, in 32
+ * bits, and rounded only into the cache; rope's head_dim is the plan's dim.
+ * Errors: LM_E_INVALID (NULL, counts, pointer alignment, a rope plan of
+ * another head_dim or without positions and table), LM_E_CAPACITY,
+ * LM_E_OVERLAP (the cache's keys and values start at the same address, or
+ * an input overlaps the cache), LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_kv_write(const lm_kv_plan* plan, const lm_kv_cache* cache,
+                const lm_rows* k, const lm_rows* v, int64_t tokens,
+                const int64_t* slots, const lm_rope_plan* rope,
+                const void* positions, int position_bytes, const float* table,
+                int64_t table_rows, void* cuda_stream);
+
+/* Enqueue the read back of whole sequences: for sequence b, rows
+ * starts[b] .. starts[b] + lens[b] - 1 of k_out and v_out get its tokens
+ * 0 .. lens[b] - 1, token j from page page_table[b * table_stride + j / P].
+ * starts has seqs + 1 entries, none below the one before; lens[b] beyond
+ * starts[b + 1] - starts[b] or max_pages * P counts as that much.  rows: the
+ * rows of the outputs; output rows that no token names, or from `rows` on,
+ * are left as they are.  out_elem: the outputs' lm_elem.  A page number
+ * outside [0, pages) is out of range and gives zeros.
+ * Errors: as lm_kv_write. */
+int lm_kv_read(const lm_kv_plan* plan, const lm_kv_cache* cache,
+               const int32_t* page_table, int64_t table_stride, int seqs,
+               int64_t max_pages, const int32_t* lens, const int32_t* starts,
+               int out_elem, const lm_rows* k_out, const lm_rows* v_out,
+               int64_t rows, void* cuda_stream);
+
+/* Bytes of the workspace of lm_kv_attend for up to seqs sequences of heads_q
+ * query heads on the current device.  Zero it once before its first use;
+ * every call leaves it ready for the next.  Calls that may overlap on the
+ * GPU need workspaces of their own.  Errors: LM_E_INVALID, LM_E_CUDA. */
+int lm_kv_attend_workspace(const lm_kv_plan* plan, int seqs, int heads_q,
+                           int64_t* bytes);
+
+/* Enqueue the attention of one new token per sequence over its cache:
+ * with n = lens[b] (clipped to [0, max_pages * P]), query head h, key head
+ * h / (heads_q / heads), and j over [max(0, n - window), n) (window 0: all
+ * of [0, n)),
+ *   s_j = scale * q[b, h] . k_j,  out[b, h] = sum_j p_j v_j,
+ *   p_j = exp(s_j) / sum_i exp(s_i),  lse[b, h] = ln sum_j exp(s_j).
+ * The new token's own key is in the cache if it is to be seen.  A sequence
+ * without keys, or whose scores are all -infinity, gives zeros and lse
+ * -infinity.  A page number outside [0, pages) is out of range and its keys
+ * are not seen.  lse (NULL: not wanted): seqs x heads_q floats, contiguous.
+ * q and out hold the plan's elem; out may be q itself with the same strides.
+ * Nothing past a sequence's length is used, whatever it holds.
+ * Errors: LM_E_INVALID (NULL, counts, heads_q not a multiple of the plan's
+ * heads, a scale that is not finite, negative window, pointer alignment),
+ * LM_E_CAPACITY (a buffer, or the workspace), LM_E_OVERLAP, LM_E_OVERFLOW,
+ * LM_E_CUDA. */
+int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
+                 const lm_rows* q, const lm_rows* out, int seqs, int heads_q,
+                 const int32_t* page_table, int64_t table_stride,
+                 int64_t max_pages, const int32_t* lens, int64_t window,
+                 float scale, float* lse, void* workspace,
+                 int64_t workspace_bytes, void* cuda_stream);
+
+void lm_kv_plan_destroy(lm_kv_plan* plan);
+
 /* Static, NUL-terminated name of a status code. */
 const char* lm_status_string(int status);
 
@@ -572,7 +784,9 @@ int lm_last_cuda_error(void);
  * in seconds mean the memory system has failed), the block has exited with
  * bulk copies still writing into shared memory it no longer owns, which can
  * corrupt a later block on that SM: after LM_E_TIMEOUT treat every result
- * on the device since the last reset as suspect.  The record is per device,
+ * on the device since the last reset as suspect.  LM_E_RANGE (reported when
+ * no wait gave up): a position, slot or page number that a kernel of the
+ * key-value cache read was out of range.  The record is per device,
  * shared by every stream and sticky; reset != 0 clears it after reading.
  * Errors: LM_E_INVALID (NULL status), LM_E_CUDA. */
 int lm_device_status(void* cuda_stream, int reset, int* status);

@@ -22,6 +22,8 @@ __all__ = [
     "layout_eval_device", "build_layout", "device_status", "STATUS",
     "TVPlan", "tv_copy", "stripmined_tune", "Exchange", "exchange_copy",
     "exchange_pack_all", "exchange_unpack_all",
+    "RopePlan", "rope_table", "rope", "KVPlan", "KVCache", "kv_write",
+    "kv_read", "kv_attend", "kv_attend_workspace",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,8 +34,23 @@ STATUS = {
     -3: "LM_E_NOT_REPRESENTABLE", -4: "LM_E_NOT_INJECTIVE",
     -5: "LM_E_OVERFLOW", -6: "LM_E_CAPACITY", -7: "LM_E_OVERLAP",
     -8: "LM_E_CUDA", -9: "LM_E_TIMEOUT", -10: "LM_E_NOMEM",
-    -11: "LM_E_BUFFER",
+    -11: "LM_E_BUFFER", -12: "LM_E_RANGE",
 }
+
+
+class _Rows(C.Structure):
+    """lm_rows"""
+    _fields_ = [("data", C.c_void_p), ("capacity", C.c_int64),
+                ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class _KVCache(C.Structure):
+    """lm_kv_cache"""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p),
+                ("k_capacity", C.c_int64), ("v_capacity", C.c_int64),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("scale_capacity", C.c_int64), ("pages", C.c_int64)]
+
 
 # (name, restype, argtypes) of every function include/layoutmove.h declares
 _P = C.c_void_p
@@ -98,6 +115,30 @@ SIGNATURES = [
     ("lm_tv_plan_args", C.c_int, [_P, _P, C.c_size_t]),
     ("lm_tv_copy", C.c_int, [_P, _P, _I64, _P, _I64, _P]),
     ("lm_tv_plan_destroy", None, [_P]),
+    ("lm_rope_plan_create", C.c_int,
+     [C.c_int, C.c_int, C.c_int, C.c_double, C.c_int, C.c_double, _I64,
+      C.c_double, C.c_double, C.POINTER(_P)]),
+    ("lm_rope_plan_frequencies", C.c_int,
+     [_P, C.POINTER(C.c_double), C.c_int, C.POINTER(C.c_double)]),
+    ("lm_rope_table", C.c_int, [_P, _P, _I64, _I64, _P]),
+    ("lm_rope", C.c_int,
+     [_P, C.c_int, C.POINTER(_Rows), C.POINTER(_Rows), _I64, C.c_int, _P,
+      C.c_int, _P, _I64, C.c_int, _P]),
+    ("lm_rope_plan_destroy", None, [_P]),
+    ("lm_kv_plan_create", C.c_int,
+     [_P, _I64, C.c_int, C.c_int, C.POINTER(_P)]),
+    ("lm_kv_plan_describe", C.c_int, [_P, C.c_char_p, C.c_size_t]),
+    ("lm_kv_write", C.c_int,
+     [_P, C.POINTER(_KVCache), C.POINTER(_Rows), C.POINTER(_Rows), _I64, _P,
+      _P, _P, C.c_int, _P, _I64, _P]),
+    ("lm_kv_read", C.c_int,
+     [_P, C.POINTER(_KVCache), _P, _I64, C.c_int, _I64, _P, _P, C.c_int,
+      C.POINTER(_Rows), C.POINTER(_Rows), _I64, _P]),
+    ("lm_kv_attend_workspace", C.c_int, [_P, C.c_int, C.c_int, _I64P]),
+    ("lm_kv_attend", C.c_int,
+     [_P, C.POINTER(_KVCache), C.POINTER(_Rows), C.POINTER(_Rows), C.c_int,
+      C.c_int, _P, _I64, _I64, _P, _I64, C.c_float, _P, _P, _I64, _P]),
+    ("lm_kv_plan_destroy", None, [_P]),
     ("lm_status_string", C.c_char_p, [C.c_int]),
     ("lm_last_cuda_error", C.c_int, []),
     ("lm_device_status", C.c_int, [_P, C.c_int, _IP]),
@@ -672,8 +713,10 @@ def layout_eval_device(layout: Layout, table, stream=None) -> None:
 
 
 def device_status(stream=None, reset: bool = False) -> int:
-    """Synchronise the stream and return LM_OK (0) or LM_E_TIMEOUT (-9) if a
-    kernel of the library gave up a bounded wait since the last reset."""
+    """Synchronise the stream and return LM_OK (0), LM_E_TIMEOUT (-9) if a
+    kernel of the library gave up a bounded wait since the last reset, or
+    LM_E_RANGE (-12) if one met a position, slot or page number out of
+    range."""
     st = C.c_int()
     _check(lib().lm_device_status(_stream_handle(stream), int(reset),
                                   C.byref(st)), "lm_device_status")
@@ -704,3 +747,306 @@ def build_layout(spec) -> Layout:
             acc = acc.concat(p)
         return acc
     raise ValueError(f"unknown layout description {kind!r}")
+
+
+# ---------------------------------------------------------------------------
+# The paged key-value cache
+# ---------------------------------------------------------------------------
+
+_ELEM = {"bfloat16": 1, "float16": 2, "float32": 3}
+_STORES = {None: 0, "same": 0, "e4m3": 1, "int8": 2}
+_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def _elem(dtype) -> int:
+    code = _ELEM.get(str(dtype).rpartition(".")[2])
+    if code is None:
+        raise ValueError(f"{dtype} is none of bfloat16, float16, float32")
+    return code
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, what: str) -> _Rows:
+    """lm_rows of a CUDA tensor [tokens, heads, dim], dim contiguous."""
+    _need(t.is_cuda and t.dim() == 3, f"{what}: a CUDA tensor [tokens, heads, "
+          "dim] is wanted")
+    n, h, d = t.shape
+    ts, hs, ds = t.stride()
+    _need(d == 1 or ds == 1, f"{what}: dim must be contiguous")
+    last = (n - 1) * ts + (h - 1) * hs + d if n and h and d else 0
+    return _Rows(t.data_ptr(), last, ts, hs)
+
+
+def _vector(t, dtypes, n, what: str):
+    """The pointer of a contiguous CUDA vector of n elements."""
+    _need(t.is_cuda and t.is_contiguous() and t.dim() == 1
+          and t.shape[0] == n and str(t.dtype).rpartition(".")[2] in dtypes,
+          f"{what}: a contiguous CUDA vector of {n} {' or '.join(dtypes)} "
+          "is wanted")
+    return t.data_ptr()
+
+
+def _extent(t) -> int:
+    """Elements from a tensor's first to its last."""
+    if t.numel() == 0:
+        return 0
+    return 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+
+
+class RopePlan:
+    """Rotary positions over the first ``rotary_dim`` elements of rows of
+    ``head_dim`` (see lm_rope_plan_create).  ``scaling``: None, "linear",
+    "ntk" or "yarn"."""
+
+    __slots__ = ("_h", "head_dim", "rotary_dim")
+
+    def __init__(self, head_dim: int, rotary_dim: int | None = None,
+                 interleaved: bool = False, base: float = 10000.0,
+                 scaling: str | None = None, factor: float = 1.0,
+                 original_positions: int = 0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0):
+        out = C.c_void_p()
+        rot = head_dim if rotary_dim is None else rotary_dim
+        _check(lib().lm_rope_plan_create(
+            int(head_dim), int(rot), int(interleaved), base,
+            _SCALINGS.get(scaling, -1), factor, int(original_positions),
+            beta_fast, beta_slow, C.byref(out)), "lm_rope_plan_create")
+        self._h = out
+        self.head_dim = int(head_dim)
+        self.rotary_dim = int(rot)
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h and _lib is not None:
+            _lib.lm_rope_plan_destroy(h)
+            self._h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    def frequencies(self) -> tuple[list[float], float]:
+        """The scaled frequencies and the factor of cos and sin."""
+        n = self.rotary_dim // 2
+        f, amp = (C.c_double * n)(), C.c_double()
+        _check(lib().lm_rope_plan_frequencies(self._h, f, n, C.byref(amp)),
+               "lm_rope_plan_frequencies")
+        return list(f), amp.value
+
+
+def rope_table(plan: RopePlan, table, stream=None) -> None:
+    """Enqueue the cosines and sines of positions 0, 1, ... into a contiguous
+    float32 CUDA tensor [positions, rotary_dim] (or [positions, 2,
+    rotary_dim / 2])."""
+    _need(table.is_cuda and table.is_contiguous() and _elem(table.dtype) == 3
+          and table.numel() == table.shape[0] * plan.rotary_dim,
+          "table: a contiguous float32 CUDA tensor [positions, rotary_dim] "
+          "is wanted")
+    _check(lib().lm_rope_table(plan._h, table.data_ptr(), table.shape[0],
+                               table.numel(), _stream_handle(stream)),
+           "lm_rope_table")
+
+
+def _turn_args(plan, positions, table, tokens):
+    _need(positions is not None and table is not None,
+          "rope needs positions and a table")
+    _need(table.is_cuda and table.is_contiguous() and _elem(table.dtype) == 3
+          and table.numel() == table.shape[0] * plan.rotary_dim,
+          "table: a contiguous float32 CUDA tensor [positions, rotary_dim] "
+          "is wanted")
+    p = _vector(positions, ("int32", "int64"), tokens, "positions")
+    return p, positions.element_size(), table.data_ptr(), table.shape[0]
+
+
+def rope(plan: RopePlan, x, positions, table, out, inverse: bool = False,
+         stream=None) -> None:
+    """Enqueue out[t, h] = x[t, h] turned by positions[t] (see lm_rope): x and
+    out [tokens, heads, head_dim] of one type, any token and head strides, out
+    may be x.  inverse=True turns back, which is also the gradient."""
+    _need(x.shape == out.shape and x.dtype == out.dtype
+          and x.shape[-1] == plan.head_dim,
+          "x and out: [tokens, heads, head_dim] of one type are wanted")
+    xr, orr = _rows(x, "x"), _rows(out, "out")
+    n, h, _ = x.shape
+    _check(lib().lm_rope(plan._h, _elem(x.dtype), xr, orr, n, h,
+                         *_turn_args(plan, positions, table, n),
+                         int(inverse), _stream_handle(stream)), "lm_rope")
+
+
+class KVPlan:
+    """A paged key-value cache's plan: ``page`` a layout of (tokens, heads,
+    dim), ``dtype`` the dense tensors' type (torch.bfloat16 or float16),
+    ``store`` how the pages hold rows: None (as they are), "e4m3" or "int8"
+    with a scale per token and head (see lm_kv_plan_create)."""
+
+    __slots__ = ("_h", "dtype", "elem", "store", "page_tokens", "heads",
+                 "dim", "page_stride", "held_bytes")
+
+    def __init__(self, page: Layout, dtype, store: str | None = None,
+                 page_stride: int = 0):
+        out = C.c_void_p()
+        self.elem = _elem(dtype)
+        self.store = None if store == "same" else store
+        _check(lib().lm_kv_plan_create(page.handle, int(page_stride),
+                                       self.elem, _STORES.get(store, -1),
+                                       C.byref(out)), "lm_kv_plan_create")
+        self._h = out
+        self.dtype = dtype
+        d = self.describe()
+        self.page_tokens, self.heads = d["page_tokens"], d["heads"]
+        self.dim, self.page_stride = d["dim"], d["page_stride"]
+        self.held_bytes = d["held_bytes"]
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h and _lib is not None:
+            _lib.lm_kv_plan_destroy(h)
+            self._h = None
+
+    @property
+    def handle(self):
+        return self._h
+
+    def describe(self) -> dict:
+        buf = C.create_string_buffer(4096)
+        _check(lib().lm_kv_plan_describe(self._h, buf, 4096),
+               "lm_kv_plan_describe")
+        return json.loads(buf.value.decode())
+
+
+class KVCache:
+    """A plan's buffers: CUDA tensors whose first element is page 0's (their
+    shape is the caller's; page p starts p * page_stride elements on), and for
+    a quantised store float32 scales of pages * heads * page_tokens each.
+    ``pages`` defaults to what k holds."""
+
+    __slots__ = ("plan", "k", "v", "k_scale", "v_scale", "pages", "_c")
+
+    def __init__(self, plan: KVPlan, k, v, k_scale=None, v_scale=None,
+                 pages: int | None = None):
+        for t, what in ((k, "k"), (v, "v")):
+            _need(t.is_cuda and t.element_size() == plan.held_bytes,
+                  f"{what}: a CUDA tensor of {plan.held_bytes}-byte elements "
+                  "is wanted")
+        scales = 0
+        if plan.store is not None:
+            for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _need(t is not None and t.is_cuda and t.is_contiguous()
+                      and _elem(t.dtype) == 3,
+                      f"{what}: a contiguous float32 CUDA tensor is wanted")
+            scales = min(k_scale.numel(), v_scale.numel())
+        ke, ve = _extent(k), _extent(v)
+        if pages is None:
+            pages = -(-ke // plan.page_stride)
+        self.plan, self.pages = plan, int(pages)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._c = _KVCache(
+            k.data_ptr(), v.data_ptr(), ke, ve,
+            k_scale.data_ptr() if scales else None,
+            v_scale.data_ptr() if scales else None, scales, self.pages)
+
+
+def _kv_rows(t, plan, heads, dtype, what):
+    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == plan.dim
+          and (dtype is None or t.dtype == dtype),
+          f"{what}: [tokens, {heads}, {plan.dim}]"
+          + (f" of {dtype}" if dtype else "") + " is wanted")
+    return _rows(t, what)
+
+
+def kv_write(cache: KVCache, k, v, slots, rope: RopePlan | None = None,
+             positions=None, table=None, stream=None) -> None:
+    """Enqueue the write of k, v [tokens, heads, dim] (any token and head
+    strides) to the cache's slots (int64 [tokens]; page * page_tokens + offset,
+    negative: skipped), quantised as the plan says; with ``rope`` the keys are
+    turned by ``positions`` on the way (see lm_kv_write)."""
+    p = cache.plan
+    kr = _kv_rows(k, p, p.heads, p.dtype, "k")
+    vr = _kv_rows(v, p, p.heads, p.dtype, "v")
+    n = k.shape[0]
+    _need(v.shape[0] == n, "k and v: as many tokens are wanted")
+    turn = (None, 0, None, 0)
+    if rope is not None:
+        turn = _turn_args(rope, positions, table, n)
+    _check(lib().lm_kv_write(p._h, cache._c, kr, vr, n,
+                             _vector(slots, ("int64",), n, "slots"),
+                             rope._h if rope is not None else None, *turn,
+                             _stream_handle(stream)), "lm_kv_write")
+
+
+def _table_args(page_table, lens):
+    seqs = lens.shape[0]
+    _need(page_table.is_cuda and page_table.dim() == 2
+          and page_table.shape[0] == seqs
+          and str(page_table.dtype) == "torch.int32"
+          and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
+          "page_table: an int32 CUDA tensor [sequences, pages] with "
+          "contiguous rows is wanted")
+    return page_table.data_ptr(), page_table.stride(0)
+
+
+def kv_read(cache: KVCache, page_table, lens, starts, k_out, v_out,
+            stream=None) -> None:
+    """Enqueue the read back of every sequence's first lens[b] tokens into
+    rows starts[b] ... of k_out and v_out [rows, heads, dim] (bfloat16,
+    float16 or float32); page_table int32 [sequences, pages], lens int32
+    [sequences], starts int32 [sequences + 1] (see lm_kv_read)."""
+    p = cache.plan
+    kr = _kv_rows(k_out, p, p.heads, None, "k_out")
+    vr = _kv_rows(v_out, p, p.heads, k_out.dtype, "v_out")
+    _need(k_out.shape == v_out.shape, "k_out and v_out: one shape is wanted")
+    n = lens.shape[0]
+    lp = _vector(lens, ("int32",), n, "lens")
+    sp = _vector(starts, ("int32",), n + 1, "starts")
+    tp, ts = _table_args(page_table, lens)
+    _check(lib().lm_kv_read(p._h, cache._c, tp, ts, n, page_table.shape[1],
+                            lp, sp, _elem(k_out.dtype), kr, vr,
+                            k_out.shape[0], _stream_handle(stream)),
+           "lm_kv_read")
+
+
+def kv_attend_workspace(plan: KVPlan, seqs: int, heads_q: int) -> int:
+    """Bytes of kv_attend's workspace on the current device; zero the buffer
+    once before its first use (see lm_kv_attend_workspace)."""
+    v = C.c_int64()
+    _check(lib().lm_kv_attend_workspace(plan._h, int(seqs), int(heads_q),
+                                        C.byref(v)), "lm_kv_attend_workspace")
+    return v.value
+
+
+def kv_attend(cache: KVCache, q, page_table, lens, out, workspace=None,
+              lse=None, scale: float | None = None, window: int = 0,
+              stream=None) -> None:
+    """Enqueue the attention of one new token per sequence, q and out
+    [sequences, query heads, dim], over the first lens[b] tokens of its pages
+    (the last ``window`` of them if given); lse (optional) float32
+    [sequences, query heads].  scale defaults to dim ** -0.5 (see
+    lm_kv_attend)."""
+    p = cache.plan
+    n, hq = q.shape[0], q.shape[1]
+    qr = _kv_rows(q, p, hq, p.dtype, "q")
+    orr = _kv_rows(out, p, hq, p.dtype, "out")
+    _need(out.shape[0] == n and lens.shape[0] == n,
+          "q, out and lens: as many sequences are wanted")
+    lp = _vector(lens, ("int32",), n, "lens")
+    tp, ts = _table_args(page_table, lens)
+    if lse is not None:
+        _need(lse.is_cuda and lse.is_contiguous() and _elem(lse.dtype) == 3
+              and lse.numel() == n * hq,
+              "lse: a contiguous float32 CUDA tensor [sequences, query heads] "
+              "is wanted")
+    wp, wb = (None, 0)
+    if workspace is not None:
+        _need(workspace.is_cuda and workspace.is_contiguous(),
+              "workspace: a contiguous CUDA tensor is wanted")
+        wp, wb = (workspace.data_ptr(),
+                  workspace.numel() * workspace.element_size())
+    _check(lib().lm_kv_attend(
+        p._h, cache._c, qr, orr, n, hq, tp, ts, page_table.shape[1], lp,
+        int(window), p.dim ** -0.5 if scale is None else scale,
+        lse.data_ptr() if lse is not None else None, wp, wb,
+        _stream_handle(stream)), "lm_kv_attend")

@@ -436,4 +436,7 @@ int launch_eval(const lm_layout& L, void* table, int offset_bytes,
                 void* stream);
 void set_cuda_error(int e);
 unsigned int* device_status_word();  // device address, current device
+// The status word's bits: 1 and 2 are waits that gave up (lm_kernels.cu), 4
+// an index read on the device that was out of range.
+constexpr unsigned int kStatusRange = 4;
 }  // namespace lm

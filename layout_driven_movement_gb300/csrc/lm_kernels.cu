@@ -2245,7 +2245,9 @@ int lm_device_status(void* cuda_stream, int reset, int* status) {
     lm::set_cuda_error(int(e));
     return LM_E_CUDA;
   }
-  *status = word ? LM_E_TIMEOUT : LM_OK;
+  *status = (word & ~lm::kStatusRange) ? LM_E_TIMEOUT
+            : word                     ? LM_E_RANGE
+                                       : LM_OK;
   return LM_OK;
 }
 

@@ -1,0 +1,70 @@
+// Device helpers of the key-value cache's kernels: element conversions,
+// aligned packs and the lookup of a position's row in the rotary table.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "lm_kv.h"
+
+namespace lm {
+
+typedef __nv_bfloat16 bf16;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) {
+  return __float2half_rn(x);
+}
+
+// V elements moved as one access (V * sizeof(T) bytes, aligned to that).
+template <class T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T v[V];
+};
+
+// Row `position` of the rotary table, or nullptr (and the status bit) when
+// the position lies outside it.
+__device__ __forceinline__ const float* turn_row(const Turn& t, uint32_t token,
+                                                 unsigned int* status) {
+  const int64_t p = t.pos64
+                        ? static_cast<const int64_t*>(t.pos)[token]
+                        : int64_t(static_cast<const int32_t*>(t.pos)[token]);
+  if (p < 0 || p >= t.rows) {
+    if (status) atomicOr(status, kStatusRange);
+    return nullptr;
+  }
+  return t.table + p * t.rot;
+}
+
+// a*c - b*s and its partner, each product and the sum rounded on its own, so
+// that the result does not depend on which of them a compiler fuses.
+__device__ __forceinline__ float turn_lo(float a, float b, float c, float s) {
+  return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+}
+__device__ __forceinline__ float turn_hi(float a, float b, float c, float s) {
+  return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+
+inline int launch_status() {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return LM_OK;
+  set_cuda_error(int(e));
+  return LM_E_CUDA;
+}
+
+}  // namespace lm

@@ -1089,6 +1089,7 @@ const char* lm_status_string(int status) {
     case LM_E_TIMEOUT: return "LM_E_TIMEOUT";
     case LM_E_NOMEM: return "LM_E_NOMEM";
     case LM_E_BUFFER: return "LM_E_BUFFER";
+    case LM_E_RANGE: return "LM_E_RANGE";
     default: return "LM_E_UNKNOWN";
   }
 }
