@@ -1,0 +1,913 @@
+// Attention of one new token per sequence over the paged cache: the kernel.
+// Each of the four lm_attend_*.cu files compiles it for one kind of cache.
+//
+// For one key head of one sequence, its G query heads q_g and its keys and
+// values k_j, v_j:  s_gj = scale q_g . k_j,  o_g = sum_j e^{s_gj} v_j / sum_j
+// e^{s_gj}.  One pass over the cache with a running maximum m, sum l and
+// unnormalised output o: a block of keys turns (m, l, o) into
+// (m', l 2^(m-m') + sum 2^(s-m'), o 2^(m-m') + sum 2^(s-m') v), scores in
+// units of ln 2; two states join by the same rule.
+//
+// The cache is read once and nothing else matters: 4 G D operations per key
+// head and token against 4 D (2 D at 8 bits) bytes.  At 6.8 TB/s an SM gets
+// some 24 bytes a cycle, that is 16 keys and values of 128 16-bit elements in
+// 340 cycles, and their two products with up to 8 queries are 16 warp-level
+// 16x8x16 matrix instructions, a tenth of what the SM does in that time.  So
+// the warp-level instruction is used and not the one that takes whole 128-row
+// tiles: keys are its 16 rows and queries its 8 columns (S^T = K Q^T, O^T =
+// V^T P^T), so that no row is wasted on a group of 8 or fewer, no barrier
+// stands between a key's arrival and its use, and 8-bit codes can be widened
+// on their way from shared memory to registers.
+//
+// Work.  Each warp of a block streams keys of its own: KW keys and their
+// values a step, through a ring of kS stages filled by 16-byte asynchronous
+// copies (a page table lookup per key, one step ahead, so any page size and
+// any strides do), consumed with no barrier but the warp's own.  The grid is
+// the resident blocks; the tiles (4 KW keys of one sequence and head) of all
+// sequences are one line cut into equal parts, so ragged batches and single
+// long sequences load all SMs alike.  A block's ring runs on across the
+// borders of sequences.  What one block holds of a head that others share
+// goes to the workspace as (m, l, o); the block that comes last by a counter
+// joins the parts, in the order of the line, so results do not depend on
+// which came last.
+#pragma once
+
+#include <atomic>
+
+#include "lm_kv_device.cuh"
+
+namespace lm {
+
+// Kinds of cache: the type of the matrix instructions' operands and how the
+// held bytes become it.
+enum AttendKind { KIND_BF16, KIND_F16, KIND_E4M3, KIND_INT8 };
+
+constexpr int kAttendWarps = 4;
+constexpr int kAttendThreads = 32 * kAttendWarps;
+
+template <int KIND, int D, int NT>
+struct AttendShape {
+  static constexpr bool kCodes = KIND == KIND_E4M3 || KIND == KIND_INT8;
+  static constexpr int kHeld = kCodes ? 1 : 2;           // bytes an element
+  static constexpr int KW = kCodes ? 32 : 16;            // keys a warp's step
+  static constexpr int TK = KW * kAttendWarps;           // keys of a tile
+  static constexpr int MT = KW / 16;                     // row tiles of S^T
+  static constexpr int Q = 8 * NT;                       // queries
+  static constexpr int kRow = D * kHeld;                 // bytes of a row
+  static constexpr int kPart = KW * kRow;                // a warp's K or V
+  static constexpr int kStage = kAttendWarps * 2 * kPart;
+  static constexpr int kS = D == 64 ? 6 : 3;             // stages
+  static constexpr int kBlocks = D == 256 ? 1 : 2;       // per SM
+  static constexpr int kScales = kCodes ? kAttendWarps * 2 * KW * 4 : 0;
+  static constexpr int kMasks = kAttendWarps * 4;
+  static constexpr int kState = kAttendWarps * Q * 2 * 4;
+  static constexpr int kSmem =
+      kS * (kStage + kScales + kMasks) + kState + 64;
+  // workspace: a part is (m, l) per query, then its output
+  static constexpr int kPartFloats = Q * (D + 2);
+  static_assert(Q * D * 4 <= 2 * kPart, "a warp's output fits its stage");
+};
+
+// --- instructions ------------------------------------------------------------
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src,
+                                     uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src,
+                                    uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst),
+               "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;\n" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void ldm_t(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(addr)
+      : "memory");
+}
+// The transpose of an 8x8 matrix of 16-bit elements held across the warp.
+__device__ __forceinline__ uint32_t mov_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n"
+               : "=r"(y)
+               : "r"(x));
+  return y;
+}
+template <bool BF>
+__device__ __forceinline__ void mma(float* c, const uint32_t* a,
+                                    const uint32_t* b) {
+  if (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two 32-bit numbers as a pair of 16-bit ones, the first in the low half.
+template <bool BF>
+__device__ __forceinline__ uint32_t pair16(float lo, float hi) {
+  if (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <bool BF>
+__device__ __forceinline__ float2 unpair16(uint32_t x) {
+  if (BF)
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+
+// --- 8-bit codes as 16-bit floats -------------------------------------------
+//
+// Keys become f16, whose 11 bits hold any scaled query (bf16 or f16) they
+// meet; values become bf16, so that weights of any size meet them.
+
+// e4m3 (sign, 4 exponent bits of bias 7, 3 mantissa bits) in the high bytes of
+// x's halves, its magnitude bits moved onto the low exponent bits and the
+// high mantissa bits of an f16 (bias 15) or bf16 (bias 127): the same number,
+// subnormals included, times 2^-8 or 2^-120.  The factor is put back where
+// products are scaled.
+template <bool BF>
+__device__ __forceinline__ uint32_t e4m3_halves(uint32_t x) {
+  return (BF ? (x >> 4) & 0x07f007f0u : (x >> 1) & 0x3f803f80u) |
+         (x & 0x80008000u);
+}
+// Whole numbers -128..127.  f16: with the sign bit turned (by the caller) the
+// byte u = code + 128 under the high byte 0x64 is 1024 + u; less 1152 it is
+// the code.  bf16 has 8 bits: the low 7 bits w under 0x43 are 128 + w, the
+// sign bit alone under 0x43 is 128 or 256, and the difference is the code.
+template <bool BF>
+__device__ __forceinline__ uint32_t int8_halves(uint32_t x) {
+  uint32_t y;
+  if (BF) {
+    const uint32_t a = x & 0xff7fff7fu, b = x & 0xff80ff80u;
+    const __nv_bfloat162 v =
+        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                *reinterpret_cast<const __nv_bfloat162*>(&b));
+    y = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const uint32_t magic = 0x64806480u;
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x),
+                              *reinterpret_cast<const __half2*>(&magic));
+    y = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return y;
+}
+// The codes of bytes (I, J) of r as a pair of f16 or bf16.
+template <int KIND, bool BF, int I, int J>
+__device__ __forceinline__ uint32_t codes2(uint32_t r) {
+  if (KIND == KIND_E4M3)
+    return e4m3_halves<BF>(__byte_perm(r, 0, 0x0404 | (I << 4) | (J << 12)));
+  return int8_halves<BF>(
+      __byte_perm(r, BF ? 0x43434343u : 0x64646464u, 0x4040 | I | (J << 8)));
+}
+
+// --- where in the line of work -----------------------------------------------
+
+struct AttendGrid {
+  int items = 1;        // (key heads) x (groups of Q queries)
+  int groups = 1;       // groups of Q queries of a key head
+  int least = 1;        // tiles a block takes at least
+  float* parts = nullptr;
+  unsigned int* counters = nullptr;
+};
+
+struct AttendAt {
+  int b, item, tile, lo, hi, first, n;
+  int64_t left;         // tiles of the block's share from here on
+};
+
+template <int TK>
+__device__ __forceinline__ void attend_span(const KvAttendArgs& a, int b,
+                                            AttendAt* at) {
+  int64_t n = a.lens[b];
+  n = n < 0 ? 0 : n > a.max_tokens ? a.max_tokens : n;
+  const int64_t first = a.window && n > a.window ? n - a.window : 0;
+  at->n = int(n);
+  at->first = int(first);
+  at->lo = int(first / TK);
+  at->hi = int((n + TK - 1) / TK);
+}
+
+// One tile on; past a head the next head, past a sequence the next one that
+// has keys.
+template <int TK>
+__device__ __forceinline__ void attend_next(const KvAttendArgs& a, int items,
+                                            AttendAt* at) {
+  --at->left;
+  if (++at->tile < at->hi || at->left <= 0) return;
+  if (++at->item == items) {
+    at->item = 0;
+    do {
+      attend_span<TK>(a, ++at->b, at);
+    } while (at->hi <= at->lo);
+  }
+  at->tile = at->lo;
+}
+
+// --- the kernel ----------------------------------------------------------------
+
+template <int KIND, int D, int NT>
+__global__ void
+__launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
+    lm_kv_attend_kernel(const __grid_constant__ KvAttendArgs a,
+                        const __grid_constant__ AttendGrid g) {
+  using S = AttendShape<KIND, D, NT>;
+  constexpr bool CODES = S::kCodes;
+  constexpr bool KBF = KIND == KIND_BF16;    // bf16 keys in the products
+  constexpr bool VBF = KIND != KIND_F16;     // bf16 values and weights
+  // what values stand for beside weights, see the weights below
+  constexpr float UP = KIND == KIND_F16    ? 0x1p15f
+                       : KIND == KIND_E4M3 ? 0x1p60f
+                                           : 1.f;
+  constexpr float DOWN = KIND == KIND_F16 ? 0x1p-15f : UP;
+  constexpr int KW = S::KW, TK = S::TK, MT = S::MT, NS = S::kS, Q = S::Q;
+  constexpr int KS = D / 16;                 // 16-element steps along dim
+  extern __shared__ __align__(128) char smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int row8 = lane / 4, col2 = (lane % 4) * 2;
+  const int dim = a.c.dim;
+
+  char* const ring = smem;
+  char* const scale_ring = ring + NS * S::kStage;
+  uint32_t* const masks =
+      reinterpret_cast<uint32_t*>(scale_ring + NS * S::kScales);
+  float* const state = reinterpret_cast<float*>(masks + NS * kAttendWarps);
+  int64_t* const share = reinterpret_cast<int64_t*>(
+      (reinterpret_cast<uintptr_t>(state + kAttendWarps * Q * 2) + 7) & ~7ull);
+  const uint32_t ring_s = uint32_t(__cvta_generic_to_shared(ring));
+  const uint32_t scale_s = uint32_t(__cvta_generic_to_shared(scale_ring));
+
+  // The line of work: every thread counts the tiles of a run of sequences;
+  // a scan over the block gives the line's length and where this block's
+  // share starts.
+  AttendAt at;
+  int64_t total, begin;
+  int64_t line_b;        // where sequence at.b starts on the line
+  {
+    const int per = (a.seqs + kAttendThreads - 1) / kAttendThreads;
+    const int b0 = min(a.seqs, int(threadIdx.x) * per);
+    const int b1 = min(a.seqs, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      AttendAt s;
+      attend_span<TK>(a, b, &s);
+      mine += int64_t(s.hi - s.lo) * g.items;
+    }
+    int64_t sum = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, k);
+      if (lane >= k) sum += v;
+    }
+    if (lane == 31) share[warp] = sum;
+    __syncthreads();
+    int64_t before = sum - mine;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttendWarps; ++w) {
+      if (w < warp) before += share[w];
+      total += share[w];
+    }
+    if (total == 0) {
+      at.left = 0;
+    } else {
+      // as many blocks as the line feeds
+      int64_t blocks = (total + g.least - 1) / g.least;
+      if (blocks > gridDim.x) blocks = gridDim.x;
+      const int64_t c = blockIdx.x;
+      begin = c * total / blocks;
+      at.left = c < blocks ? (c + 1) * total / blocks - begin : 0;
+      if (at.left > 0 && begin >= before && begin < before + mine) {
+        int b = b0;
+        AttendAt s;
+        for (;; ++b) {
+          attend_span<TK>(a, b, &s);
+          const int64_t k = int64_t(s.hi - s.lo) * g.items;
+          if (begin < before + k) break;
+          before += k;
+        }
+        share[4] = b;
+        share[5] = before;
+      }
+      total = total * 65536 + blocks;      // both, for the join
+    }
+    __syncthreads();
+  }
+  const int64_t blocks = total & 65535;
+  total >>= 16;
+
+  if (at.left > 0) {
+    at.b = int(share[4]);
+    line_b = share[5];
+    attend_span<TK>(a, at.b, &at);
+    const int tiles = at.hi - at.lo;
+    const int64_t in = begin - line_b;
+    at.item = int(in / tiles);
+    at.tile = at.lo + int(in - int64_t(at.item) * tiles);
+  }
+
+  // --- the ring's filling side ---
+  AttendAt ld = at;
+  int page = -1;           // of this lane's key of the tile to fill next
+  auto fetch = [&] {
+    const int key = ld.tile * TK + warp * KW + lane;
+    page = -1;
+    if (ld.left > 0 && lane < KW && key >= ld.first && key < ld.n)
+      page = a.table[int64_t(ld.b) * a.table_stride +
+                     fdiv(uint32_t(key), a.c.page_div)];
+  };
+  auto fill = [&](int stage) {
+    if (ld.left > 0) {
+      const int key = ld.tile * TK + warp * KW + lane;
+      const bool in = lane < KW && key >= ld.first && key < ld.n;
+      const bool ok = in && page >= 0 && page < a.c.pages;
+      if (in && !ok && a.status) atomicOr(a.status, kStatusRange);
+      const uint32_t h = uint32_t(ld.item / g.groups);
+      const uint32_t off =
+          ok ? uint32_t(key) -
+                   fdiv(uint32_t(key), a.c.page_div) * a.c.page_tokens
+             : 0;
+      const int64_t from = ok ? int64_t(page) * a.c.page_b +
+                                    int64_t(off) * a.c.token_b +
+                                    int64_t(h) * a.c.head_b
+                              : 0;
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) masks[stage * kAttendWarps + warp] = mask;
+      const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
+      constexpr int LPR = S::kRow / 16 < 32 ? S::kRow / 16 : 32;
+      constexpr int RPI = 32 / LPR;
+      const int c = lane % LPR;
+      // the products take 32 bytes of a row at a time; past dim they are 0
+      const bool held = c * 16 < dim * S::kHeld;
+      const bool used = c * 16 < (dim * S::kHeld + 31) / 32 * 32;
+#pragma unroll
+      for (int i = 0; i < KW / RPI; ++i) {
+        const int r = i * RPI + lane / LPR;
+        const int64_t o = __shfl_sync(0xffffffffu, from, r) + c * 16;
+        const uint32_t bytes = held && (mask >> r & 1) ? 16 : 0;
+        const int sw = S::kRow == 64 ? (r >> 1) & 3 : r & 7;
+        const uint32_t to = k_s + r * S::kRow + ((c ^ sw) * 16);
+        if (used) {
+          cp16(to, a.c.k + (bytes ? o : 0), bytes);
+          cp16(to + S::kPart, a.c.v + (bytes ? o : 0), bytes);
+        }
+      }
+      if (CODES && lane < KW) {
+        const int64_t so =
+            ok ? (int64_t(page) * a.c.heads + h) * a.c.page_tokens + off : 0;
+        const uint32_t to =
+            scale_s + stage * S::kScales + (warp * 2 * KW + lane) * 4;
+        cp4(to, a.c.ks + so, ok ? 4 : 0);
+        cp4(to + KW * 4, a.c.vs + so, ok ? 4 : 0);
+      }
+      attend_next<TK>(a, g.items, &ld);
+      fetch();
+    }
+    cp_commit();
+  };
+
+  if (at.left > 0) {
+    fetch();
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) fill(s);
+  }
+  // sequences without keys
+  for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
+    AttendAt s;
+    attend_span<TK>(a, b, &s);
+    if (s.hi > s.lo) continue;
+    for (int e = threadIdx.x; e < a.heads_q * dim; e += kAttendThreads) {
+      const int qi = e / dim, d = e - qi * dim;
+      reinterpret_cast<uint16_t*>(a.out.p)[int64_t(b) * a.out.ts +
+                                           int64_t(qi) * a.out.hs + d] = 0;
+    }
+    if (a.lse)
+      for (int qi = threadIdx.x; qi < a.heads_q; qi += kAttendThreads)
+        a.lse[int64_t(b) * a.heads_q + qi] = -INFINITY;
+  }
+
+  int stage = 0;
+  while (at.left > 0) {
+    // --- one head of one sequence: `steps` tiles of it ---
+    const int h = at.item / g.groups, grp = at.item - h * g.groups;
+    const int q0 = grp * Q;                          // of the key head's
+    const int nq = min(Q, a.group - q0);
+    const int steps = int(min(at.left, int64_t(at.hi - at.tile)));
+
+    // the queries as the second operand's fragments; codes are met by f16
+    // queries, scaled by a power of two so that the largest element lies in
+    // [2^14, 2^15): exact for bf16 and f16 elements down to 2^-38 of it
+    uint32_t qf[KS][NT][2];
+    float fac[NT][2];
+    const float unit = a.scale * 1.44269504088896341f *
+                       (KIND == KIND_E4M3 ? 256.f : 1.f);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int qi = nt * 8 + row8;
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q.p) +
+                          int64_t(at.b) * a.q.ts +
+                          int64_t(h * a.group + q0 + qi) * a.q.hs;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int d = k * 16 + (CODES ? 2 * col2 + 2 * j : col2 + 8 * j);
+          uint32_t x = 0;
+          if (qi < nq && d < dim) x = q[d] | uint32_t(q[d + 1]) << 16;
+          qf[k][nt][j] = x;
+        }
+      fac[nt][0] = fac[nt][1] = unit;
+      if (CODES) {
+        const bool in_bf = a.elem == LM_BF16;
+        float top = 0;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 v = in_bf ? unpair16<true>(qf[k][nt][j])
+                                   : unpair16<false>(qf[k][nt][j]);
+            top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e, e = 14 - floor(log2 top) within +-112
+        int e = 14 + 127 - int(__float_as_uint(top) >> 23);
+        if (top == 0 || top == INFINITY) e = 0;
+        e = min(112, max(-112, e));
+        const float up = __int_as_float((127 + e) << 23);
+        const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 v = in_bf ? unpair16<true>(qf[k][nt][j])
+                                   : unpair16<false>(qf[k][nt][j]);
+            qf[k][nt][j] = pair16<false>(v.x * up, v.y * up);
+          }
+        // the factor belongs to query row8; the scores' columns are
+        // queries col2 and col2 + 1
+        fac[nt][0] *= __shfl_sync(0xffffffffu, down, col2 * 4);
+        fac[nt][1] *= __shfl_sync(0xffffffffu, down, col2 * 4 + 4);
+      }
+    }
+
+    float m[NT][2], l[NT][2], o[KS][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[nt][j] = -INFINITY;
+        l[nt][j] = 0;
+      }
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[k][nt][i] = 0;
+
+    for (int step = 0; step < steps; ++step) {
+      __syncwarp();
+      fill(stage == 0 ? NS - 1 : stage - 1);
+      cp_wait<NS - 1>();
+      __syncwarp();
+      const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
+      const uint32_t v_s = k_s + S::kPart;
+      const uint32_t mask = masks[stage * kAttendWarps + warp];
+
+      // S^T = K Q^T
+      float s[MT][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0;
+#pragma unroll
+      for (int k = 0; k < KS; k += CODES ? 2 : 1) {
+        if (k * 16 >= dim) break;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int r = mt * 16 + lane % 16;
+          // 16-bit: rows 0-15, then the next 8 elements; codes: the same
+          // with the next 16
+          const int c = (CODES ? k : k * 2) + lane / 16;
+          const int sw = S::kRow == 64 ? (r >> 1) & 3 : r & 7;
+          uint32_t x[4];
+          ldm(x, k_s + r * S::kRow + ((c ^ sw) * 16));
+          if (CODES) {
+            if (KIND == KIND_INT8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] ^= 0x80808080u;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t f[4] = {codes2<KIND, false, 0, 1>(x[2 * e]),
+                                     codes2<KIND, false, 0, 1>(x[2 * e + 1]),
+                                     codes2<KIND, false, 2, 3>(x[2 * e]),
+                                     codes2<KIND, false, 2, 3>(x[2 * e + 1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<false>(s[mt][nt], f, qf[k + e][nt]);
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<KBF>(s[mt][nt], x, qf[k][nt]);
+          }
+        }
+      }
+
+      // scores in units of ln 2; -infinity where no key is seen
+      float ks[MT][2], vs[MT][2];
+      if (CODES) {
+        const float* sc = reinterpret_cast<const float*>(
+                              scale_ring + stage * S::kScales) +
+                          warp * 2 * KW;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ks[mt][i] = sc[mt * 16 + 8 * i + row8];
+            vs[mt][i] = sc[KW + mt * 16 + 8 * i + row8];
+          }
+      }
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) top[nt][j] = m[nt][j];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = i & 1, r = i >> 1;
+            float x = s[mt][nt][i] * fac[nt][j];
+            if (CODES) x *= ks[mt][r];
+            if (!(mask >> (mt * 16 + 8 * r + row8) & 1)) x = -INFINITY;
+            s[mt][nt][i] = x;
+            top[nt][j] = fmaxf(top[nt][j], x);
+          }
+      bool moved = false;
+      float keep[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // over the 8 lanes that hold the column's keys
+#pragma unroll
+          for (int k = 4; k < 32; k *= 2)
+            top[nt][j] = fmaxf(
+                top[nt][j], __shfl_xor_sync(0xffffffffu, top[nt][j], k));
+          moved |= top[nt][j] != m[nt][j];
+          // nothing seen yet: relative to 0, every weight is 0
+          const float t = top[nt][j] == -INFINITY ? 0.f : top[nt][j];
+          keep[nt][j] = ex2(m[nt][j] - t);
+          l[nt][j] *= keep[nt][j];
+          m[nt][j] = top[nt][j];
+          top[nt][j] = t;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[k][nt][i] *= keep[nt][i & 1];
+      }
+
+      // weights, and their transposes as the second operand.  A weight's 8
+      // (bf16) or 11 (f16) bits alone would cost the result about as much as
+      // its own rounding does, so what the rounding of a weight leaves goes
+      // through the products too.  A value's scale is folded into its weight.
+      // UP keeps weights and sums in range: f16 weights run up to 2^15, so
+      // that what a head's largest key has a zero for is left to keys down
+      // to 2^-29 of its weight; e4m3 values are 2^-120 of themselves.
+      uint32_t p[MT][NT][2], p2[MT][NT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float w[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              w[j] = ex2(s[mt][nt][2 * r + j] - top[nt][j]);
+              l[nt][j] += w[j];
+              if (CODES) w[j] *= vs[mt][r];
+              if (UP != 1.f) w[j] *= UP;
+            }
+            const uint32_t hi = pair16<VBF>(w[0], w[1]);
+            const float2 f = unpair16<VBF>(hi);
+            p[mt][nt][r] = mov_t(hi);
+            p2[mt][nt][r] = mov_t(pair16<VBF>(w[0] - f.x, w[1] - f.y));
+          }
+
+      // O^T += V^T P^T
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        if (k * 16 >= dim) break;
+        if (CODES) {
+          const int r = lane;                       // 32 keys, 16 elements
+          const int sw = S::kRow == 64 ? (r >> 1) & 3 : r & 7;
+          uint32_t x[4];
+          ldm_t(x, v_s + r * S::kRow + ((k ^ sw) * 16));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            // elements 2i are the tile's rows 0-7, elements 2i + 1 its rows
+            // 8-15
+            const uint32_t f[4] = {codes2<KIND, true, 0, 2>(x[2 * mt]),
+                                   codes2<KIND, true, 1, 3>(x[2 * mt]),
+                                   codes2<KIND, true, 0, 2>(x[2 * mt + 1]),
+                                   codes2<KIND, true, 1, 3>(x[2 * mt + 1])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<true>(o[k][nt], f, p[mt][nt]);
+              mma<true>(o[k][nt], f, p2[mt][nt]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int r = mt * 16 + lane % 8 + (lane / 16) * 8;
+            const int c = k * 2 + (lane / 8 & 1);
+            const int sw = r & 7;
+            uint32_t x[4];
+            ldm_t(x, v_s + r * S::kRow + ((c ^ sw) * 16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<VBF>(o[k][nt], x, p[mt][nt]);
+              mma<VBF>(o[k][nt], x, p2[mt][nt]);
+            }
+          }
+        }
+      }
+      if (++stage == NS) stage = 0;
+    }
+
+    // --- the warps' states join; each warp's output lies in the stage that
+    // it used last, which nothing fills before the next step ---
+    const int used = stage == 0 ? NS - 1 : stage - 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int k = 4; k < 32; k *= 2)
+          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], k);
+        if (row8 == 0) {
+          float* st = state + (warp * Q + nt * 8 + col2 + j) * 2;
+          st[0] = m[nt][j];
+          st[1] = l[nt][j];
+        }
+      }
+    __syncthreads();
+    float* const mine = reinterpret_cast<float*>(
+        ring + used * S::kStage + warp * 2 * S::kPart);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float t = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kAttendWarps; ++w)
+          t = fmaxf(t, state[(w * Q + nt * 8 + col2 + j) * 2]);
+        f[j] = ex2(m[nt][j] - (t == -INFINITY ? 0.f : t)) * DOWN;
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // column col2 + j of the products is a query: its elements, the
+          // words turned so that the warp's lanes hit all banks
+          float* to = mine + (nt * 8 + col2 + j) * D;
+          const int turn = col2 * 4;
+          if (CODES) {
+            const int d = (k * 16 + 2 * row8) ^ turn;
+            *reinterpret_cast<float2*>(to + d) =
+                make_float2(o[k][nt][j] * f[j], o[k][nt][2 + j] * f[j]);
+          } else {
+            to[(k * 16 + row8) ^ turn] = o[k][nt][j] * f[j];
+            to[(k * 16 + 8 + row8) ^ turn] = o[k][nt][2 + j] * f[j];
+          }
+        }
+    }
+    __syncthreads();
+    const int tiles = at.hi - at.lo;
+    const bool whole = steps == tiles;
+    const int64_t item_at = line_b + int64_t(at.item) * tiles;
+    const int64_t c0 = whole ? 0 : ((item_at + 1) * blocks - 1) / total;
+    const int64_t c1 = whole ? 0 : ((item_at + tiles) * blocks - 1) / total;
+    float* part = nullptr;
+    if (!whole)
+      part = g.parts +
+             (2 * int64_t(blockIdx.x) + (begin < item_at ? 1 : 0)) *
+                 S::kPartFloats;
+    const int64_t out_row = int64_t(at.b) * a.heads_q + h * a.group + q0;
+    char* const out0 =
+        a.out.p + (int64_t(at.b) * a.out.ts +
+                   int64_t(h * a.group + q0) * a.out.hs) * 2;
+    const bool out_bf = a.elem == LM_BF16;
+    auto put = [&](int qi, int d, float x) {
+      char* to = out0 + (int64_t(qi) * a.out.hs + d) * 2;
+      if (out_bf)
+        *reinterpret_cast<bf16*>(to) = from_f32<bf16>(x);
+      else
+        *reinterpret_cast<__half*>(to) = from_f32<__half>(x);
+    };
+    for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {
+      const int qi = e / D, d = e % D;
+      float t = -INFINITY, x = 0, sum = 0;
+#pragma unroll
+      for (int w = 0; w < kAttendWarps; ++w)
+        t = fmaxf(t, state[(w * Q + qi) * 2]);
+      const float t0 = t == -INFINITY ? 0.f : t;
+#pragma unroll
+      for (int w = 0; w < kAttendWarps; ++w) {
+        sum += state[(w * Q + qi) * 2 + 1] *
+               ex2(state[(w * Q + qi) * 2] - t0);
+        x += reinterpret_cast<const float*>(
+            ring + used * S::kStage +
+            w * 2 * S::kPart)[qi * D + (d ^ ((qi & 6) * 4))];
+      }
+      if (whole) {
+        if (d < dim) put(qi, d, sum == 0 ? 0.f : x / sum);
+        if (d == 0 && a.lse)
+          a.lse[out_row + qi] =
+              sum == 0 ? -INFINITY
+                       : (t + log2f(sum)) * 0.693147180559945309f;
+      } else {
+        part[2 * Q + qi * D + d] = x;
+        if (d == 0) {
+          part[2 * qi] = t;
+          part[2 * qi + 1] = sum;
+        }
+      }
+    }
+    if (!whole) {
+      // the block that comes last joins the parts c0 .. c1
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const unsigned before = atomicAdd(g.counters + c0, 1u);
+        share[6] = before == unsigned(c1 - c0);
+        if (share[6]) g.counters[c0] = 0;
+      }
+      __syncthreads();
+      if (share[6]) {
+        __threadfence();
+        const int64_t p0 =
+            2 * c0 + (c0 * total / blocks < item_at ? 1 : 0);
+        auto part_of = [&](int64_t c) {
+          return g.parts + (c == c0 ? p0 : 2 * c) * S::kPartFloats;
+        };
+        for (int e = threadIdx.x; e < nq * (D / 4); e += kAttendThreads) {
+          const int qi = e / (D / 4), d = e % (D / 4) * 4;
+          float t = -INFINITY;
+#pragma unroll 4
+          for (int64_t c = c0; c <= c1; ++c)
+            t = fmaxf(t, __ldcg(part_of(c) + 2 * qi));
+          const float t0 = t == -INFINITY ? 0.f : t;
+          float sum = 0, x[4] = {0, 0, 0, 0};
+#pragma unroll 4
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* pc = part_of(c);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc) + qi);
+            const float4 v = __ldcg(
+                reinterpret_cast<const float4*>(pc + 2 * Q + qi * D + d));
+            const float f = ex2(ml.x - t0);
+            sum += ml.y * f;
+            x[0] += v.x * f;
+            x[1] += v.y * f;
+            x[2] += v.z * f;
+            x[3] += v.w * f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (d + i < dim) put(qi, d + i, sum == 0 ? 0.f : x[i] / sum);
+          if (d == 0 && a.lse)
+            a.lse[out_row + qi] =
+                sum == 0 ? -INFINITY
+                         : (t + log2f(sum)) * 0.693147180559945309f;
+        }
+      }
+    }
+    __syncthreads();
+
+    // on to the next head or sequence
+    at.left -= steps;
+    at.tile += steps;
+    if (at.left > 0) {
+      if (++at.item == g.items) {
+        line_b += int64_t(tiles) * g.items;
+        at.item = 0;
+        do {
+          attend_span<TK>(a, ++at.b, &at);
+        } while (at.hi <= at.lo);
+      }
+      at.tile = at.lo;
+    }
+  }
+  cp_wait<0>();
+}
+
+// --- launch --------------------------------------------------------------------
+
+// The current device (below 64) and its SMs (lm_attend.cu).
+int attend_device(int* dev, int* sms);
+
+// Queries a block holds at once: 8 when a key head has no more, else 16; a
+// larger group reads its keys again per 16.
+inline int attend_tiles(int group) { return group <= 8 ? 1 : 2; }
+
+inline int attend_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// The workspace: a counter per block, then two parts per block.
+inline int64_t attend_counter_bytes(int blocks) {
+  return (int64_t(blocks) * 4 + 255) / 256 * 256;
+}
+
+template <int KIND, int D, int NT>
+int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
+  using S = AttendShape<KIND, D, NT>;
+  int sms = 0, dev = 0;
+  const int rc = attend_device(&dev, &sms);
+  if (rc != LM_OK) return rc;
+  auto* kernel = lm_kv_attend_kernel<KIND, D, NT>;
+  static std::atomic<uint64_t> allowed{0};    // a bit per device
+  if (!(allowed.load() >> dev & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) {
+      set_cuda_error(int(e));
+      return LM_E_CUDA;
+    }
+    allowed.fetch_or(uint64_t(1) << dev);
+  }
+  const int blocks = sms * S::kBlocks;
+  AttendGrid g;
+  g.groups = (a.group + S::Q - 1) / S::Q;
+  g.items = int(a.c.heads) * g.groups;
+  g.counters = static_cast<unsigned int*>(a.ws);
+  g.parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
+                                     attend_counter_bytes(blocks));
+  kernel<<<unsigned(blocks), kAttendThreads, S::kSmem, st>>>(a, g);
+  return launch_status();
+}
+
+template <int KIND>
+int launch_attend_kind(const KvAttendArgs& a, cudaStream_t st) {
+  const int d = attend_dim(a.c.dim), nt = attend_tiles(a.group);
+  if (d == 64)
+    return nt == 1 ? launch_attend<KIND, 64, 1>(a, st)
+                   : launch_attend<KIND, 64, 2>(a, st);
+  if (d == 128)
+    return nt == 1 ? launch_attend<KIND, 128, 1>(a, st)
+                   : launch_attend<KIND, 128, 2>(a, st);
+  return nt == 1 ? launch_attend<KIND, 256, 1>(a, st)
+                 : launch_attend<KIND, 256, 2>(a, st);
+}
+
+int launch_attend_bf16(const KvAttendArgs& a, cudaStream_t st);
+int launch_attend_f16(const KvAttendArgs& a, cudaStream_t st);
+int launch_attend_e4m3(const KvAttendArgs& a, cudaStream_t st);
+int launch_attend_int8(const KvAttendArgs& a, cudaStream_t st);
+
+}  // namespace lm

@@ -132,7 +132,9 @@ void check_table(const lm_kv_plan& p, const int32_t* table, int64_t stride,
   need(table && lens && seqs >= 0 && max_pages >= 0 && stride >= 0 &&
        addr(table) % 4 == 0 && addr(lens) % 4 == 0);
   need(seqs <= 1 || stride >= max_pages);
-  need(mul_chk(max_pages, p.page_tokens) < (int64_t(1) << 31), LM_E_OVERFLOW);
+  // key numbers, rounded up to whole tiles, fit 32 bits
+  need(mul_chk(max_pages, p.page_tokens) < (int64_t(1) << 31) - 4096,
+       LM_E_OVERFLOW);
 }
 
 }  // namespace

@@ -597,6 +597,38 @@ def test_attend_values_of_far_scales():
         check_attend(P, 3, q, out, lse)
 
 
+def test_attend_every_code():
+    """A single token's values come back as what their codes stand for, the
+    smallest (subnormal) codes beside the largest ones included; keys of all
+    codes meet a query that picks one element."""
+    for store in ("e4m3", "int8"):
+        P = kr.Pages([1] * 64, 1, 256, 1, "nhd", BF, store, seed=4)
+        codes = torch.arange(256, dtype=torch.uint8)
+        codes[codes % 128 == 127] = 0 if store == "e4m3" else 127
+        vals = kr.e4m3_values()[codes.long()] if store == "e4m3" else \
+            codes.view(torch.int8).double()
+        for b in range(64):
+            p = int(P.table[b, 0])
+            for kv, sc in ((0, 2.0 ** -5), (1, 2.0 ** (b - 40))):
+                P.codes[kv].view(torch.uint8)[p, 0, 0] = codes
+                P.scales[kv][p, 0, 0] = sc
+                P.rows[kv][b] = (vals * sc)[None, None]
+        q = torch.zeros(64, 5, 256, dtype=BF)
+        for b in range(64):
+            for h in range(4):
+                q[b, h, 4 * b + h] = 1.5
+        q, out, lse = run_attend(P, 5, q=q, scale=1.0)
+        for b in range(64):
+            want = P.rows[1][b][0]
+            # one rounding of the result, and of 1 / l
+            assert ((out[b].double() - want).abs() <=
+                    want.abs() * (2.0 ** -8 + 2.0 ** -22)).all()
+            s = vals[4 * b:4 * b + 4] * 2.0 ** -5 * 1.5
+            # the factor of ln 2 and back: three roundings
+            assert ((lse[b, :4].double() - s).abs() <=
+                    s.abs() * 2.0 ** -21 + 2.0 ** -24).all()
+
+
 def test_attend_infinite_and_nan_keys():
     """A key whose score is -infinity weighs nothing; all of them: zeros; a
     NaN key makes its own head group NaN and no other."""
