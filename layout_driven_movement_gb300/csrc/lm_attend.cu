@@ -24,12 +24,12 @@ int attend_device(int* dev_out, int* sms) {
   return LM_E_CUDA;
 }
 
-int attend_workspace(int, int dim, int group, int64_t* bytes) {
+int attend_workspace(int store, int dim, int group, int64_t* bytes) {
   int dev = 0, sms = 0;
   const int rc = attend_device(&dev, &sms);
   if (rc != LM_OK) return rc;
   const int64_t d = attend_dim(dim), q = 8 * attend_tiles(group);
-  const int64_t blocks = sms * (d == 256 ? 1 : 2);
+  const int64_t blocks = sms * (d == 256 ? 1 : store == LM_KV_SAME ? 2 : 3);
   *bytes = attend_counter_bytes(int(blocks)) + 2 * blocks * q * (d + 2) * 4;
   return LM_OK;
 }

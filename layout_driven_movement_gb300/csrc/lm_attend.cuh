@@ -56,8 +56,14 @@ struct AttendShape {
   static constexpr int kRow = D * kHeld;                 // bytes of a row
   static constexpr int kPart = KW * kRow;                // a warp's K or V
   static constexpr int kStage = kAttendWarps * 2 * kPart;
-  static constexpr int kS = D == 64 ? 6 : 3;             // stages
-  static constexpr int kBlocks = D == 256 ? 1 : 2;       // per SM
+  // blocks per SM and stages: what shared memory holds.  Widening codes is
+  // latency that only more warps hide: 128 sequences of 12288 tokens, 8 x 8 x
+  // 128 e4m3, take 390 us with three blocks of two stages an SM, 481 with two
+  // of three.
+  static constexpr int kBlocks = D == 256 ? 1 : kCodes ? 3 : 2;
+  static constexpr int kS = D == 256  ? 3
+                            : kCodes ? (D == 64 ? 4 : 2)
+                                     : (D == 64 ? 6 : 3);
   static constexpr int kScales = kCodes ? kAttendWarps * 2 * KW * 4 : 0;
   static constexpr int kMasks = kAttendWarps * 4;
   static constexpr int kState = kAttendWarps * Q * 2 * 4;
@@ -155,45 +161,78 @@ __device__ __forceinline__ float2 unpair16(uint32_t x) {
 // Keys become f16, whose 11 bits hold any scaled query (bf16 or f16) they
 // meet; values become bf16, so that weights of any size meet them.
 
-// e4m3 (sign, 4 exponent bits of bias 7, 3 mantissa bits) in the high bytes of
-// x's halves, its magnitude bits moved onto the low exponent bits and the
-// high mantissa bits of an f16 (bias 15) or bf16 (bias 127): the same number,
-// subnormals included, times 2^-8 or 2^-120.  The factor is put back where
-// products are scaled.
-template <bool BF>
-__device__ __forceinline__ uint32_t e4m3_halves(uint32_t x) {
-  return (BF ? (x >> 4) & 0x07f007f0u : (x >> 1) & 0x3f803f80u) |
-         (x & 0x80008000u);
-}
-// Whole numbers -128..127.  f16: with the sign bit turned (by the caller) the
-// byte u = code + 128 under the high byte 0x64 is 1024 + u; less 1152 it is
-// the code.  bf16 has 8 bits: the low 7 bits w under 0x43 are 128 + w, the
-// sign bit alone under 0x43 is 128 or 256, and the difference is the code.
-template <bool BF>
-__device__ __forceinline__ uint32_t int8_halves(uint32_t x) {
+// Logic and byte moves run at half the rate of the rest and are what an 8-bit
+// cache spends most of its instructions on, so each form below is the
+// cheapest known for its bytes; "2 of 4" names the ones a pair is taken from
+// (any pairing does for keys: the queries are laid out to match).
+
+// One word by masks: where p is 0, the bits of q; where p is 1, those of r,
+// turned where q is 1.
+__device__ __forceinline__ uint32_t masked(uint32_t r, uint32_t p,
+                                           uint32_t q) {
   uint32_t y;
-  if (BF) {
-    const uint32_t a = x & 0xff7fff7fu, b = x & 0xff80ff80u;
-    const __nv_bfloat162 v =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                *reinterpret_cast<const __nv_bfloat162*>(&b));
-    y = *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const uint32_t magic = 0x64806480u;
-    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x),
-                              *reinterpret_cast<const __half2*>(&magic));
-    y = *reinterpret_cast<const uint32_t*>(&v);
-  }
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;\n" : "=r"(y) : "r"(r), "r"(p), "r"(q));
   return y;
 }
-// The codes of bytes (I, J) of r as a pair of f16 or bf16.
-template <int KIND, bool BF, int I, int J>
-__device__ __forceinline__ uint32_t codes2(uint32_t r) {
-  if (KIND == KIND_E4M3)
-    return e4m3_halves<BF>(__byte_perm(r, 0, 0x0404 | (I << 4) | (J << 12)));
-  return int8_halves<BF>(
-      __byte_perm(r, BF ? 0x43434343u : 0x64646464u, 0x4040 | I | (J << 8)));
-}
+template <int KIND>
+struct Codes;
+
+// e4m3: keys by the conversion instruction (bytes 0 1 and 2 3).  Values:
+// sign, 4 exponent bits (bias 7) and 3 mantissa bits moved onto the sign, the
+// low exponent bits (bias 127) and the high mantissa bits of a bf16, the same
+// number, subnormals included, times 2^-120, which is put back where the
+// products are scaled (bytes 0 2 and 1 3).
+template <>
+struct Codes<KIND_E4M3> {
+  static __device__ __forceinline__ void keys(uint32_t r, uint32_t* y) {
+    asm("{.reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+        " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+        : "=r"(y[0]), "=r"(y[1])
+        : "r"(r));
+  }
+  static __device__ __forceinline__ void values(uint32_t r, uint32_t* y) {
+    y[0] = ((r << 4) & 0x07f007f0u) | ((r << 8) & 0x80008000u);
+    y[1] = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);
+  }
+};
+
+// Whole numbers -128..127 (bytes 0 2 and 1 3).  Keys: with its sign bit
+// turned the byte u = code + 128 under the high byte 0x64 is the f16 1024 + u;
+// less 1152 it is the code.  Values: bf16 has 8 bits; the low 7 bits w under
+// 0x43 are 128 + w, the sign bit alone under 0x43 is 128 or 256, and the
+// difference is the code.
+template <>
+struct Codes<KIND_INT8> {
+  static __device__ __forceinline__ void keys(uint32_t r, uint32_t* y) {
+    const uint32_t m = 0x64806480u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u = masked(i ? r >> 8 : r, 0x00ff00ffu, 0x64806480u);
+      const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u),
+                                *reinterpret_cast<const __half2*>(&m));
+      y[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  static __device__ __forceinline__ void values(uint32_t r, uint32_t* y) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t t = i ? r >> 8 : r;
+      const uint32_t a = (t & 0x007f007fu) | 0x43004300u;
+      const uint32_t b = (t & 0x00800080u) | 0x43004300u;
+      const __nv_bfloat162 v =
+          __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                  *reinterpret_cast<const __nv_bfloat162*>(&b));
+      y[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+};
+template <>
+struct Codes<KIND_BF16> {
+  static __device__ __forceinline__ void keys(uint32_t, uint32_t*) {}
+  static __device__ __forceinline__ void values(uint32_t, uint32_t*) {}
+};
+template <>
+struct Codes<KIND_F16> : Codes<KIND_BF16> {};
 
 // --- where in the line of work -----------------------------------------------
 
@@ -201,6 +240,7 @@ struct AttendGrid {
   int items = 1;        // (key heads) x (groups of Q queries)
   int groups = 1;       // groups of Q queries of a key head
   int least = 1;        // tiles a block takes at least
+  int shared_page = 0;  // the keys of a warp's step share a page
   float* parts = nullptr;
   unsigned int* counters = nullptr;
 };
@@ -250,13 +290,13 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   constexpr bool KBF = KIND == KIND_BF16;    // bf16 keys in the products
   constexpr bool VBF = KIND != KIND_F16;     // bf16 values and weights
   // what values stand for beside weights, see the weights below
-  constexpr float UP = KIND == KIND_F16    ? 0x1p15f
+  constexpr float UP = KIND == KIND_F16    ? 0x1p7f
                        : KIND == KIND_E4M3 ? 0x1p60f
                                            : 1.f;
-  constexpr float DOWN = KIND == KIND_F16 ? 0x1p-15f : UP;
+  constexpr float DOWN = KIND == KIND_F16 ? 0x1p-7f : UP;
   constexpr int KW = S::KW, TK = S::TK, MT = S::MT, NS = S::kS, Q = S::Q;
   constexpr int KS = D / 16;                 // 16-element steps along dim
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row8 = lane / 4, col2 = (lane % 4) * 2;
   const int dim = a.c.dim;
@@ -270,6 +310,17 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       (reinterpret_cast<uintptr_t>(state + kAttendWarps * Q * 2) + 7) & ~7ull);
   const uint32_t ring_s = uint32_t(__cvta_generic_to_shared(ring));
   const uint32_t scale_s = uint32_t(__cvta_generic_to_shared(scale_ring));
+
+  // A row's 16-byte chunks are permuted by an exclusive or with its number,
+  // so that the 8 rows of a matrix load lie in different banks.  Rows and
+  // stages are aligned to the row's size: the chunk of a step is then one
+  // exclusive or away from the lane's first.
+  auto turned = [](int r) { return S::kRow == 64 ? (r >> 1) & 3 : r & 7; };
+  const uint32_t k_lane =
+      lane % 16 * S::kRow + ((lane / 16) ^ turned(lane % 16)) * 16;
+  const int v_row = CODES ? lane : lane % 8 + lane / 16 * 8;
+  const uint32_t v_lane =
+      v_row * S::kRow + ((CODES ? 0 : lane / 8 & 1) ^ turned(v_row)) * 16;
 
   // The line of work: every thread counts the tiles of a run of sequences;
   // a scan over the block gives the line's length and where this block's
@@ -342,53 +393,80 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
 
   // --- the ring's filling side ---
   AttendAt ld = at;
-  int page = -1;           // of this lane's key of the tile to fill next
+  // of this lane's key (or, where a step's keys share a page, of its first
+  // key) of the tile to fill next
+  int page = -1;
+  constexpr int LPR = S::kRow / 16;            // lanes a row
+  constexpr int RPI = 32 / LPR;                // rows an instruction
+  const int c = lane % LPR, r0 = lane / LPR;
+  // the products take 32 bytes of a row at a time; past dim they are 0
+  const bool held = c * 16 < dim * S::kHeld;
+  const bool used = c * 16 < (dim * S::kHeld + 31) / 32 * 32;
+  const uint32_t to_lane = r0 * S::kRow;
+  const int64_t from_lane = r0 * a.c.token_b + c * 16;
+  const int64_t v_from_k = a.c.v - a.c.k;
   auto fetch = [&] {
-    const int key = ld.tile * TK + warp * KW + lane;
+    const int key = ld.tile * TK + warp * KW + (g.shared_page ? 0 : lane);
     page = -1;
-    if (ld.left > 0 && lane < KW && key >= ld.first && key < ld.n)
+    const int reach = g.shared_page ? KW : 1;
+    if (ld.left > 0 && (g.shared_page || lane < KW) &&
+        key + reach > ld.first && key < ld.n)
       page = a.table[int64_t(ld.b) * a.table_stride +
                      fdiv(uint32_t(key), a.c.page_div)];
   };
   auto fill = [&](int stage) {
     if (ld.left > 0) {
-      const int key = ld.tile * TK + warp * KW + lane;
-      const bool in = lane < KW && key >= ld.first && key < ld.n;
+      const int key0 = ld.tile * TK + warp * KW;
+      const uint32_t h = uint32_t(ld.item / g.groups);
+      const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
+      const bool in = lane < KW && key0 + lane >= ld.first &&
+                      key0 + lane < ld.n;
       const bool ok = in && page >= 0 && page < a.c.pages;
       if (in && !ok && a.status) atomicOr(a.status, kStatusRange);
-      const uint32_t h = uint32_t(ld.item / g.groups);
-      const uint32_t off =
-          ok ? uint32_t(key) -
-                   fdiv(uint32_t(key), a.c.page_div) * a.c.page_tokens
-             : 0;
-      const int64_t from = ok ? int64_t(page) * a.c.page_b +
-                                    int64_t(off) * a.c.token_b +
-                                    int64_t(h) * a.c.head_b
-                              : 0;
       const uint32_t mask = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) masks[stage * kAttendWarps + warp] = mask;
-      const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
-      constexpr int LPR = S::kRow / 16 < 32 ? S::kRow / 16 : 32;
-      constexpr int RPI = 32 / LPR;
-      const int c = lane % LPR;
-      // the products take 32 bytes of a row at a time; past dim they are 0
-      const bool held = c * 16 < dim * S::kHeld;
-      const bool used = c * 16 < (dim * S::kHeld + 31) / 32 * 32;
-#pragma unroll
-      for (int i = 0; i < KW / RPI; ++i) {
-        const int r = i * RPI + lane / LPR;
-        const int64_t o = __shfl_sync(0xffffffffu, from, r) + c * 16;
-        const uint32_t bytes = held && (mask >> r & 1) ? 16 : 0;
-        const int sw = S::kRow == 64 ? (r >> 1) & 3 : r & 7;
-        const uint32_t to = k_s + r * S::kRow + ((c ^ sw) * 16);
+      const uint32_t key = uint32_t(key0) + (g.shared_page ? 0 : lane);
+      const uint32_t off =
+          key - fdiv(key, a.c.page_div) * a.c.page_tokens;
+      const int64_t from = int64_t(page) * a.c.page_b +
+                           int64_t(off) * a.c.token_b +
+                           int64_t(h) * a.c.head_b;
+      if (g.shared_page && mask == (KW == 32 ? 0xffffffffu : 0xffffu)) {
+        const char* src = a.c.k + (from + from_lane);
         if (used) {
-          cp16(to, a.c.k + (bytes ? o : 0), bytes);
-          cp16(to + S::kPart, a.c.v + (bytes ? o : 0), bytes);
+          const uint32_t bytes = held ? 16 : 0;
+          if (!held) src = a.c.k;
+#pragma unroll
+          for (int i = 0; i < KW / RPI; ++i) {
+            const int r = i * RPI;
+            const uint32_t to =
+                k_s + to_lane + r * S::kRow + ((c ^ turned(r + r0)) * 16);
+            cp16(to, src, bytes);
+            cp16(to + S::kPart, src + v_from_k, bytes);
+            if (held) src += RPI * a.c.token_b;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KW / RPI; ++i) {
+          const int r = i * RPI + r0;
+          const int64_t o =
+              (g.shared_page
+                   ? from + r * a.c.token_b
+                   : __shfl_sync(0xffffffffu, from, r)) + c * 16;
+          const uint32_t bytes = held && (mask >> r & 1) ? 16 : 0;
+          const uint32_t to = k_s + r * S::kRow + ((c ^ turned(r)) * 16);
+          if (used) {
+            cp16(to, a.c.k + (bytes ? o : 0), bytes);
+            cp16(to + S::kPart, a.c.v + (bytes ? o : 0), bytes);
+          }
         }
       }
       if (CODES && lane < KW) {
         const int64_t so =
-            ok ? (int64_t(page) * a.c.heads + h) * a.c.page_tokens + off : 0;
+            ok ? (int64_t(page) * a.c.heads + h) * a.c.page_tokens + off +
+                     (g.shared_page ? lane : 0)
+               : 0;
         const uint32_t to =
             scale_s + stage * S::kScales + (warp * 2 * KW + lane) * 4;
         cp4(to, a.c.ks + so, ok ? 4 : 0);
@@ -433,8 +511,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
     // [2^14, 2^15): exact for bf16 and f16 elements down to 2^-38 of it
     uint32_t qf[KS][NT][2];
     float fac[NT][2];
-    const float unit = a.scale * 1.44269504088896341f *
-                       (KIND == KIND_E4M3 ? 256.f : 1.f);
+    const float unit = a.scale * 1.44269504088896341f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = nt * 8 + row8;
@@ -445,9 +522,13 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int d = k * 16 + (CODES ? 2 * col2 + 2 * j : col2 + 8 * j);
+          // as the keys' elements lie: codes come by the 4 of a lane
+          const int d = k * 16 + (!CODES               ? col2 + 8 * j
+                                  : KIND == KIND_E4M3 ? 2 * col2 + 2 * j
+                                                      : 2 * col2 + j);
+          const int d2 = d + (KIND == KIND_INT8 ? 2 : 1);
           uint32_t x = 0;
-          if (qi < nq && d < dim) x = q[d] | uint32_t(q[d + 1]) << 16;
+          if (qi < nq && d < dim) x = q[d] | uint32_t(q[d2]) << 16;
           qf[k][nt][j] = x;
         }
       fac[nt][0] = fac[nt][1] = unit;
@@ -522,28 +603,23 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         if (k * 16 >= dim) break;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int r = mt * 16 + lane % 16;
-          // 16-bit: rows 0-15, then the next 8 elements; codes: the same
-          // with the next 16
-          const int c = (CODES ? k : k * 2) + lane / 16;
-          const int sw = S::kRow == 64 ? (r >> 1) & 3 : r & 7;
+          // 16 bits: 16 rows by 16 elements; codes: by 32
           uint32_t x[4];
-          ldm(x, k_s + r * S::kRow + ((c ^ sw) * 16));
+          ldm(x, (k_s + k_lane + mt * 16 * S::kRow) ^ (k * (CODES ? 16 : 32)));
           if (CODES) {
-            if (KIND == KIND_INT8) {
+            uint32_t f[2][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] ^= 0x80808080u;
+            for (int i = 0; i < 4; ++i) {
+              uint32_t y[2];
+              Codes<KIND>::keys(x[i], y);
+              f[i / 2][i % 2] = y[0];
+              f[i / 2][i % 2 + 2] = y[1];
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t f[4] = {codes2<KIND, false, 0, 1>(x[2 * e]),
-                                     codes2<KIND, false, 0, 1>(x[2 * e + 1]),
-                                     codes2<KIND, false, 2, 3>(x[2 * e]),
-                                     codes2<KIND, false, 2, 3>(x[2 * e + 1])};
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
-                mma<false>(s[mt][nt], f, qf[k + e][nt]);
-            }
+                mma<false>(s[mt][nt], f[e], qf[k + e][nt]);
           } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma<KBF>(s[mt][nt], x, qf[k][nt]);
@@ -565,59 +641,78 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
             vs[mt][i] = sc[KW + mt * 16 + 8 * i + row8];
           }
       }
-      float top[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) top[nt][j] = m[nt][j];
+      // A head's reference m moves only when a score passes it by 8, that
+      // is when a weight would pass 2^8: one vote a step instead of the
+      // maximum over the lanes and the products' rescaling.
+      bool above = false;
+      const uint32_t full = KW == 32 ? 0xffffffffu : 0xffffu;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = i & 1, r = i >> 1;
-            float x = s[mt][nt][i] * fac[nt][j];
-            if (CODES) x *= ks[mt][r];
-            if (!(mask >> (mt * 16 + 8 * r + row8) & 1)) x = -INFINITY;
+            float x = s[mt][nt][i] * fac[nt][i & 1];
+            if (CODES) x *= ks[mt][i >> 1];
             s[mt][nt][i] = x;
-            top[nt][j] = fmaxf(top[nt][j], x);
           }
-      bool moved = false;
-      float keep[NT][2];
+      if (mask != full) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (!(mask >> (mt * 16 + 8 * r + row8) & 1)) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                s[mt][nt][2 * r] = s[mt][nt][2 * r + 1] = -INFINITY;
+            }
+      }
+      float top[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          // over the 8 lanes that hold the column's keys
+          float t = s[0][nt][j];
 #pragma unroll
-          for (int k = 4; k < 32; k *= 2)
-            top[nt][j] = fmaxf(
-                top[nt][j], __shfl_xor_sync(0xffffffffu, top[nt][j], k));
-          moved |= top[nt][j] != m[nt][j];
-          // nothing seen yet: relative to 0, every weight is 0
-          const float t = top[nt][j] == -INFINITY ? 0.f : top[nt][j];
-          keep[nt][j] = ex2(m[nt][j] - t);
-          l[nt][j] *= keep[nt][j];
-          m[nt][j] = top[nt][j];
+          for (int mt = 0; mt < MT; ++mt)
+            t = fmaxf(t, mt ? fmaxf(s[mt][nt][j], s[mt][nt][2 + j])
+                            : s[mt][nt][2 + j]);
           top[nt][j] = t;
+          above |= t > m[nt][j] + 8.f;
         }
-      if (__any_sync(0xffffffffu, moved)) {
+      if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < 2; ++j) {
+            // over the 8 lanes that hold the column's keys
+            float t = fmaxf(top[nt][j], m[nt][j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[k][nt][i] *= keep[nt][i & 1];
+            for (int k = 4; k < 32; k *= 2)
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
+            const float keep = ex2(m[nt][j] - (t == -INFINITY ? 0.f : t));
+            m[nt][j] = t;
+            l[nt][j] *= keep;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              o[k][nt][j] *= keep;
+              o[k][nt][2 + j] *= keep;
+            }
+          }
       }
+      // nothing seen yet: relative to 0, every weight is 0
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          top[nt][j] = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
 
       // weights, and their transposes as the second operand.  A weight's 8
       // (bf16) or 11 (f16) bits alone would cost the result about as much as
       // its own rounding does, so what the rounding of a weight leaves goes
       // through the products too.  A value's scale is folded into its weight.
-      // UP keeps weights and sums in range: f16 weights run up to 2^15, so
-      // that what a head's largest key has a zero for is left to keys down
-      // to 2^-29 of its weight; e4m3 values are 2^-120 of themselves.
+      // UP keeps weights and sums in range: f16 weights run up to 2^15 and
+      // down to 2^-31 of the reference; e4m3 values are 2^-120 of themselves.
       uint32_t p[MT][NT][2], p2[MT][NT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -644,18 +739,15 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       for (int k = 0; k < KS; ++k) {
         if (k * 16 >= dim) break;
         if (CODES) {
-          const int r = lane;                       // 32 keys, 16 elements
-          const int sw = S::kRow == 64 ? (r >> 1) & 3 : r & 7;
-          uint32_t x[4];
-          ldm_t(x, v_s + r * S::kRow + ((k ^ sw) * 16));
+          uint32_t x[4];                            // 32 keys, 16 elements
+          ldm_t(x, (v_s + v_lane) ^ (k * 16));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             // elements 2i are the tile's rows 0-7, elements 2i + 1 its rows
             // 8-15
-            const uint32_t f[4] = {codes2<KIND, true, 0, 2>(x[2 * mt]),
-                                   codes2<KIND, true, 1, 3>(x[2 * mt]),
-                                   codes2<KIND, true, 0, 2>(x[2 * mt + 1]),
-                                   codes2<KIND, true, 1, 3>(x[2 * mt + 1])};
+            uint32_t f[4];
+            Codes<KIND>::values(x[2 * mt], f);
+            Codes<KIND>::values(x[2 * mt + 1], f + 2);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma<true>(o[k][nt], f, p[mt][nt]);
@@ -665,11 +757,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         } else {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const int r = mt * 16 + lane % 8 + (lane / 16) * 8;
-            const int c = k * 2 + (lane / 8 & 1);
-            const int sw = r & 7;
             uint32_t x[4];
-            ldm_t(x, v_s + r * S::kRow + ((c ^ sw) * 16));
+            ldm_t(x, (v_s + v_lane + mt * 16 * S::kRow) ^ (k * 32));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma<VBF>(o[k][nt], x, p[mt][nt]);
@@ -798,34 +887,60 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         auto part_of = [&](int64_t c) {
           return g.parts + (c == c0 ? p0 : 2 * c) * S::kPartFloats;
         };
-        for (int e = threadIdx.x; e < nq * (D / 4); e += kAttendThreads) {
-          const int qi = e / (D / 4), d = e % (D / 4) * 4;
-          float t = -INFINITY;
-#pragma unroll 4
-          for (int64_t c = c0; c <= c1; ++c)
-            t = fmaxf(t, __ldcg(part_of(c) + 2 * qi));
+        // A warp per query finds its state and weighs its parts, a lane a
+        // part, up to kMost at a time; then every thread adds up 4 elements
+        // of the parts.  Both orders are the line's own.
+        constexpr int kMost = 128;
+        const int n = int(c1 - c0) + 1;
+        float* const wt = reinterpret_cast<float*>(ring + used * S::kStage);
+        static_assert(Q * kMost * 4 <= S::kStage, "the weights fit a stage");
+        for (int qi = warp; qi < nq; qi += kAttendWarps) {
+          float t = -INFINITY, sum = 0;
+          for (int i = lane; i < n; i += 32)
+            t = fmaxf(t, __ldcg(part_of(c0 + i) + 2 * qi));
+#pragma unroll
+          for (int k = 16; k; k /= 2)
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
           const float t0 = t == -INFINITY ? 0.f : t;
-          float sum = 0, x[4] = {0, 0, 0, 0};
-#pragma unroll 4
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* pc = part_of(c);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc) + qi);
-            const float4 v = __ldcg(
-                reinterpret_cast<const float4*>(pc + 2 * Q + qi * D + d));
+          for (int i = lane; i < n; i += 32) {
+            const float2 ml =
+                __ldcg(reinterpret_cast<const float2*>(part_of(c0 + i)) + qi);
             const float f = ex2(ml.x - t0);
             sum += ml.y * f;
+            if (i < kMost) wt[qi * kMost + i] = f;
+          }
+#pragma unroll
+          for (int k = 16; k; k /= 2)
+            sum += __shfl_xor_sync(0xffffffffu, sum, k);
+          if (lane == 0) {
+            state[2 * qi] = t0;
+            state[2 * qi + 1] = sum;
+            if (a.lse)
+              a.lse[out_row + qi] =
+                  sum == 0 ? -INFINITY
+                           : (t + log2f(sum)) * 0.693147180559945309f;
+          }
+        }
+        __syncthreads();
+        for (int e = threadIdx.x * 4; e < nq * D; e += kAttendThreads * 4) {
+          const int qi = e / D, d = e % D;
+          float x[4] = {0, 0, 0, 0};
+          auto add = [&](int i, float f) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(
+                part_of(c0 + i) + 2 * Q + e));
             x[0] += v.x * f;
             x[1] += v.y * f;
             x[2] += v.z * f;
             x[3] += v.w * f;
-          }
+          };
+#pragma unroll 8
+          for (int i = 0; i < min(n, kMost); ++i) add(i, wt[qi * kMost + i]);
+          for (int i = kMost; i < n; ++i)
+            add(i, ex2(__ldcg(part_of(c0 + i) + 2 * qi) - state[2 * qi]));
+          const float sum = state[2 * qi + 1];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             if (d + i < dim) put(qi, d + i, sum == 0 ? 0.f : x[i] / sum);
-          if (d == 0 && a.lse)
-            a.lse[out_row + qi] =
-                sum == 0 ? -INFINITY
-                         : (t + log2f(sum)) * 0.693147180559945309f;
         }
       }
     }
@@ -885,6 +1000,7 @@ int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
   AttendGrid g;
   g.groups = (a.group + S::Q - 1) / S::Q;
   g.items = int(a.c.heads) * g.groups;
+  g.shared_page = a.c.page_tokens % S::KW == 0;
   g.counters = static_cast<unsigned int*>(a.ws);
   g.parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
                                      attend_counter_bytes(blocks));
