@@ -49,7 +49,8 @@ template <int KIND, int D, int NT>
 struct AttendShape {
   static constexpr bool kCodes = KIND == KIND_E4M3 || KIND == KIND_INT8;
   static constexpr int kHeld = kCodes ? 1 : 2;           // bytes an element
-  static constexpr int KW = kCodes ? 32 : 16;            // keys a warp's step
+  static constexpr int KW = kCodes ? (D == 64 ? 64 : 32) : 16;  // a warp's step
+  static constexpr int KL = (KW + 31) / 32;              // keys a lane
   static constexpr int TK = KW * kAttendWarps;           // keys of a tile
   static constexpr int MT = KW / 16;                     // row tiles of S^T
   static constexpr int Q = 8 * NT;                       // queries
@@ -62,10 +63,10 @@ struct AttendShape {
   // of three.
   static constexpr int kBlocks = D == 256 ? 1 : kCodes ? 3 : 2;
   static constexpr int kS = D == 256  ? 3
-                            : kCodes ? (D == 64 ? 4 : 2)
+                            : kCodes ? 2
                                      : (D == 64 ? 6 : 3);
   static constexpr int kScales = kCodes ? kAttendWarps * 2 * KW * 4 : 0;
-  static constexpr int kMasks = kAttendWarps * 4;
+  static constexpr int kMasks = kAttendWarps * KL * 4;
   static constexpr int kState = kAttendWarps * Q * 2 * 4;
   static constexpr int kSmem =
       kS * (kStage + kScales + kMasks) + kState + 64;
@@ -241,6 +242,7 @@ struct AttendGrid {
   int groups = 1;       // groups of Q queries of a key head
   int least = 1;        // tiles a block takes at least
   int shared_page = 0;  // the keys of a warp's step share a page
+  int q_pairs = 0;      // the queries allow 4-byte loads
   float* parts = nullptr;
   unsigned int* counters = nullptr;
 };
@@ -294,7 +296,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
                        : KIND == KIND_E4M3 ? 0x1p60f
                                            : 1.f;
   constexpr float DOWN = KIND == KIND_F16 ? 0x1p-7f : UP;
-  constexpr int KW = S::KW, TK = S::TK, MT = S::MT, NS = S::kS, Q = S::Q;
+  constexpr int KW = S::KW, KL = S::KL, TK = S::TK, MT = S::MT, NS = S::kS;
+  constexpr int Q = S::Q;
   constexpr int KS = D / 16;                 // 16-element steps along dim
   extern __shared__ __align__(1024) char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -305,7 +308,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   char* const scale_ring = ring + NS * S::kStage;
   uint32_t* const masks =
       reinterpret_cast<uint32_t*>(scale_ring + NS * S::kScales);
-  float* const state = reinterpret_cast<float*>(masks + NS * kAttendWarps);
+  float* const state = reinterpret_cast<float*>(masks + NS * kAttendWarps * KL);
   int64_t* const share = reinterpret_cast<int64_t*>(
       (reinterpret_cast<uintptr_t>(state + kAttendWarps * Q * 2) + 7) & ~7ull);
   const uint32_t ring_s = uint32_t(__cvta_generic_to_shared(ring));
@@ -393,9 +396,11 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
 
   // --- the ring's filling side ---
   AttendAt ld = at;
-  // of this lane's key (or, where a step's keys share a page, of its first
-  // key) of the tile to fill next
-  int page = -1;
+  struct Pages {
+    // of this lane's keys of a tile or, where a step's keys share a page, of
+    // all of them
+    int of[KL];
+  };
   constexpr int LPR = S::kRow / 16;            // lanes a row
   constexpr int RPI = 32 / LPR;                // rows an instruction
   const int c = lane % LPR, r0 = lane / LPR;
@@ -405,83 +410,143 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   const uint32_t to_lane = r0 * S::kRow;
   const int64_t from_lane = r0 * a.c.token_b + c * 16;
   const int64_t v_from_k = a.c.v - a.c.k;
-  auto fetch = [&] {
-    const int key = ld.tile * TK + warp * KW + (g.shared_page ? 0 : lane);
-    page = -1;
-    const int reach = g.shared_page ? KW : 1;
-    if (ld.left > 0 && (g.shared_page || lane < KW) &&
-        key + reach > ld.first && key < ld.n)
-      page = a.table[int64_t(ld.b) * a.table_stride +
-                     fdiv(uint32_t(key), a.c.page_div)];
+  constexpr uint32_t full = KW >= 32 ? 0xffffffffu : (1u << KW % 32) - 1;
+  auto fetch = [&](Pages* pg) {
+    const int key0 = ld.tile * TK + warp * KW;
+#pragma unroll
+    for (int i = 0; i < KL; ++i) {
+      const int key = key0 + (g.shared_page ? 0 : lane + 32 * i);
+      const int reach = g.shared_page ? KW : 1;
+      pg->of[i] = -1;
+      if (ld.left > 0 && (g.shared_page || KW >= 32 || lane < KW) &&
+          key + reach > ld.first && key < ld.n && (i == 0 || !g.shared_page))
+        pg->of[i] = a.table[int64_t(ld.b) * a.table_stride +
+                            fdiv(uint32_t(key), a.c.page_div)];
+      if (i && g.shared_page) pg->of[i] = pg->of[0];
+    }
   };
-  auto fill = [&](int stage) {
-    if (ld.left > 0) {
-      const int key0 = ld.tile * TK + warp * KW;
-      const uint32_t h = uint32_t(ld.item / g.groups);
-      const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
-      const bool in = lane < KW && key0 + lane >= ld.first &&
-                      key0 + lane < ld.n;
-      const bool ok = in && page >= 0 && page < a.c.pages;
+  auto fill = [&](int stage, const Pages& pg) {
+    const int key0 = ld.tile * TK + warp * KW;
+    const uint32_t h = uint32_t(ld.item / g.groups);
+    const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
+    uint32_t mask[KL], off[KL];
+    int64_t from[KL];
+    bool all = g.shared_page;
+#pragma unroll
+    for (int i = 0; i < KL; ++i) {
+      const int at_key = key0 + lane + 32 * i;
+      const bool in = (KW >= 32 || lane < KW) && at_key >= ld.first &&
+                      at_key < ld.n;
+      const bool ok = in && pg.of[i] >= 0 && pg.of[i] < a.c.pages;
       if (in && !ok && a.status) atomicOr(a.status, kStatusRange);
-      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) masks[stage * kAttendWarps + warp] = mask;
-      const uint32_t key = uint32_t(key0) + (g.shared_page ? 0 : lane);
-      const uint32_t off =
-          key - fdiv(key, a.c.page_div) * a.c.page_tokens;
-      const int64_t from = int64_t(page) * a.c.page_b +
-                           int64_t(off) * a.c.token_b +
-                           int64_t(h) * a.c.head_b;
-      if (g.shared_page && mask == (KW == 32 ? 0xffffffffu : 0xffffu)) {
-        const char* src = a.c.k + (from + from_lane);
-        if (used) {
-          const uint32_t bytes = held ? 16 : 0;
-          if (!held) src = a.c.k;
-#pragma unroll
-          for (int i = 0; i < KW / RPI; ++i) {
-            const int r = i * RPI;
-            const uint32_t to =
-                k_s + to_lane + r * S::kRow + ((c ^ turned(r + r0)) * 16);
-            cp16(to, src, bytes);
-            cp16(to + S::kPart, src + v_from_k, bytes);
-            if (held) src += RPI * a.c.token_b;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < KW / RPI; ++i) {
-          const int r = i * RPI + r0;
-          const int64_t o =
-              (g.shared_page
-                   ? from + r * a.c.token_b
-                   : __shfl_sync(0xffffffffu, from, r)) + c * 16;
-          const uint32_t bytes = held && (mask >> r & 1) ? 16 : 0;
-          const uint32_t to = k_s + r * S::kRow + ((c ^ turned(r)) * 16);
-          if (used) {
-            cp16(to, a.c.k + (bytes ? o : 0), bytes);
-            cp16(to + S::kPart, a.c.v + (bytes ? o : 0), bytes);
-          }
-        }
-      }
-      if (CODES && lane < KW) {
+      mask[i] = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) masks[(stage * kAttendWarps + warp) * KL + i] = mask[i];
+      all = all && mask[i] == full;
+      // (of a shared page, the step's first key)
+      const uint32_t key = uint32_t(g.shared_page ? key0 : at_key);
+      off[i] = key - fdiv(key, a.c.page_div) * a.c.page_tokens;
+      from[i] = int64_t(pg.of[i]) * a.c.page_b +
+                int64_t(off[i]) * a.c.token_b + int64_t(h) * a.c.head_b;
+      if (CODES && (KW >= 32 || lane < KW)) {
         const int64_t so =
-            ok ? (int64_t(page) * a.c.heads + h) * a.c.page_tokens + off +
-                     (g.shared_page ? lane : 0)
+            ok ? (int64_t(pg.of[i]) * a.c.heads + h) * a.c.page_tokens +
+                     off[i] + (g.shared_page ? lane + 32 * i : 0)
                : 0;
-        const uint32_t to =
-            scale_s + stage * S::kScales + (warp * 2 * KW + lane) * 4;
+        const uint32_t to = scale_s + stage * S::kScales +
+                            (warp * 2 * KW + lane + 32 * i) * 4;
         cp4(to, a.c.ks + so, ok ? 4 : 0);
         cp4(to + KW * 4, a.c.vs + so, ok ? 4 : 0);
       }
-      attend_next<TK>(a, g.items, &ld);
-      fetch();
     }
-    cp_commit();
+    if (all) {
+      const char* src = a.c.k + (from[0] + from_lane);
+      if (used) {
+        const uint32_t bytes = held ? 16 : 0;
+        if (!held) src = a.c.k;
+#pragma unroll
+        for (int i = 0; i < KW / RPI; ++i) {
+          const int r = i * RPI;
+          const uint32_t to =
+              k_s + to_lane + r * S::kRow + ((c ^ turned(r + r0)) * 16);
+          cp16(to, src, bytes);
+          cp16(to + S::kPart, src + v_from_k, bytes);
+          if (held) src += RPI * a.c.token_b;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < KW / RPI; ++i) {
+        const int r = i * RPI + r0, kl = i * RPI / 32;
+        const int64_t o =
+            (g.shared_page ? from[0] + r * a.c.token_b
+                           : __shfl_sync(0xffffffffu, from[kl], r % 32)) +
+            c * 16;
+        const uint32_t bytes = held && (mask[kl] >> r % 32 & 1) ? 16 : 0;
+        const uint32_t to = k_s + r * S::kRow + ((c ^ turned(r)) * 16);
+        if (used) {
+          cp16(to, a.c.k + (bytes ? o : 0), bytes);
+          cp16(to + S::kPart, a.c.v + (bytes ? o : 0), bytes);
+        }
+      }
+    }
   };
 
-  if (at.left > 0) {
-    fetch();
+  // --- the queries, as they lie ---
+  // as the second operand's fragments: lane row8 of a column tile holds
+  // query row8's elements
+  uint32_t qf[KS][NT][2];
+  const bool q_pairs = g.q_pairs;
+  auto load_q = [&](const AttendAt& p) {
+    const int h = p.item / g.groups, q0 = (p.item - h * g.groups) * Q;
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s) fill(s);
+    for (int nt = 0; nt < NT; ++nt) {
+      const int qi = nt * 8 + row8;
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q.p) +
+                          int64_t(p.b) * a.q.ts +
+                          int64_t(h * a.group + q0 + qi) * a.q.hs;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        // as the keys' elements lie: codes come by the 4 of a lane
+        const int d = k * 16 + (CODES ? 2 * col2 : col2);
+        const int d2 = d + (CODES ? 2 : 8);
+        uint32_t x = 0, y = 0;
+        if (qi < a.group - q0 && d < dim) {
+          if (q_pairs) {
+            x = *reinterpret_cast<const uint32_t*>(q + d);
+            if (d2 < dim) y = *reinterpret_cast<const uint32_t*>(q + d2);
+          } else {
+            x = q[d] | uint32_t(q[d + 1]) << 16;
+            if (d2 < dim) y = q[d2] | uint32_t(q[d2 + 1]) << 16;
+          }
+        }
+        // int8 pairs are elements 0 2 and 1 3
+        qf[k][nt][0] = KIND == KIND_INT8 ? __byte_perm(x, y, 0x5410) : x;
+        qf[k][nt][1] = KIND == KIND_INT8 ? __byte_perm(x, y, 0x7632) : y;
+      }
+    }
+  };
+
+  // the first steps' pages all at once, then their fills
+  Pages next;
+  if (at.left > 0) {
+    Pages pg[NS - 1];
+    AttendAt to[NS - 1];
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      to[s] = ld;
+      fetch(&pg[s]);
+      if (ld.left > 0) attend_next<TK>(a, g.items, &ld);
+    }
+    fetch(&next);
+    load_q(at);
+    const AttendAt on = ld;
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      ld = to[s];
+      if (ld.left > 0) fill(s, pg[s]);
+      cp_commit();
+    }
+    ld = on;
   }
   // sequences without keys
   for (int b = blockIdx.x; b < a.seqs; b += gridDim.x) {
@@ -506,31 +571,13 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
     const int nq = min(Q, a.group - q0);
     const int steps = int(min(at.left, int64_t(at.hi - at.tile)));
 
-    // the queries as the second operand's fragments; codes are met by f16
-    // queries, scaled by a power of two so that the largest element lies in
-    // [2^14, 2^15): exact for bf16 and f16 elements down to 2^-38 of it
-    uint32_t qf[KS][NT][2];
+    // Codes are met by f16 queries, scaled by a power of two so that the
+    // largest element lies in [2^14, 2^15): exact for bf16 and f16 elements
+    // down to 2^-38 of it.
     float fac[NT][2];
     const float unit = a.scale * 1.44269504088896341f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int qi = nt * 8 + row8;
-      const uint16_t* q = reinterpret_cast<const uint16_t*>(a.q.p) +
-                          int64_t(at.b) * a.q.ts +
-                          int64_t(h * a.group + q0 + qi) * a.q.hs;
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          // as the keys' elements lie: codes come by the 4 of a lane
-          const int d = k * 16 + (!CODES               ? col2 + 8 * j
-                                  : KIND == KIND_E4M3 ? 2 * col2 + 2 * j
-                                                      : 2 * col2 + j);
-          const int d2 = d + (KIND == KIND_INT8 ? 2 : 1);
-          uint32_t x = 0;
-          if (qi < nq && d < dim) x = q[d] | uint32_t(q[d2]) << 16;
-          qf[k][nt][j] = x;
-        }
       fac[nt][0] = fac[nt][1] = unit;
       if (CODES) {
         const bool in_bf = a.elem == LM_BF16;
@@ -583,12 +630,23 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
 
     for (int step = 0; step < steps; ++step) {
       __syncwarp();
-      fill(stage == 0 ? NS - 1 : stage - 1);
+      if (ld.left > 0) {
+        fill(stage == 0 ? NS - 1 : stage - 1, next);
+        attend_next<TK>(a, g.items, &ld);
+        fetch(&next);
+      }
+      cp_commit();
       cp_wait<NS - 1>();
       __syncwarp();
       const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
       const uint32_t v_s = k_s + S::kPart;
-      const uint32_t mask = masks[stage * kAttendWarps + warp];
+      uint32_t mask[KL];
+      bool part = false;
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        mask[i] = masks[(stage * kAttendWarps + warp) * KL + i];
+        part |= mask[i] != full;
+      }
 
       // S^T = K Q^T
       float s[MT][NT][4];
@@ -645,7 +703,6 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       // is when a weight would pass 2^8: one vote a step instead of the
       // maximum over the lanes and the products' rescaling.
       bool above = false;
-      const uint32_t full = KW == 32 ? 0xffffffffu : 0xffffu;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -656,12 +713,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
             if (CODES) x *= ks[mt][i >> 1];
             s[mt][nt][i] = x;
           }
-      if (mask != full) {
+      if (part) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (!(mask >> (mt * 16 + 8 * r + row8) & 1)) {
+            if (!(mask[mt / 2] >> (mt % 2 * 16 + 8 * r + row8) & 1)) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 s[mt][nt][2 * r] = s[mt][nt][2 * r + 1] = -INFINITY;
@@ -740,14 +797,15 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         if (k * 16 >= dim) break;
         if (CODES) {
           uint32_t x[4];                            // 32 keys, 16 elements
-          ldm_t(x, (v_s + v_lane) ^ (k * 16));
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
+            if (mt % 2 == 0)
+              ldm_t(x, (v_s + v_lane + mt * 16 * S::kRow) ^ (k * 16));
             // elements 2i are the tile's rows 0-7, elements 2i + 1 its rows
             // 8-15
             uint32_t f[4];
-            Codes<KIND>::values(x[2 * mt], f);
-            Codes<KIND>::values(x[2 * mt + 1], f + 2);
+            Codes<KIND>::values(x[mt % 2 * 2], f);
+            Codes<KIND>::values(x[mt % 2 * 2 + 1], f + 2);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma<true>(o[k][nt], f, p[mt][nt]);
@@ -768,6 +826,24 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         }
       }
       if (++stage == NS) stage = 0;
+    }
+
+    // the next head's queries are on their way while this one's parts join
+    const AttendAt done = at;
+    const int tiles = at.hi - at.lo;
+    const int64_t item_at = line_b + int64_t(at.item) * tiles;
+    at.left -= steps;
+    at.tile += steps;
+    if (at.left > 0) {
+      if (++at.item == g.items) {
+        line_b += int64_t(tiles) * g.items;
+        at.item = 0;
+        do {
+          attend_span<TK>(a, ++at.b, &at);
+        } while (at.hi <= at.lo);
+      }
+      at.tile = at.lo;
+      load_q(at);
     }
 
     // --- the warps' states join; each warp's output lies in the stage that
@@ -819,9 +895,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         }
     }
     __syncthreads();
-    const int tiles = at.hi - at.lo;
     const bool whole = steps == tiles;
-    const int64_t item_at = line_b + int64_t(at.item) * tiles;
     const int64_t c0 = whole ? 0 : ((item_at + 1) * blocks - 1) / total;
     const int64_t c1 = whole ? 0 : ((item_at + tiles) * blocks - 1) / total;
     float* part = nullptr;
@@ -829,9 +903,9 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       part = g.parts +
              (2 * int64_t(blockIdx.x) + (begin < item_at ? 1 : 0)) *
                  S::kPartFloats;
-    const int64_t out_row = int64_t(at.b) * a.heads_q + h * a.group + q0;
+    const int64_t out_row = int64_t(done.b) * a.heads_q + h * a.group + q0;
     char* const out0 =
-        a.out.p + (int64_t(at.b) * a.out.ts +
+        a.out.p + (int64_t(done.b) * a.out.ts +
                    int64_t(h * a.group + q0) * a.out.hs) * 2;
     const bool out_bf = a.elem == LM_BF16;
     auto put = [&](int qi, int d, float x) {
@@ -896,7 +970,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
         static_assert(Q * kMost * 4 <= S::kStage, "the weights fit a stage");
         for (int qi = warp; qi < nq; qi += kAttendWarps) {
           float t = -INFINITY, sum = 0;
-          for (int i = lane; i < n; i += 32)
+          float2 ml0 = make_float2(-INFINITY, 0);
+          if (lane < n)
+            ml0 = __ldcg(reinterpret_cast<const float2*>(part_of(c0 + lane)) +
+                         qi);
+          t = ml0.x;
+          for (int i = lane + 32; i < n; i += 32)
             t = fmaxf(t, __ldcg(part_of(c0 + i) + 2 * qi));
 #pragma unroll
           for (int k = 16; k; k /= 2)
@@ -904,7 +983,9 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
           const float t0 = t == -INFINITY ? 0.f : t;
           for (int i = lane; i < n; i += 32) {
             const float2 ml =
-                __ldcg(reinterpret_cast<const float2*>(part_of(c0 + i)) + qi);
+                i < 32 ? ml0
+                       : __ldcg(reinterpret_cast<const float2*>(
+                                    part_of(c0 + i)) + qi);
             const float f = ex2(ml.x - t0);
             sum += ml.y * f;
             if (i < kMost) wt[qi * kMost + i] = f;
@@ -945,20 +1026,6 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       }
     }
     __syncthreads();
-
-    // on to the next head or sequence
-    at.left -= steps;
-    at.tile += steps;
-    if (at.left > 0) {
-      if (++at.item == g.items) {
-        line_b += int64_t(tiles) * g.items;
-        at.item = 0;
-        do {
-          attend_span<TK>(a, ++at.b, &at);
-        } while (at.hi <= at.lo);
-      }
-      at.tile = at.lo;
-    }
   }
   cp_wait<0>();
 }
@@ -1001,6 +1068,8 @@ int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
   g.groups = (a.group + S::Q - 1) / S::Q;
   g.items = int(a.c.heads) * g.groups;
   g.shared_page = a.c.page_tokens % S::KW == 0;
+  g.q_pairs = reinterpret_cast<uintptr_t>(a.q.p) % 4 == 0 &&
+              a.q.ts % 2 == 0 && a.q.hs % 2 == 0;
   g.counters = static_cast<unsigned int*>(a.ws);
   g.parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
                                      attend_counter_bytes(blocks));
