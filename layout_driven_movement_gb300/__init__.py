@@ -756,37 +756,67 @@ def build_layout(spec) -> Layout:
 _ELEM = {"bfloat16": 1, "float16": 2, "float32": 3}
 _STORES = {None: 0, "same": 0, "e4m3": 1, "int8": 2}
 _SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_dtype_names: dict = {}
+_current_stream = None
+
+# A decoding step makes a handful of these calls, each for a few microseconds
+# of device work: the helpers below keep to the tensor properties that cost
+# least and build messages only when a check fails.
+
+
+def _dtype(dtype) -> str:
+    """A torch dtype's name, looked up once."""
+    name = _dtype_names.get(dtype)
+    if name is None:
+        name = _dtype_names[dtype] = str(dtype).rpartition(".")[2]
+    return name
 
 
 def _elem(dtype) -> int:
-    code = _ELEM.get(str(dtype).rpartition(".")[2])
+    code = _ELEM.get(_dtype(dtype))
     if code is None:
         raise ValueError(f"{dtype} is none of bfloat16, float16, float32")
     return code
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _stream(stream) -> int:
+    """The stream's handle; None: torch's current stream of the current
+    device."""
+    global _current_stream
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    if _current_stream is None:
+        import torch
+        raw = torch._C._cuda_getCurrentRawStream
+        device = torch.cuda.current_device
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return _current_stream()
+
+
+def _wanted(what: str):
+    raise ValueError(what + " is wanted")
 
 
 def _rows(t, what: str) -> _Rows:
     """lm_rows of a CUDA tensor [tokens, heads, dim], dim contiguous."""
-    _need(t.is_cuda and t.dim() == 3, f"{what}: a CUDA tensor [tokens, heads, "
-          "dim] is wanted")
-    n, h, d = t.shape
+    shape = t.shape
+    if not t.is_cuda or len(shape) != 3:
+        _wanted(f"{what}: a CUDA tensor [tokens, heads, dim]")
+    n, h, d = shape
     ts, hs, ds = t.stride()
-    _need(d == 1 or ds == 1, f"{what}: dim must be contiguous")
-    last = (n - 1) * ts + (h - 1) * hs + d if n and h and d else 0
-    return _Rows(t.data_ptr(), last, ts, hs)
+    if ds != 1 and d != 1:
+        _wanted(f"{what}: a contiguous dim")
+    return _Rows(t.data_ptr(),
+                 (n - 1) * ts + (h - 1) * hs + d if n and h and d else 0,
+                 ts, hs)
 
 
 def _vector(t, dtypes, n, what: str):
     """The pointer of a contiguous CUDA vector of n elements."""
-    _need(t.is_cuda and t.is_contiguous() and t.dim() == 1
-          and t.shape[0] == n and str(t.dtype).rpartition(".")[2] in dtypes,
-          f"{what}: a contiguous CUDA vector of {n} {' or '.join(dtypes)} "
-          "is wanted")
+    if not t.is_cuda or t.shape != (n,) or _dtype(t.dtype) not in dtypes \
+            or not t.is_contiguous():
+        _wanted(f"{what}: a contiguous CUDA vector of {n} "
+                f"{' or '.join(dtypes)}")
     return t.data_ptr()
 
 
@@ -838,28 +868,30 @@ class RopePlan:
         return list(f), amp.value
 
 
+def _table(plan, table) -> tuple[int, int]:
+    """(pointer, positions) of a rotary table."""
+    if not table.is_cuda or _elem(table.dtype) != 3 \
+            or not table.is_contiguous() \
+            or table.numel() != table.shape[0] * plan.rotary_dim:
+        _wanted("table: a contiguous float32 CUDA tensor [positions, "
+                "rotary_dim]")
+    return table.data_ptr(), table.shape[0]
+
+
 def rope_table(plan: RopePlan, table, stream=None) -> None:
     """Enqueue the cosines and sines of positions 0, 1, ... into a contiguous
     float32 CUDA tensor [positions, rotary_dim] (or [positions, 2,
     rotary_dim / 2])."""
-    _need(table.is_cuda and table.is_contiguous() and _elem(table.dtype) == 3
-          and table.numel() == table.shape[0] * plan.rotary_dim,
-          "table: a contiguous float32 CUDA tensor [positions, rotary_dim] "
-          "is wanted")
-    _check(lib().lm_rope_table(plan._h, table.data_ptr(), table.shape[0],
-                               table.numel(), _stream_handle(stream)),
-           "lm_rope_table")
+    p, n = _table(plan, table)
+    _check(lib().lm_rope_table(plan._h, p, n, table.numel(),
+                               _stream(stream)), "lm_rope_table")
 
 
 def _turn_args(plan, positions, table, tokens):
-    _need(positions is not None and table is not None,
-          "rope needs positions and a table")
-    _need(table.is_cuda and table.is_contiguous() and _elem(table.dtype) == 3
-          and table.numel() == table.shape[0] * plan.rotary_dim,
-          "table: a contiguous float32 CUDA tensor [positions, rotary_dim] "
-          "is wanted")
-    p = _vector(positions, ("int32", "int64"), tokens, "positions")
-    return p, positions.element_size(), table.data_ptr(), table.shape[0]
+    if positions is None or table is None:
+        _wanted("rope: positions and a table")
+    p = _vector(positions, ("int64", "int32"), tokens, "positions")
+    return (p, positions.element_size(), *_table(plan, table))
 
 
 def rope(plan: RopePlan, x, positions, table, out, inverse: bool = False,
@@ -867,14 +899,16 @@ def rope(plan: RopePlan, x, positions, table, out, inverse: bool = False,
     """Enqueue out[t, h] = x[t, h] turned by positions[t] (see lm_rope): x and
     out [tokens, heads, head_dim] of one type, any token and head strides, out
     may be x.  inverse=True turns back, which is also the gradient."""
-    _need(x.shape == out.shape and x.dtype == out.dtype
-          and x.shape[-1] == plan.head_dim,
-          "x and out: [tokens, heads, head_dim] of one type are wanted")
+    shape, dtype = x.shape, x.dtype
+    if shape != out.shape or dtype != out.dtype or shape[-1] != plan.head_dim:
+        _wanted("x and out: [tokens, heads, head_dim] of one type")
     xr, orr = _rows(x, "x"), _rows(out, "out")
-    n, h, _ = x.shape
-    _check(lib().lm_rope(plan._h, _elem(x.dtype), xr, orr, n, h,
-                         *_turn_args(plan, positions, table, n),
-                         int(inverse), _stream_handle(stream)), "lm_rope")
+    n, h, _ = shape
+    rc = lib().lm_rope(plan._h, _elem(dtype), xr, orr, n, h,
+                       *_turn_args(plan, positions, table, n),
+                       1 if inverse else 0, _stream(stream))
+    if rc:
+        _check(rc, "lm_rope")
 
 
 class KVPlan:
@@ -929,15 +963,15 @@ class KVCache:
     def __init__(self, plan: KVPlan, k, v, k_scale=None, v_scale=None,
                  pages: int | None = None):
         for t, what in ((k, "k"), (v, "v")):
-            _need(t.is_cuda and t.element_size() == plan.held_bytes,
-                  f"{what}: a CUDA tensor of {plan.held_bytes}-byte elements "
-                  "is wanted")
+            if not t.is_cuda or t.element_size() != plan.held_bytes:
+                _wanted(f"{what}: a CUDA tensor of {plan.held_bytes}-byte "
+                        "elements")
         scales = 0
         if plan.store is not None:
             for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                _need(t is not None and t.is_cuda and t.is_contiguous()
-                      and _elem(t.dtype) == 3,
-                      f"{what}: a contiguous float32 CUDA tensor is wanted")
+                if t is None or not t.is_cuda or not t.is_contiguous() \
+                        or _elem(t.dtype) != 3:
+                    _wanted(f"{what}: a contiguous float32 CUDA tensor")
             scales = min(k_scale.numel(), v_scale.numel())
         ke, ve = _extent(k), _extent(v)
         if pages is None:
@@ -950,11 +984,10 @@ class KVCache:
             v_scale.data_ptr() if scales else None, scales, self.pages)
 
 
-def _kv_rows(t, plan, heads, dtype, what):
-    _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == plan.dim
-          and (dtype is None or t.dtype == dtype),
-          f"{what}: [tokens, {heads}, {plan.dim}]"
-          + (f" of {dtype}" if dtype else "") + " is wanted")
+def _kv_rows(t, plan, dtype, what):
+    if t.shape[-1] != plan.dim or (dtype is not None and t.dtype != dtype):
+        _wanted(f"{what}: [tokens, heads, {plan.dim}]"
+                + (f" of {dtype}" if dtype is not None else ""))
     return _rows(t, what)
 
 
@@ -965,28 +998,32 @@ def kv_write(cache: KVCache, k, v, slots, rope: RopePlan | None = None,
     negative: skipped), quantised as the plan says; with ``rope`` the keys are
     turned by ``positions`` on the way (see lm_kv_write)."""
     p = cache.plan
-    kr = _kv_rows(k, p, p.heads, p.dtype, "k")
-    vr = _kv_rows(v, p, p.heads, p.dtype, "v")
-    n = k.shape[0]
-    _need(v.shape[0] == n, "k and v: as many tokens are wanted")
-    turn = (None, 0, None, 0)
+    kr, vr = _kv_rows(k, p, p.dtype, "k"), _kv_rows(v, p, p.dtype, "v")
+    n, heads, _ = k.shape
+    if heads != p.heads or v.shape != k.shape:
+        _wanted(f"k and v: [tokens, {p.heads}, {p.dim}], as many tokens in "
+                "each,")
+    slots_p = _vector(slots, ("int64",), n, "slots")
     if rope is not None:
-        turn = _turn_args(rope, positions, table, n)
-    _check(lib().lm_kv_write(p._h, cache._c, kr, vr, n,
-                             _vector(slots, ("int64",), n, "slots"),
-                             rope._h if rope is not None else None, *turn,
-                             _stream_handle(stream)), "lm_kv_write")
+        rc = lib().lm_kv_write(p._h, cache._c, kr, vr, n, slots_p, rope._h,
+                               *_turn_args(rope, positions, table, n),
+                               _stream(stream))
+    else:
+        rc = lib().lm_kv_write(p._h, cache._c, kr, vr, n, slots_p, None, None,
+                               0, None, 0, _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_write")
 
 
-def _table_args(page_table, lens):
-    seqs = lens.shape[0]
-    _need(page_table.is_cuda and page_table.dim() == 2
-          and page_table.shape[0] == seqs
-          and str(page_table.dtype) == "torch.int32"
-          and (page_table.shape[1] <= 1 or page_table.stride(1) == 1),
-          "page_table: an int32 CUDA tensor [sequences, pages] with "
-          "contiguous rows is wanted")
-    return page_table.data_ptr(), page_table.stride(0)
+def _page_table(page_table, seqs):
+    """(pointer, row stride, pages a row)."""
+    shape = page_table.shape
+    if not page_table.is_cuda or len(shape) != 2 or shape[0] != seqs \
+            or _dtype(page_table.dtype) != "int32" \
+            or (shape[1] > 1 and page_table.stride(1) != 1):
+        _wanted("page_table: an int32 CUDA tensor [sequences, pages] with "
+                "contiguous rows")
+    return page_table.data_ptr(), page_table.stride(0), shape[1]
 
 
 def kv_read(cache: KVCache, page_table, lens, starts, k_out, v_out,
@@ -996,17 +1033,19 @@ def kv_read(cache: KVCache, page_table, lens, starts, k_out, v_out,
     float16 or float32); page_table int32 [sequences, pages], lens int32
     [sequences], starts int32 [sequences + 1] (see lm_kv_read)."""
     p = cache.plan
-    kr = _kv_rows(k_out, p, p.heads, None, "k_out")
-    vr = _kv_rows(v_out, p, p.heads, k_out.dtype, "v_out")
-    _need(k_out.shape == v_out.shape, "k_out and v_out: one shape is wanted")
+    dtype, shape = k_out.dtype, k_out.shape
+    kr, vr = _kv_rows(k_out, p, None, "k_out"), _kv_rows(v_out, p, dtype,
+                                                         "v_out")
+    if shape != v_out.shape or shape[1] != p.heads:
+        _wanted(f"k_out and v_out: [rows, {p.heads}, {p.dim}], one shape,")
     n = lens.shape[0]
     lp = _vector(lens, ("int32",), n, "lens")
     sp = _vector(starts, ("int32",), n + 1, "starts")
-    tp, ts = _table_args(page_table, lens)
-    _check(lib().lm_kv_read(p._h, cache._c, tp, ts, n, page_table.shape[1],
-                            lp, sp, _elem(k_out.dtype), kr, vr,
-                            k_out.shape[0], _stream_handle(stream)),
-           "lm_kv_read")
+    tp, ts, pages = _page_table(page_table, n)
+    rc = lib().lm_kv_read(p._h, cache._c, tp, ts, n, pages, lp, sp,
+                          _elem(dtype), kr, vr, shape[0], _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_read")
 
 
 def kv_attend_workspace(plan: KVPlan, seqs: int, heads_q: int) -> int:
@@ -1027,26 +1066,27 @@ def kv_attend(cache: KVCache, q, page_table, lens, out, workspace=None,
     [sequences, query heads].  scale defaults to dim ** -0.5 (see
     lm_kv_attend)."""
     p = cache.plan
-    n, hq = q.shape[0], q.shape[1]
-    qr = _kv_rows(q, p, hq, p.dtype, "q")
-    orr = _kv_rows(out, p, hq, p.dtype, "out")
-    _need(out.shape[0] == n and lens.shape[0] == n,
-          "q, out and lens: as many sequences are wanted")
+    qr, orr = _kv_rows(q, p, p.dtype, "q"), _kv_rows(out, p, p.dtype, "out")
+    shape = q.shape
+    if out.shape != shape:
+        _wanted("q and out: one shape")
+    n, hq, d = shape
     lp = _vector(lens, ("int32",), n, "lens")
-    tp, ts = _table_args(page_table, lens)
+    tp, ts, pages = _page_table(page_table, n)
+    lse_p = ws_p = None
+    ws_bytes = 0
     if lse is not None:
-        _need(lse.is_cuda and lse.is_contiguous() and _elem(lse.dtype) == 3
-              and lse.numel() == n * hq,
-              "lse: a contiguous float32 CUDA tensor [sequences, query heads] "
-              "is wanted")
-    wp, wb = (None, 0)
+        if not lse.is_cuda or not lse.is_contiguous() \
+                or _elem(lse.dtype) != 3 or lse.numel() != n * hq:
+            _wanted("lse: a contiguous float32 CUDA tensor [sequences, query "
+                    "heads]")
+        lse_p = lse.data_ptr()
     if workspace is not None:
-        _need(workspace.is_cuda and workspace.is_contiguous(),
-              "workspace: a contiguous CUDA tensor is wanted")
-        wp, wb = (workspace.data_ptr(),
-                  workspace.numel() * workspace.element_size())
-    _check(lib().lm_kv_attend(
-        p._h, cache._c, qr, orr, n, hq, tp, ts, page_table.shape[1], lp,
-        int(window), p.dim ** -0.5 if scale is None else scale,
-        lse.data_ptr() if lse is not None else None, wp, wb,
-        _stream_handle(stream)), "lm_kv_attend")
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            _wanted("workspace: a contiguous CUDA tensor")
+        ws_p, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    rc = lib().lm_kv_attend(p._h, cache._c, qr, orr, n, hq, tp, ts, pages, lp,
+                            window, d ** -0.5 if scale is None else scale,
+                            lse_p, ws_p, ws_bytes, _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_attend")
