@@ -5,7 +5,7 @@
 
 namespace lm {
 
-int attend_device(int* dev_out, int* sms) {
+int kv_device(int* dev_out, int* sms) {
   static std::mutex mu;
   static int known[64] = {};
   int dev = 0;
@@ -26,7 +26,7 @@ int attend_device(int* dev_out, int* sms) {
 
 int attend_workspace(int store, int dim, int group, int64_t* bytes) {
   int dev = 0, sms = 0;
-  const int rc = attend_device(&dev, &sms);
+  const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
   const int64_t d = attend_dim(dim), q = 8 * attend_tiles(group);
   const int64_t blocks = sms * (d == 256 ? 1 : store == LM_KV_SAME ? 2 : 3);

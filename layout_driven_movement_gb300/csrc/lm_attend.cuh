@@ -1032,9 +1032,6 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
 
 // --- launch --------------------------------------------------------------------
 
-// The current device (below 64) and its SMs (lm_attend.cu).
-int attend_device(int* dev, int* sms);
-
 // Queries a block holds at once: 8 when a key head has no more, else 16; a
 // larger group reads its keys again per 16.
 inline int attend_tiles(int group) { return group <= 8 ? 1 : 2; }
@@ -1050,7 +1047,7 @@ template <int KIND, int D, int NT>
 int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
   using S = AttendShape<KIND, D, NT>;
   int sms = 0, dev = 0;
-  const int rc = attend_device(&dev, &sms);
+  const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
   auto* kernel = lm_kv_attend_kernel<KIND, D, NT>;
   static std::atomic<uint64_t> allowed{0};    // a bit per device

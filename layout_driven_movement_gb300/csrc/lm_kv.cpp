@@ -351,6 +351,7 @@ int lm_kv_write(const lm_kv_plan* plan, const lm_kv_cache* cache,
       need(rope->head_dim == plan->dim);
       a.turn = lm::check_turn(*rope, positions, position_bytes, table,
                               table_rows, 0);
+      a.table16 = lm::addr(table) % 16 == 0 && rope->rotary % 8 == 0;
     }
     a.k = lm::rows_of(*k);
     a.v = lm::rows_of(*v);

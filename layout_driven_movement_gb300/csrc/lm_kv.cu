@@ -31,10 +31,11 @@ __device__ __forceinline__ float row_scale(uint32_t top, float* by) {
   return fmaxf(__fdiv_rn(m, 127.f), 0x1p-126f);
 }
 
-// 8 elements' codes.  A row that is not finite has by == 0: its codes are 0.
+// 8 elements' codes.  Whole numbers: with 1.5 * 2^23 added a number's last
+// bit is 1, so it is rounded to a whole one, ties to even, whose low byte is
+// the sum's.
 template <int STORE>
-__device__ __forceinline__ uint2 row_codes(const float* x, float by,
-                                           bool finite) {
+__device__ __forceinline__ uint2 row_codes(const float* x, float by) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -47,136 +48,180 @@ __device__ __forceinline__ uint2 row_codes(const float* x, float by,
           __NV_E4M3);
       w[i] = a | b << 16;
     } else {
-      w[i] = 0;
+      uint32_t r[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[i] |= uint32_t(__float2int_rn(x[4 * i + j] * by) & 255) << (8 * j);
+        r[j] = __float_as_uint(
+            __fadd_rn(__fmul_rn(x[4 * i + j], by), 12582912.f));
+      w[i] = __byte_perm(__byte_perm(r[0], r[1], 0x0040),
+                         __byte_perm(r[2], r[3], 0x0040), 0x5410);
     }
-    if (!finite) w[i] = 0;
   }
   return make_uint2(w[0], w[1]);
 }
 
-// A row's 8 elements at `at`; one 16-byte load when the rows allow it.
-template <class T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int at, T* x) {
-  if (VEC) {
-    *reinterpret_cast<Pack<T, 8>*>(x) =
-        *reinterpret_cast<const Pack<T, 8>*>(row + at);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = row[at + i];
-  }
+// The largest magnitude of 8, NaN above all, as bits.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;\n" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t top_of(const float* x) {
+  const float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
+  return __float_as_uint(max3(max3(x[6], x[7], a), b, 0.f));
 }
 
-// L lanes hold a token-head's rows, 8 elements a lane of its key and its
-// value: the row's largest magnitude is then a few shuffles away, and its
-// codes leave as 8-byte stores of adjacent lanes.  Bound by memory: each
-// input element is read once (the turn's partner elements come from the
-// cache lines that the same lanes just read), each code written once.
-template <class T, int STORE, int L, bool VEC>
-__global__ void __launch_bounds__(256) lm_kv_write_kernel(
+// A row's 8 elements at `at`, as words; one 16-byte load when the rows allow
+// it.
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int at) {
+  if (VEC) return *reinterpret_cast<const uint4*>(row + at);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = row[at + 2 * i] | uint32_t(row[at + 2 * i + 1]) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <class T>
+__device__ __forceinline__ void get8(const uint4& u, float* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  get_words<T, 4>(w, x);
+}
+
+// L lanes hold a row in chunks of 8 elements, lane c the chunks c and c + L of
+// a key and of its value: four 16-byte loads are in flight before the first is
+// used, a row's largest magnitude is log2 L shuffles away, its codes leave as
+// 8-byte stores of adjacent lanes, and the turn of a whole row of 16 L
+// elements (partners 8 L apart) stays inside a thread, one cosine and sine
+// for both partners.  Bound by memory and, within a factor of two, by the
+// instructions of the rounding: inputs read once, codes written once.
+//
+// TURN: 0 no turn, 1 partners 8 L apart, 2 any other.  Two heads a thread, to
+// share a token's slot and angles, spill or halve the resident warps: 70 us
+// for 8 x 8192 tokens of 8 x 128 turned into e4m3, 60 with one.
+template <class T, int STORE, int L, bool VEC, int TURN>
+__global__ void __launch_bounds__(256, TURN == 0 ? 6 : 4) lm_kv_write_kernel(
     const __grid_constant__ KvWriteArgs a) {
   const uint32_t row = (blockIdx.x * 256 + threadIdx.x) / L;
-  const int at = int(threadIdx.x % L) * 8;
-  const uint32_t rows = a.tokens * a.c.heads;
-  const uint32_t t = row < rows ? fdiv(row, a.heads_div) : 0;
-  const uint32_t h = row < rows ? row - t * a.c.heads : 0;
-  const bool in = row < rows && at < a.c.dim;
-  alignas(16) T xr[2][8];
-  const T* src[2] = {
-      reinterpret_cast<const T*>(a.k.p) + int64_t(t) * a.k.ts +
-          int64_t(h) * a.k.hs,
-      reinterpret_cast<const T*>(a.v.p) + int64_t(t) * a.v.ts +
-          int64_t(h) * a.v.hs};
-  if (in) {
-    load8<T, VEC>(src[0], at, xr[0]);
-    load8<T, VEC>(src[1], at, xr[1]);
+  const int c = int(threadIdx.x % L);
+  const bool live = row < a.tokens * a.c.heads;
+  const uint32_t t = live ? fdiv(row, a.heads_div) : 0;
+  const uint32_t h = live ? row - t * a.c.heads : 0;
+  const int at[2] = {c * 8, (c + L) * 8};
+  const bool has[2] = {at[0] < a.c.dim, at[1] < a.c.dim};
+  const uint16_t* k = reinterpret_cast<const uint16_t*>(a.k.p) +
+                      int64_t(t) * a.k.ts + int64_t(h) * a.k.hs;
+  const uint16_t* v = reinterpret_cast<const uint16_t*>(a.v.p) +
+                      int64_t(t) * a.v.ts + int64_t(h) * a.v.hs;
+  uint4 xr[2][2];                            // key or value, chunk
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    xr[0][p] = xr[1][p] = make_uint4(0, 0, 0, 0);
+    if (live && has[p]) {
+      xr[0][p] = load8<VEC>(k, at[p]);
+      xr[1][p] = load8<VEC>(v, at[p]);
+    }
   }
-  const int64_t slot = row < rows ? a.slots[t] : -1;
-  const bool turned = a.turn.pos != nullptr;
-  float x[2][8];
+  const int64_t slot = live ? a.slots[t] : -1;
+  const int half = a.turn.rot / 2;
+  const float* tr = nullptr;
+  float cs[8], sn[8];
+  const float nan = __int_as_float(0x7fc00000);
+  if (TURN && live && a.turn.pos) {
+    tr = turn_row(a.turn, t, c == 0 ? a.status : nullptr);
+    if (TURN == 1) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[0][i] = in ? to_f32(xr[0][i]) : 0.f;
-    x[1][i] = in ? to_f32(xr[1][i]) : 0.f;
-  }
-  if (turned && in && at < a.turn.rot) {
-    const float* tr = turn_row(a.turn, t, at == 0 ? a.status : nullptr);
-    const int half = a.turn.rot / 2;
-    const float nan = __int_as_float(0x7fc00000);
-    if (a.turn.inter) {
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const int p = (at + i) / 2;
-        if (at + i < a.turn.rot) {
-          const float c = tr ? tr[p] : nan, s = tr ? tr[half + p] : nan;
-          const float u = x[0][i], w = x[0][i + 1];
-          x[0][i] = turn_lo(u, w, c, s);
-          x[0][i + 1] = turn_hi(u, w, c, s);
-        }
-      }
-    } else {
-      // the partner of element i is half a rotated part away; when halves
-      // are whole chunks it is one more aligned load
-      alignas(16) T pr[8];
-      if (half % 8 == 0) {
-        load8<T, VEC>(src[0], at < half ? at + half : at - half, pr);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = at + i;
-          pr[i] = e < a.turn.rot ? src[0][e < half ? e + half : e - half]
-                                 : xr[0][i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int e = at + i;
-        if (e < a.turn.rot) {
-          const int p = e < half ? e : e - half;
-          const float c = tr ? tr[p] : nan, s = tr ? tr[half + p] : nan;
-          const float o = to_f32(pr[i]);
-          x[0][i] = e < half ? turn_lo(x[0][i], o, c, s)
-                             : turn_hi(o, x[0][i], c, s);
-        }
+      for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<float4*>(cs + i) =
+            tr ? *reinterpret_cast<const float4*>(tr + at[0] + i)
+               : make_float4(nan, nan, nan, nan);
+        *reinterpret_cast<float4*>(sn + i) =
+            tr ? *reinterpret_cast<const float4*>(tr + half + at[0] + i)
+               : make_float4(nan, nan, nan, nan);
       }
     }
   }
   const int64_t tokens = a.c.pages * int64_t(a.c.page_tokens);
-  if (slot >= tokens && at == 0 && a.status) atomicOr(a.status, kStatusRange);
-  const bool to = in && slot >= 0 && slot < tokens;
-  const int64_t page = to ? slot / a.c.page_tokens : 0;
+  if (slot >= tokens && c == 0 && a.status) atomicOr(a.status, kStatusRange);
+  const bool to = slot >= 0 && slot < tokens;
+  int64_t page = 0;
+  if (to)
+    page = tokens <= INT32_MAX ? int64_t(fdiv(uint32_t(slot), a.c.page_div))
+                               : slot / a.c.page_tokens;
   const uint32_t off = to ? uint32_t(slot - page * a.c.page_tokens) : 0;
   const int64_t base = page * a.c.page_b + int64_t(off) * a.c.token_b +
                        int64_t(h) * a.c.head_b;
+
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
+    float x[2][8];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) get8<T>(xr[kv][p], x[p]);
+    if (TURN == 1 && kv == 0 && live) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = x[0][i], w = x[1][i];
+        x[0][i] = turn_lo(u, w, cs[i], sn[i]);
+        x[1][i] = turn_hi(u, w, cs[i], sn[i]);
+      }
+    }
+    if (TURN == 2 && kv == 0 && live) {
+      // part of a row, odd halves or interleaved pairs: an element's partner
+      // and angle one by one (their lines are at hand)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        float own[8];
+        get8<T>(xr[0][p], own);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = at[p] + i;
+          if (e >= a.turn.rot) continue;
+          const bool first = a.turn.inter ? i % 2 == 0 : e < half;
+          const int n = a.turn.inter ? e / 2 : first ? e : e - half;
+          const float o =
+              a.turn.inter
+                  ? own[i ^ 1]
+                  : to_f32(reinterpret_cast<const T*>(
+                        k)[first ? e + half : e - half]);
+          const float cn = tr ? tr[n] : nan, s = tr ? tr[half + n] : nan;
+          x[p][i] = first ? turn_lo(own[i], o, cn, s)
+                          : turn_hi(o, own[i], cn, s);
+        }
+      }
+    }
     char* dst = (kv ? a.c.v : a.c.k) + base;
     if (STORE == LM_KV_SAME) {
-      if (kv == 0 && turned && at < a.turn.rot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (at + i < a.turn.rot) xr[0][i] = from_f32<T>(x[0][i]);
+      for (int p = 0; p < 2; ++p) {
+        uint4 y = xr[kv][p];
+        if (kv == 0 && TURN && at[p] < a.turn.rot) {
+          // what is not turned keeps its bits
+          const uint32_t* raw = reinterpret_cast<const uint32_t*>(&xr[0][p]);
+          uint32_t w[4];
+          put_words<T, 4>(x[p], w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (at[p] + 2 * i >= a.turn.rot) w[i] = raw[i];
+          y = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (to && has[p]) *reinterpret_cast<uint4*>(dst + at[p] * 2) = y;
       }
-      if (to)
-        *reinterpret_cast<Pack<T, 8>*>(dst + at * 2) =
-            *reinterpret_cast<const Pack<T, 8>*>(xr[kv]);
       continue;
     }
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      top = max(top, __float_as_uint(x[kv][i]) & 0x7fffffffu);
+    uint32_t top = max(top_of(x[0]), top_of(x[1]));
 #pragma unroll
     for (int m = L / 2; m; m /= 2)
       top = max(top, __shfl_xor_sync(0xffffffffu, top, m, L));
     float by;
     const float scale = row_scale<STORE>(top, &by);
     if (to) {
-      *reinterpret_cast<uint2*>(dst + at) =
-          row_codes<STORE>(x[kv], by, top < 0x7f800000u);
-      if (at == 0)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+        if (has[p])
+          *reinterpret_cast<uint2*>(dst + at[p]) =
+              top < 0x7f800000u ? row_codes<STORE>(x[p], by)
+                                : make_uint2(0, 0);
+      if (c == 0)
         (kv ? a.c.vs : a.c.ks)[(page * a.c.heads + h) * a.c.page_tokens +
                                off] = scale;
     }
@@ -187,18 +232,24 @@ template <class T, int STORE, int L>
 int launch_write_l(const KvWriteArgs& a, cudaStream_t st) {
   const uint64_t threads = uint64_t(a.tokens) * a.c.heads * L;
   const unsigned grid = unsigned((threads + 255) / 256);
-  if (a.vec)
-    lm_kv_write_kernel<T, STORE, L, true><<<grid, 256, 0, st>>>(a);
+  // (dim == 16 L: whole chunks, every lane has both)
+  const bool own = a.table16 && !a.turn.inter && a.turn.rot == 16 * L;
+  if (!a.vec)
+    lm_kv_write_kernel<T, STORE, L, false, 2><<<grid, 256, 0, st>>>(a);
+  else if (!a.turn.pos)
+    lm_kv_write_kernel<T, STORE, L, true, 0><<<grid, 256, 0, st>>>(a);
+  else if (own)
+    lm_kv_write_kernel<T, STORE, L, true, 1><<<grid, 256, 0, st>>>(a);
   else
-    lm_kv_write_kernel<T, STORE, L, false><<<grid, 256, 0, st>>>(a);
+    lm_kv_write_kernel<T, STORE, L, true, 2><<<grid, 256, 0, st>>>(a);
   return launch_status();
 }
 
 template <class T, int STORE>
 int launch_write_s(const KvWriteArgs& a, cudaStream_t st) {
-  if (a.c.dim <= 64) return launch_write_l<T, STORE, 8>(a, st);
-  if (a.c.dim <= 128) return launch_write_l<T, STORE, 16>(a, st);
-  return launch_write_l<T, STORE, 32>(a, st);
+  if (a.c.dim <= 64) return launch_write_l<T, STORE, 4>(a, st);
+  if (a.c.dim <= 128) return launch_write_l<T, STORE, 8>(a, st);
+  return launch_write_l<T, STORE, 16>(a, st);
 }
 
 template <class T>
@@ -216,9 +267,7 @@ __device__ __forceinline__ void held_values(const uint4& w, float scale,
                                             float* x) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
   if (STORE == LM_KV_SAME) {
-    const T* e = reinterpret_cast<const T*>(r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(e[i]);
+    get_words<T, 4>(r, x);
   } else if (STORE == LM_KV_E4M3) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -235,39 +284,47 @@ __device__ __forceinline__ void held_values(const uint4& w, float scale,
   }
 }
 
-constexpr int kReadTokens = 32;
+constexpr int kReadTokens = 32;   // tokens of a block at most
+constexpr int kReadUnits = 2;     // 16-byte loads of a thread in flight
 
-// A block takes 32 output rows (tokens): its first threads find each row's
-// sequence (a binary search of starts), page and offset, then all threads
-// move 16 held bytes at a time, heads and dim fastest, so that a token's rows
-// leave as one run.  Bound by memory: codes and scales read once, rows
-// written once.
+struct ReadGrid {
+  int32_t tokens = 1;        // of a block
+  uint32_t chunks = 1;       // 16-byte units of a row
+  uint32_t row_units = 1;    // of a token: keys and values of all heads
+  FastDiv chunk_div, row_div;
+};
+
+// A block takes a few output rows (tokens).  It finds the first one's sequence
+// by counting the starts at or below it, all at once; the threads of the rows
+// go on from there to their page and offset.  Then all threads move 16 held
+// bytes at a time, heads and dim fastest, so that a token's rows leave as one
+// run.  Bound by memory: codes and scales read once, rows written once.
+// Small blocks in many waves measured best (16 x 16384 tokens of 8 x 128 e4m3:
+// 165 us with two loads a thread, 180 with four, 206 with resident blocks that
+// look the next rows up while they move these).
 template <class T, int STORE, class TO, bool VEC>
 __global__ void __launch_bounds__(256) lm_kv_read_kernel(
-    const __grid_constant__ KvReadArgs a, const FastDiv chunk_div,
-    const uint32_t chunks, const FastDiv row_div, const uint32_t row_units) {
+    const __grid_constant__ KvReadArgs a, const __grid_constant__ ReadGrid g) {
   __shared__ int64_t s_page[kReadTokens];   // -1: no token, -2: zeros
   __shared__ uint32_t s_off[kReadTokens];
-  const int64_t t0 = int64_t(blockIdx.x) * kReadTokens;
-  if (threadIdx.x < kReadTokens) {
+  const int64_t t0 = int64_t(blockIdx.x) * g.tokens;
+  int below = 0;                             // starts[0 .. seqs) <= t0
+  for (int b = 0; b < a.seqs; b += 256)
+    below += __syncthreads_count(b + int(threadIdx.x) < a.seqs &&
+                                 a.starts[b + threadIdx.x] <= t0);
+  if (threadIdx.x < g.tokens) {
     const int64_t r = t0 + threadIdx.x;
     int64_t page = -1;
     uint32_t off = 0;
+    int b = max(below - 1, 0);
+    while (b + 1 < a.seqs && a.starts[b + 1] <= r) ++b;
     if (r < a.rows) {
-      int lo = 0, hi = a.seqs;             // the last b with starts[b] <= r
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (a.starts[mid] <= r)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      const int64_t j = r - a.starts[lo];
-      const int64_t n = a.lens[lo] < a.max_tokens ? a.lens[lo] : a.max_tokens;
-      if (j >= 0 && j < n && r < a.starts[lo + 1]) {
+      const int64_t j = r - a.starts[b];
+      const int64_t n = a.lens[b] < a.max_tokens ? a.lens[b] : a.max_tokens;
+      if (j >= 0 && j < n && r < a.starts[b + 1]) {
         const uint32_t p = fdiv(uint32_t(j), a.c.page_div);
         off = uint32_t(j) - p * a.c.page_tokens;
-        page = a.table[int64_t(lo) * a.table_stride + p];
+        page = a.table[int64_t(b) * a.table_stride + p];
         if (page < 0 || page >= a.c.pages) {
           if (a.status) atomicOr(a.status, kStatusRange);
           page = -2;
@@ -279,62 +336,79 @@ __global__ void __launch_bounds__(256) lm_kv_read_kernel(
   }
   __syncthreads();
   constexpr int N = STORE == LM_KV_SAME ? 8 : 16;   // elements of a unit
-  const uint32_t units = kReadTokens * row_units;   // keys and values
-  for (uint32_t u = threadIdx.x; u < units; u += 256) {
-    const uint32_t i = fdiv(u, row_div);
-    const uint32_t w = u - i * row_units;
-    const int64_t page = s_page[i];
-    if (page == -1) continue;
-    const uint32_t hk = fdiv(w, chunk_div);         // kv * heads + head
-    const int at = int(w - hk * chunks) * N;
-    const bool kv = hk >= a.c.heads;
-    const uint32_t h = kv ? hk - a.c.heads : hk;
-    uint4 held = make_uint4(0, 0, 0, 0);
-    float scale = 1.f;
-    if (page >= 0) {
-      const char* src = (kv ? a.c.v : a.c.k) + page * a.c.page_b +
-                        int64_t(s_off[i]) * a.c.token_b +
-                        int64_t(h) * a.c.head_b;
-      held = *reinterpret_cast<const uint4*>(
-          src + at * (STORE == LM_KV_SAME ? 2 : 1));
-      if (STORE != LM_KV_SAME)
-        scale = (kv ? a.c.vs : a.c.ks)[(page * a.c.heads + h) *
-                                           a.c.page_tokens +
-                                       s_off[i]];
+  const uint32_t units = g.tokens * g.row_units;
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += 256 * kReadUnits) {
+    uint4 held[kReadUnits];
+    float scale[kReadUnits];
+    TO* dst[kReadUnits];
+#pragma unroll
+    for (int k = 0; k < kReadUnits; ++k) {
+      const uint32_t u = u0 + 256 * k;
+      dst[k] = nullptr;
+      if (u >= units) continue;
+      const uint32_t i = fdiv(u, g.row_div);
+      const uint32_t w = u - i * g.row_units;
+      const int64_t page = s_page[i];
+      if (page == -1) continue;
+      const uint32_t hk = fdiv(w, g.chunk_div);     // kv * heads + head
+      const int at = int(w - hk * g.chunks) * N;
+      const bool kv = hk >= a.c.heads;
+      const uint32_t h = kv ? hk - a.c.heads : hk;
+      held[k] = make_uint4(0, 0, 0, 0);
+      scale[k] = 1.f;
+      if (page >= 0) {
+        const char* src = (kv ? a.c.v : a.c.k) + page * a.c.page_b +
+                          int64_t(s_off[i]) * a.c.token_b +
+                          int64_t(h) * a.c.head_b;
+        held[k] = *reinterpret_cast<const uint4*>(
+            src + at * (STORE == LM_KV_SAME ? 2 : 1));
+        if (STORE != LM_KV_SAME)
+          scale[k] = (kv ? a.c.vs : a.c.ks)[(page * a.c.heads + h) *
+                                                a.c.page_tokens + s_off[i]];
+      }
+      const Rows& out = kv ? a.v : a.k;
+      dst[k] = reinterpret_cast<TO*>(out.p) + (t0 + i) * out.ts +
+               int64_t(h) * out.hs + at;
     }
-    const Rows& out = kv ? a.v : a.k;
-    TO* dst = reinterpret_cast<TO*>(out.p) + (t0 + i) * out.ts +
-              int64_t(h) * out.hs + at;
-    float x[N];
-    held_values<T, STORE>(held, scale, x);
-    alignas(16) TO y[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) y[k] = from_f32<TO>(x[k]);
-    if (VEC) {
-      constexpr int V = 16 / int(sizeof(TO));
+    for (int k = 0; k < kReadUnits; ++k) {
+      if (!dst[k]) continue;
+      float x[N];
+      held_values<T, STORE>(held[k], scale[k], x);
+      if (VEC) {
+        constexpr int V = 16 / int(sizeof(TO));
 #pragma unroll
-      for (int k = 0; k < N; k += V)
-        *reinterpret_cast<Pack<TO, V>*>(dst + k) =
-            *reinterpret_cast<const Pack<TO, V>*>(y + k);
-    } else {
+        for (int e = 0; e < N; e += V) {
+          Words<4> y;
+          put_words<TO, 4>(x + e, y.w);
+          *reinterpret_cast<Words<4>*>(dst[k] + e) = y;
+        }
+      } else {
 #pragma unroll
-      for (int k = 0; k < N; ++k) dst[k] = y[k];
+        for (int e = 0; e < N; ++e) dst[k][e] = from_f32<TO>(x[e]);
+      }
     }
   }
 }
 
 template <class T, int STORE, class TO>
 int launch_read_o(const KvReadArgs& a, cudaStream_t st) {
-  const uint32_t chunks = uint32_t(a.c.dim) / (STORE == LM_KV_SAME ? 8 : 16);
-  const uint32_t row_units = 2 * a.c.heads * chunks;
-  const unsigned grid = unsigned((a.rows + kReadTokens - 1) / kReadTokens);
-  const FastDiv cd = make_fastdiv(chunks), rd = make_fastdiv(row_units);
+  ReadGrid g;
+  g.chunks = uint32_t(a.c.dim) / (STORE == LM_KV_SAME ? 8 : 16);
+  g.row_units = 2 * a.c.heads * g.chunks;
+  g.chunk_div = make_fastdiv(g.chunks);
+  g.row_div = make_fastdiv(g.row_units);
+  // a round of the block's loads, or less where that leaves SMs idle
+  const uint32_t most = (256 * kReadUnits + g.row_units - 1) / g.row_units;
+  const int64_t spread = a.rows / 608;
+  int64_t tokens = most < kReadTokens ? most : kReadTokens;
+  if (tokens > spread) tokens = spread;
+  g.tokens = int(tokens < 1 ? 1 : tokens);
+  const unsigned grid = unsigned((a.rows + g.tokens - 1) / g.tokens);
   if (a.vec)
-    lm_kv_read_kernel<T, STORE, TO, true><<<grid, 256, 0, st>>>(
-        a, cd, chunks, rd, row_units);
+    lm_kv_read_kernel<T, STORE, TO, true><<<grid, 256, 0, st>>>(a, g);
   else
-    lm_kv_read_kernel<T, STORE, TO, false><<<grid, 256, 0, st>>>(
-        a, cd, chunks, rd, row_units);
+    lm_kv_read_kernel<T, STORE, TO, false><<<grid, 256, 0, st>>>(a, g);
   return launch_status();
 }
 

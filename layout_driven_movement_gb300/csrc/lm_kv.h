@@ -67,6 +67,7 @@ struct KvWriteArgs {
   uint32_t tokens = 0;
   FastDiv heads_div;
   int32_t vec = 0;       // the inputs allow 16-byte loads
+  int32_t table16 = 0;   // and so does the rotary table
   unsigned int* status = nullptr;
 };
 
@@ -103,6 +104,8 @@ int launch_kv_write(const KvWriteArgs& a, int elem, int store, void* stream);
 int launch_kv_read(const KvReadArgs& a, int elem, int store, int out_elem,
                    void* stream);
 int launch_kv_attend(const KvAttendArgs& a, int store, void* stream);
+// The current device (below 64) and its SMs.
+int kv_device(int* dev, int* sms);
 // Bytes of the attention's workspace on the current device.
 int attend_workspace(int store, int dim, int group, int64_t* bytes);
 

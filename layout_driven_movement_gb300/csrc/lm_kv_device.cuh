@@ -37,6 +37,63 @@ struct alignas(sizeof(T) * V) Pack {
   T v[V];
 };
 
+// The elements of a word: two of 16 bits (the first in the low half), or one.
+// Pairs convert in one or two instructions; element by element a 16-bit
+// element takes a register and its moves.
+template <class T>
+struct Word;
+template <>
+struct Word<float> {
+  static constexpr int N = 1;
+  static __device__ __forceinline__ void get(uint32_t w, float* x) {
+    x[0] = __uint_as_float(w);
+  }
+  static __device__ __forceinline__ uint32_t put(const float* x) {
+    return __float_as_uint(x[0]);
+  }
+};
+template <>
+struct Word<bf16> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void get(uint32_t w, float* x) {
+    x[0] = __uint_as_float(w << 16);
+    x[1] = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t put(const float* x) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[0], x[1]);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+template <>
+struct Word<__half> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void get(uint32_t w, float* x) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    x[0] = f.x;
+    x[1] = f.y;
+  }
+  static __device__ __forceinline__ uint32_t put(const float* x) {
+    const __half2 v = __floats2half2_rn(x[0], x[1]);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+};
+
+// N words, moved as one access.
+template <int N>
+struct alignas(4 * N) Words {
+  uint32_t w[N];
+};
+template <class T, int N>
+__device__ __forceinline__ void get_words(const uint32_t* w, float* x) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) Word<T>::get(w[i], x + i * Word<T>::N);
+}
+template <class T, int N>
+__device__ __forceinline__ void put_words(const float* x, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = Word<T>::put(x + i * Word<T>::N);
+}
+
 // Row `position` of the rotary table, or nullptr (and the status bit) when
 // the position lies outside it.
 __device__ __forceinline__ const float* turn_row(const Turn& t, uint32_t token,

@@ -27,7 +27,8 @@ __global__ void __launch_bounds__(256) lm_rope_table_kernel(
 // part -- two chunks of V elements rot/2 apart, or with INTER one chunk of V
 // elements holding V/2 pairs -- or one chunk of the rest.  The unit's cosines
 // and sines serve all H heads of the group, which lie HG heads apart, so that
-// a warp's accesses stay whole rows.
+// a warp's accesses stay whole rows.  Bound by memory: x read once, out
+// written once.
 struct RopeGrid {
   uint32_t units = 0;      // of all tokens
   uint32_t chunks = 0;     // units of one head
@@ -36,120 +37,174 @@ struct RopeGrid {
   FastDiv chunk_div, group_div;
 };
 
-template <class T, int V, bool INTER, int H>
-__global__ void __launch_bounds__(256) lm_rope_kernel(
-    const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
-  const uint32_t u = blockIdx.x * 256 + threadIdx.x;
-  if (u >= g.units) return;
-  const uint32_t th = fdiv(u, g.chunk_div);
-  const uint32_t c = u - th * g.chunks;
-  const uint32_t t = fdiv(th, g.group_div);
-  const uint32_t h0 = th - t * g.groups;
-  const T* x = reinterpret_cast<const T*>(a.x.p) + int64_t(t) * a.x.ts;
-  T* o = reinterpret_cast<T*>(a.out.p) + int64_t(t) * a.out.ts;
-  constexpr int E = INTER && V == 1 ? 2 : V;   // elements of a chunk
-  typedef Pack<T, V> P;
-  if (c >= g.turned) {
-    const int at = a.turn.rot + int(c - g.turned) * V;
-#pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const uint32_t h = h0 + k * g.groups;
-      if (h < a.heads)
-        *reinterpret_cast<P*>(o + int64_t(h) * a.out.hs + at) =
-            *reinterpret_cast<const P*>(x + int64_t(h) * a.x.hs + at);
-    }
-    return;
+// The unit `u`: token, first head and chunk.
+struct RopeUnit {
+  uint32_t t, h0, c;
+  __device__ __forceinline__ RopeUnit(const RopeGrid& g, uint32_t u) {
+    const uint32_t th = fdiv(u, g.chunk_div);
+    c = u - th * g.chunks;
+    t = fdiv(th, g.group_div);
+    h0 = th - t * g.groups;
   }
-  const int half = a.turn.rot / 2;
-  constexpr int N = INTER ? E / 2 : V;         // pairs of a unit
-  const int lo = int(c) * E, hi = INTER ? lo + V : lo + half;
-  // the rows first, then the position and its table row: their latencies
-  // overlap
-  P xl[H], xh[H];
-#pragma unroll
-  for (int k = 0; k < H; ++k) {
-    const uint32_t h = h0 + k * g.groups;
-    if (h < a.heads) {
-      const T* r = x + int64_t(h) * a.x.hs;
-      xl[k] = *reinterpret_cast<const P*>(r + lo);
-      if (!INTER || V == 1) xh[k] = *reinterpret_cast<const P*>(r + hi);
-    }
-  }
-  const float* row = turn_row(a.turn, t, a.status);
-  const int i0 = int(c) * N;
-  float cs[N], sn[N];
+};
+
+// N cosines and as many sines from pair i0 on; NaN without a table row.
+template <int N>
+__device__ __forceinline__ void angles(const Turn& turn, const float* row,
+                                       int i0, float* cs, float* sn) {
   if (row) {
     constexpr int W = N % 4 == 0 ? 4 : N % 2 == 0 ? 2 : 1;
     typedef Pack<float, W> F;
+    const float* sines = row + turn.rot / 2;
 #pragma unroll
     for (int i = 0; i < N; i += W) {
       *reinterpret_cast<F*>(cs + i) =
           *reinterpret_cast<const F*>(row + i0 + i);
       *reinterpret_cast<F*>(sn + i) =
-          *reinterpret_cast<const F*>(row + half + i0 + i);
+          *reinterpret_cast<const F*>(sines + i0 + i);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) cs[i] = sn[i] = __int_as_float(0x7fc00000);
   }
-  if (a.turn.inverse) {
+  if (turn.inverse) {
 #pragma unroll
     for (int i = 0; i < N; ++i) sn[i] = -sn[i];
   }
+}
+
+template <class T, bool INTER, int H>
+__global__ void __launch_bounds__(256) lm_rope_kernel(
+    const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
+  const uint32_t u = blockIdx.x * 256 + threadIdx.x;
+  if (u >= g.units) return;
+  const RopeUnit at(g, u);
+  constexpr int V = 16 / int(sizeof(T));       // elements of a chunk
+  constexpr int N = INTER ? V / 2 : V;         // pairs of a unit
+  typedef Words<4> P;
+  const T* x = reinterpret_cast<const T*>(a.x.p) + int64_t(at.t) * a.x.ts;
+  T* o = reinterpret_cast<T*>(a.out.p) + int64_t(at.t) * a.out.ts;
+  const bool rest = at.c >= g.turned;
+  const int lo = rest ? a.turn.rot + int(at.c - g.turned) * V : int(at.c) * V;
+  const int hi = lo + a.turn.rot / 2;
+  // the rows first, then the position and its table row: their latencies
+  // overlap
+  P xl[H], xh[H];
 #pragma unroll
   for (int k = 0; k < H; ++k) {
-    const uint32_t h = h0 + k * g.groups;
-    if (h >= a.heads) break;
-    T* r = o + int64_t(h) * a.out.hs;
-    if (INTER && V > 1) {
+    const uint32_t h = at.h0 + k * g.groups;
+    if (h < a.heads) {
+      const T* r = x + int64_t(h) * a.x.hs;
+      xl[k] = *reinterpret_cast<const P*>(r + lo);
+      if (!INTER && !rest) xh[k] = *reinterpret_cast<const P*>(r + hi);
+    }
+  }
+  if (!rest) {
+    float cs[N], sn[N];
+    angles<N>(a.turn, turn_row(a.turn, at.t, a.status), int(at.c) * N, cs,
+              sn);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float p = to_f32(xl[k].v[2 * i]), q = to_f32(xl[k].v[2 * i + 1]);
-        xl[k].v[2 * i] = from_f32<T>(turn_lo(p, q, cs[i], sn[i]));
-        xl[k].v[2 * i + 1] = from_f32<T>(turn_hi(p, q, cs[i], sn[i]));
-      }
-      *reinterpret_cast<P*>(r + lo) = xl[k];
-    } else {
+    for (int k = 0; k < H; ++k) {
+      float p[V], q[V];
+      get_words<T, 4>(xl[k].w, p);
+      if (INTER) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float p = to_f32(xl[k].v[i]), q = to_f32(xh[k].v[i]);
-        xl[k].v[i] = from_f32<T>(turn_lo(p, q, cs[i], sn[i]));
-        xh[k].v[i] = from_f32<T>(turn_hi(p, q, cs[i], sn[i]));
+        for (int i = 0; i < N; ++i) {
+          q[2 * i] = turn_lo(p[2 * i], p[2 * i + 1], cs[i], sn[i]);
+          q[2 * i + 1] = turn_hi(p[2 * i], p[2 * i + 1], cs[i], sn[i]);
+        }
+        put_words<T, 4>(q, xl[k].w);
+      } else {
+        float y[V], z[V];
+        get_words<T, 4>(xh[k].w, q);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          y[i] = turn_lo(p[i], q[i], cs[i], sn[i]);
+          z[i] = turn_hi(p[i], q[i], cs[i], sn[i]);
+        }
+        put_words<T, 4>(y, xl[k].w);
+        put_words<T, 4>(z, xh[k].w);
       }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < H; ++k) {
+    const uint32_t h = at.h0 + k * g.groups;
+    if (h < a.heads) {
+      T* r = o + int64_t(h) * a.out.hs;
       *reinterpret_cast<P*>(r + lo) = xl[k];
-      *reinterpret_cast<P*>(r + hi) = xh[k];
+      if (!INTER && !rest) *reinterpret_cast<P*>(r + hi) = xh[k];
     }
   }
 }
 
-template <class T, int V, bool INTER, int H>
-int launch_h(const RopeArgs& a, cudaStream_t st) {
+// The same for rows that allow no 16-byte accesses: a pair or an element of
+// the rest a unit.
+template <class T>
+__global__ void __launch_bounds__(256) lm_rope_single_kernel(
+    const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
+  const uint32_t u = blockIdx.x * 256 + threadIdx.x;
+  if (u >= g.units) return;
+  const RopeUnit at(g, u);
+  const T* x = reinterpret_cast<const T*>(a.x.p) + int64_t(at.t) * a.x.ts +
+               int64_t(at.h0) * a.x.hs;
+  T* o = reinterpret_cast<T*>(a.out.p) + int64_t(at.t) * a.out.ts +
+         int64_t(at.h0) * a.out.hs;
+  if (at.c >= g.turned) {
+    const int e = a.turn.rot + int(at.c - g.turned);
+    o[e] = x[e];
+    return;
+  }
+  const int lo = a.turn.inter ? 2 * int(at.c) : int(at.c);
+  const int hi = a.turn.inter ? lo + 1 : lo + a.turn.rot / 2;
+  const float p = to_f32(x[lo]), q = to_f32(x[hi]);
+  float cs, sn;
+  angles<1>(a.turn, turn_row(a.turn, at.t, a.status), int(at.c), &cs, &sn);
+  o[lo] = from_f32<T>(turn_lo(p, q, cs, sn));
+  o[hi] = from_f32<T>(turn_hi(p, q, cs, sn));
+}
+
+// Chunks of V elements (1: single elements, a pair a unit), H heads a thread.
+RopeGrid rope_grid(const RopeArgs& a, int v, int h) {
   RopeGrid g;
-  constexpr int E = INTER && V == 1 ? 2 : V;
-  g.turned = uint32_t(INTER ? a.turn.rot / E : a.turn.rot / 2 / V);
+  g.turned = uint32_t(v > 1 && a.turn.inter ? a.turn.rot / v
+                                            : a.turn.rot / 2 / v);
   g.chunks = g.turned;
-  if (a.copy_rest) g.chunks += uint32_t(a.dim - a.turn.rot) / V;
-  g.groups = (a.heads + H - 1) / H;
+  if (a.copy_rest) g.chunks += uint32_t((a.dim - a.turn.rot) / v);
+  g.groups = (a.heads + h - 1) / h;
   g.chunk_div = make_fastdiv(g.chunks);
   g.group_div = make_fastdiv(g.groups);
   g.units = a.tokens * g.groups * g.chunks;
-  lm_rope_kernel<T, V, INTER, H><<<(g.units + 255) / 256, 256, 0, st>>>(a, g);
+  return g;
+}
+
+template <class T, bool INTER, int H>
+int launch_h(const RopeArgs& a, cudaStream_t st) {
+  const RopeGrid g = rope_grid(a, 16 / int(sizeof(T)), H);
+  lm_rope_kernel<T, INTER, H><<<(g.units + 255) / 256, 256, 0, st>>>(a, g);
   return launch_status();
 }
 
-template <class T, int V, bool INTER>
+constexpr uint64_t kRopeShare = 152 * 2048;
+
+template <class T, bool INTER>
 int launch_v(const RopeArgs& a, cudaStream_t st) {
-  return launch_h<T, V, INTER, 1>(a, st);
+  // few rows spread over as many threads as they can; many share a token's
+  // angles between two heads
+  constexpr int V = 16 / int(sizeof(T));
+  if (a.heads > 1 &&
+      uint64_t(a.tokens) * a.heads * uint32_t(a.dim / V) >= 2 * kRopeShare)
+    return launch_h<T, INTER, 2>(a, st);
+  return launch_h<T, INTER, 1>(a, st);
 }
 
 template <class T>
 int launch_t(const RopeArgs& a, cudaStream_t st) {
-  constexpr int V = 16 / int(sizeof(T));
   if (a.vec)
-    return a.turn.inter ? launch_v<T, V, true>(a, st)
-                        : launch_v<T, V, false>(a, st);
-  return a.turn.inter ? launch_v<T, 1, true>(a, st)
-                      : launch_v<T, 1, false>(a, st);
+    return a.turn.inter ? launch_v<T, true>(a, st) : launch_v<T, false>(a, st);
+  const RopeGrid g = rope_grid(a, 1, 1);
+  lm_rope_single_kernel<T><<<(g.units + 255) / 256, 256, 0, st>>>(a, g);
+  return launch_status();
 }
 
 }  // namespace
