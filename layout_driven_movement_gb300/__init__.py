@@ -147,6 +147,25 @@ SIGNATURES = [
 ]
 
 _lib = None
+_pycall_module = None
+
+
+def _pycall():
+    """The extension of the calls that a decoding step makes (raises if it has
+    not been built)."""
+    global _pycall_module
+    if _pycall_module is None:
+        lib()
+        from importlib.machinery import ExtensionFileLoader
+        from importlib.util import module_from_spec, spec_from_file_location
+        path = os.path.join(_PKG, "_pycall.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build the library")
+        spec = spec_from_file_location(
+            "_pycall", path, loader=ExtensionFileLoader("_pycall", path))
+        _pycall_module = module_from_spec(spec)
+        spec.loader.exec_module(_pycall_module)
+    return _pycall_module
 
 
 def lib() -> C.CDLL:
@@ -759,11 +778,6 @@ _SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _dtype_names: dict = {}
 _current_stream = None
 
-# A decoding step makes a handful of these calls, each for a few microseconds
-# of device work: the helpers below keep to the tensor properties that cost
-# least and build messages only when a check fails.
-
-
 def _dtype(dtype) -> str:
     """A torch dtype's name, looked up once."""
     name = _dtype_names.get(dtype)
@@ -787,6 +801,8 @@ def _stream(stream) -> int:
         return stream if isinstance(stream, int) else stream.cuda_stream
     if _current_stream is None:
         import torch
+        if not torch.cuda.is_available():
+            return 0                      # no tensor will pass the checks
         raw = torch._C._cuda_getCurrentRawStream
         device = torch.cuda.current_device
         _current_stream = lambda: raw(device())  # noqa: E731
@@ -795,29 +811,6 @@ def _stream(stream) -> int:
 
 def _wanted(what: str):
     raise ValueError(what + " is wanted")
-
-
-def _rows(t, what: str) -> _Rows:
-    """lm_rows of a CUDA tensor [tokens, heads, dim], dim contiguous."""
-    shape = t.shape
-    if not t.is_cuda or len(shape) != 3:
-        _wanted(f"{what}: a CUDA tensor [tokens, heads, dim]")
-    n, h, d = shape
-    ts, hs, ds = t.stride()
-    if ds != 1 and d != 1:
-        _wanted(f"{what}: a contiguous dim")
-    return _Rows(t.data_ptr(),
-                 (n - 1) * ts + (h - 1) * hs + d if n and h and d else 0,
-                 ts, hs)
-
-
-def _vector(t, dtypes, n, what: str):
-    """The pointer of a contiguous CUDA vector of n elements."""
-    if not t.is_cuda or t.shape != (n,) or _dtype(t.dtype) not in dtypes \
-            or not t.is_contiguous():
-        _wanted(f"{what}: a contiguous CUDA vector of {n} "
-                f"{' or '.join(dtypes)}")
-    return t.data_ptr()
 
 
 def _extent(t) -> int:
@@ -832,7 +825,7 @@ class RopePlan:
     ``head_dim`` (see lm_rope_plan_create).  ``scaling``: None, "linear",
     "ntk" or "yarn"."""
 
-    __slots__ = ("_h", "head_dim", "rotary_dim")
+    __slots__ = ("_h", "_p", "head_dim", "rotary_dim")
 
     def __init__(self, head_dim: int, rotary_dim: int | None = None,
                  interleaved: bool = False, base: float = 10000.0,
@@ -845,7 +838,7 @@ class RopePlan:
             int(head_dim), int(rot), int(interleaved), base,
             _SCALINGS.get(scaling, -1), factor, int(original_positions),
             beta_fast, beta_slow, C.byref(out)), "lm_rope_plan_create")
-        self._h = out
+        self._h, self._p = out, out.value
         self.head_dim = int(head_dim)
         self.rotary_dim = int(rot)
 
@@ -868,45 +861,28 @@ class RopePlan:
         return list(f), amp.value
 
 
-def _table(plan, table) -> tuple[int, int]:
-    """(pointer, positions) of a rotary table."""
+def rope_table(plan: RopePlan, table, stream=None) -> None:
+    """Enqueue the cosines and sines of positions 0, 1, ... into a contiguous
+    float32 CUDA tensor [positions, rotary_dim] (or [positions, 2,
+    rotary_dim / 2])."""
     if not table.is_cuda or _elem(table.dtype) != 3 \
             or not table.is_contiguous() \
             or table.numel() != table.shape[0] * plan.rotary_dim:
         _wanted("table: a contiguous float32 CUDA tensor [positions, "
                 "rotary_dim]")
-    return table.data_ptr(), table.shape[0]
-
-
-def rope_table(plan: RopePlan, table, stream=None) -> None:
-    """Enqueue the cosines and sines of positions 0, 1, ... into a contiguous
-    float32 CUDA tensor [positions, rotary_dim] (or [positions, 2,
-    rotary_dim / 2])."""
-    p, n = _table(plan, table)
-    _check(lib().lm_rope_table(plan._h, p, n, table.numel(),
-                               _stream(stream)), "lm_rope_table")
-
-
-def _turn_args(plan, positions, table, tokens):
-    if positions is None or table is None:
-        _wanted("rope: positions and a table")
-    p = _vector(positions, ("int64", "int32"), tokens, "positions")
-    return (p, positions.element_size(), *_table(plan, table))
+    _check(lib().lm_rope_table(plan.handle, table.data_ptr(), table.shape[0],
+                               table.numel(), _stream(stream)),
+           "lm_rope_table")
 
 
 def rope(plan: RopePlan, x, positions, table, out, inverse: bool = False,
          stream=None) -> None:
     """Enqueue out[t, h] = x[t, h] turned by positions[t] (see lm_rope): x and
     out [tokens, heads, head_dim] of one type, any token and head strides, out
-    may be x.  inverse=True turns back, which is also the gradient."""
-    shape, dtype = x.shape, x.dtype
-    if shape != out.shape or dtype != out.dtype or shape[-1] != plan.head_dim:
-        _wanted("x and out: [tokens, heads, head_dim] of one type")
-    xr, orr = _rows(x, "x"), _rows(out, "out")
-    n, h, _ = shape
-    rc = lib().lm_rope(plan._h, _elem(dtype), xr, orr, n, h,
-                       *_turn_args(plan, positions, table, n),
-                       1 if inverse else 0, _stream(stream))
+    may be x; positions int32 or int64 [tokens].  inverse=True turns back,
+    which is also the gradient."""
+    rc = _pycall().rope(plan._p, plan.head_dim, plan.rotary_dim, x, positions,
+                        table, out, inverse, _stream(stream))
     if rc:
         _check(rc, "lm_rope")
 
@@ -917,7 +893,7 @@ class KVPlan:
     ``store`` how the pages hold rows: None (as they are), "e4m3" or "int8"
     with a scale per token and head (see lm_kv_plan_create)."""
 
-    __slots__ = ("_h", "dtype", "elem", "store", "page_tokens", "heads",
+    __slots__ = ("_h", "_p", "dtype", "elem", "store", "page_tokens", "heads",
                  "dim", "page_stride", "held_bytes")
 
     def __init__(self, page: Layout, dtype, store: str | None = None,
@@ -928,7 +904,7 @@ class KVPlan:
         _check(lib().lm_kv_plan_create(page.handle, int(page_stride),
                                        self.elem, _STORES.get(store, -1),
                                        C.byref(out)), "lm_kv_plan_create")
-        self._h = out
+        self._h, self._p = out, out.value
         self.dtype = dtype
         d = self.describe()
         self.page_tokens, self.heads = d["page_tokens"], d["heads"]
@@ -958,7 +934,7 @@ class KVCache:
     a quantised store float32 scales of pages * heads * page_tokens each.
     ``pages`` defaults to what k holds."""
 
-    __slots__ = ("plan", "k", "v", "k_scale", "v_scale", "pages", "_c")
+    __slots__ = ("plan", "k", "v", "k_scale", "v_scale", "pages", "_c", "_p")
 
     def __init__(self, plan: KVPlan, k, v, k_scale=None, v_scale=None,
                  pages: int | None = None):
@@ -982,13 +958,7 @@ class KVCache:
             k.data_ptr(), v.data_ptr(), ke, ve,
             k_scale.data_ptr() if scales else None,
             v_scale.data_ptr() if scales else None, scales, self.pages)
-
-
-def _kv_rows(t, plan, dtype, what):
-    if t.shape[-1] != plan.dim or (dtype is not None and t.dtype != dtype):
-        _wanted(f"{what}: [tokens, heads, {plan.dim}]"
-                + (f" of {dtype}" if dtype is not None else ""))
-    return _rows(t, what)
+        self._p = C.addressof(self._c)
 
 
 def kv_write(cache: KVCache, k, v, slots, rope: RopePlan | None = None,
@@ -998,32 +968,12 @@ def kv_write(cache: KVCache, k, v, slots, rope: RopePlan | None = None,
     negative: skipped), quantised as the plan says; with ``rope`` the keys are
     turned by ``positions`` on the way (see lm_kv_write)."""
     p = cache.plan
-    kr, vr = _kv_rows(k, p, p.dtype, "k"), _kv_rows(v, p, p.dtype, "v")
-    n, heads, _ = k.shape
-    if heads != p.heads or v.shape != k.shape:
-        _wanted(f"k and v: [tokens, {p.heads}, {p.dim}], as many tokens in "
-                "each,")
-    slots_p = _vector(slots, ("int64",), n, "slots")
-    if rope is not None:
-        rc = lib().lm_kv_write(p._h, cache._c, kr, vr, n, slots_p, rope._h,
-                               *_turn_args(rope, positions, table, n),
-                               _stream(stream))
-    else:
-        rc = lib().lm_kv_write(p._h, cache._c, kr, vr, n, slots_p, None, None,
-                               0, None, 0, _stream(stream))
+    turn, rot = (0, 0) if rope is None else (rope._p, rope.rotary_dim)
+    rc = _pycall().kv_write(p._p, cache._p, p.heads, p.dim, p.elem, k, v,
+                            slots, turn, rot, positions, table,
+                            _stream(stream))
     if rc:
         _check(rc, "lm_kv_write")
-
-
-def _page_table(page_table, seqs):
-    """(pointer, row stride, pages a row)."""
-    shape = page_table.shape
-    if not page_table.is_cuda or len(shape) != 2 or shape[0] != seqs \
-            or _dtype(page_table.dtype) != "int32" \
-            or (shape[1] > 1 and page_table.stride(1) != 1):
-        _wanted("page_table: an int32 CUDA tensor [sequences, pages] with "
-                "contiguous rows")
-    return page_table.data_ptr(), page_table.stride(0), shape[1]
 
 
 def kv_read(cache: KVCache, page_table, lens, starts, k_out, v_out,
@@ -1033,17 +983,8 @@ def kv_read(cache: KVCache, page_table, lens, starts, k_out, v_out,
     float16 or float32); page_table int32 [sequences, pages], lens int32
     [sequences], starts int32 [sequences + 1] (see lm_kv_read)."""
     p = cache.plan
-    dtype, shape = k_out.dtype, k_out.shape
-    kr, vr = _kv_rows(k_out, p, None, "k_out"), _kv_rows(v_out, p, dtype,
-                                                         "v_out")
-    if shape != v_out.shape or shape[1] != p.heads:
-        _wanted(f"k_out and v_out: [rows, {p.heads}, {p.dim}], one shape,")
-    n = lens.shape[0]
-    lp = _vector(lens, ("int32",), n, "lens")
-    sp = _vector(starts, ("int32",), n + 1, "starts")
-    tp, ts, pages = _page_table(page_table, n)
-    rc = lib().lm_kv_read(p._h, cache._c, tp, ts, n, pages, lp, sp,
-                          _elem(dtype), kr, vr, shape[0], _stream(stream))
+    rc = _pycall().kv_read(p._p, cache._p, p.heads, p.dim, page_table, lens,
+                           starts, k_out, v_out, _stream(stream))
     if rc:
         _check(rc, "lm_kv_read")
 
@@ -1066,27 +1007,9 @@ def kv_attend(cache: KVCache, q, page_table, lens, out, workspace=None,
     [sequences, query heads].  scale defaults to dim ** -0.5 (see
     lm_kv_attend)."""
     p = cache.plan
-    qr, orr = _kv_rows(q, p, p.dtype, "q"), _kv_rows(out, p, p.dtype, "out")
-    shape = q.shape
-    if out.shape != shape:
-        _wanted("q and out: one shape")
-    n, hq, d = shape
-    lp = _vector(lens, ("int32",), n, "lens")
-    tp, ts, pages = _page_table(page_table, n)
-    lse_p = ws_p = None
-    ws_bytes = 0
-    if lse is not None:
-        if not lse.is_cuda or not lse.is_contiguous() \
-                or _elem(lse.dtype) != 3 or lse.numel() != n * hq:
-            _wanted("lse: a contiguous float32 CUDA tensor [sequences, query "
-                    "heads]")
-        lse_p = lse.data_ptr()
-    if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            _wanted("workspace: a contiguous CUDA tensor")
-        ws_p, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    rc = lib().lm_kv_attend(p._h, cache._c, qr, orr, n, hq, tp, ts, pages, lp,
-                            window, d ** -0.5 if scale is None else scale,
-                            lse_p, ws_p, ws_bytes, _stream(stream))
+    rc = _pycall().kv_attend(p._p, cache._p, p.dim, p.elem, q, page_table,
+                             lens, out, workspace, lse,
+                             p.dim ** -0.5 if scale is None else scale,
+                             window, _stream(stream))
     if rc:
         _check(rc, "lm_kv_attend")

@@ -5,7 +5,8 @@ copy, tile-copy and exchange planners (plain C++17, compiled with g++) and
 the kernels (CUDA, compiled with nvcc for sm_103a only) -- is built in
 parallel into ``_build/`` and linked into ``liblayoutmove.so`` next to this
 file.  The CUDA runtime is linked
-statically, so the library loads without any other CUDA shared object.
+statically, so the library loads without any other CUDA shared object.  The
+Python extension ``pycall/lm_pycall.c`` is linked to it as ``_pycall.so``.
 """
 
 from __future__ import annotations
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblayoutmove.so")
+PYCALL_SRC = os.path.join(PKG, "pycall", "lm_pycall.c")
+PYCALL = os.path.join(PKG, "_pycall.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -41,14 +45,15 @@ def _newest_input() -> float:
     files = _sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                           if f.endswith((".h", ".cuh"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    files.append(os.path.abspath(__file__))
+    files += [os.path.abspath(__file__), PYCALL_SRC]
     return max(os.path.getmtime(f) for f in files)
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
     """Build (if stale) and return the path of liblayoutmove.so."""
-    if (not force and os.path.exists(LIB)
-            and os.path.getmtime(LIB) >= _newest_input()):
+    if (not force and os.path.exists(LIB) and os.path.exists(PYCALL)
+            and min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
+            >= _newest_input()):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -84,6 +89,15 @@ def build(verbose: bool = False, force: bool = False) -> str:
         raise RuntimeError("layoutmove link failed:\n" +
                            res.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+    tmp = PYCALL + ".tmp"
+    link = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared",
+            "-fPIC", f"-I{INCLUDE}", f"-I{sysconfig.get_path('include')}",
+            PYCALL_SRC, LIB, "-Wl,-rpath,$ORIGIN", "-o", tmp]
+    res = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if res.returncode != 0:
+        raise RuntimeError("layoutmove extension failed:\n" +
+                           res.stdout.decode(errors="replace"))
+    os.replace(tmp, PYCALL)
     return LIB
 
 

@@ -292,3 +292,6 @@ def test_python_checks_before_the_library():
         lm.KVCache(lm.KVPlan(page(), torch.bfloat16), x, x)
     with pytest.raises(ValueError):
         lm.KVPlan(page(), torch.int32)
+    for fn in ("rope", "kv_write", "kv_read", "kv_attend"):
+        with pytest.raises(TypeError):
+            getattr(lm._pycall(), fn)(1, 2)
