@@ -30,7 +30,9 @@ int attend_workspace(int store, int dim, int group, int64_t* bytes) {
   if (rc != LM_OK) return rc;
   const int64_t d = attend_dim(dim), q = 8 * attend_tiles(group);
   const int64_t blocks = sms * (d == 256 ? 1 : store == LM_KV_SAME ? 2 : 3);
-  *bytes = attend_counter_bytes(int(blocks)) + 2 * blocks * q * (d + 2) * 4;
+  // (codes may take two heads a block)
+  const int64_t heads = store == LM_KV_SAME || d == 256 ? 1 : 2;
+  *bytes = attend_space(blocks, heads * q * (d + 2)).bytes;
   return LM_OK;
 }
 

@@ -26,7 +26,8 @@
 // the resident blocks; the tiles (4 KW keys of one sequence and head) of all
 // sequences are one line cut into equal parts, so ragged batches and single
 // long sequences load all SMs alike.  A block's ring runs on across the
-// borders of sequences.  What one block holds of a head that others share
+// borders of sequences.  HP adjacent heads share a block (its warps take them
+// in turn) where their rows share memory lines.  What one block holds of a head that others share
 // goes to the workspace as (m, l, o); the block that comes last by a counter
 // joins the parts, in the order of the line, so results do not depend on
 // which came last.
@@ -44,14 +45,16 @@ enum AttendKind { KIND_BF16, KIND_F16, KIND_E4M3, KIND_INT8 };
 
 constexpr int kAttendWarps = 4;
 constexpr int kAttendThreads = 32 * kAttendWarps;
+constexpr int kAttendRun = 16;   // parts of a head joined at once, at most
 
-template <int KIND, int D, int NT>
+template <int KIND, int D, int NT, int HP>
 struct AttendShape {
   static constexpr bool kCodes = KIND == KIND_E4M3 || KIND == KIND_INT8;
   static constexpr int kHeld = kCodes ? 1 : 2;           // bytes an element
   static constexpr int KW = kCodes ? (D == 64 ? 64 : 32) : 16;  // a warp's step
   static constexpr int KL = (KW + 31) / 32;              // keys a lane
-  static constexpr int TK = KW * kAttendWarps;           // keys of a tile
+  static constexpr int WK = kAttendWarps / HP;           // warps a head
+  static constexpr int TK = KW * WK;                     // keys of a tile
   static constexpr int MT = KW / 16;                     // row tiles of S^T
   static constexpr int Q = 8 * NT;                       // queries
   static constexpr int kRow = D * kHeld;                 // bytes of a row
@@ -70,8 +73,9 @@ struct AttendShape {
   static constexpr int kState = kAttendWarps * Q * 2 * 4;
   static constexpr int kSmem =
       kS * (kStage + kScales + kMasks) + kState + 64;
-  // workspace: a part is (m, l) per query, then its output
-  static constexpr int kPartFloats = Q * (D + 2);
+  // workspace: a part is, for each head, (m, l) per query, then its output
+  static constexpr int kHeadFloats = Q * (D + 2);
+  static constexpr int kPartFloats = HP * kHeadFloats;
   static_assert(Q * D * 4 <= 2 * kPart, "a warp's output fits its stage");
 };
 
@@ -238,14 +242,21 @@ struct Codes<KIND_F16> : Codes<KIND_BF16> {};
 // --- where in the line of work -----------------------------------------------
 
 struct AttendGrid {
-  int items = 1;        // (key heads) x (groups of Q queries)
+  int items = 1;        // (HP key heads) x (groups of Q queries)
   int groups = 1;       // groups of Q queries of a key head
-  int least = 1;        // tiles a block takes at least
   int shared_page = 0;  // the keys of a warp's step share a page
   int q_pairs = 0;      // the queries allow 4-byte loads
-  float* parts = nullptr;
-  unsigned int* counters = nullptr;
+  // workspace: see attend_space
+  unsigned int *counters = nullptr, *run_counters = nullptr;
+  float *parts = nullptr, *runs = nullptr;
 };
+
+// a / b of numbers that are not negative; most are small, and a 64-bit
+// division takes several times a 32-bit one's time.
+__device__ __forceinline__ int64_t line_div(int64_t a, int64_t b) {
+  if ((a | b) >> 31 == 0) return uint32_t(a) / uint32_t(b);
+  return a / b;
+}
 
 struct AttendAt {
   int b, item, tile, lo, hi, first, n;
@@ -282,12 +293,12 @@ __device__ __forceinline__ void attend_next(const KvAttendArgs& a, int items,
 
 // --- the kernel ----------------------------------------------------------------
 
-template <int KIND, int D, int NT>
+template <int KIND, int D, int NT, int HP>
 __global__ void
-__launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
+__launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     lm_kv_attend_kernel(const __grid_constant__ KvAttendArgs a,
                         const __grid_constant__ AttendGrid g) {
-  using S = AttendShape<KIND, D, NT>;
+  using S = AttendShape<KIND, D, NT, HP>;
   constexpr bool CODES = S::kCodes;
   constexpr bool KBF = KIND == KIND_BF16;    // bf16 keys in the products
   constexpr bool VBF = KIND != KIND_F16;     // bf16 values and weights
@@ -302,6 +313,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   extern __shared__ __align__(1024) char smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int row8 = lane / 4, col2 = (lane % 4) * 2;
+  const int sub = warp % HP, wk = warp / HP;   // the warp's head and keys
   const int dim = a.c.dim;
 
   char* const ring = smem;
@@ -359,12 +371,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
     if (total == 0) {
       at.left = 0;
     } else {
-      // as many blocks as the line feeds
-      int64_t blocks = (total + g.least - 1) / g.least;
-      if (blocks > gridDim.x) blocks = gridDim.x;
+      // as many blocks as the line feeds (at least two or four tiles for each
+      // measured no faster, and slower from eight on)
+      const int64_t blocks = min(total, int64_t(gridDim.x));
       const int64_t c = blockIdx.x;
-      begin = c * total / blocks;
-      at.left = c < blocks ? (c + 1) * total / blocks - begin : 0;
+      begin = line_div(c * total, blocks);
+      at.left = c < blocks ? line_div((c + 1) * total, blocks) - begin : 0;
       if (at.left > 0 && begin >= before && begin < before + mine) {
         int b = b0;
         AttendAt s;
@@ -390,7 +402,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
     attend_span<TK>(a, at.b, &at);
     const int tiles = at.hi - at.lo;
     const int64_t in = begin - line_b;
-    at.item = int(in / tiles);
+    at.item = int(line_div(in, tiles));
     at.tile = at.lo + int(in - int64_t(at.item) * tiles);
   }
 
@@ -412,7 +424,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   const int64_t v_from_k = a.c.v - a.c.k;
   constexpr uint32_t full = KW >= 32 ? 0xffffffffu : (1u << KW % 32) - 1;
   auto fetch = [&](Pages* pg) {
-    const int key0 = ld.tile * TK + warp * KW;
+    const int key0 = ld.tile * TK + wk * KW;
 #pragma unroll
     for (int i = 0; i < KL; ++i) {
       const int key = key0 + (g.shared_page ? 0 : lane + 32 * i);
@@ -426,8 +438,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
     }
   };
   auto fill = [&](int stage, const Pages& pg) {
-    const int key0 = ld.tile * TK + warp * KW;
-    const uint32_t h = uint32_t(ld.item / g.groups);
+    const int key0 = ld.tile * TK + wk * KW;
+    const uint32_t h = uint32_t(ld.item / g.groups * HP + sub);
     const uint32_t k_s = ring_s + stage * S::kStage + warp * 2 * S::kPart;
     uint32_t mask[KL], off[KL];
     int64_t from[KL];
@@ -497,7 +509,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   uint32_t qf[KS][NT][2];
   const bool q_pairs = g.q_pairs;
   auto load_q = [&](const AttendAt& p) {
-    const int h = p.item / g.groups, q0 = (p.item - h * g.groups) * Q;
+    const int hp = p.item / g.groups, q0 = (p.item - hp * g.groups) * Q;
+    const int h = hp * HP + sub;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int qi = nt * 8 + row8;
@@ -566,8 +579,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
   int stage = 0;
   while (at.left > 0) {
     // --- one head of one sequence: `steps` tiles of it ---
-    const int h = at.item / g.groups, grp = at.item - h * g.groups;
-    const int q0 = grp * Q;                          // of the key head's
+    const int hp = at.item / g.groups;
+    const int q0 = (at.item - hp * g.groups) * Q;    // of a key head's
     const int nq = min(Q, a.group - q0);
     const int steps = int(min(at.left, int64_t(at.hi - at.tile)));
 
@@ -872,8 +885,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
       for (int j = 0; j < 2; ++j) {
         float t = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kAttendWarps; ++w)
-          t = fmaxf(t, state[(w * Q + nt * 8 + col2 + j) * 2]);
+        for (int w = 0; w < S::WK; ++w)
+          t = fmaxf(t, state[((w * HP + sub) * Q + nt * 8 + col2 + j) * 2]);
         f[j] = ex2(m[nt][j] - (t == -INFINITY ? 0.f : t)) * DOWN;
       }
 #pragma unroll
@@ -896,133 +909,165 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT>::kBlocks)
     }
     __syncthreads();
     const bool whole = steps == tiles;
-    const int64_t c0 = whole ? 0 : ((item_at + 1) * blocks - 1) / total;
-    const int64_t c1 = whole ? 0 : ((item_at + tiles) * blocks - 1) / total;
+    const int64_t c0 = whole ? 0 : line_div((item_at + 1) * blocks - 1, total);
+    const int64_t c1 =
+        whole ? 0 : line_div((item_at + tiles) * blocks - 1, total);
     float* part = nullptr;
     if (!whole)
       part = g.parts +
              (2 * int64_t(blockIdx.x) + (begin < item_at ? 1 : 0)) *
                  S::kPartFloats;
-    const int64_t out_row = int64_t(done.b) * a.heads_q + h * a.group + q0;
-    char* const out0 =
-        a.out.p + (int64_t(done.b) * a.out.ts +
-                   int64_t(h * a.group + q0) * a.out.hs) * 2;
     const bool out_bf = a.elem == LM_BF16;
-    auto put = [&](int qi, int d, float x) {
-      char* to = out0 + (int64_t(qi) * a.out.hs + d) * 2;
+    // query qi of the block's head i: its row, its outputs and its lse
+    auto row_of = [&](int i, int qi) {
+      return (hp * HP + i) * a.group + q0 + qi;
+    };
+    auto put = [&](int i, int qi, int d, float x) {
+      char* to = a.out.p + (int64_t(done.b) * a.out.ts +
+                            int64_t(row_of(i, qi)) * a.out.hs + d) * 2;
       if (out_bf)
         *reinterpret_cast<bf16*>(to) = from_f32<bf16>(x);
       else
         *reinterpret_cast<__half*>(to) = from_f32<__half>(x);
     };
-    for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {
-      const int qi = e / D, d = e % D;
-      float t = -INFINITY, x = 0, sum = 0;
+    auto put_lse = [&](int i, int qi, float t, float sum) {
+      if (a.lse)
+        a.lse[int64_t(done.b) * a.heads_q + row_of(i, qi)] =
+            sum == 0 ? -INFINITY
+                     : (t + log2f(sum)) * 0.693147180559945309f;
+    };
+    for (int i = 0; i < HP; ++i)
+      for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {
+        const int qi = e / D, d = e % D;
+        float t = -INFINITY, x = 0, sum = 0;
 #pragma unroll
-      for (int w = 0; w < kAttendWarps; ++w)
-        t = fmaxf(t, state[(w * Q + qi) * 2]);
-      const float t0 = t == -INFINITY ? 0.f : t;
+        for (int w = 0; w < S::WK; ++w)
+          t = fmaxf(t, state[((w * HP + i) * Q + qi) * 2]);
+        const float t0 = t == -INFINITY ? 0.f : t;
 #pragma unroll
-      for (int w = 0; w < kAttendWarps; ++w) {
-        sum += state[(w * Q + qi) * 2 + 1] *
-               ex2(state[(w * Q + qi) * 2] - t0);
-        x += reinterpret_cast<const float*>(
-            ring + used * S::kStage +
-            w * 2 * S::kPart)[qi * D + (d ^ ((qi & 6) * 4))];
-      }
-      if (whole) {
-        if (d < dim) put(qi, d, sum == 0 ? 0.f : x / sum);
-        if (d == 0 && a.lse)
-          a.lse[out_row + qi] =
-              sum == 0 ? -INFINITY
-                       : (t + log2f(sum)) * 0.693147180559945309f;
-      } else {
-        part[2 * Q + qi * D + d] = x;
-        if (d == 0) {
-          part[2 * qi] = t;
-          part[2 * qi + 1] = sum;
+        for (int w = 0; w < S::WK; ++w) {
+          const float* st = state + ((w * HP + i) * Q + qi) * 2;
+          sum += st[1] * ex2(st[0] - t0);
+          x += reinterpret_cast<const float*>(
+              ring + used * S::kStage + (w * HP + i) * 2 * S::kPart)
+              [qi * D + (d ^ ((qi & 6) * 4))];
+        }
+        if (whole) {
+          if (d < dim) put(i, qi, d, sum == 0 ? 0.f : x / sum);
+          if (d == 0) put_lse(i, qi, t, sum);
+        } else {
+          float* to = part + i * S::kHeadFloats;
+          to[2 * Q + qi * D + d] = x;
+          if (d == 0) {
+            to[2 * qi] = t;
+            to[2 * qi + 1] = sum;
+          }
         }
       }
-    }
+    __syncthreads();
     if (!whole) {
-      // the block that comes last joins the parts c0 .. c1
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const unsigned before = atomicAdd(g.counters + c0, 1u);
-        share[6] = before == unsigned(c1 - c0);
-        if (share[6]) g.counters[c0] = 0;
-      }
-      __syncthreads();
-      if (share[6]) {
-        __threadfence();
-        const int64_t p0 =
-            2 * c0 + (c0 * total / blocks < item_at ? 1 : 0);
-        auto part_of = [&](int64_t c) {
-          return g.parts + (c == c0 ? p0 : 2 * c) * S::kPartFloats;
-        };
-        // A warp per query finds its state and weighs its parts, a lane a
-        // part, up to kMost at a time; then every thread adds up 4 elements
-        // of the parts.  Both orders are the line's own.
-        constexpr int kMost = 128;
-        const int n = int(c1 - c0) + 1;
-        float* const wt = reinterpret_cast<float*>(ring + used * S::kStage);
-        static_assert(Q * kMost * 4 <= S::kStage, "the weights fit a stage");
-        for (int qi = warp; qi < nq; qi += kAttendWarps) {
-          float t = -INFINITY, sum = 0;
-          float2 ml0 = make_float2(-INFINITY, 0);
-          if (lane < n)
-            ml0 = __ldcg(reinterpret_cast<const float2*>(part_of(c0 + lane)) +
-                         qi);
-          t = ml0.x;
-          for (int i = lane + 32; i < n; i += 32)
-            t = fmaxf(t, __ldcg(part_of(c0 + i) + 2 * qi));
-#pragma unroll
-          for (int k = 16; k; k /= 2)
-            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
-          const float t0 = t == -INFINITY ? 0.f : t;
-          for (int i = lane; i < n; i += 32) {
-            const float2 ml =
-                i < 32 ? ml0
-                       : __ldcg(reinterpret_cast<const float2*>(
-                                    part_of(c0 + i)) + qi);
-            const float f = ex2(ml.x - t0);
-            sum += ml.y * f;
-            if (i < kMost) wt[qi * kMost + i] = f;
-          }
-#pragma unroll
-          for (int k = 16; k; k /= 2)
-            sum += __shfl_xor_sync(0xffffffffu, sum, k);
-          if (lane == 0) {
-            state[2 * qi] = t0;
-            state[2 * qi + 1] = sum;
-            if (a.lse)
-              a.lse[out_row + qi] =
-                  sum == 0 ? -INFINITY
-                           : (t + log2f(sum)) * 0.693147180559945309f;
-          }
+      // The block that comes last joins the parts c0 .. c1.  Where they are
+      // more than 16, even runs of up to 16 are joined first, each by the
+      // last of its own blocks, and then the runs: no block reads more than a
+      // few rounds of parts, 8 at once.
+      const int n = int(c1 - c0) + 1;
+      const int runs = (n + kAttendRun - 1) / kAttendRun;
+      const int run = ((int(blockIdx.x) - int(c0) + 1) * runs - 1) / n;
+      const int from = run * n / runs;
+      const int size = (run + 1) * n / runs - from;
+      // whether this block is the last of `count` to come by a counter, which
+      // it then leaves at zero
+      auto last_of = [&](unsigned int* counter, int count) {
+        if (threadIdx.x == 0) {
+          __threadfence();
+          const unsigned before = atomicAdd(counter, 1u);
+          __threadfence();
+          share[6] = before == unsigned(count - 1);
+          if (share[6]) *counter = 0;
         }
         __syncthreads();
-        for (int e = threadIdx.x * 4; e < nq * D; e += kAttendThreads * 4) {
-          const int qi = e / D, d = e % D;
-          float x[4] = {0, 0, 0, 0};
-          auto add = [&](int i, float f) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(
-                part_of(c0 + i) + 2 * Q + e));
-            x[0] += v.x * f;
-            x[1] += v.y * f;
-            x[2] += v.z * f;
-            x[3] += v.w * f;
-          };
-#pragma unroll 8
-          for (int i = 0; i < min(n, kMost); ++i) add(i, wt[qi * kMost + i]);
-          for (int i = kMost; i < n; ++i)
-            add(i, ex2(__ldcg(part_of(c0 + i) + 2 * qi) - state[2 * qi]));
-          const float sum = state[2 * qi + 1];
+        const bool last = share[6];
+        __syncthreads();
+        return last;
+      };
+      // adds up parts 0 .. m - 1, 4 elements a thread at a time
+      auto join = [&](int m, auto&& part_of, auto&& emit) {
+        for (int i = 0; i < HP; ++i)
+          for (int e = threadIdx.x * 4; e < nq * D; e += kAttendThreads * 4) {
+            float t = -INFINITY, sum = 0, x[4] = {0, 0, 0, 0};
+            for (int k0 = 0; k0 < m; k0 += 8) {
+              float2 ml[8];
+              float4 v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (d + i < dim) put(qi, d + i, sum == 0 ? 0.f : x[i] / sum);
-        }
+              for (int k = 0; k < 8; ++k) {
+                ml[k] = make_float2(-INFINITY, 0);
+                v[k] = make_float4(0, 0, 0, 0);
+                if (k0 + k < m) {
+                  const float* pk = part_of(k0 + k) + i * S::kHeadFloats;
+                  ml[k] = __ldcg(reinterpret_cast<const float2*>(pk) + e / D);
+                  v[k] = __ldcg(
+                      reinterpret_cast<const float4*>(pk + 2 * Q + e));
+                }
+              }
+              float top = t;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
+              const float t0 = top == -INFINITY ? 0.f : top;
+              const float keep = ex2(t - t0);
+              sum *= keep;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] *= keep;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float f = ex2(ml[k].x - t0);
+                sum += ml[k].y * f;
+                x[0] += v[k].x * f;
+                x[1] += v[k].y * f;
+                x[2] += v[k].z * f;
+                x[3] += v[k].w * f;
+              }
+              t = top;
+            }
+            emit(i, e, t, sum, x);
+          }
+      };
+      auto finish = [&](int i, int e, float t, float sum, const float* x) {
+        const int qi = e / D, d = e % D;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (d + k < dim) put(i, qi, d + k, sum == 0 ? 0.f : x[k] / sum);
+        if (d == 0) put_lse(i, qi, t, sum);
+      };
+      const int64_t p0 = 2 * c0 + (line_div(c0 * total, blocks) < item_at ? 1 : 0);
+      auto block_part = [&](int k) -> const float* {
+        const int c = from + k;
+        return g.parts + (c == 0 ? p0 : 2 * (c0 + c)) * S::kPartFloats;
+      };
+      // Runs of a head that has several hold 8 parts or more, so that their
+      // first blocks lie 7 or more apart (neighbouring heads share a block).
+      auto run_slot = [&](int r) {
+        return (int(c0) + r * n / runs) / (kAttendRun / 2 - 1);
+      };
+      auto run_part = [&](int r) {
+        return g.runs + run_slot(r) * int64_t(S::kPartFloats);
+      };
+      if (runs == 1) {
+        if (last_of(g.counters + c0, n)) join(n, block_part, finish);
+      } else if (last_of(g.run_counters + run_slot(run), size)) {
+        join(size, block_part,
+             [&](int i, int e, float t, float sum, const float* x) {
+               float* to = run_part(run) + i * S::kHeadFloats;
+               *reinterpret_cast<float4*>(to + 2 * Q + e) =
+                   make_float4(x[0], x[1], x[2], x[3]);
+               if (e % D == 0) {
+                 to[2 * (e / D)] = t;
+                 to[2 * (e / D) + 1] = sum;
+               }
+             });
+        __syncthreads();
+        if (last_of(g.counters + c0, runs))
+          join(runs, [&](int r) -> const float* { return run_part(r); },
+               finish);
       }
     }
     __syncthreads();
@@ -1038,18 +1083,28 @@ inline int attend_tiles(int group) { return group <= 8 ? 1 : 2; }
 
 inline int attend_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// The workspace: a counter per block, then two parts per block.
-inline int64_t attend_counter_bytes(int blocks) {
-  return (int64_t(blocks) * 4 + 255) / 256 * 256;
+// The workspace of a grid of `blocks` and parts of `floats`: a counter per
+// block and one per run of parts, then two parts per block and one per run.
+struct AttendSpace {
+  int64_t run_counters, parts, runs, bytes;
+};
+inline AttendSpace attend_space(int64_t blocks, int64_t floats) {
+  const int64_t most = blocks / (kAttendRun / 2 - 1) + 1;
+  AttendSpace s;
+  s.run_counters = blocks * 4;
+  s.parts = (s.run_counters + most * 4 + 255) / 256 * 256;
+  s.runs = s.parts + 2 * blocks * floats * 4;
+  s.bytes = s.runs + most * floats * 4;
+  return s;
 }
 
-template <int KIND, int D, int NT>
+template <int KIND, int D, int NT, int HP>
 int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
-  using S = AttendShape<KIND, D, NT>;
+  using S = AttendShape<KIND, D, NT, HP>;
   int sms = 0, dev = 0;
   const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  auto* kernel = lm_kv_attend_kernel<KIND, D, NT>;
+  auto* kernel = lm_kv_attend_kernel<KIND, D, NT, HP>;
   static std::atomic<uint64_t> allowed{0};    // a bit per device
   if (!(allowed.load() >> dev & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -1063,28 +1118,42 @@ int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
   const int blocks = sms * S::kBlocks;
   AttendGrid g;
   g.groups = (a.group + S::Q - 1) / S::Q;
-  g.items = int(a.c.heads) * g.groups;
+  g.items = int(a.c.heads) / HP * g.groups;
   g.shared_page = a.c.page_tokens % S::KW == 0;
   g.q_pairs = reinterpret_cast<uintptr_t>(a.q.p) % 4 == 0 &&
               a.q.ts % 2 == 0 && a.q.hs % 2 == 0;
-  g.counters = static_cast<unsigned int*>(a.ws);
-  g.parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) +
-                                     attend_counter_bytes(blocks));
+  char* const ws = static_cast<char*>(a.ws);
+  const AttendSpace at = attend_space(blocks, S::kPartFloats);
+  g.counters = reinterpret_cast<unsigned int*>(ws);
+  g.run_counters = reinterpret_cast<unsigned int*>(ws + at.run_counters);
+  g.parts = reinterpret_cast<float*>(ws + at.parts);
+  g.runs = reinterpret_cast<float*>(ws + at.runs);
   kernel<<<unsigned(blocks), kAttendThreads, S::kSmem, st>>>(a, g);
   return launch_status();
 }
 
+template <int KIND, int D>
+int launch_attend_dim(const KvAttendArgs& a, cudaStream_t st) {
+  const bool few = attend_tiles(a.group) == 1;
+  if constexpr ((KIND == KIND_E4M3 || KIND == KIND_INT8) && D <= 128) {
+    // Rows that are no whole 128-byte lines, heads side by side: lines that
+    // two heads share come in once when one block takes both (3 x 131072
+    // tokens of 4 x 64 int8: @HP1@ us a head at a time, @HP2@ in pairs).
+    if (a.c.dim % 128 != 0 && a.c.heads % 2 == 0 &&
+        a.c.head_b < a.c.token_b)
+      return few ? launch_attend<KIND, D, 1, 2>(a, st)
+                 : launch_attend<KIND, D, 2, 2>(a, st);
+  }
+  return few ? launch_attend<KIND, D, 1, 1>(a, st)
+             : launch_attend<KIND, D, 2, 1>(a, st);
+}
+
 template <int KIND>
 int launch_attend_kind(const KvAttendArgs& a, cudaStream_t st) {
-  const int d = attend_dim(a.c.dim), nt = attend_tiles(a.group);
-  if (d == 64)
-    return nt == 1 ? launch_attend<KIND, 64, 1>(a, st)
-                   : launch_attend<KIND, 64, 2>(a, st);
-  if (d == 128)
-    return nt == 1 ? launch_attend<KIND, 128, 1>(a, st)
-                   : launch_attend<KIND, 128, 2>(a, st);
-  return nt == 1 ? launch_attend<KIND, 256, 1>(a, st)
-                 : launch_attend<KIND, 256, 2>(a, st);
+  const int d = attend_dim(a.c.dim);
+  return d == 64    ? launch_attend_dim<KIND, 64>(a, st)
+         : d == 128 ? launch_attend_dim<KIND, 128>(a, st)
+                    : launch_attend_dim<KIND, 256>(a, st);
 }
 
 int launch_attend_bf16(const KvAttendArgs& a, cudaStream_t st);
