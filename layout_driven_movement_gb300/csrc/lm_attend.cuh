@@ -340,6 +340,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   // The line of work: every thread counts the tiles of a run of sequences;
   // a scan over the block gives the line's length and where this block's
   // share starts.
+  stream_order();
   AttendAt at;
   int64_t total, begin;
   int64_t line_b;        // where sequence at.b starts on the line
@@ -1128,8 +1129,7 @@ int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
   g.run_counters = reinterpret_cast<unsigned int*>(ws + at.run_counters);
   g.parts = reinterpret_cast<float*>(ws + at.parts);
   g.runs = reinterpret_cast<float*>(ws + at.runs);
-  kernel<<<unsigned(blocks), kAttendThreads, S::kSmem, st>>>(a, g);
-  return launch_status();
+  return launch(kernel, blocks, kAttendThreads, S::kSmem, st, a, g);
 }
 
 template <int KIND, int D>

@@ -102,6 +102,7 @@ __device__ __forceinline__ void get8(const uint4& u, float* x) {
 template <class T, int STORE, int L, bool VEC, int TURN>
 __global__ void __launch_bounds__(256, TURN == 0 ? 6 : 4) lm_kv_write_kernel(
     const __grid_constant__ KvWriteArgs a) {
+  stream_order();
   const uint32_t row = (blockIdx.x * 256 + threadIdx.x) / L;
   const int c = int(threadIdx.x % L);
   const bool live = row < a.tokens * a.c.heads;
@@ -231,18 +232,14 @@ __global__ void __launch_bounds__(256, TURN == 0 ? 6 : 4) lm_kv_write_kernel(
 template <class T, int STORE, int L>
 int launch_write_l(const KvWriteArgs& a, cudaStream_t st) {
   const uint64_t threads = uint64_t(a.tokens) * a.c.heads * L;
-  const unsigned grid = unsigned((threads + 255) / 256);
+  const uint64_t grid = (threads + 255) / 256;
+  auto run = [&](auto* kernel) { return launch(kernel, grid, 256, 0, st, a); };
   // (dim == 16 L: whole chunks, every lane has both)
   const bool own = a.table16 && !a.turn.inter && a.turn.rot == 16 * L;
-  if (!a.vec)
-    lm_kv_write_kernel<T, STORE, L, false, 2><<<grid, 256, 0, st>>>(a);
-  else if (!a.turn.pos)
-    lm_kv_write_kernel<T, STORE, L, true, 0><<<grid, 256, 0, st>>>(a);
-  else if (own)
-    lm_kv_write_kernel<T, STORE, L, true, 1><<<grid, 256, 0, st>>>(a);
-  else
-    lm_kv_write_kernel<T, STORE, L, true, 2><<<grid, 256, 0, st>>>(a);
-  return launch_status();
+  if (!a.vec) return run(lm_kv_write_kernel<T, STORE, L, false, 2>);
+  if (!a.turn.pos) return run(lm_kv_write_kernel<T, STORE, L, true, 0>);
+  if (own) return run(lm_kv_write_kernel<T, STORE, L, true, 1>);
+  return run(lm_kv_write_kernel<T, STORE, L, true, 2>);
 }
 
 template <class T, int STORE>
@@ -307,6 +304,7 @@ __global__ void __launch_bounds__(256) lm_kv_read_kernel(
     const __grid_constant__ KvReadArgs a, const __grid_constant__ ReadGrid g) {
   __shared__ int64_t s_page[kReadTokens];   // -1: no token, -2: zeros
   __shared__ uint32_t s_off[kReadTokens];
+  stream_order();
   const int64_t t0 = int64_t(blockIdx.x) * g.tokens;
   int below = 0;                             // starts[0 .. seqs) <= t0
   for (int b = 0; b < a.seqs; b += 256)
@@ -404,12 +402,11 @@ int launch_read_o(const KvReadArgs& a, cudaStream_t st) {
   int64_t tokens = most < kReadTokens ? most : kReadTokens;
   if (tokens > spread) tokens = spread;
   g.tokens = int(tokens < 1 ? 1 : tokens);
-  const unsigned grid = unsigned((a.rows + g.tokens - 1) / g.tokens);
-  if (a.vec)
-    lm_kv_read_kernel<T, STORE, TO, true><<<grid, 256, 0, st>>>(a, g);
-  else
-    lm_kv_read_kernel<T, STORE, TO, false><<<grid, 256, 0, st>>>(a, g);
-  return launch_status();
+  const uint64_t grid = uint64_t((a.rows + g.tokens - 1) / g.tokens);
+  return a.vec ? launch(lm_kv_read_kernel<T, STORE, TO, true>, grid, 256, 0,
+                        st, a, g)
+               : launch(lm_kv_read_kernel<T, STORE, TO, false>, grid, 256, 0,
+                        st, a, g);
 }
 
 template <class TO>

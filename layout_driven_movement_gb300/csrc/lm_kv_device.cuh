@@ -117,9 +117,32 @@ __device__ __forceinline__ float turn_hi(float a, float b, float c, float s) {
   return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
-inline int launch_status() {
-  const cudaError_t e = cudaGetLastError();
+// First in every kernel of this section, before it touches global memory: the
+// next kernel on the stream may take the room that this one leaves, and this
+// one goes on when all before it are done and their writes visible.
+__device__ __forceinline__ void stream_order() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
+// Launches a kernel that begins with stream_order(): its launch overlaps the
+// end of the kernel before it.
+template <class... P, class... A>
+int launch(void (*kernel)(P...), uint64_t grid, int block, int smem,
+           cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(block));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e == cudaSuccess) return LM_OK;
+  cudaGetLastError();                      // not left for a later call
   set_cuda_error(int(e));
   return LM_E_CUDA;
 }

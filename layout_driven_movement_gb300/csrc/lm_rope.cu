@@ -10,6 +10,7 @@ namespace {
 // Run once per plan; bound by the 64-bit sine and cosine.
 __global__ void __launch_bounds__(256) lm_rope_table_kernel(
     const __grid_constant__ RopeTableArgs a) {
+  stream_order();
   const int64_t n = a.rows * a.half;
   for (int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x; at < n;
        at += int64_t(gridDim.x) * 256) {
@@ -76,6 +77,7 @@ __device__ __forceinline__ void angles(const Turn& turn, const float* row,
 template <class T, bool INTER, int H>
 __global__ void __launch_bounds__(256) lm_rope_kernel(
     const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
+  stream_order();
   const uint32_t u = blockIdx.x * 256 + threadIdx.x;
   if (u >= g.units) return;
   const RopeUnit at(g, u);
@@ -143,6 +145,7 @@ __global__ void __launch_bounds__(256) lm_rope_kernel(
 template <class T>
 __global__ void __launch_bounds__(256) lm_rope_single_kernel(
     const __grid_constant__ RopeArgs a, const __grid_constant__ RopeGrid g) {
+  stream_order();
   const uint32_t u = blockIdx.x * 256 + threadIdx.x;
   if (u >= g.units) return;
   const RopeUnit at(g, u);
@@ -181,8 +184,8 @@ RopeGrid rope_grid(const RopeArgs& a, int v, int h) {
 template <class T, bool INTER, int H>
 int launch_h(const RopeArgs& a, cudaStream_t st) {
   const RopeGrid g = rope_grid(a, 16 / int(sizeof(T)), H);
-  lm_rope_kernel<T, INTER, H><<<(g.units + 255) / 256, 256, 0, st>>>(a, g);
-  return launch_status();
+  return launch(lm_rope_kernel<T, INTER, H>, (uint64_t(g.units) + 255) / 256,
+                256, 0, st, a, g);
 }
 
 constexpr uint64_t kRopeShare = 152 * 2048;
@@ -203,8 +206,8 @@ int launch_t(const RopeArgs& a, cudaStream_t st) {
   if (a.vec)
     return a.turn.inter ? launch_v<T, true>(a, st) : launch_v<T, false>(a, st);
   const RopeGrid g = rope_grid(a, 1, 1);
-  lm_rope_single_kernel<T><<<(g.units + 255) / 256, 256, 0, st>>>(a, g);
-  return launch_status();
+  return launch(lm_rope_single_kernel<T>, (uint64_t(g.units) + 255) / 256, 256,
+                0, st, a, g);
 }
 
 }  // namespace
@@ -218,9 +221,8 @@ int launch_rope(const RopeArgs& a, int elem, void* stream) {
 
 int launch_rope_table(const RopeTableArgs& a, void* stream) {
   const int64_t blocks = (a.rows * a.half + 255) / 256;
-  lm_rope_table_kernel<<<unsigned(blocks < (1 << 20) ? blocks : (1 << 20)),
-                         256, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return launch_status();
+  return launch(lm_rope_table_kernel, blocks < (1 << 20) ? blocks : (1 << 20),
+                256, 0, static_cast<cudaStream_t>(stream), a);
 }
 
 }  // namespace lm
