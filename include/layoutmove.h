@@ -705,7 +705,8 @@ int lm_kv_plan_describe(const lm_kv_plan* plan, char* buf, size_t cap);
 
 /* Enqueue the write of tokens' rows into the cache: k[t, h] and v[t, h] go
  * to token slots[t] % P of page slots[t] / P, P tokens a page, held as the
- * plan's store says.  A negative slot skips its token; one past the last
+ * plan's store says.  A negative slot skips its token (whatever its position
+ * says); one past the last
  * page is out of range and skipped too.  The slots of a call are distinct.
  * With rope (NULL: none), keys are first turned as lm_rope turns them, in 32
  * bits, and rounded only into the cache; rope's head_dim is the plan's dim.
@@ -734,10 +735,12 @@ int lm_kv_read(const lm_kv_plan* plan, const lm_kv_cache* cache,
                int out_elem, const lm_rows* k_out, const lm_rows* v_out,
                int64_t rows, void* cuda_stream);
 
-/* Bytes of the workspace of lm_kv_attend for up to seqs sequences of heads_q
- * query heads on the current device.  Zero it once before its first use;
- * every call leaves it ready for the next.  Calls that may overlap on the
- * GPU need workspaces of their own.  Errors: LM_E_INVALID, LM_E_CUDA. */
+/* Bytes of the workspace of lm_kv_attend for seqs sequences of heads_q query
+ * heads on the current device (a few MB; the same for every seqs).  Zero it
+ * once before its first use; every call leaves it ready for the next, of any
+ * plan that asks for no more.  Calls that may overlap on the GPU need
+ * workspaces of their own.
+ * Errors: LM_E_INVALID, LM_E_CUDA. */
 int lm_kv_attend_workspace(const lm_kv_plan* plan, int seqs, int heads_q,
                            int64_t* bytes);
 
@@ -752,9 +755,13 @@ int lm_kv_attend_workspace(const lm_kv_plan* plan, int seqs, int heads_q,
  * -infinity.  A page number outside [0, pages) is out of range and its keys
  * are not seen.  lse (NULL: not wanted): seqs x heads_q floats, contiguous.
  * q and out hold the plan's elem; out may be q itself with the same strides.
- * Nothing past a sequence's length is used, whatever it holds.
+ * Nothing past a sequence's length is used, whatever it holds.  Scores and
+ * sums are in 32 bits; a NaN in a query, key, value or scale that is used
+ * comes out as NaN, an infinite value as infinity or NaN.  The same inputs
+ * give the same bits.
  * Errors: LM_E_INVALID (NULL, counts, heads_q not a multiple of the plan's
- * heads, a scale that is not finite, negative window, pointer alignment),
+ * heads or above 2^20, a scale that is not finite, negative window, pointer
+ * alignment),
  * LM_E_CAPACITY (a buffer, or the workspace), LM_E_OVERLAP, LM_E_OVERFLOW,
  * LM_E_CUDA. */
 int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,

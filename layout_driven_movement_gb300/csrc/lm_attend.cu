@@ -32,7 +32,7 @@ int attend_workspace(int store, int dim, int group, int64_t* bytes) {
   const int64_t blocks = sms * (d == 256 ? 1 : store == LM_KV_SAME ? 2 : 3);
   // (codes may take two heads a block)
   const int64_t heads = store == LM_KV_SAME || d == 256 ? 1 : 2;
-  *bytes = attend_space(blocks, heads * q * (d + 2)).bytes;
+  *bytes = attend_space(sms, blocks, heads * q * (d + 2)).bytes;
   return LM_OK;
 }
 

@@ -129,8 +129,8 @@ CacheArgs check_cache(const lm_kv_plan& p, const lm_kv_cache* c, Range* k,
 // Pages, tokens and sequences as the kernels count them.
 void check_table(const lm_kv_plan& p, const int32_t* table, int64_t stride,
                  int seqs, int64_t max_pages, const int32_t* lens) {
-  need(table && lens && seqs >= 0 && max_pages >= 0 && stride >= 0 &&
-       addr(table) % 4 == 0 && addr(lens) % 4 == 0);
+  need((table || max_pages == 0) && lens && seqs >= 0 && max_pages >= 0 &&
+       stride >= 0 && addr(table) % 4 == 0 && addr(lens) % 4 == 0);
   need(seqs <= 1 || stride >= max_pages);
   // key numbers, rounded up to whole tiles, fit 32 bits
   need(mul_chk(max_pages, p.page_tokens) < (int64_t(1) << 31) - 4096,
@@ -419,7 +419,7 @@ int lm_kv_attend_workspace(const lm_kv_plan* plan, int seqs, int heads_q,
   int rc = LM_OK;
   const int checked = lm::guarded([&] {
     need(plan && bytes && seqs >= 0 && heads_q >= 1 &&
-         heads_q % plan->heads == 0);
+         heads_q <= (1 << 20) && heads_q % plan->heads == 0);
     rc = lm::attend_workspace(plan->store, int(plan->dim),
                               int(heads_q / plan->heads), bytes);
   });
@@ -435,7 +435,7 @@ int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
   int rc = LM_OK;
   const int checked = lm::guarded([&] {
     need(plan && seqs >= 0 && heads_q >= 1 && heads_q % plan->heads == 0 &&
-         heads_q / plan->heads < 65536 && std::isfinite(scale) && window >= 0);
+         heads_q <= (1 << 20) && std::isfinite(scale) && window >= 0);
     lm::Range rk, rv;
     lm::KvAttendArgs a;
     a.c = lm::check_cache(*plan, cache, &rk, &rv);

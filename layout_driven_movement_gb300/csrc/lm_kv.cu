@@ -93,8 +93,11 @@ __device__ __forceinline__ void get8(const uint4& u, float* x) {
 // used, a row's largest magnitude is log2 L shuffles away, its codes leave as
 // 8-byte stores of adjacent lanes, and the turn of a whole row of 16 L
 // elements (partners 8 L apart) stays inside a thread, one cosine and sine
-// for both partners.  Bound by memory and, within a factor of two, by the
-// instructions of the rounding: inputs read once, codes written once.
+// for both partners.  Bound by memory: inputs read once, codes written once (8
+// sequences of up to 8192 tokens of 8 x 128 into e4m3, 234 MB: 35 us, 6.6
+// TB/s).  With the turn, 49 us, the angles' loads (a quarter of the rows' bytes
+// again, from L2) and the turn's instructions show: a third of the issue slots
+// go to the roundings as it is.
 //
 // TURN: 0 no turn, 1 partners 8 L apart, 2 any other.  Two heads a thread, to
 // share a token's slot and angles, spill or halve the resident warps: 70 us
@@ -129,7 +132,8 @@ __global__ void __launch_bounds__(256, TURN == 0 ? 6 : 4) lm_kv_write_kernel(
   float cs[8], sn[8];
   const float nan = __int_as_float(0x7fc00000);
   if (TURN && live && a.turn.pos) {
-    tr = turn_row(a.turn, t, c == 0 ? a.status : nullptr);
+    // (a skipped token's position may be anything)
+    tr = turn_row(a.turn, t, c == 0 && slot >= 0 ? a.status : nullptr);
     if (TURN == 1) {
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
@@ -282,6 +286,7 @@ __device__ __forceinline__ void held_values(const uint4& w, float scale,
 }
 
 constexpr int kReadTokens = 32;   // tokens of a block at most
+constexpr int kReadThreads = 128;
 constexpr int kReadUnits = 2;     // 16-byte loads of a thread in flight
 
 struct ReadGrid {
@@ -296,18 +301,19 @@ struct ReadGrid {
 // go on from there to their page and offset.  Then all threads move 16 held
 // bytes at a time, heads and dim fastest, so that a token's rows leave as one
 // run.  Bound by memory: codes and scales read once, rows written once.
-// Small blocks in many waves measured best (16 x 16384 tokens of 8 x 128 e4m3:
-// 165 us with two loads a thread, 180 with four, 206 with resident blocks that
-// look the next rows up while they move these).
+// Small blocks in many waves measured best (16 x 16384 tokens of 8 x 128 e4m3,
+// 1.02 GB: 162 us, 6.3 TB/s; 166 and 176 with 256 and 512 threads, 174 with
+// four loads a thread, 206 with resident blocks that look the next rows up
+// while they move these).
 template <class T, int STORE, class TO, bool VEC>
-__global__ void __launch_bounds__(256) lm_kv_read_kernel(
+__global__ void __launch_bounds__(kReadThreads) lm_kv_read_kernel(
     const __grid_constant__ KvReadArgs a, const __grid_constant__ ReadGrid g) {
   __shared__ int64_t s_page[kReadTokens];   // -1: no token, -2: zeros
   __shared__ uint32_t s_off[kReadTokens];
   stream_order();
   const int64_t t0 = int64_t(blockIdx.x) * g.tokens;
   int below = 0;                             // starts[0 .. seqs) <= t0
-  for (int b = 0; b < a.seqs; b += 256)
+  for (int b = 0; b < a.seqs; b += kReadThreads)
     below += __syncthreads_count(b + int(threadIdx.x) < a.seqs &&
                                  a.starts[b + threadIdx.x] <= t0);
   if (threadIdx.x < g.tokens) {
@@ -335,13 +341,13 @@ __global__ void __launch_bounds__(256) lm_kv_read_kernel(
   __syncthreads();
   constexpr int N = STORE == LM_KV_SAME ? 8 : 16;   // elements of a unit
   const uint32_t units = g.tokens * g.row_units;
-  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += 256 * kReadUnits) {
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kReadThreads * kReadUnits) {
     uint4 held[kReadUnits];
     float scale[kReadUnits];
     TO* dst[kReadUnits];
 #pragma unroll
     for (int k = 0; k < kReadUnits; ++k) {
-      const uint32_t u = u0 + 256 * k;
+      const uint32_t u = u0 + kReadThreads * k;
       dst[k] = nullptr;
       if (u >= units) continue;
       const uint32_t i = fdiv(u, g.row_div);
@@ -397,15 +403,15 @@ int launch_read_o(const KvReadArgs& a, cudaStream_t st) {
   g.chunk_div = make_fastdiv(g.chunks);
   g.row_div = make_fastdiv(g.row_units);
   // a round of the block's loads, or less where that leaves SMs idle
-  const uint32_t most = (256 * kReadUnits + g.row_units - 1) / g.row_units;
+  const uint32_t most = (kReadThreads * kReadUnits + g.row_units - 1) / g.row_units;
   const int64_t spread = a.rows / 608;
   int64_t tokens = most < kReadTokens ? most : kReadTokens;
   if (tokens > spread) tokens = spread;
   g.tokens = int(tokens < 1 ? 1 : tokens);
   const uint64_t grid = uint64_t((a.rows + g.tokens - 1) / g.tokens);
-  return a.vec ? launch(lm_kv_read_kernel<T, STORE, TO, true>, grid, 256, 0,
+  return a.vec ? launch(lm_kv_read_kernel<T, STORE, TO, true>, grid, kReadThreads, 0,
                         st, a, g)
-               : launch(lm_kv_read_kernel<T, STORE, TO, false>, grid, 256, 0,
+               : launch(lm_kv_read_kernel<T, STORE, TO, false>, grid, kReadThreads, 0,
                         st, a, g);
 }
 

@@ -521,6 +521,152 @@ def test_attend_workspace_serves_call_after_call():
     check_attend(Q, 4, q, out, lse)
 
 
+@pytest.mark.parametrize("store,dtype,dim,heads,group,order", [
+    ("int8", BF, 64, 4, 5, "nhd"), ("e4m3", HF, 64, 2, 12, "nhd"),
+    ("e4m3", BF, 80, 6, 4, "nhd"), ("int8", HF, 112, 2, 16, "nhd"),
+    ("int8", BF, 64, 3, 5, "nhd"), ("e4m3", BF, 64, 4, 3, "hnd"),
+    (None, HF, 256, 1, 9, "nhd"), ("e4m3", HF, 256, 2, 3, "nhd"),
+    (None, BF, 64, 1, 1, "hnd"),
+])
+def test_attend_one_long_sequence(store, dtype, dim, heads, group, order):
+    """Heads shared by many blocks (joined in two levels), in pairs where rows
+    are narrow and side by side; page sizes a step does and does not divide."""
+    for page, n in ((40, 30011), (64, 9000), (1, 2500)):
+        P = kr.Pages([n, 100], heads, dim, page, order, dtype, store, seed=n)
+        q, out, lse = run_attend(P, group)
+        check_attend(P, group, q, out, lse)
+
+
+def test_attend_one_workspace_for_several_plans():
+    """The largest workspace serves every plan, call after call."""
+    Ps = [kr.Pages([3000, 40], 2, 64, 16, "nhd", BF, "int8", seed=1),
+          kr.Pages([5000], 1, 256, 16, "nhd", HF, None, seed=2),
+          kr.Pages([2000, 0, 700], 2, 128, 16, "hnd", BF, "e4m3", seed=3),
+          kr.Pages([2500], 2, 64, 16, "nhd", BF, None, seed=4)]
+    need = []
+    for P in Ps:
+        plan = lm.KVPlan(lm.Layout.make(*P.page_layout()), P.dtype, P.store)
+        need.append(lm.kv_attend_workspace(plan, len(P.lens), 12 * P.heads))
+    ws = torch.zeros(max(need), dtype=torch.uint8, device="cuda")
+    for P in Ps + Ps[::-1]:
+        q, out, lse = run_attend(P, 12, workspace=ws)
+        check_attend(P, 12, q, out, lse)
+
+
+def test_attend_workspace_too_small():
+    P = kr.Pages([50], 1, 64, 16, "nhd", BF, None)
+    cache, plan = make_cache(P)
+    n = lm.kv_attend_workspace(plan, 1, 2)
+    q = torch.zeros(1, 2, 64, dtype=BF, device="cuda")
+    args = (cache, q, P.table.cuda(), torch.tensor([50]).int().cuda(),
+            torch.zeros_like(q))
+    for ws, status in ((torch.zeros(n - 1, dtype=torch.uint8, device="cuda"),
+                        -6), (None, -1)):
+        with pytest.raises(lm.LayoutMoveError) as e:
+            lm.kv_attend(*args, ws)
+        assert e.value.status == status
+
+
+@pytest.mark.parametrize("store", [None, "e4m3", "int8"])
+def test_tensors_that_allow_no_wide_accesses(store):
+    """Rows that start at odd elements: keys, values, queries and outputs of
+    every call, against the same call on aligned copies."""
+    P = kr.Pages([37], 3, 48, 5, "nhd", HF, store, seed=6)
+    cache, plan = make_cache(P)
+    wide = torch.randn(37, 6, 51, device="cuda").to(HF)
+    k, v = wide[:, :3, 1:49], wide[:, 3:, 3:51]
+    rope = lm.RopePlan(48, 40)
+    angles = torch.empty(64, 40, device="cuda")
+    lm.rope_table(rope, angles)
+    pos = torch.arange(37, device="cuda")
+    slots = pos + 2
+    pages = torch.arange(P.pool).int()[None].cuda()
+    lens, starts = torch.tensor([39]).int().cuda(), \
+        torch.tensor([0, 39]).int().cuda()
+    got = []
+    for a, b in ((k, v), (k.contiguous(), v.contiguous())):
+        for turn in ({}, {"rope": rope, "positions": pos, "table": angles}):
+            cache.k.fill_(0), cache.v.fill_(0)
+            lm.kv_write(cache, a, b, slots, **turn)
+            out = torch.full((2, 39, 3, 49), 2.0, dtype=HF, device="cuda")
+            dense = torch.empty(2, 39, 3, 48, dtype=HF, device="cuda")
+            lm.kv_read(cache, pages, lens, starts, out[0, :, :, 1:],
+                       out[1, :, :, 1:])
+            lm.kv_read(cache, pages, lens, starts, dense[0], dense[1])
+            assert (out[..., 0] == 2).all()
+            assert torch.equal(out[:, 2:, :, 1:], dense[:, 2:])
+            got.append(dense[:, 2:].clone())
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+    assert not torch.equal(got[0][0], got[1][0])
+    ws = torch.zeros(lm.kv_attend_workspace(plan, 1, 6), dtype=torch.uint8,
+                     device="cuda")
+    q = torch.randn(1, 6, 49, device="cuda").to(HF)
+    odd, even = torch.zeros(1, 6, 49, dtype=HF, device="cuda"), \
+        torch.zeros(1, 6, 48, dtype=HF, device="cuda")
+    lm.kv_attend(cache, q[:, :, 1:], pages, lens, odd[:, :, 1:], ws)
+    lm.kv_attend(cache, q[:, :, 1:].contiguous(), pages, lens, even, ws)
+    assert torch.equal(odd[:, :, 1:], even) and (odd[:, :, 0] == 0).all()
+
+
+def test_write_skips_tokens_whatever_their_position():
+    P = kr.Pages([8], 2, 32, 4, "nhd", BF, "e4m3")
+    cache, plan = make_cache(P)
+    rope = lm.RopePlan(32)
+    table = torch.ones(3, 32, device="cuda")
+    x = torch.ones(2, 2, 32, dtype=BF, device="cuda")
+    before = cache.k.clone()
+    lm.kv_write(cache, x, x, torch.tensor([-1, -5]).cuda(), rope=rope,
+                positions=torch.tensor([-1, 1 << 40]).cuda(), table=table)
+    assert torch.equal(before, cache.k)      # and no status: see clean_status
+
+
+def test_attend_without_pages():
+    P = kr.Pages([0, 0], 2, 64, 16, "nhd", BF, None)
+    P.table = torch.zeros(2, 0, dtype=torch.int32)
+    q, out, lse = run_attend(P, 3, lens=[5, 0])
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_calls_in_a_graph():
+    """A decoding step captured once and replayed with new inputs."""
+    P = kr.Pages([60, 7], 2, 64, 16, "nhd", BF, "e4m3", seed=2)
+    cache, plan = make_cache(P)
+    rope = lm.RopePlan(64)
+    table = torch.empty(128, 64, device="cuda")
+    lm.rope_table(rope, table)
+    x = torch.randn(2, 12, 64, device="cuda").to(BF)
+    pos = torch.tensor([59, 6]).cuda()
+    slots = torch.stack([P.table[0, 3].long() * 16 + 11,
+                         P.table[1, 0].long() * 16 + 6]).cuda()
+    pages, lens = P.table.cuda(), torch.tensor(P.lens).int().cuda()
+    q, out = torch.empty(2, 8, 64, dtype=BF, device="cuda"), \
+        torch.empty(2, 8, 64, dtype=BF, device="cuda")
+    ws = torch.zeros(lm.kv_attend_workspace(plan, 2, 8), dtype=torch.uint8,
+                     device="cuda")
+
+    def step():
+        lm.rope(rope, x[:, :8], pos, table, q)
+        lm.kv_write(cache, x[:, 8:10], x[:, 10:], slots, rope=rope,
+                    positions=pos, table=table)
+        lm.kv_attend(cache, q, pages, lens, out, ws)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            step()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        x.copy_(torch.randn(2, 12, 64, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, out)
+
+
 def test_attend_strides_interleaved_pages_and_no_lse():
     P = kr.Pages([77, 300], 2, 64, 16, "nhd", BF, "int8", seed=8)
     q, out, lse = run_attend(P, 4, interleave=True, wide=True)
@@ -643,8 +789,6 @@ def test_attend_infinite_and_nan_keys():
     q, out, lse = run_attend(P, 2, q=q)
     assert out[2, 2:].isnan().all() and lse[2, 2:].isnan().all()
     out[2, 2:], lse[2, 2:] = 0, 0
-    for b in (0, 1, 3):
-        pass
     keep0 = [j for j in range(20) if j not in (4, 17)]
     for kv in range(2):
         P.rows[kv][0] = P.rows[kv][0][keep0]

@@ -244,7 +244,7 @@ def call_attend(store=None, c=None, q=None, out=None, seqs=3, hq=32,
 
 
 @pytest.mark.parametrize("kw,want", [
-    ({"hq": 0}, INVALID), ({"hq": 12}, INVALID), ({"seqs": -1}, INVALID),
+    ({"hq": 0}, INVALID), ({"hq": 12}, INVALID), ({"hq": 1 << 21}, INVALID), ({"seqs": -1}, INVALID),
     ({"scale": math.inf}, INVALID), ({"scale": math.nan}, INVALID),
     ({"window": -1}, INVALID), ({"table": None}, INVALID),
     ({"lens": None}, INVALID), ({"stride": 3}, INVALID),
