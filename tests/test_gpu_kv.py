@@ -885,3 +885,16 @@ def test_decoding_steps_follow_the_dense_model():
         bo, _ = kr.attend_bounds(BF, dim, want, lse, mag, dot)
         bo = bo + 4 * 2.0 ** -8 * dot[:, None] * mag
         assert ((out[0].cpu().double() - want).abs() <= bo).all()
+
+
+@pytest.mark.parametrize("store", [[], ["--store", "e4m3"],
+                                   ["--store", "int8"]])
+def test_the_example_runs(store):
+    """examples/decode_cache.py: its outputs are bfloat16 (2^-8 of each,
+    2^-9 in the mean) of the same cached rows, whose int8 values were rounded
+    to bfloat16 on their way back."""
+    import os
+    import runpy
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    main = runpy.run_path(os.path.join(root, "examples", "decode_cache.py"))
+    assert main["main"](store + ["--steps", "9"]) <= 2.0 ** -7
