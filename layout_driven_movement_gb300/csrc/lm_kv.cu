@@ -100,8 +100,8 @@ __device__ __forceinline__ void get8(const uint4& u, float* x) {
 // go to the roundings as it is.
 //
 // TURN: 0 no turn, 1 partners 8 L apart, 2 any other.  Two heads a thread, to
-// share a token's slot and angles, spill or halve the resident warps: 70 us
-// for 8 x 8192 tokens of 8 x 128 turned into e4m3, 60 with one.
+// share a token's slot and angles, leave fewer warps resident and gain 3% (8 x
+// 8192 tokens of 8 x 128 turned into e4m3: 47.7 us against 49.2): not kept.
 template <class T, int STORE, int L, bool VEC, int TURN>
 __global__ void __launch_bounds__(256, TURN == 0 ? 6 : 4) lm_kv_write_kernel(
     const __grid_constant__ KvWriteArgs a) {
@@ -302,7 +302,7 @@ struct ReadGrid {
 // bytes at a time, heads and dim fastest, so that a token's rows leave as one
 // run.  Bound by memory: codes and scales read once, rows written once.
 // Small blocks in many waves measured best (16 x 16384 tokens of 8 x 128 e4m3,
-// 1.02 GB: 162 us, 6.3 TB/s; 166 and 176 with 256 and 512 threads, 174 with
+// 1.02 GB: 161 us, 6.4 TB/s; 166 and 176 with 256 and 512 threads, 174 with
 // four loads a thread, 206 with resident blocks that look the next rows up
 // while they move these).
 template <class T, int STORE, class TO, bool VEC>
@@ -403,7 +403,7 @@ int launch_read_o(const KvReadArgs& a, cudaStream_t st) {
   g.chunk_div = make_fastdiv(g.chunks);
   g.row_div = make_fastdiv(g.row_units);
   // a round of the block's loads, or less where that leaves SMs idle
-  const uint32_t most = (kReadThreads * kReadUnits + g.row_units - 1) / g.row_units;
+  const uint32_t most = kReadThreads * kReadUnits / g.row_units;
   const int64_t spread = a.rows / 608;
   int64_t tokens = most < kReadTokens ? most : kReadTokens;
   if (tokens > spread) tokens = spread;
