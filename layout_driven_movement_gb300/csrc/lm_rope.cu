@@ -29,7 +29,8 @@ __global__ void __launch_bounds__(256) lm_rope_table_kernel(
 // elements holding V/2 pairs -- or one chunk of the rest.  The unit's cosines
 // and sines serve all H heads of the group, which lie HG heads apart, so that
 // a warp's accesses stay whole rows.  Bound by memory: x read once, out
-// written once.
+// written once (16384 x 32 x 128 bf16, 268 MB: 40 us, 6.7 TB/s; 45 us with one
+// head a thread, 42 with four).
 struct RopeGrid {
   uint32_t units = 0;      // of all tokens
   uint32_t chunks = 0;     // units of one head

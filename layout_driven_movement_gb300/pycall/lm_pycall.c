@@ -51,6 +51,7 @@ static int ints(PyObject* tuple, int64_t* out) {
 static int look(PyObject* o, const char* what, tensor* t) {
   PyObject *a = PyObject_GetAttr(o, n_is_cuda), *b;
   const int cuda = a == Py_True;
+  if (!a) PyErr_Clear(); /* no tensor at all, None among others */
   Py_XDECREF(a);
   if (!cuda) return (int)wrong(what, "a CUDA tensor");
   a = PyObject_GetAttr(o, n_shape);

@@ -627,6 +627,61 @@ def test_attend_without_pages():
     assert (out == 0).all() and (lse == -math.inf).all()
 
 
+def test_tensors_of_the_wrong_kind_are_refused():
+    """What the binding itself checks, on tensors that are on the GPU; nothing
+    is launched."""
+    P = kr.Pages([20], 2, 64, 16, "nhd", BF, "int8")
+    cache, plan = make_cache(P)
+    rope = lm.RopePlan(64)
+    angles = torch.zeros(8, 64, device="cuda")
+    k = torch.zeros(20, 2, 64, dtype=BF, device="cuda")
+    slots = torch.arange(20, device="cuda")
+    pages, lens = P.table.cuda(), torch.tensor([20]).int().cuda()
+    starts = torch.tensor([0, 20]).int().cuda()
+    q = torch.zeros(1, 4, 64, dtype=BF, device="cuda")
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    lse = torch.zeros(1, 4, device="cuda")
+    wrong = [
+        lambda: lm.rope(rope, k, slots, angles, k[:, :1]),
+        lambda: lm.rope(rope, k, slots, angles, k.float()),
+        lambda: lm.rope(rope, k, slots[:5], angles, k),
+        lambda: lm.rope(rope, k, slots.float(), angles, k),
+        lambda: lm.rope(rope, k, slots, angles.half(), k),
+        lambda: lm.rope(rope, k, slots, angles[:, :32], k),
+        lambda: lm.rope(rope, k[..., ::2], slots, angles, k[..., ::2]),
+        lambda: lm.rope(rope, k[0], slots, angles, k[0]),
+        lambda: lm.kv_write(cache, k.half(), k.half(), slots),
+        lambda: lm.kv_write(cache, k[:, :1], k[:, :1], slots),
+        lambda: lm.kv_write(cache, k, k[:5], slots),
+        lambda: lm.kv_write(cache, k, k, slots.int()),
+        lambda: lm.kv_write(cache, k, k, slots, rope=rope),
+        lambda: lm.kv_write(cache, k, k.cpu(), slots),
+        lambda: lm.kv_read(cache, pages.long(), lens, starts, k, k),
+        lambda: lm.kv_read(cache, pages, lens.long(), starts, k, k),
+        lambda: lm.kv_read(cache, pages, lens, starts[:1], k, k),
+        lambda: lm.kv_read(cache, pages, lens, starts, k, k.float()),
+        lambda: lm.kv_read(cache, pages, lens, starts, k, k[:3]),
+        lambda: lm.kv_attend(cache, q.half(), pages, lens, q, ws),
+        lambda: lm.kv_attend(cache, q, pages[0], lens, q, ws),
+        lambda: lm.kv_attend(cache, q, pages.t(), lens, q, ws),
+        lambda: lm.kv_attend(cache, q, pages, starts, q, ws),
+        lambda: lm.kv_attend(cache, q, pages, lens, q[:, :2], ws),
+        lambda: lm.kv_attend(cache, q, pages, lens, q, ws[::2]),
+        lambda: lm.kv_attend(cache, q, pages, lens, q, ws, lse=lse[:, :2]),
+        lambda: lm.KVCache(plan, cache.k.to(BF), cache.v),
+        lambda: lm.KVCache(plan, cache.k, cache.v, cache.k_scale),
+        lambda: lm.rope_table(rope, angles[:, ::2]),
+    ]
+    for i, call in enumerate(wrong):
+        with pytest.raises(ValueError):
+            call()
+            raise AssertionError(i)
+    with pytest.raises(lm.LayoutMoveError):    # keys heads do not divide
+        lm.kv_attend(cache, q[:, :3], pages, lens, q[:, :3], ws)
+    with pytest.raises(lm.LayoutMoveError):    # one buffer for both
+        lm.kv_read(cache, pages, lens, starts, k, k)
+
+
 def test_calls_in_a_graph():
     """A decoding step captured once and replayed with new inputs."""
     P = kr.Pages([60, 7], 2, 64, 16, "nhd", BF, "e4m3", seed=2)

@@ -285,6 +285,8 @@ def test_python_checks_before_the_library():
     with pytest.raises(ValueError):
         lm.rope(plan, x, torch.zeros(2), torch.zeros(4, 64), x)   # not CUDA
     with pytest.raises(ValueError):
+        lm.rope(plan, None, None, None, None)
+    with pytest.raises(ValueError):
         lm.rope(plan, x, torch.zeros(2), torch.zeros(4, 64), x[:1])
     with pytest.raises(ValueError):
         lm.rope_table(plan, torch.zeros(4, 64))
