@@ -28,10 +28,11 @@ int attend_workspace(int store, int dim, int group, int64_t* bytes) {
   int dev = 0, sms = 0;
   const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  const int64_t d = attend_dim(dim), q = 8 * attend_tiles(group);
-  const int64_t blocks = sms * (d == 256 ? 1 : store == LM_KV_SAME ? 2 : 3);
+  const bool codes = store != LM_KV_SAME;
+  const int64_t d = attend_dim(dim), q = 8 * attend_tiles(codes, dim, group);
+  const int64_t blocks = sms * ((codes ? 3 : 2) - (d == 256 ? 1 : 0));
   // (codes may take two heads a block)
-  const int64_t heads = store == LM_KV_SAME || d == 256 ? 1 : 2;
+  const int64_t heads = !codes || d == 256 ? 1 : 2;
   *bytes = attend_space(sms, blocks, heads * q * (d + 2)).bytes;
   return LM_OK;
 }

@@ -58,7 +58,8 @@ template <int KIND, int D, int NT, int HP>
 struct AttendShape {
   static constexpr bool kCodes = KIND == KIND_E4M3 || KIND == KIND_INT8;
   static constexpr int kHeld = kCodes ? 1 : 2;           // bytes an element
-  static constexpr int KW = kCodes ? (D == 64 ? 64 : 32) : 16;  // a warp's step
+  // keys of a warp's step
+  static constexpr int KW = kCodes ? (D == 64 ? 64 : D == 128 ? 32 : 16) : 16;
   static constexpr int KL = (KW + 31) / 32;              // keys a lane
   static constexpr int WK = kAttendWarps / HP;           // warps a head
   static constexpr int TK = KW * WK;                     // keys of a tile
@@ -71,7 +72,7 @@ struct AttendShape {
   // latency that only more warps hide: 128 sequences of 12288 tokens, 8 x 8 x
   // 128 e4m3, take 390 us with three blocks of two stages an SM, 481 with two
   // of three.
-  static constexpr int kBlocks = D == 256 ? 1 : kCodes ? 3 : 2;
+  static constexpr int kBlocks = kCodes ? (D == 256 ? 2 : 3) : D == 256 ? 1 : 2;
   static constexpr int kS = D == 256  ? 3
                             : kCodes ? 2
                                      : (D == 64 ? 6 : 3);
@@ -340,9 +341,13 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   auto turned = [](int r) { return S::kRow == 64 ? (r >> 1) & 3 : r & 7; };
   const uint32_t k_lane =
       lane % 16 * S::kRow + ((lane / 16) ^ turned(lane % 16)) * 16;
-  const int v_row = CODES ? lane : lane % 8 + lane / 16 * 8;
-  const uint32_t v_lane =
-      v_row * S::kRow + ((CODES ? 0 : lane / 8 & 1) ^ turned(v_row)) * 16;
+  // values: 16 keys by two chunks, or codes of 32 keys by one
+  constexpr bool LONG = CODES && KW >= 32;
+  const int v_row = LONG    ? lane
+                    : CODES ? lane % 16
+                            : lane % 8 + lane / 16 * 8;
+  const int v_chunk = LONG ? 0 : CODES ? lane / 16 : lane / 8 & 1;
+  const uint32_t v_lane = v_row * S::kRow + (v_chunk ^ turned(v_row)) * 16;
 
   // The line of work: every thread counts the tiles of a run of sequences;
   // a scan over the block gives the line's length and where this block's
@@ -814,9 +819,23 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 
       // O^T += V^T P^T
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; k += CODES && !LONG ? 2 : 1) {
         if (k * 16 >= dim) break;
-        if (CODES) {
+        if constexpr (CODES && !LONG) {
+          uint32_t x[4];                            // 16 keys, 32 elements
+          ldm_t(x, (v_s + v_lane) ^ (k * 16));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t f[4];
+            Codes<KIND>::values(x[2 * e], f);
+            Codes<KIND>::values(x[2 * e + 1], f + 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<true>(o[k + e][nt], f, p[0][nt]);
+              mma<true>(o[k + e][nt], f, p2[0][nt]);
+            }
+          }
+        } else if constexpr (LONG) {
           uint32_t x[4];                            // 32 keys, 16 elements
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -1085,11 +1104,17 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 
 // --- launch --------------------------------------------------------------------
 
-// Queries a block holds at once: 8 when a key head has no more, else 16; a
-// larger group reads its keys again per 16.
-inline int attend_tiles(int group) { return group <= 8 ? 1 : 2; }
-
 inline int attend_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// Queries a block holds at once: 8 when a key head has no more, else 16; a
+// larger group reads its keys again per 16.  Codes of 256 elements: always 8,
+// with steps of 16 keys and two blocks an SM, as shared memory then allows (32
+// sequences of up to 8192 tokens, 4 key heads: 113 us for 8 queries each in
+// e4m3, 233 for 16 in int8; 159 and 273 with steps of 32 keys, 16 queries at
+// once and one block).
+inline int attend_tiles(bool codes, int dim, int group) {
+  return group <= 8 || (codes && attend_dim(dim) == 256) ? 1 : 2;
+}
 
 // The workspace: a counter per block and one per run of parts, as many as the
 // largest grid has whatever the kernel (so that one buffer serves them all),
@@ -1145,8 +1170,10 @@ int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
 
 template <int KIND, int D>
 int launch_attend_dim(const KvAttendArgs& a, cudaStream_t st) {
-  const bool few = attend_tiles(a.group) == 1;
-  if constexpr ((KIND == KIND_E4M3 || KIND == KIND_INT8) && D <= 128) {
+  constexpr bool kCodes = KIND == KIND_E4M3 || KIND == KIND_INT8;
+  const bool few = attend_tiles(kCodes, D, a.group) == 1;
+  if constexpr (kCodes && D == 256) return launch_attend<KIND, D, 1, 1>(a, st);
+  if constexpr (kCodes && D <= 128) {
     // Rows that are no whole 128-byte lines, heads side by side: lines that
     // two heads share come in once when one block takes both (3 x 131072
     // tokens of 4 x 64 int8, 145 MB: 220 MB read in 55 us a head at a time,
@@ -1156,8 +1183,9 @@ int launch_attend_dim(const KvAttendArgs& a, cudaStream_t st) {
       return few ? launch_attend<KIND, D, 1, 2>(a, st)
                  : launch_attend<KIND, D, 2, 2>(a, st);
   }
-  return few ? launch_attend<KIND, D, 1, 1>(a, st)
-             : launch_attend<KIND, D, 2, 1>(a, st);
+  if constexpr (!(kCodes && D == 256))
+    return few ? launch_attend<KIND, D, 1, 1>(a, st)
+               : launch_attend<KIND, D, 2, 1>(a, st);
 }
 
 template <int KIND>
