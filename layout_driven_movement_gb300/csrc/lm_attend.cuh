@@ -6,7 +6,10 @@
 // e^{s_gj}.  One pass over the cache with a running maximum m, sum l and
 // unnormalised output o: a block of keys turns (m, l, o) into
 // (m', l 2^(m-m') + sum 2^(s-m'), o 2^(m-m') + sum 2^(s-m') v), scores in
-// units of ln 2; two states join by the same rule.
+// units of ln 2.  Where two states join they hold the weighted mean o / l in
+// o's place, (m, l, a): with c = l 2^(m-t) for each, t the larger m, the joined
+// mean is sum (c / sum c) a, which is finite where the values are, however
+// large they and their number.
 //
 // The cache is read once and nothing else matters: 4 G D operations per key
 // head and token against 4 D (2 D at 8 bits) bytes.  At 6.8 TB/s an SM gets
@@ -28,7 +31,7 @@
 // long sequences load all SMs alike.  A block's ring runs on across the
 // borders of sequences.  HP adjacent heads share a block (its warps take them
 // in turn) where their rows share memory lines.  What one block holds of a head that others share
-// goes to the workspace as (m, l, o); the block that comes last by a counter
+// goes to the workspace as (m, l, a); the block that comes last by a counter
 // joins the parts, in the order of the line, so results do not depend on
 // which came last.
 //
@@ -81,7 +84,7 @@ struct AttendShape {
   static constexpr int kState = kAttendWarps * Q * 2 * 4;
   static constexpr int kSmem =
       kS * (kStage + kScales + kMasks) + kState + 64;
-  // workspace: a part is, for each head, (m, l) per query, then its output
+  // workspace: a part is, for each head, (m, l) per query, then its mean
   static constexpr int kHeadFloats = Q * (D + 2);
   static constexpr int kPartFloats = HP * kHeadFloats;
   static_assert(Q * D * 4 <= 2 * kPart, "a warp's output fits its stage");
@@ -315,6 +318,10 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
                        : KIND == KIND_E4M3 ? 0x1p60f
                                            : 1.f;
   constexpr float DOWN = KIND == KIND_F16 ? 0x1p-7f : UP;
+  // bf16 values reach the end of 32 bits' range, so their weights' sum stays
+  // below 1: a weight's reference lies ROOM above the largest score
+  constexpr bool LOW = KIND == KIND_BF16;
+  constexpr float ROOM = LOW ? 13.f : 0.f;
   constexpr int KW = S::KW, KL = S::KL, TK = S::TK, MT = S::MT, NS = S::kS;
   constexpr int Q = S::Q;
   constexpr int KS = D / 16;                 // 16-element steps along dim
@@ -725,9 +732,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
             vs[mt][i] = sc[KW + mt * 16 + 8 * i + row8];
           }
       }
-      // A head's reference m moves only when a score passes it by 8, that
-      // is when a weight would pass 2^8: one vote a step instead of the
-      // maximum over the lanes and the products' rescaling.
+      // A head's reference m moves only when a score passes the largest one
+      // that it was set for by 8, that is when a weight would pass 2^8 (LOW:
+      // 2^-5): one vote a step instead of the maximum over the lanes and the
+      // products' rescaling.  LOW: and when a lane's sum passes 2^-4, so that
+      // the 8 lanes' sums, with the step's 2 weights each, stay below 1 and
+      // the products below the largest value.
       bool above = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -761,7 +771,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
             t = fmaxf(t, mt ? fmaxf(s[mt][nt][j], s[mt][nt][2 + j])
                             : s[mt][nt][2 + j]);
           top[nt][j] = t;
-          above |= t > m[nt][j] + 8.f;
+          above |= t > m[nt][j] + (8.f - ROOM);
+          if (LOW) above |= l[nt][j] > 0x1p-4f;
         }
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
@@ -769,10 +780,19 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // over the 8 lanes that hold the column's keys
-            float t = fmaxf(top[nt][j], m[nt][j]);
+            float t = fmaxf(top[nt][j] + ROOM, m[nt][j]);
 #pragma unroll
             for (int k = 4; k < 32; k *= 2)
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
+            if (LOW) {
+              float sum = l[nt][j];
+#pragma unroll
+              for (int k = 4; k < 32; k *= 2)
+                sum += __shfl_xor_sync(0xffffffffu, sum, k);
+              // 2^e or more: down to 2^-9
+              const int e = int(__float_as_uint(sum) >> 23) - 127;
+              if (sum > 0x1p-5f) t = fmaxf(t, m[nt][j] + float(e + 9));
+            }
             const float keep = ex2(m[nt][j] - (t == -INFINITY ? 0.f : t));
             m[nt][j] = t;
             l[nt][j] *= keep;
@@ -868,6 +888,30 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       if (++stage == NS) stage = 0;
     }
 
+    // the warp's state: the sums over its lanes, and the means.  (Formed before
+    // the next queries take registers: 32 sequences of 8192 tokens, 4 x 16 x
+    // 256 bf16, 247 us so and 260 where the means are written.)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int k = 4; k < 32; k *= 2)
+          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], k);
+        f[j] = l[nt][j] == 0 ? 0.f : __fdividef(DOWN, l[nt][j]);
+        if (row8 == 0) {
+          float* st = state + (warp * Q + nt * 8 + col2 + j) * 2;
+          st[0] = m[nt][j];
+          st[1] = l[nt][j];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[k][nt][i] *= f[i & 1];
+    }
+
     // the next head's queries are on their way while this one's parts join
     const AttendAt done = at;
     const int tiles = at.hi - at.lo;
@@ -886,36 +930,14 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       load_q(at);
     }
 
-    // --- the warps' states join; each warp's output lies in the stage that
+    // --- the warps' states join; each warp's means lie in the stage that
     // it used last, which nothing fills before the next step ---
     const int used = stage == 0 ? NS - 1 : stage - 1;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-#pragma unroll
-        for (int k = 4; k < 32; k *= 2)
-          l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], k);
-        if (row8 == 0) {
-          float* st = state + (warp * Q + nt * 8 + col2 + j) * 2;
-          st[0] = m[nt][j];
-          st[1] = l[nt][j];
-        }
-      }
-    __syncthreads();
     float* const mine = reinterpret_cast<float*>(
         ring + used * S::kStage + warp * 2 * S::kPart);
+    __syncwarp();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float t = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < S::WK; ++w)
-          t = fmaxf(t, state[((w * HP + sub) * Q + nt * 8 + col2 + j) * 2]);
-        f[j] = ex2(m[nt][j] - (t == -INFINITY ? 0.f : t)) * DOWN;
-      }
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -927,10 +949,10 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
           if (CODES) {
             const int d = (k * 16 + 2 * row8) ^ turn;
             *reinterpret_cast<float2*>(to + d) =
-                make_float2(o[k][nt][j] * f[j], o[k][nt][2 + j] * f[j]);
+                make_float2(o[k][nt][j], o[k][nt][2 + j]);
           } else {
-            to[(k * 16 + row8) ^ turn] = o[k][nt][j] * f[j];
-            to[(k * 16 + 8 + row8) ^ turn] = o[k][nt][2 + j] * f[j];
+            to[(k * 16 + row8) ^ turn] = o[k][nt][j];
+            to[(k * 16 + 8 + row8) ^ turn] = o[k][nt][2 + j];
           }
         }
     }
@@ -966,7 +988,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     for (int i = 0; i < HP; ++i)
       for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {
         const int qi = e / D, d = e % D;
-        float t = -INFINITY, x = 0, sum = 0;
+        float t = -INFINITY, x = 0, sum = 0, c[S::WK];
 #pragma unroll
         for (int w = 0; w < S::WK; ++w)
           t = fmaxf(t, state[((w * HP + i) * Q + qi) * 2]);
@@ -974,13 +996,18 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 #pragma unroll
         for (int w = 0; w < S::WK; ++w) {
           const float* st = state + ((w * HP + i) * Q + qi) * 2;
-          sum += st[1] * ex2(st[0] - t0);
-          x += reinterpret_cast<const float*>(
-              ring + used * S::kStage + (w * HP + i) * 2 * S::kPart)
-              [qi * D + (d ^ ((qi & 6) * 4))];
+          c[w] = st[1] * ex2(st[0] - t0);
+          sum += c[w];
         }
+        const float part_of = sum == 0 ? 0.f : __fdividef(1.f, sum);
+#pragma unroll
+        for (int w = 0; w < S::WK; ++w)
+          x += c[w] * part_of *
+               reinterpret_cast<const float*>(
+                   ring + used * S::kStage + (w * HP + i) * 2 * S::kPart)
+                   [qi * D + (d ^ ((qi & 6) * 4))];
         if (whole) {
-          if (d < dim) put(i, qi, d, sum == 0 ? 0.f : x / sum);
+          if (d < dim) put(i, qi, d, sum == 0 ? 0.f : x);
           if (d == 0) put_lse(i, qi, t, sum);
         } else {
           float* to = part + i * S::kHeadFloats;
@@ -1017,7 +1044,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
         __syncthreads();
         return last;
       };
-      // adds up parts 0 .. m - 1, 4 elements a thread at a time
+      // the mean over parts 0 .. m - 1, 4 elements a thread at a time
       auto join = [&](int m, auto&& part_of, auto&& emit) {
         for (int i = 0; i < HP; ++i)
           for (int e = threadIdx.x * 4; e < nq * D; e += kAttendThreads * 4) {
@@ -1040,14 +1067,19 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 #pragma unroll
               for (int k = 0; k < 8; ++k) top = fmaxf(top, ml[k].x);
               const float t0 = top == -INFINITY ? 0.f : top;
-              const float keep = ex2(t - t0);
-              sum *= keep;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] *= keep;
+              const float kept = sum * ex2(t - t0);
+              sum = kept;
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                const float f = ex2(ml[k].x - t0);
-                sum += ml[k].y * f;
+                ml[k].y *= ex2(ml[k].x - t0);
+                sum += ml[k].y;
+              }
+              const float share_of = sum == 0 ? 0.f : __fdividef(1.f, sum);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] *= kept * share_of;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float f = ml[k].y * share_of;
                 x[0] += v[k].x * f;
                 x[1] += v[k].y * f;
                 x[2] += v[k].z * f;
@@ -1062,7 +1094,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
         const int qi = e / D, d = e % D;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (d + k < dim) put(i, qi, d + k, sum == 0 ? 0.f : x[k] / sum);
+          if (d + k < dim) put(i, qi, d + k, sum == 0 ? 0.f : x[k]);
         if (d == 0) put_lse(i, qi, t, sum);
       };
       const int64_t p0 = 2 * c0 + (line_div(c0 * total, blocks) < item_at ? 1 : 0);

@@ -1,0 +1,122 @@
+"""Attention over the paged cache where the numbers are extreme: values near
+the ends of their type's range, scales of every size, codes that are not
+numbers, weights far below the largest.  Each against the 64-bit definition on
+the rows that the cache holds.
+
+The bounds.  A score of dim products in 32 bits is off by e = (dim + 4) 2^-24
+sum |q||k| scale at most, a weight then by the factor 1 + 2e.  A weight meets
+its value as two 16-bit parts: the first leaves 2^-8 of it (bfloat16), the
+second 2^-8 of that, so 2^-16; its exponential and the sums of up to 2^7 steps
+a warp and a few joins, each good to 2^-23, take as much again at most: 2^-15
+of sum p |v|.  The result is rounded once to its type."""
+
+import math
+
+import pytest
+
+import kv_reference as kr
+from test_gpu_kv import BF, HF, built, clean_status, run_attend  # noqa: F401
+
+torch = pytest.importorskip("torch")
+lm = pytest.importorskip("layout_driven_movement_gb300")
+
+pytestmark = pytest.mark.gpu
+
+CODES = ["e4m3", "int8"]
+
+
+def numbers(P, codes):
+    """What held codes stand for under a scale of 1, in 64 bits."""
+    if P.store is None:
+        return codes.double()
+    codes = codes.view(torch.uint8)
+    return kr.e4m3_values()[codes.long()] if P.store == "e4m3" else \
+        codes.view(torch.int8).double()
+
+
+def refresh(P):
+    """P.rows from the codes and scales as they are now."""
+    for kv in range(2):
+        x = numbers(P, P.codes[kv])
+        if P.store is not None:
+            x = x * P.scales[kv].double()[..., None]
+        for b, n in enumerate(P.lens):
+            ids = P.table[b, :-(-n // P.page)].long()
+            P.rows[kv][b] = x[ids].flatten(0, 1)[:n]
+    return P
+
+
+def tokens(P):
+    """[pool, page]: whether a sequence's token lies there."""
+    used = torch.zeros(P.pool, P.page, dtype=torch.bool)
+    for b, n in enumerate(P.lens):
+        for j in range(0, n, P.page):
+            used[int(P.table[b, j // P.page]), :min(P.page, n - j)] = True
+    return used
+
+
+def check(P, group, q, out, scale=None, rel=2.0 ** -15):
+    scale = P.dim ** -0.5 if scale is None else scale
+    for b, n in enumerate(P.lens):
+        want, _, mag, dot = kr.attend(q[b].double(), P.rows[0][b],
+                                      P.rows[1][b], group, scale)
+        e = ((P.dim + 4) * 2.0 ** -24 * dot)[:, None]
+        bound = (2 * e + rel) * mag + want.abs() * kr.ROUND[P.dtype] * 1.01 \
+            + kr.TINY[P.dtype]
+        off = (out[b].double() - want).abs()
+        assert (off <= bound).all(), (b, n, (off / bound).max())
+
+
+def aim(P, scores):
+    """Keys whose first element is their score (0 elsewhere): with a query of
+    1, 0, 0, ... and a softmax scale of 1 the scores are `scores(b, j)`."""
+    for b, n in enumerate(P.lens):
+        for j in range(n):
+            at = int(P.table[b, j // P.page]), j % P.page
+            s = scores(b, j)
+            P.codes[0][at] = 0
+            if P.store is None:
+                P.codes[0][at][:, 0] = s
+            else:
+                one = {"e4m3": 0x38, "int8": 1}[P.store]
+                P.codes[0][at][:, 0] = one if s >= 0 else \
+                    {"e4m3": 0xb8, "int8": 255}[P.store]
+                P.scales[0][at] = abs(s)
+    q = torch.zeros(len(P.lens), P.heads, P.dim, dtype=P.dtype)
+    q[..., 0] = 1
+    return q
+
+
+# --- values near the top of bfloat16 ----------------------------------------
+
+@pytest.mark.parametrize("lens", [[1, 2, 20, 300], [6000], [2500, 33, 700]],
+                         ids=str)
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 4), (256, 9)])
+def test_values_near_the_top_of_their_type(lens, dim, group):
+    """The weighted mean of finite values is finite, however many there are:
+    magnitudes in [2^126, 2^128), of one sign in one head and of either in the
+    other."""
+    P = kr.Pages(lens, 2, dim, 16, "nhd", BF, None, seed=dim)
+    g = torch.Generator().manual_seed(dim)
+    x = (1 + torch.rand(P.codes[1].shape, generator=g, dtype=torch.float64))
+    x = x * 2.0 ** torch.randint(126, 128, x.shape, generator=g)
+    x[:, :, 1] *= torch.randint(0, 2, x[:, :, 1].shape, generator=g) * 2 - 1
+    x = x.clamp(-2.0 ** 128 * (1 - 2.0 ** -8), 2.0 ** 128 * (1 - 2.0 ** -8))
+    P.codes[1] = torch.where(P.codes[1].isnan(), P.codes[1], x.to(BF))
+    refresh(P)
+    q, out, lse = run_attend(P, group)
+    assert out.isfinite().all()
+    check(P, group, q, out)
+
+
+def test_large_values_under_growing_scores():
+    """Every key outweighs the ones before it, so that the reference moves
+    again and again under sums that are near the top of the range."""
+    P = kr.Pages([700], 1, 64, 16, "nhd", BF, None, seed=1)
+    q = aim(P, lambda b, j: j / 4)
+    P.codes[1] = torch.where(P.codes[1].isnan(), P.codes[1],
+                             P.codes[1].sign() * 2.0 ** 127 * 1.5)
+    refresh(P)
+    q, out, lse = run_attend(P, 1, q=q, scale=1.0)
+    assert out.isfinite().all()
+    check(P, 1, q, out, scale=1.0)
