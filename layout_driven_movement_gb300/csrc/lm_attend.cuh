@@ -74,10 +74,13 @@ struct AttendShape {
   // blocks per SM and stages: what shared memory holds.  Widening codes is
   // latency that only more warps hide: 128 sequences of 12288 tokens, 8 x 8 x
   // 128 e4m3, take 390 us with three blocks of two stages an SM, 481 with two
-  // of three.
-  static constexpr int kBlocks = kCodes ? (D == 256 ? 2 : 3) : D == 256 ? 1 : 2;
+  // of three.  16 queries of 128 elements do not fit a third block's
+  // registers: 64 sequences of 8192 tokens, 8 x 16, take 256 us (80 elements,
+  // e4m3) and 327 (128, int8) with two blocks, 263 and 330 with three.
+  static constexpr bool kTwo = D == 256 || (D == 128 && NT == 2);
+  static constexpr int kBlocks = kCodes ? (kTwo ? 2 : 3) : D == 256 ? 1 : 2;
   static constexpr int kS = D == 256  ? 3
-                            : kCodes ? 2
+                            : kCodes ? (kTwo ? 3 : 2)
                                      : (D == 64 ? 6 : 3);
   static constexpr int kScales = kCodes ? kAttendWarps * 2 * KW * 4 : 0;
   static constexpr int kMasks = kAttendWarps * KL * 4;
@@ -197,7 +200,7 @@ struct Codes;
 // sign, 4 exponent bits (bias 7) and 3 mantissa bits moved onto the sign, the
 // low exponent bits (bias 127) and the high mantissa bits of a bf16, the same
 // number, subnormals included, times 2^-120, which is put back where the
-// products are scaled (bytes 0 2 and 1 3).
+// means are formed (bytes 0 2 and 1 3).
 template <>
 struct Codes<KIND_E4M3> {
   static __device__ __forceinline__ void keys(uint32_t r, uint32_t* y) {
@@ -313,11 +316,18 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   constexpr bool CODES = S::kCodes;
   constexpr bool KBF = KIND == KIND_BF16;    // bf16 keys in the products
   constexpr bool VBF = KIND != KIND_F16;     // bf16 values and weights
-  // what values stand for beside weights, see the weights below
-  constexpr float UP = KIND == KIND_F16    ? 0x1p7f
-                       : KIND == KIND_E4M3 ? 0x1p60f
-                                           : 1.f;
-  constexpr float DOWN = KIND == KIND_F16 ? 0x1p-7f : UP;
+  // f16 weights are held times UP, see the weights below
+  constexpr float UP = KIND == KIND_F16 ? 0x1p7f : 1.f;
+  constexpr float DOWN = 1 / UP;
+  // Scales of 8-bit values may be any; a head's are taken times `gain`, a
+  // power of two that the largest so far decides: it lies at 2^TOP when the
+  // gain is set and passes MOST before it is set again, smaller ones are not
+  // raised by more than 2^120.  With weights up to 2^8 and sums of 2^31 of
+  // them the products stay finite (e4m3's are 2^-120 of themselves), and
+  // values beside scales 2^95 (e4m3) or 2^170 (int8) times their own keep
+  // their bits.
+  constexpr int TOP = KIND == KIND_E4M3 ? 106 : 60;
+  constexpr float MOST = KIND == KIND_E4M3 ? 0x1p118f : 0x1p76f;
   // bf16 values reach the end of 32 bits' range, so their weights' sum stays
   // below 1: a weight's reference lies ROOM above the largest score
   constexpr bool LOW = KIND == KIND_BF16;
@@ -646,7 +656,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       }
     }
 
-    float m[NT][2], l[NT][2], o[KS][NT][4];
+    float m[NT][2], l[NT][2], o[KS][NT][4], gain = 0x1p120f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -720,16 +730,18 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 
       // scores in units of ln 2; -infinity where no key is seen
       float ks[MT][2], vs[MT][2];
+      const float* const sc = reinterpret_cast<const float*>(
+                                  scale_ring + stage * S::kScales) +
+                              warp * 2 * KW + row8;
+      bool above = false;
       if (CODES) {
-        const float* sc = reinterpret_cast<const float*>(
-                              scale_ring + stage * S::kScales) +
-                          warp * 2 * KW;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            ks[mt][i] = sc[mt * 16 + 8 * i + row8];
-            vs[mt][i] = sc[KW + mt * 16 + 8 * i + row8];
+            ks[mt][i] = sc[mt * 16 + 8 * i];
+            vs[mt][i] = sc[KW + mt * 16 + 8 * i] * gain;
+            above |= fabsf(vs[mt][i]) > MOST;
           }
       }
       // A head's reference m moves only when a score passes the largest one
@@ -738,7 +750,6 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       // products' rescaling.  LOW: and when a lane's sum passes 2^-4, so that
       // the 8 lanes' sums, with the step's 2 weights each, stay below 1 and
       // the products below the largest value.
-      bool above = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -802,6 +813,40 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
               o[k][nt][2 + j] *= keep;
             }
           }
+        if (CODES) {
+          float big = 0;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              big = fmaxf(big, fabsf(sc[KW + mt * 16 + 8 * i]));
+#pragma unroll
+          for (int k = 4; k < 32; k *= 2)
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, k));
+          const int up =
+              min(120, TOP + 127 - int(__float_as_uint(big) >> 23));
+          const float next = fminf(gain, __int_as_float((127 + up) << 23));
+          if (next != gain) {
+            // (in two halves: the whole may be below 2^-126)
+            const int by =
+                (__float_as_int(next) >> 23) - (__float_as_int(gain) >> 23);
+            const float by1 = __int_as_float((127 + by / 2) << 23);
+            const float by2 = __int_as_float((127 + by - by / 2) << 23);
+            gain = next;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  o[k][nt][i] = o[k][nt][i] * by1 * by2;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                vs[mt][i] = sc[KW + mt * 16 + 8 * i] * gain;
+          }
+        }
       }
       // nothing seen yet: relative to 0, every weight is 0
 #pragma unroll
@@ -814,8 +859,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       // (bf16) or 11 (f16) bits alone would cost the result about as much as
       // its own rounding does, so what the rounding of a weight leaves goes
       // through the products too.  A value's scale is folded into its weight.
-      // UP keeps weights and sums in range: f16 weights run up to 2^15 and
-      // down to 2^-31 of the reference; e4m3 values are 2^-120 of themselves.
+      // UP: f16 weights run up to 2^15 and down to 2^-31 of the reference.
       uint32_t p[MT][NT][2], p2[MT][NT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -893,13 +937,22 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     // 256 bf16, 247 us so and 260 where the means are written.)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
+      float f[2], f2 = 1;
+      if (CODES) {
+        // 1 / gain, and the 2^120 of e4m3 values, in two halves
+        const int e = (KIND == KIND_E4M3 ? 120 : 0) + 127 -
+                      (__float_as_int(gain) >> 23);
+        f[0] = f[1] = __int_as_float((127 + e / 2) << 23);
+        f2 = __int_as_float((127 + e - e / 2) << 23);
+      } else {
+        f[0] = f[1] = DOWN;
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int k = 4; k < 32; k *= 2)
           l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], k);
-        f[j] = l[nt][j] == 0 ? 0.f : __fdividef(DOWN, l[nt][j]);
+        f[j] = l[nt][j] == 0 ? 0.f : __fdividef(f[j], l[nt][j]);
         if (row8 == 0) {
           float* st = state + (warp * Q + nt * 8 + col2 + j) * 2;
           st[0] = m[nt][j];
@@ -909,7 +962,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[k][nt][i] *= f[i & 1];
+        for (int i = 0; i < 4; ++i)
+          o[k][nt][i] = o[k][nt][i] * f[i & 1] * f2;
     }
 
     // the next head's queries are on their way while this one's parts join

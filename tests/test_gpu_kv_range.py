@@ -120,3 +120,63 @@ def test_large_values_under_growing_scores():
     q, out, lse = run_attend(P, 1, q=q, scale=1.0)
     assert out.isfinite().all()
     check(P, 1, q, out, scale=1.0)
+
+
+# --- scales of every size ---------------------------------------------------
+
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("power", [-115, -90, -60, -20, 20, 60, 70, 100, 118])
+@pytest.mark.parametrize("dim,group", [(64, 12), (128, 4), (256, 9)])
+def test_value_scales_of_every_size(store, power, dim, group):
+    """All rows of a head small or large alike, up to the largest that fit."""
+    P = kr.Pages([1, 40, 700, 1500], 2, dim, 16, "nhd", BF, store, seed=power)
+    P.scales[1] = P.scales[1] * 2.0 ** power
+    refresh(P)
+    q, out, lse = run_attend(P, group)
+    check(P, group, q, out)
+
+
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("size", [1e-37, 1e-25, 1e25, 1.2e38])
+def test_rows_that_the_write_takes(store, size):
+    """Finite rows, written by kv_write, come out of the attention as the
+    definition says for the codes and scales that the cache then holds."""
+    P = kr.Pages([33], 2, 64, 16, "nhd", BF, store, seed=3)
+    plan = lm.KVPlan(lm.Layout.make(*P.page_layout()), BF, store)
+    k, v = (torch.zeros(P.pool, 16, 2, 64, dtype=torch.uint8, device="cuda")
+            for _ in range(2))
+    scales = [torch.ones(P.pool, 2, 16, device="cuda") for _ in range(2)]
+    cache = lm.KVCache(plan, k, v, *scales)
+    x = torch.randn(2, 33, 2, 64, generator=torch.Generator().manual_seed(4))
+    x[1] = x[1].clamp(-2.5, 2.5) * size
+    j = torch.arange(33)
+    slots = P.table[0].long()[j // 16] * 16 + j % 16
+    lm.kv_write(cache, *x.to(BF).cuda(), slots.cuda())
+    for kv, t in enumerate((k, v)):
+        P.codes[kv] = t.cpu()
+        P.scales[kv] = scales[kv].cpu().transpose(1, 2)
+    refresh(P)
+    q, out, lse = run_attend(P, 4)
+    assert out.isfinite().all() and (out != 0).any()
+    check(P, 4, q, out)
+
+
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("order", ["large first", "small first", "mixed"])
+@pytest.mark.parametrize("gap", [0, -160])
+def test_scales_far_apart_in_one_head(store, order, gap):
+    """Values 2^80 (e4m3) or 2^120 (int8) apart in one head: the large ones
+    decide where they weigh as much; where their weights vanish (e^-160 of the
+    others') the small ones come out as they are."""
+    n, far = 400, 40 if store == "e4m3" else 60
+    P = kr.Pages([n], 1, 64, 16, "nhd", BF, store, seed=6)
+    large = {"large first": lambda j: j < n // 2,
+             "small first": lambda j: j >= n // 2,
+             "mixed": lambda j: j % 7 == 3}[order]
+    q = aim(P, lambda b, j: (gap if large(j) else 0) + (j % 5) / 4)
+    for j in range(n):
+        at = int(P.table[0, j // 16]), j % 16
+        P.scales[1][at] = P.scales[1][at] * 2.0 ** (far if large(j) else -far)
+    refresh(P)
+    q, out, lse = run_attend(P, 1, q=q, scale=1.0)
+    check(P, 1, q, out, scale=1.0)
