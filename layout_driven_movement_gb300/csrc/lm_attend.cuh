@@ -44,6 +44,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "lm_kv_device.cuh"
 
@@ -209,9 +210,25 @@ struct Codes<KIND_E4M3> {
         : "=r"(y[0]), "=r"(y[1])
         : "r"(r));
   }
-  static __device__ __forceinline__ void values(uint32_t r, uint32_t* y) {
-    y[0] = ((r << 4) & 0x07f007f0u) | ((r << 8) & 0x80008000u);
-    y[1] = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);
+  static __device__ __forceinline__ void values(uint32_t r, uint32_t* y,
+                                                uint32_t* top) {
+    const uint32_t a = (r << 4) & 0x07f007f0u, b = (r >> 4) & 0x07f007f0u;
+    *top = __vimax3_u16x2(*top, a, b);
+    y[0] = a | ((r << 8) & 0x80008000u);
+    y[1] = b | (r & 0x80008000u);
+  }
+  // Codes 0x7f and 0xff are not numbers, but become 480 * 2^-120 here, 0x07f0
+  // above all others.  So the largest magnitudes' bits of a step are kept,
+  // and where one is that, `nans` gives the step's elements again: NaN for
+  // such a code and 0 for any other.
+  static __device__ __forceinline__ uint32_t nans(uint32_t y) {
+    return ((((y & 0x07f007f0u) + 0x00100010u) >> 11) & 0x00010001u) * 0x7fc0u;
+  }
+  static __device__ __forceinline__ void values_nan(uint32_t r, uint32_t* y) {
+    uint32_t top = 0;
+    values(r, y, &top);
+    y[0] = nans(y[0]);
+    y[1] = nans(y[1]);
   }
 };
 
@@ -232,7 +249,8 @@ struct Codes<KIND_INT8> {
       y[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
-  static __device__ __forceinline__ void values(uint32_t r, uint32_t* y) {
+  static __device__ __forceinline__ void values(uint32_t r, uint32_t* y,
+                                                uint32_t*) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t t = i ? r >> 8 : r;
@@ -248,7 +266,8 @@ struct Codes<KIND_INT8> {
 template <>
 struct Codes<KIND_BF16> {
   static __device__ __forceinline__ void keys(uint32_t, uint32_t*) {}
-  static __device__ __forceinline__ void values(uint32_t, uint32_t*) {}
+  static __device__ __forceinline__ void values(uint32_t, uint32_t*,
+                                                uint32_t*) {}
 };
 template <>
 struct Codes<KIND_F16> : Codes<KIND_BF16> {};
@@ -882,41 +901,59 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
           }
 
       // O^T += V^T P^T
+      // codes: widened by `widen`, met by both parts of the weights or one
+      auto code_products = [&](auto&& widen, auto both) {
 #pragma unroll
-      for (int k = 0; k < KS; k += CODES && !LONG ? 2 : 1) {
-        if (k * 16 >= dim) break;
-        if constexpr (CODES && !LONG) {
-          uint32_t x[4];                            // 16 keys, 32 elements
-          ldm_t(x, (v_s + v_lane) ^ (k * 16));
+        for (int k = 0; k < KS; k += CODES && !LONG ? 2 : 1) {
+          if (k * 16 >= dim) break;
+          uint32_t x[4];
+          if constexpr (LONG) {                       // 32 keys, 16 elements
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t f[4];
-            Codes<KIND>::values(x[2 * e], f);
-            Codes<KIND>::values(x[2 * e + 1], f + 2);
+            for (int mt = 0; mt < MT; ++mt) {
+              if (mt % 2 == 0)
+                ldm_t(x, (v_s + v_lane + mt * 16 * S::kRow) ^ (k * 16));
+              // elements 2i are the tile's rows 0-7, elements 2i + 1 its
+              // rows 8-15
+              uint32_t f[4];
+              widen(x[mt % 2 * 2], f);
+              widen(x[mt % 2 * 2 + 1], f + 2);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<true>(o[k + e][nt], f, p[0][nt]);
-              mma<true>(o[k + e][nt], f, p2[0][nt]);
+              for (int nt = 0; nt < NT; ++nt) {
+                mma<true>(o[k][nt], f, p[mt][nt]);
+                if constexpr (decltype(both)::value) mma<true>(o[k][nt], f, p2[mt][nt]);
+              }
+            }
+          } else {                                    // 16 keys, 32 elements
+            ldm_t(x, (v_s + v_lane) ^ (k * 16));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t f[4];
+              widen(x[2 * e], f);
+              widen(x[2 * e + 1], f + 2);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma<true>(o[k + e][nt], f, p[0][nt]);
+                if constexpr (decltype(both)::value) mma<true>(o[k + e][nt], f, p2[0][nt]);
+              }
             }
           }
-        } else if constexpr (LONG) {
-          uint32_t x[4];                            // 32 keys, 16 elements
+        }
+      };
+      if constexpr (CODES) {
+        uint32_t code_top = 0;
+        code_products(
+            [&](uint32_t r, uint32_t* y) {
+              Codes<KIND>::values(r, y, &code_top);
+            },
+            std::true_type{});
+        if constexpr (KIND == KIND_E4M3) {
+          if (__any_sync(0xffffffffu, (code_top + 0x00100010u) & 0x08000800u))
+            code_products(Codes<KIND>::values_nan, std::false_type{});
+        }
+      } else {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if (mt % 2 == 0)
-              ldm_t(x, (v_s + v_lane + mt * 16 * S::kRow) ^ (k * 16));
-            // elements 2i are the tile's rows 0-7, elements 2i + 1 its rows
-            // 8-15
-            uint32_t f[4];
-            Codes<KIND>::values(x[mt % 2 * 2], f);
-            Codes<KIND>::values(x[mt % 2 * 2 + 1], f + 2);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<true>(o[k][nt], f, p[mt][nt]);
-              mma<true>(o[k][nt], f, p2[mt][nt]);
-            }
-          }
-        } else {
+        for (int k = 0; k < KS; ++k) {
+          if (k * 16 >= dim) break;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t x[4];

@@ -180,3 +180,61 @@ def test_scales_far_apart_in_one_head(store, order, gap):
     refresh(P)
     q, out, lse = run_attend(P, 1, q=q, scale=1.0)
     check(P, 1, q, out, scale=1.0)
+
+
+# --- codes that are not numbers ----------------------------------------------
+
+@pytest.mark.parametrize("code", [127, 255])
+@pytest.mark.parametrize("heads,group,dim,order", [
+    (2, 4, 64, "nhd"), (2, 9, 64, "nhd"), (2, 4, 128, "hnd"),
+    (1, 16, 128, "nhd"), (2, 5, 80, "nhd"), (2, 3, 256, "nhd"),
+    (1, 12, 256, "hnd")])
+def test_value_codes_that_are_not_numbers(code, heads, group, dim, order):
+    """A NaN code makes the element it belongs to NaN in the outputs of its
+    key head's queries, as the read back of the same page is, and no other."""
+    lens = [1, 20, 64, 130, 700, 90]
+    P = kr.Pages(lens, heads, dim, 16, order, BF, "e4m3", seed=dim)
+    at = [(0, 0, 0, 3), (1, 19, heads - 1, dim - 1), (2, 0, 0, 16),
+          (3, 77, 0, 9), (3, 77, heads - 1, 8), (4, 650, heads - 1, 40),
+          (4, 3, 0, 2), (4, 699, 0, 33)]
+    bad = torch.zeros(len(lens), heads * group, dim, dtype=torch.bool)
+    for b, j, h, d in at:
+        P.codes[1][int(P.table[b, j // 16]), j % 16, h, d] = code
+        bad[b, h * group:(h + 1) * group, d] = True
+    refresh(P)
+    q, out, lse = run_attend(P, group)
+    assert torch.equal(out.isnan(), bad)
+    assert lse.isfinite().all()
+    for rows in P.rows[1]:
+        rows[rows.isnan()] = 0
+    check(P, group, q, torch.where(bad, kr_clean(P, group, q), out.double()))
+
+
+def kr_clean(P, group, q):
+    """The definition on P's rows, [sequences, query heads, dim]."""
+    return torch.stack([
+        kr.attend(q[b].double(), P.rows[0][b], P.rows[1][b], group,
+                  P.dim ** -0.5)[0] for b in range(len(P.lens))])
+
+
+@pytest.mark.parametrize("code", [127, 255])
+def test_key_codes_that_are_not_numbers(code):
+    P = kr.Pages([30, 30], 2, 64, 16, "nhd", BF, "e4m3", seed=2)
+    P.codes[0][int(P.table[1, 1]), 3, 1, 7] = code
+    refresh(P)
+    q, out, lse = run_attend(P, 4)
+    bad = torch.zeros(2, 8, dtype=torch.bool)
+    bad[1, 4:] = True
+    assert torch.equal(out.isnan().all(-1), bad)
+    assert torch.equal(out.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad)
+
+
+def test_codes_that_are_not_numbers_past_the_window():
+    """Keys that are not seen do not count, whatever they hold."""
+    P = kr.Pages([100], 1, 64, 16, "nhd", BF, "e4m3", seed=2)
+    q, want, lse = run_attend(P, 2, window=40)
+    for j in range(60):
+        P.codes[1][int(P.table[0, j // 16]), j % 16, 0, j % 64] = 127
+    q, out, lse = run_attend(P, 2, window=40)
+    assert torch.equal(out, want) and out.isfinite().all()
