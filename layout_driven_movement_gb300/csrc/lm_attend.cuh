@@ -335,9 +335,11 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   constexpr bool CODES = S::kCodes;
   constexpr bool KBF = KIND == KIND_BF16;    // bf16 keys in the products
   constexpr bool VBF = KIND != KIND_F16;     // bf16 values and weights
-  // f16 weights are held times UP, see the weights below
-  constexpr float UP = KIND == KIND_F16 ? 0x1p7f : 1.f;
+  // f16 weights are held times UP, see the weights below; the largest passes
+  // 1 by up to 2^SLACK
+  constexpr float UP = KIND == KIND_F16 ? 0x1p12f : 1.f;
   constexpr float DOWN = 1 / UP;
+  constexpr float SLACK = KIND == KIND_F16 ? 3.f : 8.f;
   // Scales of 8-bit values may be any; a head's are taken times `gain`, a
   // power of two that the largest so far decides: it lies at 2^TOP when the
   // gain is set and passes MOST before it is set again, smaller ones are not
@@ -764,8 +766,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
           }
       }
       // A head's reference m moves only when a score passes the largest one
-      // that it was set for by 8, that is when a weight would pass 2^8 (LOW:
-      // 2^-5): one vote a step instead of the maximum over the lanes and the
+      // that it was set for by SLACK, that is when a weight would pass 2^SLACK
+      // (LOW: 2^-5): one vote a step instead of the maximum over the lanes and the
       // products' rescaling.  LOW: and when a lane's sum passes 2^-4, so that
       // the 8 lanes' sums, with the step's 2 weights each, stay below 1 and
       // the products below the largest value.
@@ -801,7 +803,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
             t = fmaxf(t, mt ? fmaxf(s[mt][nt][j], s[mt][nt][2 + j])
                             : s[mt][nt][2 + j]);
           top[nt][j] = t;
-          above |= t > m[nt][j] + (8.f - ROOM);
+          above |= t > m[nt][j] + (SLACK - ROOM);
           if (LOW) above |= l[nt][j] > 0x1p-4f;
         }
       if (__any_sync(0xffffffffu, above)) {
@@ -878,8 +880,22 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       // (bf16) or 11 (f16) bits alone would cost the result about as much as
       // its own rounding does, so what the rounding of a weight leaves goes
       // through the products too.  A value's scale is folded into its weight.
-      // UP: f16 weights run up to 2^15 and down to 2^-31 of the reference.
+      //
+      // f16 weights, held times UP, run up to 2^15.  Two f16 parts of one
+      // below WEAK leave more than 2^-14 of it, and nothing at all of one
+      // below 2^-26.  Such weak ones wait for products of their own; below
+      // 2^-71 of the largest they add less than f16 holds, whatever their
+      // number.
+      constexpr float WEAK = 0x1p-11f;
+      float weak[MT][NT][4];
+      bool some_weak = false;
       uint32_t p[MT][NT][2], p2[MT][NT][2];
+      auto operand = [&](int mt, int nt, int r, const float* w) {
+        const uint32_t hi = pair16<VBF>(w[0], w[1]);
+        const float2 f = unpair16<VBF>(hi);
+        p[mt][nt][r] = mov_t(hi);
+        p2[mt][nt][r] = mov_t(pair16<VBF>(w[0] - f.x, w[1] - f.y));
+      };
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -893,11 +909,15 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
               l[nt][j] += w[j];
               if (CODES) w[j] *= vs[mt][r];
               if (UP != 1.f) w[j] *= UP;
+              if (KIND == KIND_F16) {
+                const bool is = w[j] < WEAK;
+                float& x = weak[mt][nt][2 * r + j];
+                x = is && w[j] >= WEAK * 0x1p-48f ? w[j] : 0.f;
+                some_weak |= x > 0;
+                if (is) w[j] = 0;
+              }
             }
-            const uint32_t hi = pair16<VBF>(w[0], w[1]);
-            const float2 f = unpair16<VBF>(hi);
-            p[mt][nt][r] = mov_t(hi);
-            p2[mt][nt][r] = mov_t(pair16<VBF>(w[0] - f.x, w[1] - f.y));
+            operand(mt, nt, r, w);
           }
 
       // O^T += V^T P^T
@@ -939,18 +959,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
           }
         }
       };
-      if constexpr (CODES) {
-        uint32_t code_top = 0;
-        code_products(
-            [&](uint32_t r, uint32_t* y) {
-              Codes<KIND>::values(r, y, &code_top);
-            },
-            std::true_type{});
-        if constexpr (KIND == KIND_E4M3) {
-          if (__any_sync(0xffffffffu, (code_top + 0x00100010u) & 0x08000800u))
-            code_products(Codes<KIND>::values_nan, std::false_type{});
-        }
-      } else {
+      auto products = [&] {
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           if (k * 16 >= dim) break;
@@ -965,6 +974,62 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
             }
           }
         }
+      };
+      if constexpr (CODES) {
+        uint32_t code_top = 0;
+        code_products(
+            [&](uint32_t r, uint32_t* y) {
+              Codes<KIND>::values(r, y, &code_top);
+            },
+            std::true_type{});
+        if constexpr (KIND == KIND_E4M3) {
+          if (__any_sync(0xffffffffu, (code_top + 0x00100010u) & 0x08000800u))
+            code_products(Codes<KIND>::values_nan, std::false_type{});
+        }
+      } else {
+        products();
+      }
+      if constexpr (KIND == KIND_F16) {
+        // Weak weights 2^24 up, those that are still weak 2^48; the sums go
+        // up with them and down again.  A step with a round of it takes about
+        // half as long again: 64 sequences of 8192 tokens, 8 x 4 x 128, 325 us
+        // where scores lie within some 15 of each other, 356 where they
+        // deviate by 4 and 432 where by 12 (4 x 16 x 256, 32 sequences: 267,
+        // 367 and 458).
+        auto scale = [&](float by) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[k][nt][i] *= by;
+        };
+        float down = 1;
+        while (__any_sync(0xffffffffu, some_weak)) {
+          some_weak = false;
+          down *= 0x1p-24f;
+          scale(0x1p24f);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float w[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float& x = weak[mt][nt][2 * r + j];
+                  x *= 0x1p24f;
+                  const bool now = x >= WEAK;
+                  w[j] = now ? x : 0;
+                  if (now) x = 0;
+                  some_weak |= x > 0;
+                }
+                operand(mt, nt, r, w);
+              }
+          products();
+        }
+        if (down != 1) scale(down);
       }
       if (++stage == NS) stage = 0;
     }

@@ -238,3 +238,84 @@ def test_codes_that_are_not_numbers_past_the_window():
         P.codes[1][int(P.table[0, j // 16]), j % 16, 0, j % 64] = 127
     q, out, lse = run_attend(P, 2, window=40)
     assert torch.equal(out, want) and out.isfinite().all()
+
+
+# --- weights far below the largest -------------------------------------------
+
+@pytest.mark.parametrize("store,dtype", [(None, HF), (None, BF),
+                                         ("e4m3", HF), ("int8", HF)])
+@pytest.mark.parametrize("n,drop", [(16, 23.5), (16, 30.0), (64, 12.0),
+                                    (3000, 23.0), (3000, 17.0)])
+@pytest.mark.parametrize("at", [0, 5])
+@pytest.mark.parametrize("sink", [0.0, 2.0 ** -10])
+def test_many_weak_keys_beside_a_sink(store, dtype, n, drop, at, sink):
+    """One key takes nearly all of the weight and adds nearly nothing; what
+    the others, e^drop weaker each, add with values of 2^15 must not be
+    lost."""
+    P = kr.Pages([n], 2, 64, 16, "nhd", dtype, store, seed=n)
+    q = aim(P, lambda b, j: drop if j == at else (j % 8) / 16)
+    g = torch.Generator().manual_seed(n)
+    page, off = int(P.table[0, at // 16]), at % 16
+    if store is None:
+        x = (1 + torch.rand(P.codes[1].shape, generator=g)) * 2.0 ** 14
+        P.codes[1] = torch.where(P.codes[1].isnan(), P.codes[1], x.to(dtype))
+        P.codes[1][page, off] = sink
+    else:
+        P.codes[1] = torch.where(
+            tokens(P)[..., None, None],
+            torch.randint(64, 127, P.codes[1].shape, generator=g).byte(),
+            P.codes[1])
+        P.scales[1] = torch.where(P.scales[1].isnan(), P.scales[1],
+                                  torch.full_like(P.scales[1], 2.0 ** 7))
+        P.codes[1][page, off] = 8 if sink else 0
+        P.scales[1][page, off] = 2.0 ** -10
+    refresh(P)
+    q, out, lse = run_attend(P, 1, q=q, scale=1.0)
+    check(P, 1, q, out, scale=1.0)
+
+
+@pytest.mark.parametrize("dim,group", [(128, 9), (256, 1), (72, 4)])
+def test_weak_keys_among_several_queries(dim, group):
+    """The same where the queries of a head weigh the keys differently."""
+    P = kr.Pages([200, 17], 2, dim, 16, "nhd", HF, None, seed=dim)
+    g = torch.Generator().manual_seed(dim)
+    aim(P, lambda b, j: 24.0 if j == 4 else -16.0 if j % 3 else 0.5)
+    q = torch.zeros(2, 2 * group, dim, dtype=HF)
+    q[..., 0] = torch.linspace(-1, 1, 2 * group)
+    x = torch.randn(P.codes[1].shape, generator=g) * 2.0 ** 10
+    P.codes[1] = torch.where(P.codes[1].isnan(), P.codes[1], x.to(HF))
+    for b in range(2):
+        P.codes[1][int(P.table[b, 0]), 4] = 2.0 ** -12
+    refresh(P)
+    q, out, lse = run_attend(P, group, q=q, scale=1.0)
+    check(P, group, q, out, scale=1.0)
+
+
+@pytest.mark.parametrize("store,dtype,rel", [
+    (None, BF, 2.0 ** -15), (None, HF, 2.0 ** -18), ("e4m3", BF, 2.0 ** -15),
+    ("int8", HF, 2.0 ** -15)])
+def test_weights_keep_their_bits(store, dtype, rel):
+    """Values +c and -c that cancel all but fully: what is left is the
+    weights' own error.  float16 weights' parts leave 2^-22."""
+    n = 64
+    P = kr.Pages([n] * 4, 1, 16, 16, "nhd", dtype, store, seed=5)
+    r = torch.Generator().manual_seed(8)
+    s = [[round(float(x) * 64) / 64 for x in torch.randn(n, generator=r)]
+         for _ in range(4)]
+    q = aim(P, lambda b, j: s[b][j])
+    for b in range(4):
+        left = 0.0
+        for j in sorted(range(n), key=lambda j: -s[b][j]):
+            at = int(P.table[b, j // 16]), j % 16
+            sign = -1 if left > 0 else 1
+            left += sign * math.exp(s[b][j])
+            if store is None:
+                P.codes[1][at] = sign * 3.0
+            else:
+                P.codes[1][at] = {"e4m3": 0x44, "int8": 3}[store] if sign > 0 \
+                    else {"e4m3": 0xc4, "int8": 253}[store]
+                P.scales[1][at] = 1.0
+    refresh(P)
+    assert all(r.abs().eq(3).all() for r in P.rows[1])
+    q, out, lse = run_attend(P, 1, q=q, scale=1.0)
+    check(P, 1, q, out, scale=1.0, rel=rel)
