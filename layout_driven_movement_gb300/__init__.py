@@ -774,6 +774,8 @@ def build_layout(spec) -> Layout:
 
 _ELEM = {"bfloat16": 1, "float16": 2, "float32": 3}
 _STORES = {None: 0, "same": 0, "e4m3": 1, "int8": 2}
+# what quantised pages may be: the codes' type, or their bytes
+_HELD = {"e4m3": ("float8_e4m3fn", "uint8"), "int8": ("int8", "uint8")}
 _SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _dtype_names: dict = {}
 _current_stream = None
@@ -930,18 +932,19 @@ class KVPlan:
 
 class KVCache:
     """A plan's buffers: CUDA tensors whose first element is page 0's (their
-    shape is the caller's; page p starts p * page_stride elements on), and for
-    a quantised store float32 scales of pages * heads * page_tokens each.
+    shape is the caller's; page p starts p * page_stride elements on) of the
+    plan's dtype -- for a quantised store float8_e4m3fn or int8, or bytes --
+    and for such a store float32 scales of pages * heads * page_tokens each.
     ``pages`` defaults to what k holds."""
 
     __slots__ = ("plan", "k", "v", "k_scale", "v_scale", "pages", "_c", "_p")
 
     def __init__(self, plan: KVPlan, k, v, k_scale=None, v_scale=None,
                  pages: int | None = None):
+        held = _HELD.get(plan.store) or (_dtype(plan.dtype),)
         for t, what in ((k, "k"), (v, "v")):
-            if not t.is_cuda or t.element_size() != plan.held_bytes:
-                _wanted(f"{what}: a CUDA tensor of {plan.held_bytes}-byte "
-                        "elements")
+            if not t.is_cuda or _dtype(t.dtype) not in held:
+                _wanted(f"{what}: a CUDA tensor of {' or '.join(held)}")
         scales = 0
         if plan.store is not None:
             for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
