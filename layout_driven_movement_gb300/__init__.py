@@ -896,7 +896,7 @@ class KVPlan:
     with a scale per token and head (see lm_kv_plan_create)."""
 
     __slots__ = ("_h", "_p", "dtype", "elem", "store", "page_tokens", "heads",
-                 "dim", "page_stride", "held_bytes")
+                 "dim", "page_stride", "page_cosize", "held_bytes")
 
     def __init__(self, page: Layout, dtype, store: str | None = None,
                  page_stride: int = 0):
@@ -911,7 +911,7 @@ class KVPlan:
         d = self.describe()
         self.page_tokens, self.heads = d["page_tokens"], d["heads"]
         self.dim, self.page_stride = d["dim"], d["page_stride"]
-        self.held_bytes = d["held_bytes"]
+        self.held_bytes, self.page_cosize = d["held_bytes"], page.cosize
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -935,7 +935,7 @@ class KVCache:
     shape is the caller's; page p starts p * page_stride elements on) of the
     plan's dtype -- for a quantised store float8_e4m3fn or int8, or bytes --
     and for such a store float32 scales of pages * heads * page_tokens each.
-    ``pages`` defaults to what k holds."""
+    ``pages`` defaults to the whole pages that k holds."""
 
     __slots__ = ("plan", "k", "v", "k_scale", "v_scale", "pages", "_c", "_p")
 
@@ -954,7 +954,8 @@ class KVCache:
             scales = min(k_scale.numel(), v_scale.numel())
         ke, ve = _extent(k), _extent(v)
         if pages is None:
-            pages = -(-ke // plan.page_stride)
+            whole, rest = divmod(ke, plan.page_stride)
+            pages = max(1, whole + (rest >= plan.page_cosize))
         self.plan, self.pages = plan, int(pages)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self._c = _KVCache(

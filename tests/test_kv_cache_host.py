@@ -74,3 +74,22 @@ def test_pages_are_of_the_plans_type(dtype, store, held, taken):
         else:
             with pytest.raises(ValueError):
                 cache_of("torch." + dtype, store, k, v)
+
+
+@pytest.mark.parametrize("elements,pages", [
+    (8 * 128, 8), (8 * 128 + 1, 8), (8 * 128 + 127, 8), (9 * 128, 9),
+    (128, 1), (129, 1)])
+def test_pages_that_a_buffer_holds(elements, pages):
+    """What a buffer has past its last whole page is no page."""
+    k = Tensor("torch.bfloat16", elements)
+    assert cache_of("torch.bfloat16", None, k).pages == pages
+
+
+@pytest.mark.parametrize("elements,pages", [
+    (7 * 200 + 128, 8), (7 * 200 + 127, 7), (8 * 200, 8), (7 * 200, 7)])
+def test_pages_of_a_stride_above_their_size(elements, pages):
+    """The last page needs its own elements, not the gap after them."""
+    plan = lm.KVPlan(lm.Layout.parse("(4,2,16):(32,16,1)"), "torch.bfloat16",
+                     page_stride=200)
+    k = Tensor("torch.bfloat16", elements)
+    assert lm.KVCache(plan, k, k).pages == pages
