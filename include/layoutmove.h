@@ -727,8 +727,9 @@ int lm_kv_write(const lm_kv_plan* plan, const lm_kv_cache* cache,
  * starts[b + 1] - starts[b] or max_pages * P counts as that much.  rows: the
  * rows of the outputs; output rows that no token names, or from `rows` on,
  * are left as they are.  out_elem: the outputs' lm_elem.  A page number
- * outside [0, pages) is out of range and gives zeros.
- * Errors: as lm_kv_write. */
+ * outside [0, pages) is out of range and gives zeros.  The two outputs may lie
+ * in one buffer, their tokens the same distance apart, but share no element.
+ * Errors: as lm_kv_write, and LM_E_OVERLAP for outputs that meet. */
 int lm_kv_read(const lm_kv_plan* plan, const lm_kv_cache* cache,
                const int32_t* page_table, int64_t table_stride, int seqs,
                int64_t max_pages, const int32_t* lens, const int32_t* starts,

@@ -57,6 +57,55 @@ Range check_rows(const lm_rows* r, int64_t tokens, int64_t heads, int64_t dim,
   return {addr(r->data), addr(r->data) + uintptr_t(mul_chk(last, es))};
 }
 
+typedef __int128 wide;
+
+// Whether |r + i big + j small| < w for an i in [i0, i1] and a j in [j0, j1].
+// Few i come near where a span of j's is no longer than big, as the rows of an
+// output are.
+bool near_zero(wide r, wide big, wide i0, wide i1, wide small, wide j0,
+               wide j1, wide w) {
+  auto down = [](wide a, wide b) { return a / b - (a % b < 0); };
+  if (big == 0) i0 = i1 = 0;
+  if (small == 0) j0 = j1 = 0;
+  if (big > 0) {
+    const wide lo = down(-w - j1 * small - r, big);
+    const wide hi = down(w - j0 * small - r, big) + 1;
+    if (i0 < lo) i0 = lo;
+    if (i1 > hi) i1 = hi;
+  }
+  for (wide i = i0; i <= i1; ++i) {
+    const wide rest = r + i * big;
+    const wide at = small == 0 ? 0 : down(-rest, small);
+    for (wide j = at; j <= at + 1; ++j) {
+      const wide k = j < j0 ? j0 : j > j1 ? j1 : j;
+      const wide d = rest + k * small;
+      if (d < w && d > -w) return true;
+    }
+  }
+  return false;
+}
+
+// Whether two outputs of one shape share elements.  Each one's own rows are
+// apart.  Tokens a different distance apart in the two: taken as shared.
+bool rows_meet(const lm_rows& a, const lm_rows& b, int64_t tokens,
+               int64_t heads, int64_t dim, int es) {
+  const wide w = wide(dim) * es;
+  const wide r = wide(addr(b.data)) - wide(addr(a.data));
+  const wide ts = tokens > 1 ? wide(b.token_stride) * es : 0;
+  const wide ah = heads > 1 ? wide(a.head_stride) * es : 0;
+  const wide bh = heads > 1 ? wide(b.head_stride) * es : 0;
+  if (tokens > 1 && a.token_stride != b.token_stride) return true;
+  const wide t = tokens - 1;
+  auto meet = [&](wide from, wide h0, wide h1) {
+    return ts >= bh ? near_zero(from, ts, -t, t, bh, h0, h1, w)
+                    : near_zero(from, bh, h0, h1, ts, -t, t, w);
+  };
+  if (ah == bh) return meet(r, 1 - heads, heads - 1);
+  for (int64_t h = 0; h < heads; ++h)
+    if (meet(r - h * ah, 0, heads - 1)) return true;
+  return false;
+}
+
 bool vector_rows(const lm_rows& r, int es) {
   const int64_t v = 16 / es;
   return addr(r.data) % 16 == 0 && r.token_stride % v == 0 &&
@@ -396,7 +445,9 @@ int lm_kv_read(const lm_kv_plan* plan, const lm_kv_cache* cache,
       o[i] = lm::check_rows(outs[i], rows, plan->heads, plan->dim, es, true);
       need(!o[i].meets(rk) && !o[i].meets(rv), LM_E_OVERLAP);
     }
-    need(k_out->data != v_out->data, LM_E_OVERLAP);
+    need(!o[0].meets(o[1]) ||
+             !lm::rows_meet(*k_out, *v_out, rows, plan->heads, plan->dim, es),
+         LM_E_OVERLAP);
     a.k = lm::rows_of(*k_out);
     a.v = lm::rows_of(*v_out);
     a.table = page_table;
