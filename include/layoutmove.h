@@ -712,8 +712,9 @@ int lm_kv_plan_describe(const lm_kv_plan* plan, char* buf, size_t cap);
  * bits, and rounded only into the cache; rope's head_dim is the plan's dim.
  * Errors: LM_E_INVALID (NULL, counts, pointer alignment, a rope plan of
  * another head_dim or without positions and table), LM_E_CAPACITY,
- * LM_E_OVERLAP (the cache's keys and values start at the same address, or
- * an input overlaps the cache), LM_E_OVERFLOW, LM_E_CUDA. */
+ * LM_E_OVERLAP (the cache's keys and values start at the same address, its
+ * scales overlap each other or a page, or an input overlaps the cache or its
+ * scales), LM_E_OVERFLOW, LM_E_CUDA. */
 int lm_kv_write(const lm_kv_plan* plan, const lm_kv_cache* cache,
                 const lm_rows* k, const lm_rows* v, int64_t tokens,
                 const int64_t* slots, const lm_rope_plan* rope,
@@ -763,8 +764,9 @@ int lm_kv_attend_workspace(const lm_kv_plan* plan, int seqs, int heads_q,
  * Errors: LM_E_INVALID (NULL, counts, heads_q not a multiple of the plan's
  * heads or above 2^20, a scale that is not finite, negative window, pointer
  * alignment),
- * LM_E_CAPACITY (a buffer, or the workspace), LM_E_OVERLAP, LM_E_OVERFLOW,
- * LM_E_CUDA. */
+ * LM_E_CAPACITY (a buffer, or the workspace), LM_E_OVERLAP (out, lse or the
+ * workspace with each other, with q or with the cache or its scales; out and
+ * q as above), LM_E_OVERFLOW, LM_E_CUDA. */
 int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
                  const lm_rows* q, const lm_rows* out, int seqs, int heads_q,
                  const int32_t* page_table, int64_t table_stride,

@@ -137,9 +137,30 @@ Turn check_turn(const lm_rope_plan& rope, const void* positions,
   return t;
 }
 
-// Checks a cache against its plan.  k and v: the bytes each can span.
-CacheArgs check_cache(const lm_kv_plan& p, const lm_kv_cache* c, Range* k,
-                      Range* v) {
+// Whether a range meets one of the pages that lie in `all` (not the room
+// between them).
+bool pages_meet(const lm_kv_plan& p, const lm_kv_cache* c, const Range& all,
+                const Range& o) {
+  if (!o.meets(all)) return false;
+  const uintptr_t stride = uintptr_t(p.page_stride) * uintptr_t(p.held);
+  const uintptr_t page = uintptr_t(p.page_cosize) * uintptr_t(p.held);
+  const uintptr_t lo = o.lo > all.lo ? o.lo - all.lo : 0, hi = o.hi - all.lo;
+  const uintptr_t n = lo / stride;      // the last page that starts at or below
+  return lo - n * stride < page ||
+         (n + 1 < uintptr_t(c->pages) && (n + 1) * stride < hi);
+}
+
+// The bytes that a cache's keys, values and scales (empty for SAME) span.
+struct CacheRanges {
+  Range k, v, ks, vs;
+  bool meet(const Range& o) const {
+    return o.meets(k) || o.meets(v) || o.meets(ks) || o.meets(vs);
+  }
+};
+
+// Checks a cache against its plan.
+CacheArgs check_cache(const lm_kv_plan& p, const lm_kv_cache* c,
+                      CacheRanges* r) {
   need(c && c->k && c->v && c->pages >= 1 && c->k_capacity >= 0 &&
        c->v_capacity >= 0);
   need(addr(c->k) % 16 == 0 && addr(c->v) % 16 == 0);
@@ -152,10 +173,12 @@ CacheArgs check_cache(const lm_kv_plan& p, const lm_kv_cache* c, Range* k,
   if (p.store != LM_KV_SAME) {
     need(c->k_scale && c->v_scale && addr(c->k_scale) % 4 == 0 &&
          addr(c->v_scale) % 4 == 0);
-    need(c->k_scale != c->v_scale, LM_E_OVERLAP);
-    need(mul_chk(c->pages, mul_chk(p.heads, p.page_tokens)) <=
-             c->scale_capacity,
-         LM_E_CAPACITY);
+    const int64_t scales = mul_chk(c->pages, mul_chk(p.heads, p.page_tokens));
+    need(scales <= c->scale_capacity, LM_E_CAPACITY);
+    const uintptr_t bytes = uintptr_t(mul_chk(scales, 4));
+    r->ks = {addr(c->k_scale), addr(c->k_scale) + bytes};
+    r->vs = {addr(c->v_scale), addr(c->v_scale) + bytes};
+    need(!r->ks.meets(r->vs), LM_E_OVERLAP);
     a.ks = c->k_scale;
     a.vs = c->v_scale;
   }
@@ -170,8 +193,11 @@ CacheArgs check_cache(const lm_kv_plan& p, const lm_kv_cache* c, Range* k,
   a.page_div = make_fastdiv(uint32_t(p.page_tokens));
   a.dim = int32_t(p.dim);
   const uintptr_t bytes = uintptr_t(mul_chk(span, p.held));
-  *k = {addr(c->k), addr(c->k) + bytes};
-  *v = {addr(c->v), addr(c->v) + bytes};
+  r->k = {addr(c->k), addr(c->k) + bytes};
+  r->v = {addr(c->v), addr(c->v) + bytes};
+  for (const Range& scale : {r->ks, r->vs})
+    need(!pages_meet(p, c, r->k, scale) && !pages_meet(p, c, r->v, scale),
+         LM_E_OVERLAP);
   return a;
 }
 
@@ -386,15 +412,15 @@ int lm_kv_write(const lm_kv_plan* plan, const lm_kv_cache* cache,
   int rc = LM_OK;
   const int checked = lm::guarded([&] {
     need(plan && tokens >= 0);
-    lm::Range rk, rv;
+    lm::CacheRanges held;
     lm::KvWriteArgs a;
-    a.c = lm::check_cache(*plan, cache, &rk, &rv);
+    a.c = lm::check_cache(*plan, cache, &held);
     if (tokens == 0) return;
     need(slots && lm::addr(slots) % 8 == 0);
     for (const lm_rows* r : {k, v}) {
       const lm::Range ri =
           lm::check_rows(r, tokens, plan->heads, plan->dim, 2, false);
-      need(!ri.meets(rk) && !ri.meets(rv), LM_E_OVERLAP);
+      need(!held.meet(ri), LM_E_OVERLAP);
     }
     if (rope) {
       need(rope->head_dim == plan->dim);
@@ -431,9 +457,9 @@ int lm_kv_read(const lm_kv_plan* plan, const lm_kv_cache* cache,
   int rc = LM_OK;
   const int checked = lm::guarded([&] {
     need(plan && rows >= 0 && out_elem >= LM_BF16 && out_elem <= LM_F32);
-    lm::Range rk, rv;
+    lm::CacheRanges held;
     lm::KvReadArgs a;
-    a.c = lm::check_cache(*plan, cache, &rk, &rv);
+    a.c = lm::check_cache(*plan, cache, &held);
     if (rows == 0 || seqs == 0 || max_pages == 0) return;
     lm::check_table(*plan, page_table, table_stride, seqs, max_pages, lens);
     need(starts && lm::addr(starts) % 4 == 0);
@@ -443,7 +469,7 @@ int lm_kv_read(const lm_kv_plan* plan, const lm_kv_cache* cache,
     const lm_rows* outs[2] = {k_out, v_out};
     for (int i = 0; i < 2; ++i) {
       o[i] = lm::check_rows(outs[i], rows, plan->heads, plan->dim, es, true);
-      need(!o[i].meets(rk) && !o[i].meets(rv), LM_E_OVERLAP);
+      need(!held.meet(o[i]), LM_E_OVERLAP);
     }
     need(!o[0].meets(o[1]) ||
              !lm::rows_meet(*k_out, *v_out, rows, plan->heads, plan->dim, es),
@@ -487,9 +513,9 @@ int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
   const int checked = lm::guarded([&] {
     need(plan && seqs >= 0 && heads_q >= 1 && heads_q % plan->heads == 0 &&
          heads_q <= (1 << 20) && std::isfinite(scale) && window >= 0);
-    lm::Range rk, rv;
+    lm::CacheRanges held;
     lm::KvAttendArgs a;
-    a.c = lm::check_cache(*plan, cache, &rk, &rv);
+    a.c = lm::check_cache(*plan, cache, &held);
     if (seqs == 0) return;
     lm::check_table(*plan, page_table, table_stride, seqs, max_pages, lens);
     const lm::Range rq =
@@ -501,8 +527,14 @@ int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
         (seqs == 1 || q->token_stride == out->token_stride) &&
         (heads_q == 1 || q->head_stride == out->head_stride);
     need(in_place || !rq.meets(ro), LM_E_OVERLAP);
-    need(!ro.meets(rk) && !ro.meets(rv), LM_E_OVERLAP);
+    need(!held.meet(ro), LM_E_OVERLAP);
     need(lse == nullptr || lm::addr(lse) % 4 == 0);
+    lm::Range rl;
+    if (lse) {
+      rl = {lm::addr(lse),
+            lm::addr(lse) + uintptr_t(int64_t(seqs) * heads_q * 4)};
+      need(!held.meet(rl) && !rl.meets(rq) && !rl.meets(ro), LM_E_OVERLAP);
+    }
     a.q = lm::rows_of(*q);
     a.out = lm::rows_of(*out);
     a.table = page_table;
@@ -523,6 +555,10 @@ int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
     if (rc != LM_OK) return;
     need(want == 0 || (workspace && lm::addr(workspace) % 16 == 0));
     need(workspace_bytes >= want, LM_E_CAPACITY);
+    const lm::Range rw = {lm::addr(workspace),
+                          lm::addr(workspace) + uintptr_t(want)};
+    need(!held.meet(rw) && !rw.meets(rq) && !rw.meets(ro) && !rw.meets(rl),
+         LM_E_OVERLAP);
     rc = lm::launch_kv_attend(a, plan->store, cuda_stream);
   });
   return checked != LM_OK ? checked : rc;

@@ -45,3 +45,37 @@ def test_read_whatever_the_order_of_the_outputs():
     for at in (64, 1024, 99 * 1024):
         kw = outs(at)
         assert call_read(k=kw["v"], v=kw["k"]) == OVERLAP
+
+
+KS, VS, ONE = BASE * 4, BASE * 5, 64 * 8 * 16 * 4     # scales, their bytes
+
+
+@pytest.mark.parametrize("store", ["e4m3", "int8"])
+@pytest.mark.parametrize("kw", [
+    {"vs": KS + 4}, {"vs": KS + ONE - 4}, {"vs": KS - 4},
+    {"ks": BASE * 2 + 64}, {"vs": BASE * 2 - 4},
+    {"ks": BASE * 3 + (64 << 14) - 4},           # the last page's last bytes
+])
+def test_scales_that_meet(store, kw):
+    """Each other or a page, in every call."""
+    c = cache(**kw)
+    assert call_write(store, c) == OVERLAP
+    assert call_read(store, c) == OVERLAP
+    assert call_attend(store, c) == OVERLAP
+
+
+def test_rows_that_meet_the_scales():
+    for at in (KS, VS - 2, KS + ONE - 2):
+        assert call_write("int8", k=rows(at)) == OVERLAP
+        assert call_write("e4m3", v=rows(at)) == OVERLAP
+        assert call_read("int8", k=rows(at)) == OVERLAP
+        assert call_read("e4m3", v=rows(at)) == OVERLAP
+        assert call_attend("int8", out=rows(at, ts=4096)) == OVERLAP
+
+
+@pytest.mark.parametrize("store,at", [
+    ("e4m3", KS), ("int8", VS + ONE - 4), (None, BASE * 2), (None, BASE * 3),
+    (None, BASE), (None, BASE + 2 * 3 * 4096 - 4),    # the queries
+    (None, BASE * 12 - 4), (None, BASE * 12 + 4096)])  # the outputs
+def test_lse_that_meets(store, at):
+    assert call_attend(store, lse=at) == OVERLAP
