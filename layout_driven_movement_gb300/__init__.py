@@ -152,15 +152,19 @@ _pycall_module = None
 
 def _pycall():
     """The extension of the calls that a decoding step makes (raises if it has
-    not been built)."""
+    not been built for this interpreter)."""
     global _pycall_module
     if _pycall_module is None:
         lib()
         from importlib.machinery import ExtensionFileLoader
         from importlib.util import module_from_spec, spec_from_file_location
-        path = os.path.join(_PKG, "_pycall.so")
+        from ._build import PYCALL as path, PYCALL_LOG
         if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build the library")
+            why = "build the library"
+            if os.path.exists(PYCALL_LOG):
+                with open(PYCALL_LOG) as f:
+                    why = f.read() or why
+            raise RuntimeError(f"{path} is missing: {why}")
         spec = spec_from_file_location(
             "_pycall", path, loader=ExtensionFileLoader("_pycall", path))
         _pycall_module = module_from_spec(spec)

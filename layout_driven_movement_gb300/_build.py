@@ -6,7 +6,10 @@ the kernels (CUDA, compiled with nvcc for sm_103a only) -- is built in
 parallel into ``_build/`` and linked into ``liblayoutmove.so`` next to this
 file.  The CUDA runtime is linked
 statically, so the library loads without any other CUDA shared object.  The
-Python extension ``pycall/lm_pycall.c`` is linked to it as ``_pycall.so``.
+Python extension ``pycall/lm_pycall.c`` is linked to it as ``_pycall`` with
+the interpreter's own suffix.  It alone needs Python's headers: where it cannot
+be built the library still is, and the calls that go through it say why they
+cannot be made.
 """
 
 from __future__ import annotations
@@ -24,7 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblayoutmove.so")
 PYCALL_SRC = os.path.join(PKG, "pycall", "lm_pycall.c")
-PYCALL = os.path.join(PKG, "_pycall.so")
+PYCALL = os.path.join(PKG, "_pycall" + sysconfig.get_config_var("EXT_SUFFIX"))
+PYCALL_LOG = os.path.join(BUILD, "pycall.log")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -45,17 +49,23 @@ def _newest_input() -> float:
     files = _sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                           if f.endswith((".h", ".cuh"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    files += [os.path.abspath(__file__), PYCALL_SRC]
+    files.append(os.path.abspath(__file__))
     return max(os.path.getmtime(f) for f in files)
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Build (if stale) and return the path of liblayoutmove.so."""
-    if (not force and os.path.exists(LIB) and os.path.exists(PYCALL)
-            and min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
-            >= _newest_input()):
-        return LIB
+    """Build what is stale; return the path of liblayoutmove.so."""
     os.makedirs(BUILD, exist_ok=True)
+    if (force or not os.path.exists(LIB)
+            or os.path.getmtime(LIB) < _newest_input()):
+        _build_library(verbose)
+    if (force or not os.path.exists(PYCALL) or os.path.getmtime(PYCALL)
+            < max(os.path.getmtime(f) for f in (LIB, PYCALL_SRC))):
+        _build_extension()
+    return LIB
+
+
+def _build_library(verbose: bool) -> None:
     nvcc = _nvcc()
     common = ["-O3", "-std=c++17", f"-I{INCLUDE}", f"-I{CSRC}"]
     jobs = []
@@ -89,16 +99,30 @@ def build(verbose: bool = False, force: bool = False) -> str:
         raise RuntimeError("layoutmove link failed:\n" +
                            res.stdout.decode(errors="replace"))
     os.replace(tmp, LIB)
+
+
+def _build_extension() -> None:
+    """Links the extension to the library as it is now; where that fails, none
+    is left and the log tells why."""
     tmp = PYCALL + ".tmp"
     link = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-shared",
             "-fPIC", f"-I{INCLUDE}", f"-I{sysconfig.get_path('include')}",
             PYCALL_SRC, LIB, "-Wl,-rpath,$ORIGIN", "-o", tmp]
-    res = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if res.returncode != 0:
-        raise RuntimeError("layoutmove extension failed:\n" +
-                           res.stdout.decode(errors="replace"))
-    os.replace(tmp, PYCALL)
-    return LIB
+    try:
+        res = subprocess.run(link, stdout=subprocess.PIPE,
+                             stderr=subprocess.STDOUT)
+        text, ok = res.stdout.decode(errors="replace"), res.returncode == 0
+    except OSError as e:
+        text, ok = str(e), False
+    with open(PYCALL_LOG, "w") as f:
+        f.write(text)
+    if ok:
+        os.replace(tmp, PYCALL)
+        return
+    if os.path.exists(PYCALL):
+        os.remove(PYCALL)
+    sys.stderr.write("layoutmove: the Python extension was not built (rope, "
+                     "kv_write, kv_read and kv_attend need it):\n" + text)
 
 
 if __name__ == "__main__":
