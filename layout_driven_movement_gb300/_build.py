@@ -93,7 +93,9 @@ def _build_library(verbose: bool) -> None:
     if failed:
         raise RuntimeError("layoutmove build failed:\n" + "\n".join(failed))
     tmp = LIB + ".tmp"
-    link = [nvcc, *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp]
+    # (by its name alone, so that what is linked to it finds the one beside it)
+    link = [nvcc, *ARCH, "-shared", "-cudart", "static", "-Xlinker",
+            "-soname=" + os.path.basename(LIB), *objs, "-o", tmp]
     res = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if res.returncode != 0:
         raise RuntimeError("layoutmove link failed:\n" +

@@ -61,3 +61,24 @@ def test_the_extension_is_linked_again_when_the_library_is_newer():
     os.utime(_build.PYCALL, (0, 0))
     _build.build()
     assert os.path.getmtime(_build.PYCALL) >= os.path.getmtime(_build.LIB)
+
+
+def test_a_moved_tree_uses_its_own_library(tmp_path):
+    """The extension names the library beside it, not the place where it was
+    built: a copy of the package works where the first one is still there, and
+    loads the library once."""
+    import shutil
+    place = tmp_path / "layout_driven_movement_gb300"
+    shutil.copytree(_build.PKG, place,
+                    ignore=shutil.ignore_patterns("_build", "__pycache__"))
+    code = ("import layout_driven_movement_gb300 as lm\n"
+            "lm.lib(); lm._pycall()\n"
+            "print(*sorted({l.split()[-1] for l in open('/proc/self/maps')\n"
+            "               if 'liblayoutmove' in l or '_pycall' in l}),\n"
+            "      sep='\\n')\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=tmp_path,
+                         env={**os.environ, "PYTHONPATH": str(tmp_path)},
+                         capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.split() == sorted(
+        str(place / os.path.basename(f)) for f in (_build.LIB, _build.PYCALL))
