@@ -7,7 +7,8 @@ namespace {
 // --- write -----------------------------------------------------------------
 
 // The scale of a row from the bits of its largest magnitude, and what its
-// elements are multiplied by.  E4M3: 448 = 1.75 * 2^8, so with max|x| =
+// elements are multiplied by (INT8: the last 32-bit number up to 127 / max|x|,
+// the one above it is the next).  E4M3: 448 = 1.75 * 2^8, so with max|x| =
 // m * 2^E, 1 <= m < 2, the smallest e with max|x| <= 448 * 2^e is E - 8 for
 // m <= 1.75 and E - 7 above; 2^-e multiplies exactly.
 template <int STORE>
@@ -28,15 +29,20 @@ __device__ __forceinline__ float row_scale(uint32_t top, float* by) {
   }
   const float m = __uint_as_float(top);
   *by = fminf(__fdiv_rn(127.f, m), 0x1p126f);
+  if (__fmaf_rn(-*by, m, 127.f) < 0)
+    *by = __int_as_float(__float_as_int(*by) - 1);
   return fmaxf(__fdiv_rn(m, 127.f), 0x1p-126f);
 }
 
-// 8 elements' codes.  Whole numbers: with 1.5 * 2^23 added a number's last
-// bit is 1, so it is rounded to a whole one, ties to even, whose low byte is
-// the sum's.
+// 8 elements' codes.  Whole numbers: with 1.5 * 2^23 added a product's last bit
+// is 1, so it is rounded to a whole one, once, whose low byte is the sum's.  An
+// element exactly between two codes (x = max / 2 is one) gets the lower one
+// from the factor up to 127 / max|x| and the upper one from the next, any other
+// the same from both: the even one of the two is the formula's.
 template <int STORE>
 __device__ __forceinline__ uint2 row_codes(const float* x, float by) {
   uint32_t w[2];
+  const float next = __int_as_float(__float_as_int(by) + 1);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (STORE == LM_KV_E4M3) {
@@ -48,13 +54,17 @@ __device__ __forceinline__ uint2 row_codes(const float* x, float by) {
           __NV_E4M3);
       w[i] = a | b << 16;
     } else {
-      uint32_t r[4];
+      auto codes = [&](float f) {
+        uint32_t r[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        r[j] = __float_as_uint(
-            __fadd_rn(__fmul_rn(x[4 * i + j], by), 12582912.f));
-      w[i] = __byte_perm(__byte_perm(r[0], r[1], 0x0040),
-                         __byte_perm(r[2], r[3], 0x0040), 0x5410);
+        for (int j = 0; j < 4; ++j)
+          r[j] = __float_as_uint(__fmaf_rn(x[4 * i + j], f, 12582912.f));
+        return __byte_perm(__byte_perm(r[0], r[1], 0x0040),
+                           __byte_perm(r[2], r[3], 0x0040), 0x5410);
+      };
+      const uint32_t lower = codes(by), upper = codes(next);
+      const uint32_t odd = (upper & 0x01010101u) * 0xffu;
+      w[i] = (lower & odd) | (upper & ~odd);
     }
   }
   return make_uint2(w[0], w[1]);
