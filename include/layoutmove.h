@@ -574,7 +574,8 @@ void lm_tv_plan_destroy(lm_tv_plan* plan);
  * Conventions of this section, besides those above:
  *  - Nothing here allocates; every buffer is the caller's.  Only the calls
  *    that take a cuda_stream enqueue work.
- *  - Arithmetic is in 32 bits whatever the types, each result rounded once.
+ *  - Arithmetic is in 32 bits whatever the types, each result rounded once;
+ *    what the attention holds in fewer is said with it.
  *  - Numbers that only the device holds (positions, slots, page numbers,
  *    lengths) are checked there: one out of range reads and writes nothing
  *    out of bounds, has the effect given with its call, and is recorded for
@@ -723,7 +724,8 @@ int lm_kv_write(const lm_kv_plan* plan, const lm_kv_cache* cache,
 
 /* Enqueue the read back of whole sequences: for sequence b, rows
  * starts[b] .. starts[b] + lens[b] - 1 of k_out and v_out get its tokens
- * 0 .. lens[b] - 1, token j from page page_table[b * table_stride + j / P].
+ * 0 .. lens[b] - 1, token j from page page_table[b * table_stride + j / P]
+ * (table_stride >= max_pages where there is more than one sequence).
  * starts has seqs + 1 entries, none below the one before; lens[b] beyond
  * starts[b + 1] - starts[b] or max_pages * P counts as that much.  rows: the
  * rows of the outputs; output rows that no token names, or from `rows` on,
@@ -757,10 +759,21 @@ int lm_kv_attend_workspace(const lm_kv_plan* plan, int seqs, int heads_q,
  * -infinity.  A page number outside [0, pages) is out of range and its keys
  * are not seen.  lse (NULL: not wanted): seqs x heads_q floats, contiguous.
  * q and out hold the plan's elem; out may be q itself with the same strides.
- * Nothing past a sequence's length is used, whatever it holds.  Scores and
- * sums are in 32 bits; a NaN in a query, key, value or scale that is used
- * comes out as NaN, an infinite value as infinity or NaN.  The same inputs
- * give the same bits.
+ * Nothing past a sequence's length is used, whatever it holds.  A NaN in a
+ * query, key, value or scale that is used comes out as NaN, an infinite value
+ * as infinity or NaN.  The same inputs give the same bits.
+ *
+ * Scores and sums are in 32 bits (2^x and log2 are within a few units in the
+ * last place).  A weight p_j meets its value as two 16-bit parts: 2^-16 of it
+ * is lost for bfloat16 rows and 8-bit codes, 2^-22 for float16 rows (up to
+ * 2^-14 of weights below 2^-15 of the largest).  Weights below 2^-100 of the
+ * largest lose more and below 2^-110 all, for float16 rows below 2^-71.
+ * Finite values give finite results, whatever their size and number, with
+ *  - bfloat16 values below 2^-100 good to 2^-136 a key;
+ *  - scales of values any number of 32 bits, those beside scales 2^95 (E4M3) or
+ *    2^170 (INT8) times their own losing bits;
+ *  - queries of 8-bit caches up to 2^100, elements below 2^-28 of a query
+ *    head's largest good to 2^-39 of that.
  * Errors: LM_E_INVALID (NULL, counts, heads_q not a multiple of the plan's
  * heads or above 2^20, a scale that is not finite, negative window, pointer
  * alignment),

@@ -36,10 +36,10 @@
 // which came last.
 //
 // Measured (bytes that cannot be done without / time): 64 sequences of up to
-// 8192 tokens, 8 key heads x 4 queries x 128 bf16, pages of 16: 246 us, 6.4
-// TB/s; 128 of up to 12288, 8 x 8 x 128 e4m3, pages of 64: 384 us, 6.5 TB/s; 3
+// 8192 tokens, 8 key heads x 4 queries x 128 bf16, pages of 16: 248 us, 6.4
+// TB/s; 128 of up to 12288, 8 x 8 x 128 e4m3, pages of 64: 405 us, 6.1 TB/s; 3
 // of up to 131072, 4 x 5 x 64 int8, pages of 40: 52 us, 2.8 TB/s (its step's
-// instructions are as many for rows half as long); one of 500 tokens: 8.3 us
+// instructions are as many for rows half as long); one of 500 tokens: 8.4 us
 // of latency.
 #pragma once
 
@@ -179,7 +179,7 @@ __device__ __forceinline__ float2 unpair16(uint32_t x) {
 // --- 8-bit codes as 16-bit floats -------------------------------------------
 //
 // Keys become f16, whose 11 bits hold any scaled query (bf16 or f16) they
-// meet; values become bf16, so that weights of any size meet them.
+// meet; values become bf16, so that weights of nearly any size meet them.
 
 // Logic and byte moves run at half the rate of the rest and are what an 8-bit
 // cache spends most of its instructions on, so each form below is the
@@ -220,7 +220,9 @@ struct Codes<KIND_E4M3> {
   // Codes 0x7f and 0xff are not numbers, but become 480 * 2^-120 here, 0x07f0
   // above all others.  So the largest magnitudes' bits of a step are kept,
   // and where one is that, `nans` gives the step's elements again: NaN for
-  // such a code and 0 for any other.
+  // such a code and 0 for any other.  (128 sequences of up to 12288 tokens, 8
+  // x 8 x 128: 389 us without the look, 405 with it; 411 and 425 where twice
+  // the codes as bf16, or their product with 0, show that one is no number.)
   static __device__ __forceinline__ uint32_t nans(uint32_t y) {
     return ((((y & 0x07f007f0u) + 0x00100010u) >> 11) & 0x00010001u) * 0x7fc0u;
   }
@@ -636,8 +638,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     const int steps = int(min(at.left, int64_t(at.hi - at.tile)));
 
     // Codes are met by f16 queries, scaled by a power of two so that the
-    // largest element lies in [2^14, 2^15): exact for bf16 and f16 elements
-    // down to 2^-38 of it.
+    // largest element lies in [2^14, 2^15): exact for bf16 elements down to
+    // 2^-31 of it and f16 ones down to 2^-28, below that within 2^-39 of it.
     float fac[NT][2];
     const float unit = a.scale * 1.44269504088896341f;
 #pragma unroll
