@@ -787,6 +787,136 @@ int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
                  float scale, float* lse, void* workspace,
                  int64_t workspace_bytes, void* cuda_stream);
 
+/* Bytes of the workspace of an lm_kv_attend_weigh that is given weights, over
+ * tables of max_pages pages: lm_kv_attend's, and 4 (max_pages * P + 1) bytes
+ * for every sequence and query head.  Zero it once before its first use, as
+ * lm_kv_attend's, whose calls it serves too.
+ * Errors: LM_E_INVALID, LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_kv_attend_weigh_workspace(const lm_kv_plan* plan, int seqs,
+                                 int heads_q, int64_t max_pages,
+                                 int64_t* bytes);
+
+/* lm_kv_attend with a page table per key head, weights, or both.
+ *
+ * Key head h of sequence b has the pages page_table[b * table_stride + h *
+ * head_stride + i]; head_stride 0: the heads share them.  lens[b] counts the
+ * tokens of every head.
+ *
+ * weights (NULL: none): pages x heads x P floats, tokens fastest, laid out as
+ * a quantised cache's scales are.  To the weight of every token that is seen
+ * is added what the sequence's queries give it, sum over the key head's query
+ * heads of p_j, summed in 32 bits.  A token of a page that several sequences
+ * (or entries of a table) name gets the sum of theirs, added in any order.  A
+ * query head whose scores are all -infinity adds nothing, one whose lse is NaN
+ * or infinite NaN.  weights_capacity: the floats of the buffer.
+ * Errors: as lm_kv_attend, LM_E_CAPACITY also for the weights, LM_E_OVERLAP
+ * also for weights that meet the cache, q, out, lse or the workspace. */
+int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
+                       const lm_rows* q, const lm_rows* out, int seqs,
+                       int heads_q, const int32_t* page_table,
+                       int64_t table_stride, int64_t head_stride,
+                       int64_t max_pages, const int32_t* lens, int64_t window,
+                       float scale, float* lse, float* weights,
+                       int64_t weights_capacity, void* workspace,
+                       int64_t workspace_bytes, void* cuda_stream);
+
+/* The bounds of a cache's pages: for each page and key head the least and the
+ * largest element d of its keys, as whole numbers under one power of two.
+ * data: pages x heads x 2 x dim bytes (16-byte aligned), lo then hi; scale:
+ * pages x heads floats.  With top the largest magnitude of the keys (as a read
+ * back into 32 bits gives them), scale is the smallest power of two 2^e, e >=
+ * -126, with top / 2^e <= 127, and the bytes are floor(lo / 2^e) and ceil(hi /
+ * 2^e).  Keys of zeros, or none: zeros under the scale 1.  A key with an
+ * infinity or a NaN: zeros under the scale NaN.  The capacities count bytes
+ * and floats. */
+typedef struct lm_kv_bounds {
+  int8_t* data;
+  float* scale;
+  int64_t capacity;
+  int64_t scale_capacity;
+} lm_kv_bounds;
+
+/* Enqueue the bounds of pages[i] for i in [0, n), from its first counts[i]
+ * tokens (clipped to [0, P]): of all pages after a prefill, of the page that a
+ * step has written to after each step.  The pages of a call are distinct; a
+ * negative one is skipped, one past the last is out of range and skipped too.
+ * Errors: LM_E_INVALID (NULL, n < 0, pointer alignment), LM_E_CAPACITY,
+ * LM_E_OVERLAP (the bounds with each other, with the cache or its scales, with
+ * pages or counts), LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_kv_bound(const lm_kv_plan* plan, const lm_kv_cache* cache,
+                const int32_t* pages, const int32_t* counts, int64_t n,
+                const lm_kv_bounds* bounds, void* cuda_stream);
+
+/* Bytes of lm_kv_select's workspace: a score per sequence, key head and page
+ * of a table.  It needs no zeros.
+ * Errors: LM_E_INVALID, LM_E_OVERFLOW. */
+int lm_kv_select_workspace(const lm_kv_plan* plan, int seqs,
+                           int64_t max_pages, int64_t* bytes);
+
+/* Enqueue the choice of the pages that each sequence's new token attends over:
+ * for each key head h of sequence b, `keep` of its n = ceil(lens[b] / P) pages
+ * (lens[b] clipped to [0, max_pages * P]), in their order, to selected[(b *
+ * heads + h) * keep ...], and the number of their tokens, the same for all
+ * heads, to selected_lens[b]: the page table and lengths of an
+ * lm_kv_attend_weigh with table_stride heads * keep and head_stride keep.
+ * Entries past the last page are -1.  All are chosen where n <= keep.
+ * Otherwise the `first` first and `last` last ones are (last >= 1, so that a
+ * page that is not full stays the last; first + last <= keep), and those of the
+ * rest with the largest scores, the earlier ones of equals:
+ *   score = max_g 2^e_g sum_d (c_gd > 0 ? c_gd hi_d : c_gd lo_d) * scale
+ * over the key head's query heads g, with c_g = rint(q_g / 2^e_g), ties to
+ * even, 2^e_g the smallest power of two, e_g >= -126, with max|q_g| / 2^e_g <=
+ * 127 (1 for a query of zeros) and the page's bounds.  Up to the rounding of
+ * the query, at most half of 2^e_g an element, that is no less than its
+ * product with any key of the page.  The sums are exact, the powers multiply
+ * in 32 bits, in the order written.  A NaN (of a query, or of a page's scale)
+ * counts as the largest score of all; a page number outside [0, pages) is out
+ * of range and has the lowest.
+ * pages: those that the bounds hold.  The queries' type is the plan's elem.
+ * Errors: LM_E_INVALID (NULL, counts, pointer alignment), LM_E_CAPACITY,
+ * LM_E_OVERLAP (selected, selected_lens or the workspace with each other or an
+ * input), LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_kv_select(const lm_kv_plan* plan, int64_t pages,
+                 const lm_kv_bounds* bounds, const lm_rows* q, int seqs,
+                 int heads_q, const int32_t* page_table, int64_t table_stride,
+                 int64_t max_pages, const int32_t* lens, int keep, int first,
+                 int last, int32_t* selected, int32_t* selected_lens,
+                 void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
+/* Bytes of lm_kv_evict's workspace: a token's number per sequence, key head
+ * and kept token.  It needs no zeros.
+ * Errors: LM_E_INVALID, LM_E_OVERFLOW. */
+int lm_kv_evict_workspace(const lm_kv_plan* plan, int seqs, int keep,
+                          int64_t* bytes);
+
+/* Enqueue the eviction of tokens by weight.  Of a sequence of n = lens[b]
+ * tokens (clipped to [0, max_pages * P]), each key head keeps all if n <=
+ * keep, else the `recent` last ones and the keep - recent others with the
+ * largest weights (laid out as lm_kv_attend_weigh's), the earlier ones of
+ * equals; -0 equals 0, and a NaN is above all.  The kept tokens' keys, values,
+ * scales and weights go to the slots 0, 1, ... of the pages of kept_table, in
+ * their order, and kept_lens[b] is their number.  kept_table may be the page
+ * table itself (the sequence goes on in its own first pages) or name other
+ * pages; page i of a sequence is its own page i in page_table or one that
+ * page_table does not name anywhere, and no page is named for two sequences
+ * in kept_table, or written for one and read for another.  kept_lens may be
+ * lens itself.  What is not written to is left as it is.  A page number
+ * outside [0, pages) is out of range: a token there weighs least, and a row
+ * from or to there is not moved.
+ * kept_pages: the pages of a row of kept_table, enough for min(keep, max_pages
+ * * P) tokens.
+ * Errors: LM_E_INVALID (NULL, counts, recent > keep, pointer alignment),
+ * LM_E_CAPACITY, LM_E_OVERLAP (weights, kept_lens or the workspace with each
+ * other, the cache, its scales, a table or, kept_lens apart, lens),
+ * LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_kv_evict(const lm_kv_plan* plan, const lm_kv_cache* cache,
+                float* weights, int64_t weights_capacity,
+                const int32_t* page_table, int64_t table_stride, int seqs,
+                int64_t max_pages, const int32_t* lens,
+                const int32_t* kept_table, int64_t kept_stride,
+                int64_t kept_pages, int32_t* kept_lens, int keep, int recent,
+                void* workspace, int64_t workspace_bytes, void* cuda_stream);
+
 void lm_kv_plan_destroy(lm_kv_plan* plan);
 
 /* Static, NUL-terminated name of a status code. */

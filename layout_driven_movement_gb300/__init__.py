@@ -52,6 +52,11 @@ class _KVCache(C.Structure):
                 ("scale_capacity", C.c_int64), ("pages", C.c_int64)]
 
 
+class _KVBounds(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("scale", C.c_void_p),
+                ("capacity", C.c_int64), ("scale_capacity", C.c_int64)]
+
+
 # (name, restype, argtypes) of every function include/layoutmove.h declares
 _P = C.c_void_p
 _I64 = C.c_int64
@@ -138,6 +143,22 @@ SIGNATURES = [
     ("lm_kv_attend", C.c_int,
      [_P, C.POINTER(_KVCache), C.POINTER(_Rows), C.POINTER(_Rows), C.c_int,
       C.c_int, _P, _I64, _I64, _P, _I64, C.c_float, _P, _P, _I64, _P]),
+    ("lm_kv_attend_weigh_workspace", C.c_int,
+     [_P, C.c_int, C.c_int, _I64, _I64P]),
+    ("lm_kv_attend_weigh", C.c_int,
+     [_P, C.POINTER(_KVCache), C.POINTER(_Rows), C.POINTER(_Rows), C.c_int,
+      C.c_int, _P, _I64, _I64, _I64, _P, _I64, C.c_float, _P, _P, _I64, _P,
+      _I64, _P]),
+    ("lm_kv_bound", C.c_int,
+     [_P, C.POINTER(_KVCache), _P, _P, _I64, C.POINTER(_KVBounds), _P]),
+    ("lm_kv_select_workspace", C.c_int, [_P, C.c_int, _I64, _I64P]),
+    ("lm_kv_select", C.c_int,
+     [_P, _I64, C.POINTER(_KVBounds), C.POINTER(_Rows), C.c_int, C.c_int, _P,
+      _I64, _I64, _P, C.c_int, C.c_int, C.c_int, _P, _P, _P, _I64, _P]),
+    ("lm_kv_evict_workspace", C.c_int, [_P, C.c_int, C.c_int, _I64P]),
+    ("lm_kv_evict", C.c_int,
+     [_P, C.POINTER(_KVCache), _P, _I64, _P, _I64, C.c_int, _I64, _P, _P,
+      _I64, _I64, _P, C.c_int, C.c_int, _P, _I64, _P]),
     ("lm_kv_plan_destroy", None, [_P]),
     ("lm_status_string", C.c_char_p, [C.c_int]),
     ("lm_last_cuda_error", C.c_int, []),
@@ -997,27 +1018,102 @@ def kv_read(cache: KVCache, page_table, lens, starts, k_out, v_out,
         _check(rc, "lm_kv_read")
 
 
-def kv_attend_workspace(plan: KVPlan, seqs: int, heads_q: int) -> int:
+def kv_attend_workspace(plan: KVPlan, seqs: int, heads_q: int,
+                        max_pages: int | None = None) -> int:
     """Bytes of kv_attend's workspace on the current device; zero the buffer
-    once before its first use (see lm_kv_attend_workspace)."""
+    once before its first use (see lm_kv_attend_workspace).  With ``max_pages``
+    (of a sequence in the page table): those of a call that is given weights,
+    which serve any other call too."""
     v = C.c_int64()
-    _check(lib().lm_kv_attend_workspace(plan._h, int(seqs), int(heads_q),
-                                        C.byref(v)), "lm_kv_attend_workspace")
+    if max_pages is None:
+        _check(lib().lm_kv_attend_workspace(plan._h, int(seqs), int(heads_q),
+                                            C.byref(v)),
+               "lm_kv_attend_workspace")
+    else:
+        _check(lib().lm_kv_attend_weigh_workspace(
+            plan._h, int(seqs), int(heads_q), int(max_pages), C.byref(v)),
+            "lm_kv_attend_weigh_workspace")
     return v.value
 
 
 def kv_attend(cache: KVCache, q, page_table, lens, out, workspace=None,
               lse=None, scale: float | None = None, window: int = 0,
-              stream=None) -> None:
+              stream=None, weights=None) -> None:
     """Enqueue the attention of one new token per sequence, q and out
     [sequences, query heads, dim], over the first lens[b] tokens of its pages
     (the last ``window`` of them if given); lse (optional) float32
     [sequences, query heads].  scale defaults to dim ** -0.5 (see
-    lm_kv_attend)."""
+    lm_kv_attend).  page_table int32 [sequences, pages], or [sequences, key
+    heads, pages] for pages of each head's own; weights (optional) float32
+    [pages, key heads, page_tokens]: the weight of each token is added to its
+    entry (see lm_kv_attend_weigh)."""
     p = cache.plan
-    rc = _pycall().kv_attend(p._p, cache._p, p.dim, p.elem, q, page_table,
-                             lens, out, workspace, lse,
+    rc = _pycall().kv_attend(p._p, cache._p, p.heads, p.dim, p.elem, q,
+                             page_table, lens, out, workspace, lse,
                              p.dim ** -0.5 if scale is None else scale,
-                             window, _stream(stream))
+                             window, weights, _stream(stream))
     if rc:
-        _check(rc, "lm_kv_attend")
+        _check(rc, "lm_kv_attend_weigh" if weights is not None
+               or page_table.dim() == 3 else "lm_kv_attend")
+
+
+def kv_bound(cache: KVCache, pages, counts, bounds, bound_scale,
+             stream=None) -> None:
+    """Enqueue the bounds of the keys in the first counts[i] tokens of
+    pages[i] (both int32 [n]) into bounds int8 [pages, key heads, 2, dim] and
+    bound_scale float32 [pages, key heads] (see lm_kv_bound)."""
+    p = cache.plan
+    rc = _pycall().kv_bound(p._p, cache._p, p.heads, p.dim, pages, counts,
+                            bounds, bound_scale, _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_bound")
+
+
+def kv_select_workspace(plan: KVPlan, seqs: int, max_pages: int) -> int:
+    """Bytes of kv_select's workspace for page tables [seqs, max_pages]."""
+    v = C.c_int64()
+    _check(lib().lm_kv_select_workspace(plan._h, int(seqs), int(max_pages),
+                                        C.byref(v)), "lm_kv_select_workspace")
+    return v.value
+
+
+def kv_select(cache: KVCache, q, bounds, bound_scale, page_table, lens,
+              selected, selected_lens, workspace, first: int = 0,
+              last: int = 1, stream=None) -> None:
+    """Enqueue the choice of the pages that each sequence's new token, q
+    [sequences, query heads, dim], attends over: the ``first`` first and
+    ``last`` last ones and those whose bounds promise the largest products,
+    as many as selected, int32 [sequences, key heads, pages], has room for;
+    selected_lens int32 [sequences] their tokens.  The two are a kv_attend's
+    page_table and lens (see lm_kv_select)."""
+    p = cache.plan
+    rc = _pycall().kv_select(p._p, p.heads, p.dim, p.elem, q, bounds,
+                             bound_scale, page_table, lens, selected,
+                             selected_lens, workspace, first, last,
+                             _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_select")
+
+
+def kv_evict_workspace(plan: KVPlan, seqs: int, keep: int) -> int:
+    """Bytes of kv_evict's workspace."""
+    v = C.c_int64()
+    _check(lib().lm_kv_evict_workspace(plan._h, int(seqs), int(keep),
+                                       C.byref(v)), "lm_kv_evict_workspace")
+    return v.value
+
+
+def kv_evict(cache: KVCache, weights, page_table, lens, kept_table, kept_lens,
+             keep: int, workspace, recent: int = 0, stream=None) -> None:
+    """Enqueue the eviction of all but ``keep`` tokens of every sequence and
+    key head: the ``recent`` last ones stay, and of the others those with the
+    largest weights, float32 [pages, key heads, page_tokens].  Rows, scales and
+    weights of the kept ones move up into the pages of kept_table, int32
+    [sequences, pages], which may be page_table; kept_lens int32 [sequences],
+    which may be lens, gets their number (see lm_kv_evict)."""
+    p = cache.plan
+    rc = _pycall().kv_evict(p._p, cache._p, weights, page_table, lens,
+                            kept_table, kept_lens, keep, recent, workspace,
+                            _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_evict")

@@ -328,7 +328,9 @@ __device__ __forceinline__ void attend_next(const KvAttendArgs& a, int items,
 
 // --- the kernel ----------------------------------------------------------------
 
-template <int KIND, int D, int NT, int HP>
+// SC: the scores are wanted (a form of its own: the branch alone made the 256
+// element kernel spill).
+template <int KIND, int D, int NT, int HP, bool SC>
 __global__ void
 __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     lm_kv_attend_kernel(const __grid_constant__ KvAttendArgs a,
@@ -486,6 +488,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       if (ld.left > 0 && (g.shared_page || KW >= 32 || lane < KW) &&
           key + reach > ld.first && key < ld.n && (i == 0 || !g.shared_page))
         pg->of[i] = a.table[int64_t(ld.b) * a.table_stride +
+                            int64_t(ld.item / g.groups * HP + sub) *
+                                a.table_head +
                             fdiv(uint32_t(key), a.c.page_div)];
       if (i && g.shared_page) pg->of[i] = pg->of[0];
     }
@@ -621,12 +625,19 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     if (s.hi > s.lo) continue;
     for (int e = threadIdx.x; e < a.heads_q * dim; e += kAttendThreads) {
       const int qi = e / dim, d = e - qi * dim;
-      reinterpret_cast<uint16_t*>(a.out.p)[int64_t(b) * a.out.ts +
-                                           int64_t(qi) * a.out.hs + d] = 0;
+      if (a.mean)
+        a.mean[int64_t(b) * a.heads_q * dim + e] = 0;
+      else
+        reinterpret_cast<uint16_t*>(a.out.p)[int64_t(b) * a.out.ts +
+                                             int64_t(qi) * a.out.hs + d] = 0;
     }
-    if (a.lse)
-      for (int qi = threadIdx.x; qi < a.heads_q; qi += kAttendThreads)
-        a.lse[int64_t(b) * a.heads_q + qi] = -INFINITY;
+    for (int qi = threadIdx.x; qi < a.heads_q; qi += kAttendThreads) {
+      const int64_t row = int64_t(b) * a.heads_q + qi;
+      if (a.state)
+        reinterpret_cast<float2*>(a.state)[row] = make_float2(-INFINITY, 0);
+      if (a.lse) a.lse[row] = -INFINITY;
+      if (a.lse2) a.lse2[row] = -INFINITY;
+    }
   }
 
   int stage = 0;
@@ -793,6 +804,34 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
               for (int nt = 0; nt < NT; ++nt)
                 s[mt][nt][2 * r] = s[mt][nt][2 * r + 1] = -INFINITY;
             }
+      }
+      // the scores themselves, where the weights are wanted (the launch that
+      // turns them into weights reads those of keys that are seen)
+      if constexpr (SC) {
+        const int key0 = (at.tile + step) * TK + wk * KW + row8;
+        float* const to =
+            a.scores + (int64_t(at.b) * a.c.heads + hp * HP + sub) *
+                           a.max_tokens * a.group;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int key = key0 + mt * 16 + 8 * r;
+            if (key >= at.n) continue;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int qi = q0 + nt * 8 + col2;
+              float* const p = to + int64_t(key) * a.group + qi;
+              if (a.group % 2 == 0) {
+                if (qi < a.group)
+                  *reinterpret_cast<float2*>(p) =
+                      make_float2(s[mt][nt][2 * r], s[mt][nt][2 * r + 1]);
+              } else {
+                if (qi < a.group) p[0] = s[mt][nt][2 * r];
+                if (qi + 1 < a.group) p[1] = s[mt][nt][2 * r + 1];
+              }
+            }
+          }
       }
       float top[NT][2];
 #pragma unroll
@@ -1130,6 +1169,10 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       return (hp * HP + i) * a.group + q0 + qi;
     };
     auto put = [&](int i, int qi, int d, float x) {
+      if (a.mean) {
+        a.mean[(int64_t(done.b) * a.heads_q + row_of(i, qi)) * dim + d] = x;
+        return;
+      }
       char* to = a.out.p + (int64_t(done.b) * a.out.ts +
                             int64_t(row_of(i, qi)) * a.out.hs + d) * 2;
       if (out_bf)
@@ -1138,10 +1181,13 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
         *reinterpret_cast<__half*>(to) = from_f32<__half>(x);
     };
     auto put_lse = [&](int i, int qi, float t, float sum) {
-      if (a.lse)
-        a.lse[int64_t(done.b) * a.heads_q + row_of(i, qi)] =
-            sum == 0 ? -INFINITY
-                     : (t + log2f(sum)) * 0.693147180559945309f;
+      const int64_t row = int64_t(done.b) * a.heads_q + row_of(i, qi);
+      if (a.state)
+        reinterpret_cast<float2*>(a.state)[row] = make_float2(t, sum);
+      if (!a.lse && !a.lse2) return;
+      const float lse2 = sum == 0 ? -INFINITY : t + log2f(sum);
+      if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;
+      if (a.lse2) a.lse2[row] = lse2;
     };
     for (int i = 0; i < HP; ++i)
       for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {
@@ -1324,13 +1370,13 @@ inline AttendSpace attend_space(int64_t sms, int64_t blocks, int64_t floats) {
   return s;
 }
 
-template <int KIND, int D, int NT, int HP>
-int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
+template <int KIND, int D, int NT, int HP, bool SC>
+int launch_attend_sc(const KvAttendArgs& a, cudaStream_t st) {
   using S = AttendShape<KIND, D, NT, HP>;
   int sms = 0, dev = 0;
   const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  auto* kernel = lm_kv_attend_kernel<KIND, D, NT, HP>;
+  auto* kernel = lm_kv_attend_kernel<KIND, D, NT, HP, SC>;
   static std::atomic<uint64_t> allowed{0};    // a bit per device
   if (!(allowed.load() >> dev & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -1356,6 +1402,12 @@ int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
   g.parts = reinterpret_cast<float*>(ws + at.parts);
   g.runs = reinterpret_cast<float*>(ws + at.runs);
   return launch(kernel, blocks, kAttendThreads, S::kSmem, st, a, g);
+}
+
+template <int KIND, int D, int NT, int HP>
+int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
+  return a.scores ? launch_attend_sc<KIND, D, NT, HP, true>(a, st)
+                  : launch_attend_sc<KIND, D, NT, HP, false>(a, st);
 }
 
 template <int KIND, int D>

@@ -272,29 +272,6 @@ int launch_write_t(const KvWriteArgs& a, int store, cudaStream_t st) {
 
 // --- read ------------------------------------------------------------------
 
-// 16 held bytes as 32-bit values: 16 codes times their scale, or 8 elements.
-template <class T, int STORE>
-__device__ __forceinline__ void held_values(const uint4& w, float scale,
-                                            float* x) {
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-  if (STORE == LM_KV_SAME) {
-    get_words<T, 4>(r, x);
-  } else if (STORE == LM_KV_E4M3) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2(
-          __nv_fp8x2_storage_t(r[i / 2] >> (16 * (i & 1))), __NV_E4M3));
-      const float2 f = __half22float2(h);
-      x[2 * i] = f.x * scale;
-      x[2 * i + 1] = f.y * scale;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      x[i] = float(int8_t(r[i / 4] >> (8 * (i & 3)))) * scale;
-  }
-}
-
 constexpr int kReadTokens = 32;   // tokens of a block at most
 constexpr int kReadThreads = 128;
 constexpr int kReadUnits = 2;     // 16-byte loads of a thread in flight

@@ -96,6 +96,15 @@ struct KvAttendArgs {
   float* lse = nullptr;
   void* ws = nullptr;
   unsigned int* status = nullptr;
+  // elements of the page table from one key head's pages to the next one's
+  // (0: the heads share them)
+  int64_t table_head = 0;
+  // where set: the scores in units of ln 2, [seqs, key heads, max_tokens,
+  // group], and the logarithms of their sums to base 2, [seqs, heads_q]
+  float *scores = nullptr, *lse2 = nullptr;
+  // where set: the state (m, l) and the mean of each row in 32 bits, [seqs,
+  // heads_q] and [seqs, heads_q, dim], in the output's place
+  float *state = nullptr, *mean = nullptr;
 };
 
 int launch_rope(const RopeArgs& a, int elem, void* stream);

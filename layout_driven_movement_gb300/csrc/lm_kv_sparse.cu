@@ -1,0 +1,387 @@
+// Which pages a sparse attention reads: the bounds of a page's keys, and the
+// choice of the pages whose bounds promise the largest products.
+//
+// For a page and key head, lo_d and hi_d are the least and the largest element
+// d of its keys.  sum_d (c_d > 0 ? c_d hi_d : c_d lo_d) is no less than the
+// product of c with any of them, so it ranks pages without their keys: 2 dim bytes for a
+// page of P keys of 2 dim bytes each.  Bounds are held as whole numbers, lo
+// rounded down and hi up, under a power of two, and the query as whole numbers
+// under one of its own: products and their sums are whole numbers below 2^24,
+// the same in any order and in 32-bit floats, so that ties are ties and the
+// choice depends on nothing but the inputs.
+#include "lm_kv_long.h"
+#include "lm_kv_top.cuh"
+#include "lm_line.cuh"
+
+namespace lm {
+namespace {
+
+// The exponent e >= -126 of the smallest power of two with top / 2^e <= 127 =
+// 1.984375 * 2^6, from the bits of a finite top > 0.
+__device__ __forceinline__ int power_of(uint32_t top) {
+  const int e =
+      int(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x7e0000u ? 6 : 5);
+  return max(e, -126);
+}
+__device__ __forceinline__ float pow2f(int e) {
+  return __int_as_float((127 + e) << 23);
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// --- bounds ----------------------------------------------------------------
+
+constexpr int kBoundThreads = 128;
+
+// A warp has one page and head: L lanes hold a row in 16-byte chunks, 32 / L
+// of them take turns with the tokens, kAhead loads each in flight.
+template <class T, int STORE, int L>
+__global__ void __launch_bounds__(kBoundThreads)
+    lm_kv_bound_kernel(const __grid_constant__ KvBoundArgs a) {
+  constexpr int N = STORE == LM_KV_SAME ? 8 : 16;   // elements of a chunk
+  constexpr int TL = 32 / L;                        // tokens at once
+  constexpr int kAhead = 8;
+  stream_order();
+  const int lane = threadIdx.x % 32, c = lane % L, t0 = lane / L;
+  const uint32_t unit =
+      blockIdx.x * (kBoundThreads / 32) + threadIdx.x / 32;
+  const uint32_t i = fdiv(unit, a.heads_div), h = unit - i * a.c.heads;
+  if (i >= a.n) return;
+  const int64_t page = a.pages[i];
+  if (page < 0 || page >= a.c.pages) {
+    if (page >= 0 && lane == 0 && a.status) atomicOr(a.status, kStatusRange);
+    return;
+  }
+  const int count = min(max(a.counts[i], 0), int(a.c.page_tokens));
+  const bool has = c * N < a.c.dim;
+  const char* src = a.c.k + page * a.c.page_b + int64_t(h) * a.c.head_b +
+                    int64_t(t0) * a.c.token_b + c * 16;
+  const float* scales =
+      a.c.ks + (page * a.c.heads + h) * a.c.page_tokens + t0;
+  float lo[N], hi[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    lo[e] = INFINITY;
+    hi[e] = -INFINITY;
+  }
+  if (has)
+    for (int t = t0; t < count; t += TL * kAhead) {
+      uint4 w[kAhead];
+      float scale[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        scale[k] = 1;
+        if (t + k * TL >= count) continue;
+        w[k] = *reinterpret_cast<const uint4*>(
+            src + int64_t(t - t0 + k * TL) * a.c.token_b);
+        if (STORE != LM_KV_SAME) scale[k] = scales[t - t0 + k * TL];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (t + k * TL >= count) continue;
+        float x[N];
+        held_values<T, STORE>(w[k], scale[k], x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          lo[e] = min_nan(lo[e], x[e]);
+          hi[e] = max_nan(hi[e], x[e]);
+        }
+      }
+    }
+  float top = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+#pragma unroll
+    for (int k = L; k < 32; k *= 2) {
+      lo[e] = min_nan(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], k));
+      hi[e] = max_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], k));
+    }
+    if (has) top = max_nan(top, max_nan(fabsf(lo[e]), fabsf(hi[e])));
+  }
+#pragma unroll
+  for (int k = 1; k < L; k *= 2)
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
+  // no tokens, or nothing but zeros; a key that is no number, or infinite
+  float scale = 1, by = 0;
+  if (count == 0) {
+    top = 0;
+  } else if (!(top < INFINITY)) {
+    scale = __int_as_float(0x7fc00000);
+  } else if (top > 0) {
+    const int e = power_of(__float_as_uint(top));
+    scale = pow2f(e);
+    by = pow2f(-e);
+  }
+  if (!has || t0 > 0) return;
+  const bool zero = by == 0;
+  int8_t* to = a.bounds + (page * a.c.heads + h) * 2 * a.c.dim + c * N;
+  uint32_t y[2][N / 4];
+#pragma unroll
+  for (int e = 0; e < N; e += 4) {
+    uint32_t l = 0, u = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int f = zero ? 0 : __float2int_rd(lo[e + k] * by);
+      const int g = zero ? 0 : __float2int_ru(hi[e + k] * by);
+      l |= uint32_t(f & 0xff) << (8 * k);
+      u |= uint32_t(g & 0xff) << (8 * k);
+    }
+    y[0][e / 4] = l;
+    y[1][e / 4] = u;
+  }
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int e = 0; e < N / 4; e += 2)
+      *reinterpret_cast<uint2*>(to + side * a.c.dim + e * 4) =
+          make_uint2(y[side][e], y[side][e + 1]);
+  if (c == 0) a.scale[page * a.c.heads + h] = scale;
+}
+
+// --- scores ----------------------------------------------------------------
+
+constexpr int kScoreThreads = 256;
+constexpr int kScorePages = 32;      // of a warp's unit
+
+// A unit is kScorePages pages of one sequence and head.  L lanes of 8 elements
+// hold a row, 32 / L pages at a time: a query's positive and negative parts
+// meet hi and lo in four 4-way byte products, and the sums of up to 8 queries
+// over the L lanes are added up by halving: each exchange leaves a lane half
+// the queries, until each has one.
+template <class T, int L, int GQ>
+__global__ void __launch_bounds__(kScoreThreads)
+    lm_kv_score_kernel(const __grid_constant__ KvSelectArgs a) {
+  constexpr int PW = 32 / L;
+  stream_order();
+  auto pages_of = [&](int b) {
+    const int64_t most = a.max_pages * a.page_tokens;
+    int64_t n = a.lens[b];
+    n = n < 0 ? 0 : n > most ? most : n;
+    return int((n + a.page_tokens - 1) / a.page_tokens);
+  };
+  // a sequence that keeps all of its pages needs no scores
+  auto tiles_of = [&](int b) {
+    const int n = pages_of(b);
+    return n <= a.keep ? 0 : (n + kScorePages - 1) / kScorePages;
+  };
+  LineShare at = line_share<kScoreThreads>(
+      a.seqs, blockIdx.x, gridDim.x,
+      [&](int b) { return int64_t(tiles_of(b)) * a.heads; });
+  if (at.left <= 0) return;
+  const int lane = threadIdx.x % 32, c = lane % L, pw = lane / L;
+  const bool has = c * 8 < a.dim;
+  const int warp = threadIdx.x / 32;
+  // this warp's units: every eighth of the block's
+  int tiles = tiles_of(at.b);
+  at.in += warp;
+  at.left -= warp;
+  for (; at.left > 0; at.left -= kScoreThreads / 32) {
+    while (at.in >= int64_t(tiles) * a.heads) {
+      at.in -= int64_t(tiles) * a.heads;
+      tiles = tiles_of(++at.b);
+    }
+    // the heads of a tile of pages one after the other: their bounds are
+    const int tile = int(small_div(at.in, a.heads));
+    const uint32_t h = uint32_t(at.in - int64_t(tile) * a.heads);
+    at.in += kScoreThreads / 32;
+    const int p0 = tile * kScorePages, pages = pages_of(at.b);
+    const int p1 = min(pages, p0 + kScorePages);
+    const int mine = p0 + lane < p1
+                         ? a.table[at.b * a.table_stride + p0 + lane]
+                         : -1;
+    float best = -INFINITY;            // of page p0 + lane
+    for (int g0 = 0; g0 < a.group; g0 += GQ) {
+      // the queries as whole numbers
+      uint32_t qp[GQ][2], qn[GQ][2];
+      float qs[GQ];
+#pragma unroll
+      for (int g = 0; g < GQ; ++g) {
+        float x[8] = {};
+        if (has && g0 + g < a.group) {
+          const T* q = reinterpret_cast<const T*>(a.q.p) +
+                       int64_t(at.b) * a.q.ts +
+                       int64_t(h * a.group + g0 + g) * a.q.hs + c * 8;
+          if (a.q16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(q);
+            const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+            get_words<T, 4>(r, x);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = to_f32(q[e]);
+          }
+        }
+        float top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
+#pragma unroll
+        for (int k = 1; k < L; k *= 2)
+          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
+        float by = 0;
+        qs[g] = 1;
+        if (!(top < INFINITY)) {
+          qs[g] = __int_as_float(0x7fc00000);
+        } else if (top > 0) {
+          const int e = power_of(__float_as_uint(top));
+          qs[g] = pow2f(e);
+          by = pow2f(-e);
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          qp[g][w] = qn[g][w] = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int v = by == 0 ? 0 : __float2int_rn(x[4 * w + k] * by);
+            qp[g][w] |= uint32_t(max(v, 0)) << (8 * k);
+            qn[g][w] |= uint32_t(min(v, 0) & 0xff) << (8 * k);
+          }
+        }
+      }
+      for (int p = 0; p < p1 - p0; p += PW) {
+        const int64_t page = __shfl_sync(0xffffffffu, mine, (p + pw) & 31);
+        const bool ok = page >= 0 && page < a.pages;
+        uint2 lo = make_uint2(0, 0), hi = lo;
+        float scale = 0;
+        if (ok) {
+          const int8_t* from = a.bounds + (page * a.heads + h) * 2 * a.dim;
+          if (has) {
+            lo = *reinterpret_cast<const uint2*>(from + c * 8);
+            hi = *reinterpret_cast<const uint2*>(from + a.dim + c * 8);
+          }
+          scale = a.bound_scale[page * a.heads + h];
+        }
+        float score = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < GQ; ++g) {
+          int s = __dp4a(int(qp[g][0]), int(hi.x), 0);
+          s = __dp4a(int(qp[g][1]), int(hi.y), s);
+          s = __dp4a(int(qn[g][0]), int(lo.x), s);
+          s = __dp4a(int(qn[g][1]), int(lo.y), s);
+#pragma unroll
+          for (int k = 1; k < L; k *= 2)
+            s += __shfl_xor_sync(0xffffffffu, s, k);
+          if (g0 + g < a.group) score = max_nan(score, float(s) * qs[g]);
+        }
+        score *= scale;
+        if (!ok) score = -INFINITY;
+        // to the lane that has the page
+        const float got =
+            __shfl_sync(0xffffffffu, score, (lane - p) * L & 31);
+        if (lane >= p && lane < p + PW) best = max_nan(best, got);
+      }
+    }
+    if (p0 + lane < p1) {
+      if ((mine < 0 || mine >= a.pages) && h == 0 && a.status)
+        atomicOr(a.status, kStatusRange);
+      a.scores[(int64_t(at.b) * a.heads + h) * a.max_pages + p0 + lane] = best;
+    }
+  }
+}
+
+// --- the choice --------------------------------------------------------------
+
+// A cluster of C blocks has one sequence and head.
+template <int T, int C>
+__global__ void __launch_bounds__(T)
+    lm_kv_select_kernel(const __grid_constant__ KvSelectArgs a, int cap) {
+  extern __shared__ uint32_t cache[];
+  __shared__ TopSpace<T> sh;
+  stream_order();
+  const int unit = blockIdx.x / C, rank = blockIdx.x % C;
+  const int b = unit / int(a.heads), h = unit - b * int(a.heads);
+  const int64_t most = a.max_pages * a.page_tokens;
+  int64_t len = a.lens[b];
+  len = len < 0 ? 0 : len > most ? most : len;
+  const int n = int((len + a.page_tokens - 1) / a.page_tokens);
+  const int count = min(n, a.keep);
+  const int32_t* table = a.table + b * a.table_stride;
+  int32_t* to = a.selected + int64_t(unit) * a.keep;
+  if (h == 0 && rank == 0 && threadIdx.x == 0)
+    a.selected_lens[b] =
+        int32_t(len - int64_t(n - count) * a.page_tokens);
+  const int threads = T * C, me = rank * T + int(threadIdx.x);
+  for (int i = count + me; i < a.keep; i += threads) to[i] = -1;
+  if (n <= a.keep) {
+    for (int i = me; i < n; i += threads) to[i] = table[i];
+    return;
+  }
+  for (int i = me; i < a.first; i += threads) to[i] = table[i];
+  for (int i = me; i < a.last; i += threads)
+    to[a.keep - a.last + i] = table[n - a.last + i];
+  const int need = a.keep - a.first - a.last;
+  if (need == 0) return;
+  const float* scores =
+      a.scores + (int64_t(b) * a.heads + h) * a.max_pages + a.first;
+  take_top<T, C>(
+      n - a.first - a.last, need, cache, cap, &sh,
+      [&](int i) { return order_of(scores[i]); },
+      [&](int place, int i) {
+        to[a.first + place] = table[a.first + i];
+      });
+}
+
+template <class T, int L>
+int launch_score_l(const KvSelectArgs& a, uint64_t grid, cudaStream_t st) {
+  if (a.group == 1)
+    return launch(lm_kv_score_kernel<T, L, 1>, grid, kScoreThreads, 0, st, a);
+  if (a.group == 2)
+    return launch(lm_kv_score_kernel<T, L, 2>, grid, kScoreThreads, 0, st, a);
+  if (a.group <= 4)
+    return launch(lm_kv_score_kernel<T, L, 4>, grid, kScoreThreads, 0, st, a);
+  return launch(lm_kv_score_kernel<T, L, 8>, grid, kScoreThreads, 0, st, a);
+}
+
+template <class T>
+int launch_score(const KvSelectArgs& a, int sms, cudaStream_t st) {
+  const uint64_t grid = uint64_t(sms) * 4;
+  if (a.dim <= 64) return launch_score_l<T, 8>(a, grid, st);
+  if (a.dim <= 128) return launch_score_l<T, 16>(a, grid, st);
+  return launch_score_l<T, 32>(a, grid, st);
+}
+
+template <class T, int STORE>
+int launch_bound_s(const KvBoundArgs& a, cudaStream_t st) {
+  const uint64_t units = uint64_t(a.n) * a.c.heads;
+  const uint64_t grid = (units + kBoundThreads / 32 - 1) / (kBoundThreads / 32);
+  const int bytes = a.c.dim * (STORE == LM_KV_SAME ? 2 : 1);
+  if (bytes <= 128)
+    return launch(lm_kv_bound_kernel<T, STORE, 8>, grid, kBoundThreads, 0, st, a);
+  if (bytes <= 256)
+    return launch(lm_kv_bound_kernel<T, STORE, 16>, grid, kBoundThreads, 0, st, a);
+  return launch(lm_kv_bound_kernel<T, STORE, 32>, grid, kBoundThreads, 0, st, a);
+}
+
+}  // namespace
+
+int launch_kv_bound(const KvBoundArgs& a, int elem, int store, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (store == LM_KV_E4M3) return launch_bound_s<bf16, LM_KV_E4M3>(a, st);
+  if (store == LM_KV_INT8) return launch_bound_s<bf16, LM_KV_INT8>(a, st);
+  return elem == LM_BF16 ? launch_bound_s<bf16, LM_KV_SAME>(a, st)
+                         : launch_bound_s<__half, LM_KV_SAME>(a, st);
+}
+
+int launch_kv_select(const KvSelectArgs& a, int elem, void* stream) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int dev = 0, sms = 0;
+  int rc = kv_device(&dev, &sms);
+  if (rc != LM_OK) return rc;
+  if (a.max_pages > a.keep) {
+    rc = elem == LM_BF16 ? launch_score<bf16>(a, sms, st)
+                         : launch_score<__half>(a, sms, st);
+    if (rc != LM_OK) return rc;
+  }
+  constexpr int T = 256;
+  const int cap = int(a.max_pages < 8192 ? a.max_pages : 8192);
+  return launch(lm_kv_select_kernel<T, 1>, uint64_t(a.seqs) * a.heads, T,
+                cap * 4, st, a, cap);
+}
+
+}  // namespace lm

@@ -1,0 +1,75 @@
+// A line of work: the units of all sequences one after the other, cut into
+// equal parts, so that ragged batches and single long sequences load all
+// blocks alike.
+#pragma once
+
+#include <cstdint>
+
+namespace lm {
+
+// a / b of numbers that are not negative; most are small, and a 64-bit
+// division takes several times a 32-bit one's time.
+__device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
+  if ((a | b) >> 31 == 0) return uint32_t(a) / uint32_t(b);
+  return a / b;
+}
+
+struct LineShare {
+  int64_t total = 0;     // units of the line
+  int64_t begin = 0;     // the part: units begin .. begin + left - 1
+  int64_t left = 0;
+  int b = 0;             // the sequence that unit `begin` belongs to
+  int64_t in = 0;        // and its number there
+};
+
+// Part `part` of `parts` of the line, for all T threads of the block at once:
+// every thread counts the units of a run of sequences, a scan over the block
+// does the rest.  units(b): those of sequence b, the same whenever asked.
+template <int T, class F>
+__device__ __forceinline__ LineShare line_share(int seqs, int64_t part,
+                                                int64_t parts, F&& units) {
+  __shared__ int64_t sums[T / 32], found[2];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int per = (seqs + T - 1) / T;
+  const int b0 = min(seqs, int(threadIdx.x) * per);
+  const int b1 = min(seqs, b0 + per);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += units(b);
+  int64_t sum = mine;
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, sum, k);
+    if (lane >= k) sum += v;
+  }
+  if (lane == 31) sums[warp] = sum;
+  __syncthreads();
+  LineShare s;
+  int64_t before = sum - mine;
+#pragma unroll
+  for (int w = 0; w < T / 32; ++w) {
+    if (w < warp) before += sums[w];
+    s.total += sums[w];
+  }
+  // (the line of any cache is far below 2^63 / parts)
+  s.begin = small_div(part * s.total, parts);
+  s.left = small_div((part + 1) * s.total, parts) - s.begin;
+  if (s.left > 0 && s.begin >= before && s.begin < before + mine) {
+    int b = b0;
+    for (;; ++b) {
+      const int64_t k = units(b);
+      if (s.begin < before + k) break;
+      before += k;
+    }
+    found[0] = b;
+    found[1] = s.begin - before;
+  }
+  __syncthreads();
+  if (s.left > 0) {
+    s.b = int(found[0]);
+    s.in = found[1];
+  }
+  __syncthreads();
+  return s;
+}
+
+}  // namespace lm

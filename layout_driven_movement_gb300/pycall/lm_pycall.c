@@ -13,7 +13,7 @@
 #include "layoutmove.h"
 
 static PyObject *n_is_cuda, *n_shape, *n_dtype, *n_stride, *n_data_ptr;
-static PyObject *t_bf16, *t_f16, *t_f32, *t_i32, *t_i64;
+static PyObject *t_bf16, *t_f16, *t_f32, *t_i8, *t_i32, *t_i64;
 
 static int64_t wrong(const char* what, const char* wanted) {
   if (!PyErr_Occurred())
@@ -32,7 +32,7 @@ static int elem_of(PyObject* dtype) {
 typedef struct {
   char* data;
   int dims;
-  int64_t size[3], stride[3];
+  int64_t size[4], stride[4];
   PyObject* dtype; /* a singleton of torch's, borrowed */
 } tensor;
 
@@ -40,14 +40,14 @@ static int ints(PyObject* tuple, int64_t* out) {
   Py_ssize_t i, n;
   if (!tuple || !PyTuple_Check(tuple)) return -1;
   n = PyTuple_GET_SIZE(tuple);
-  for (i = 0; i < n && i < 3; ++i) {
+  for (i = 0; i < n && i < 4; ++i) {
     out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(tuple, i));
     if (out[i] == -1 && PyErr_Occurred()) return -1;
   }
   return (int)n;
 }
 
-/* A CUDA tensor of 1 to 3 dimensions. */
+/* A CUDA tensor of 1 to 4 dimensions. */
 static int look(PyObject* o, const char* what, tensor* t) {
   PyObject *a = PyObject_GetAttr(o, n_is_cuda), *b;
   const int cuda = a == Py_True;
@@ -60,8 +60,8 @@ static int look(PyObject* o, const char* what, tensor* t) {
   if (ints(b, t->stride) != t->dims) t->dims = -1;
   Py_XDECREF(a);
   Py_XDECREF(b);
-  if (t->dims < 1 || t->dims > 3)
-    return (int)wrong(what, "a tensor of 1 to 3 dimensions");
+  if (t->dims < 1 || t->dims > 4)
+    return (int)wrong(what, "a tensor of 1 to 4 dimensions");
   t->dtype = PyObject_GetAttr(o, n_dtype);
   if (!t->dtype) return -1;
   Py_DECREF(t->dtype);
@@ -272,66 +272,245 @@ static PyObject* py_kv_read(PyObject* self, PyObject* const* a,
   return PyLong_FromLong(rc);
 }
 
-/* kv_attend(plan, cache, dim, elem, q, page_table, lens, out, workspace,
- * lse, scale, window, stream); workspace and lse may be None */
+/* A workspace's address and bytes; None: none. */
+static int space(PyObject* o, char** data, int64_t* bytes) {
+  tensor w;
+  PyObject* b;
+  *data = NULL;
+  *bytes = 0;
+  if (o == Py_None) return 0;
+  if (look(o, "workspace", &w)) return -1;
+  if (w.dims != 1 || !dense(&w))
+    return (int)wrong("workspace", "a contiguous vector");
+  b = PyObject_GetAttrString(o, "nbytes");
+  if (!b) return -1;
+  *bytes = PyLong_AsLongLong(b);
+  Py_DECREF(b);
+  *data = w.data;
+  return PyErr_Occurred() ? -1 : 0;
+}
+
+/* A contiguous tensor of a type. */
+static int buffer(PyObject* o, const char* what, PyObject* dtype,
+                  const char* wanted, tensor* t) {
+  if (look(o, what, t)) return -1;
+  if (t->dtype != dtype || !dense(t)) return (int)wrong(what, wanted);
+  return 0;
+}
+
+/* lse [sequences, query heads]; None: none. */
+static int lse_of(PyObject* o, const tensor* q, char** data) {
+  tensor e;
+  *data = NULL;
+  if (o == Py_None) return 0;
+  if (look(o, "lse", &e)) return -1;
+  if (e.dtype != t_f32 || !dense(&e) || count(&e) != q->size[0] * q->size[1])
+    return (int)wrong("lse",
+                      "a contiguous float32 tensor [sequences, query heads]");
+  *data = e.data;
+  return 0;
+}
+
+/* kv_attend(plan, cache, heads, dim, elem, q, page_table, lens, out,
+ * workspace, lse, scale, window, weights, stream); workspace, lse and weights
+ * may be None, the page table have a dimension for the key heads */
 static PyObject* py_kv_attend(PyObject* self, PyObject* const* a,
                               Py_ssize_t n) {
-  tensor q, o, p, l, w, e;
+  tensor q, o, p, l, m;
   lm_rows qr, orr;
   int rc, elem;
   void *plan, *cache, *stream;
-  int64_t dim, window, ws_bytes = 0;
+  int64_t heads, dim, window, ws_bytes, by_head = 0, n_weights = 0;
   double scale;
-  char *ws = NULL, *lse = NULL;
+  char *ws, *lse, *weights = NULL;
   (void)self;
-  if (want(n, 13, "kv_attend")) return NULL;
+  if (want(n, 15, "kv_attend")) return NULL;
   plan = PTR(0);
   cache = PTR(1);
-  dim = I64(2);
-  elem = (int)I64(3);
-  if (rows(a[4], "q", dim, elem, &q, &qr) ||
-      rows(a[7], "out", dim, elem, &o, &orr))
+  heads = I64(2);
+  dim = I64(3);
+  elem = (int)I64(4);
+  if (rows(a[5], "q", dim, elem, &q, &qr) ||
+      rows(a[8], "out", dim, elem, &o, &orr))
     return NULL;
   if (o.size[0] != q.size[0] || o.size[1] != q.size[1]) {
     wrong("out", "q's shape");
     return NULL;
   }
-  if (vector(a[6], "lens", q.size[0], t_i32, &l) ||
-      page_table(a[5], q.size[0], &p))
+  if (vector(a[7], "lens", q.size[0], t_i32, &l) || look(a[6], "page_table", &p))
     return NULL;
-  if (a[8] != Py_None) {
-    if (look(a[8], "workspace", &w)) return NULL;
-    if (w.dims != 1 || !dense(&w)) {
-      wrong("workspace", "a contiguous vector");
+  if (p.dims == 3) {
+    if (p.size[0] != q.size[0] || p.size[1] != heads || p.dtype != t_i32 ||
+        (p.size[2] > 1 && p.stride[2] != 1)) {
+      wrong("page_table", "an int32 tensor [sequences, key heads, pages] with "
+                          "contiguous rows");
       return NULL;
     }
-    ws = w.data;
-    {
-      PyObject* b = PyObject_GetAttrString(a[8], "nbytes");
-      if (!b) return NULL;
-      ws_bytes = PyLong_AsLongLong(b);
-      Py_DECREF(b);
-    }
-  }
-  if (a[9] != Py_None) {
-    if (look(a[9], "lse", &e)) return NULL;
-    if (e.dtype != t_f32 || !dense(&e) || count(&e) != q.size[0] * q.size[1]) {
-      wrong("lse", "a contiguous float32 tensor [sequences, query heads]");
+    by_head = p.stride[1];
+    p.size[1] = p.size[2];
+    /* (of heads and sequences that share pages, a stride may be 0) */
+    if (p.size[0] > 1 && p.stride[0] < p.size[1]) {
+      wrong("page_table", "rows of its own for every sequence");
       return NULL;
     }
-    lse = e.data;
+  } else if (page_table(a[6], q.size[0], &p)) {
+    return NULL;
   }
-  scale = PyFloat_AsDouble(a[10]);
-  window = I64(11);
-  stream = PTR(12);
+  if (space(a[9], &ws, &ws_bytes) || lse_of(a[10], &q, &lse)) return NULL;
+  if (a[13] != Py_None) {
+    if (buffer(a[13], "weights", t_f32,
+               "a contiguous float32 tensor [pages, key heads, page_tokens]",
+               &m))
+      return NULL;
+    weights = m.data;
+    n_weights = count(&m);
+  }
+  scale = PyFloat_AsDouble(a[11]);
+  window = I64(12);
+  stream = PTR(14);
   if (PyErr_Occurred()) return NULL;
   Py_BEGIN_ALLOW_THREADS
   rc = q.size[0] > INT32_MAX || q.size[1] > INT32_MAX
            ? LM_E_INVALID
-           : lm_kv_attend(plan, cache, &qr, &orr, (int)q.size[0],
+           : lm_kv_attend_weigh(plan, cache, &qr, &orr, (int)q.size[0],
+                                (int)q.size[1], (int32_t*)p.data, p.stride[0],
+                                by_head, p.size[1], (int32_t*)l.data, window,
+                                (float)scale, (float*)lse, (float*)weights,
+                                n_weights, ws, ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* bounds [pages, heads, 2, dim] int8 and scale [pages, heads] float32 */
+static int bounds_of(PyObject* bo, PyObject* so, int64_t heads, int64_t dim,
+                     lm_kv_bounds* out, int64_t* pages) {
+  tensor b, s;
+  if (buffer(bo, "bounds", t_i8,
+             "a contiguous int8 tensor [pages, key heads, 2, dim]", &b) ||
+      buffer(so, "bound_scale", t_f32,
+             "a contiguous float32 tensor [pages, key heads]", &s))
+    return -1;
+  if (b.dims != 4 || b.size[1] != heads || b.size[2] != 2 ||
+      b.size[3] != dim)
+    return (int)wrong("bounds", "[pages, key heads, 2, dim]");
+  if (s.dims != 2 || s.size[0] != b.size[0] || s.size[1] != heads)
+    return (int)wrong("bound_scale", "[pages, key heads]");
+  out->data = (int8_t*)b.data;
+  out->scale = (float*)s.data;
+  out->capacity = count(&b);
+  out->scale_capacity = count(&s);
+  *pages = b.size[0];
+  return 0;
+}
+
+/* kv_bound(plan, cache, heads, dim, pages, counts, bounds, bound_scale,
+ * stream) */
+static PyObject* py_kv_bound(PyObject* self, PyObject* const* a,
+                             Py_ssize_t n) {
+  tensor p, c;
+  lm_kv_bounds b;
+  int rc;
+  void *plan, *cache, *stream;
+  int64_t pages;
+  (void)self;
+  if (want(n, 9, "kv_bound")) return NULL;
+  plan = PTR(0);
+  cache = PTR(1);
+  if (look(a[4], "pages", &p) ||
+      vector(a[4], "pages", p.size[0], t_i32, &p) ||
+      vector(a[5], "counts", p.size[0], t_i32, &c) ||
+      bounds_of(a[6], a[7], I64(2), I64(3), &b, &pages))
+    return NULL;
+  stream = PTR(8);
+  if (PyErr_Occurred()) return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  rc = lm_kv_bound(plan, cache, (int32_t*)p.data, (int32_t*)c.data, p.size[0],
+                   &b, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* kv_select(plan, heads, dim, elem, q, bounds, bound_scale, page_table, lens,
+ * selected, selected_lens, workspace, first, last, stream) */
+static PyObject* py_kv_select(PyObject* self, PyObject* const* a,
+                              Py_ssize_t n) {
+  tensor q, p, l, s, sl;
+  lm_rows qr;
+  lm_kv_bounds b;
+  int rc;
+  void *plan, *stream;
+  int64_t heads, dim, pages, ws_bytes, first, last;
+  char* ws;
+  (void)self;
+  if (want(n, 15, "kv_select")) return NULL;
+  plan = PTR(0);
+  heads = I64(1);
+  dim = I64(2);
+  if (rows(a[4], "q", dim, (int)I64(3), &q, &qr) ||
+      bounds_of(a[5], a[6], heads, dim, &b, &pages) ||
+      page_table(a[7], q.size[0], &p) ||
+      vector(a[8], "lens", q.size[0], t_i32, &l) ||
+      buffer(a[9], "selected", t_i32,
+             "a contiguous int32 tensor [sequences, key heads, pages]", &s) ||
+      vector(a[10], "selected_lens", q.size[0], t_i32, &sl) ||
+      space(a[11], &ws, &ws_bytes))
+    return NULL;
+  if (s.dims != 3 || s.size[0] != q.size[0] || s.size[1] != heads) {
+    wrong("selected", "[sequences, key heads, pages]");
+    return NULL;
+  }
+  first = I64(12);
+  last = I64(13);
+  stream = PTR(14);
+  if (PyErr_Occurred()) return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  rc = q.size[0] > INT32_MAX || q.size[1] > INT32_MAX ||
+               s.size[2] > INT32_MAX || first > INT32_MAX ||
+               last > INT32_MAX || first < 0 || last < 0
+           ? LM_E_INVALID
+           : lm_kv_select(plan, pages, &b, &qr, (int)q.size[0],
                           (int)q.size[1], (int32_t*)p.data, p.stride[0],
-                          p.size[1], (int32_t*)l.data, window, (float)scale,
-                          (float*)lse, ws, ws_bytes, stream);
+                          p.size[1], (int32_t*)l.data, (int)s.size[2],
+                          (int)first, (int)last, (int32_t*)s.data,
+                          (int32_t*)sl.data, ws, ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
+/* kv_evict(plan, cache, weights, page_table, lens, kept_table, kept_lens,
+ * keep, recent, workspace, stream) */
+static PyObject* py_kv_evict(PyObject* self, PyObject* const* a,
+                             Py_ssize_t n) {
+  tensor m, p, l, k, kl;
+  int rc;
+  void *plan, *cache, *stream;
+  int64_t ws_bytes, keep, recent;
+  char* ws;
+  (void)self;
+  if (want(n, 11, "kv_evict")) return NULL;
+  plan = PTR(0);
+  cache = PTR(1);
+  if (buffer(a[2], "weights", t_f32,
+             "a contiguous float32 tensor [pages, key heads, page_tokens]",
+             &m) ||
+      look(a[4], "lens", &l) || vector(a[4], "lens", l.size[0], t_i32, &l) ||
+      page_table(a[3], l.size[0], &p) || page_table(a[5], l.size[0], &k) ||
+      vector(a[6], "kept_lens", l.size[0], t_i32, &kl) ||
+      space(a[9], &ws, &ws_bytes))
+    return NULL;
+  keep = I64(7);
+  recent = I64(8);
+  stream = PTR(10);
+  if (PyErr_Occurred()) return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  rc = l.size[0] > INT32_MAX || keep < 1 || keep > INT32_MAX || recent < 0 ||
+               recent > keep
+           ? LM_E_INVALID
+           : lm_kv_evict(plan, cache, (float*)m.data, count(&m),
+                         (int32_t*)p.data, p.stride[0], (int)l.size[0],
+                         p.size[1], (int32_t*)l.data, (int32_t*)k.data,
+                         k.stride[0], k.size[1], (int32_t*)kl.data, (int)keep,
+                         (int)recent, ws, ws_bytes, stream);
   Py_END_ALLOW_THREADS
   return PyLong_FromLong(rc);
 }
@@ -342,6 +521,12 @@ static PyMethodDef methods[] = {
      NULL},
     {"kv_read", (PyCFunction)(void (*)(void))py_kv_read, METH_FASTCALL, NULL},
     {"kv_attend", (PyCFunction)(void (*)(void))py_kv_attend, METH_FASTCALL,
+     NULL},
+    {"kv_bound", (PyCFunction)(void (*)(void))py_kv_bound, METH_FASTCALL,
+     NULL},
+    {"kv_select", (PyCFunction)(void (*)(void))py_kv_select, METH_FASTCALL,
+     NULL},
+    {"kv_evict", (PyCFunction)(void (*)(void))py_kv_evict, METH_FASTCALL,
      NULL},
     {NULL, NULL, 0, NULL}};
 
@@ -359,11 +544,12 @@ PyMODINIT_FUNC PyInit__pycall(void) {
   t_bf16 = PyObject_GetAttrString(torch, "bfloat16");
   t_f16 = PyObject_GetAttrString(torch, "float16");
   t_f32 = PyObject_GetAttrString(torch, "float32");
+  t_i8 = PyObject_GetAttrString(torch, "int8");
   t_i32 = PyObject_GetAttrString(torch, "int32");
   t_i64 = PyObject_GetAttrString(torch, "int64");
   Py_DECREF(torch);
   if (!n_data_ptr || !n_is_cuda || !n_shape || !n_dtype || !n_stride ||
-      !t_bf16 || !t_f16 || !t_f32 || !t_i32 || !t_i64)
+      !t_bf16 || !t_f16 || !t_f32 || !t_i8 || !t_i32 || !t_i64)
     return NULL;
   return PyModule_Create(&module);
 }
