@@ -820,6 +820,44 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
                        int64_t weights_capacity, void* workspace,
                        int64_t workspace_bytes, void* cuda_stream);
 
+/* Bytes of lm_kv_attend_shared's workspace for seqs sequences of heads_q query
+ * heads on the current device: lm_kv_attend's, some 40 MB for the parts of rows
+ * that several blocks share, and 12 (dim + 2) bytes for every sequence and
+ * query head.  Zero it once before its first use, as lm_kv_attend's, whose
+ * calls it serves too.
+ * Errors: LM_E_INVALID, LM_E_OVERFLOW, LM_E_CUDA. */
+int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
+                                  int heads_q, int64_t* bytes);
+
+/* lm_kv_attend for sequences that share a prefix in groups: sequences
+ * starts[g] .. starts[g + 1] - 1 attend over the first shared_lens[g] tokens
+ * (clipped to [0, max_shared_pages * P]) of the pages shared_table[g *
+ * shared_stride + i], and each over the first lens[b] tokens of its own pages,
+ * as if these followed those:
+ *   out[b, h] = sum_j p_j v_j,  p_j = exp(s_j) / sum_i exp(s_i),  j and i over
+ * both.  A group's prefix is read once for all of its sequences.  starts has
+ * groups + 1 entries, none below the one before; a sequence that no group
+ * names has its own pages alone, a group may have no sequences or no tokens.
+ * (Entries are clipped to [0, seqs].  Of a sequence that several groups name
+ * the outputs are not defined.)
+ *
+ * A weight p_j of a shared token meets its value rounded to 16 bits: to
+ * bfloat16 (2^-8 of itself at most; for float16 queries of an 8-bit cache, as
+ * two parts, 2^-16), or, where the cache holds float16 rows, to float16 (2^-11
+ * of itself or 2^-36 of the largest weight of its row, whichever is more).
+ * Otherwise precision and range are lm_kv_attend's, weights below 2^-80 of the
+ * largest are lost, and scales of values any number of 32 bits, those beside
+ * scales 2^60 times their own losing bits.  The same inputs give the same bits.
+ * Errors: as lm_kv_attend. */
+int lm_kv_attend_shared(
+    const lm_kv_plan* plan, const lm_kv_cache* cache, const lm_rows* q,
+    const lm_rows* out, int seqs, int heads_q, const int32_t* shared_table,
+    int64_t shared_stride, int groups, int64_t max_shared_pages,
+    const int32_t* shared_lens, const int32_t* starts,
+    const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+    const int32_t* lens, float scale, float* lse, void* workspace,
+    int64_t workspace_bytes, void* cuda_stream);
+
 /* The bounds of a cache's pages: for each page and key head the least and the
  * largest element d of its keys, as whole numbers under one power of two.
  * data: pages x heads x 2 x dim bytes (16-byte aligned), lo then hi; scale:

@@ -149,6 +149,12 @@ SIGNATURES = [
      [_P, C.POINTER(_KVCache), C.POINTER(_Rows), C.POINTER(_Rows), C.c_int,
       C.c_int, _P, _I64, _I64, _I64, _P, _I64, C.c_float, _P, _P, _I64, _P,
       _I64, _P]),
+    ("lm_kv_attend_shared_workspace", C.c_int,
+     [_P, C.c_int, C.c_int, _I64P]),
+    ("lm_kv_attend_shared", C.c_int,
+     [_P, C.POINTER(_KVCache), C.POINTER(_Rows), C.POINTER(_Rows), C.c_int,
+      C.c_int, _P, _I64, C.c_int, _I64, _P, _P, _P, _I64, _I64, _P,
+      C.c_float, _P, _P, _I64, _P]),
     ("lm_kv_bound", C.c_int,
      [_P, C.POINTER(_KVCache), _P, _P, _I64, C.POINTER(_KVBounds), _P]),
     ("lm_kv_select_workspace", C.c_int, [_P, C.c_int, _I64, _I64P]),
@@ -1055,6 +1061,34 @@ def kv_attend(cache: KVCache, q, page_table, lens, out, workspace=None,
     if rc:
         _check(rc, "lm_kv_attend_weigh" if weights is not None
                or page_table.dim() == 3 else "lm_kv_attend")
+
+
+def kv_attend_shared_workspace(plan: KVPlan, seqs: int, heads_q: int) -> int:
+    """Bytes of kv_attend_shared's workspace on the current device; zero the
+    buffer once before its first use.  It serves kv_attend's calls too."""
+    v = C.c_int64()
+    _check(lib().lm_kv_attend_shared_workspace(plan._h, int(seqs),
+                                               int(heads_q), C.byref(v)),
+           "lm_kv_attend_shared_workspace")
+    return v.value
+
+
+def kv_attend_shared(cache: KVCache, q, shared_table, shared_lens, starts,
+                     page_table, lens, out, workspace, lse=None,
+                     scale: float | None = None, stream=None) -> None:
+    """Enqueue kv_attend for sequences that share a prefix in groups: those
+    from starts[g] up to starts[g + 1] attend over the first shared_lens[g]
+    tokens of the pages shared_table[g], read once for all of them, and each
+    over the first lens[b] tokens of its own pages behind those.  shared_table
+    int32 [groups, pages], shared_lens int32 [groups], starts int32
+    [groups + 1]; the rest as kv_attend's (see lm_kv_attend_shared)."""
+    p = cache.plan
+    rc = _pycall().kv_attend_shared(
+        p._p, cache._p, p.dim, p.elem, q, shared_table, shared_lens, starts,
+        page_table, lens, out, workspace, lse,
+        p.dim ** -0.5 if scale is None else scale, _stream(stream))
+    if rc:
+        _check(rc, "lm_kv_attend_shared")
 
 
 def kv_bound(cache: KVCache, pages, counts, bounds, bound_scale,

@@ -480,6 +480,9 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   constexpr uint32_t full = KW >= 32 ? 0xffffffffu : (1u << KW % 32) - 1;
   auto fetch = [&](Pages* pg) {
     const int key0 = ld.tile * TK + wk * KW;
+    const int32_t* table = a.table + int64_t(ld.b) * a.table_stride;
+    if (a.table_head)
+      table += int64_t(ld.item / g.groups * HP + sub) * a.table_head;
 #pragma unroll
     for (int i = 0; i < KL; ++i) {
       const int key = key0 + (g.shared_page ? 0 : lane + 32 * i);
@@ -487,10 +490,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       pg->of[i] = -1;
       if (ld.left > 0 && (g.shared_page || KW >= 32 || lane < KW) &&
           key + reach > ld.first && key < ld.n && (i == 0 || !g.shared_page))
-        pg->of[i] = a.table[int64_t(ld.b) * a.table_stride +
-                            int64_t(ld.item / g.groups * HP + sub) *
-                                a.table_head +
-                            fdiv(uint32_t(key), a.c.page_div)];
+        pg->of[i] = table[fdiv(uint32_t(key), a.c.page_div)];
       if (i && g.shared_page) pg->of[i] = pg->of[0];
     }
   };

@@ -438,5 +438,6 @@ void set_cuda_error(int e);
 unsigned int* device_status_word();  // device address, current device
 // The status word's bits: 1 and 2 are waits that gave up (lm_kernels.cu), 4
 // an index read on the device that was out of range.
+constexpr unsigned int kStatusTimeout = 1;  // a bounded wait gave up
 constexpr unsigned int kStatusRange = 4;
 }  // namespace lm

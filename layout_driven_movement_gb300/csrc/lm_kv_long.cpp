@@ -24,6 +24,26 @@ WeighSpace weigh_space(int64_t plain, int64_t rows, int64_t max_tokens) {
   return s;
 }
 
+// What an attention over shared prefixes keeps behind the plain attention's:
+// each row's state over its own pages, up to two over its group's, and the
+// parts of rows that several blocks share.
+struct SharedSpace {
+  int64_t state = 0, mean = 0, shared_state = 0, shared_mean = 0, parts = 0,
+          bytes = 0;
+};
+SharedSpace shared_space(int64_t plain, int64_t rows, int dim, int sms) {
+  const int64_t states = whole(mul_chk(rows, 8));
+  const int64_t means = whole(mul_chk(rows, int64_t(dim) * 4));
+  SharedSpace s;
+  s.state = whole(plain);
+  s.mean = add_chk(s.state, states);
+  s.shared_state = add_chk(s.mean, means);
+  s.shared_mean = add_chk(s.shared_state, 2 * states);
+  s.parts = add_chk(s.shared_mean, mul_chk(means, 2));
+  s.bytes = add_chk(s.parts, 2 * int64_t(sms) * shared_part(dim) * 4);
+  return s;
+}
+
 Range range_of(const void* p, int64_t bytes) {
   return {addr(p), addr(p) + uintptr_t(bytes)};
 }
@@ -179,6 +199,136 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
     w.lse2 = a.lse2;
     w.weights = weights;
     rc = lm::launch_kv_weigh(w, cuda_stream);
+  });
+  return checked != LM_OK ? checked : rc;
+}
+
+int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
+                                  int heads_q, int64_t* bytes) {
+  int rc = LM_OK;
+  const int checked = lm::guarded([&] {
+    need(plan && bytes);
+    lm::check_queries(*plan, seqs, heads_q);
+    int64_t plain = 0;
+    rc = lm::attend_workspace(plan->store, int(plan->dim),
+                              int(heads_q / plan->heads), &plain);
+    int dev = 0, sms = 0;
+    if (rc == LM_OK) rc = lm::kv_device(&dev, &sms);
+    if (rc != LM_OK) return;
+    *bytes = lm::shared_space(plain, int64_t(seqs) * heads_q, int(plan->dim),
+                              sms)
+                 .bytes;
+  });
+  return checked != LM_OK ? checked : rc;
+}
+
+int lm_kv_attend_shared(
+    const lm_kv_plan* plan, const lm_kv_cache* cache, const lm_rows* q,
+    const lm_rows* out, int seqs, int heads_q, const int32_t* shared_table,
+    int64_t shared_stride, int groups, int64_t max_shared_pages,
+    const int32_t* shared_lens, const int32_t* starts,
+    const int32_t* page_table, int64_t table_stride, int64_t max_pages,
+    const int32_t* lens, float scale, float* lse, void* workspace,
+    int64_t workspace_bytes, void* cuda_stream) {
+  int rc = LM_OK;
+  const int checked = lm::guarded([&] {
+    need(plan && std::isfinite(scale));
+    lm::check_queries(*plan, seqs, heads_q);
+    lm::CacheRanges held;
+    lm::KvAttendArgs a;
+    a.c = lm::check_cache(*plan, cache, &held);
+    if (seqs == 0) return;
+    lm::check_table(*plan, page_table, table_stride, seqs, max_pages, lens);
+    need(groups >= 0);
+    if (groups > 0) {
+      lm::check_table(*plan, shared_table, shared_stride, groups,
+                      max_shared_pages, shared_lens);
+      need(starts && lm::addr(starts) % 4 == 0);
+    }
+    const int64_t rows = lm::mul_chk(seqs, heads_q);
+    need(rows < (int64_t(1) << 31) - 4096, LM_E_OVERFLOW);
+    const lm::Range rq =
+        lm::check_rows(q, seqs, heads_q, plan->dim, 2, false);
+    const lm::Range ro =
+        lm::check_rows(out, seqs, heads_q, plan->dim, 2, true);
+    const bool in_place =
+        q->data == out->data &&
+        (seqs == 1 || q->token_stride == out->token_stride) &&
+        (heads_q == 1 || q->head_stride == out->head_stride);
+    need(in_place || !rq.meets(ro), LM_E_OVERLAP);
+    need(!held.meet(ro), LM_E_OVERLAP);
+    need(lse == nullptr || lm::addr(lse) % 4 == 0);
+    lm::Range rl;
+    if (lse) {
+      rl = lm::range_of(lse, rows * 4);
+      need(!held.meet(rl) && !rl.meets(rq) && !rl.meets(ro), LM_E_OVERLAP);
+    }
+    const int group = int(heads_q / plan->heads);
+    int64_t plain = 0;
+    int dev = 0, sms = 0;
+    rc = lm::attend_workspace(plan->store, int(plan->dim), group, &plain);
+    if (rc == LM_OK) rc = lm::kv_device(&dev, &sms);
+    if (rc != LM_OK) return;
+    const lm::SharedSpace space =
+        lm::shared_space(plain, rows, int(plan->dim), sms);
+    lm::check_workspace(workspace, workspace_bytes, space.bytes);
+    const lm::Range rs = lm::range_of(workspace, space.bytes);
+    need(!held.meet(rs) && !rs.meets(rq) && !rs.meets(ro) && !rs.meets(rl),
+         LM_E_OVERLAP);
+    char* const ws = static_cast<char*>(workspace);
+    auto floats = [&](int64_t at) { return reinterpret_cast<float*>(ws + at); };
+    a.q = lm::rows_of(*q);
+    a.out = lm::rows_of(*out);
+    a.table = page_table;
+    a.table_stride = table_stride;
+    a.max_tokens = max_pages * plan->page_tokens;
+    a.lens = lens;
+    a.seqs = seqs;
+    a.heads_q = heads_q;
+    a.group = group;
+    a.elem = plan->elem;
+    a.scale = scale;
+    a.ws = workspace;
+    a.status = lm::device_status_word();
+    if (groups == 0 || max_shared_pages == 0) {
+      a.lse = lse;
+      rc = lm::launch_kv_attend(a, plan->store, cuda_stream);
+      return;
+    }
+    lm::KvJoinArgs j;
+    lm::KvSharedArgs& s = j.s;
+    s.c = a.c;
+    s.q = a.q;
+    s.table = shared_table;
+    s.table_stride = shared_stride;
+    s.max_tokens = max_shared_pages * plan->page_tokens;
+    s.lens = shared_lens;
+    s.starts = starts;
+    s.groups = groups;
+    s.seqs = seqs;
+    s.group = group;
+    s.heads_q = heads_q;
+    s.q16 = lm::vector_rows(*q, 2);
+    s.elem = plan->elem;
+    s.scale = scale;
+    s.state = floats(space.shared_state);
+    s.mean = floats(space.shared_mean);
+    s.parts = floats(space.parts);
+    s.status = a.status;
+    rc = lm::launch_kv_shared(s, plan->store, cuda_stream);
+    if (rc != LM_OK) return;
+    a.state = floats(space.state);
+    a.mean = floats(space.mean);
+    rc = lm::launch_kv_attend(a, plan->store, cuda_stream);
+    if (rc != LM_OK) return;
+    j.out = a.out;
+    j.state = a.state;
+    j.mean = a.mean;
+    j.lse = lse;
+    j.tile_keys = lm::shared_keys(int(plan->dim));
+    j.tile_rows = lm::shared_rows(int(plan->dim));
+    j.blocks = sms;
+    rc = lm::launch_kv_join(j, cuda_stream);
   });
   return checked != LM_OK ? checked : rc;
 }

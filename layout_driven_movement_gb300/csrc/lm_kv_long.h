@@ -63,6 +63,47 @@ struct KvEvictArgs {
   unsigned int* status = nullptr;
 };
 
+// Attention of groups of sequences over the pages that each group shares, and
+// its join with that over each sequence's own.
+struct KvSharedArgs {
+  CacheArgs c;
+  Rows q;
+  const int32_t* table = nullptr;         // [groups, pages]
+  int64_t table_stride = 0, max_tokens = 0;
+  const int32_t *lens = nullptr, *starts = nullptr;
+  int32_t groups = 0, seqs = 0, group = 1, heads_q = 1;
+  int32_t q16 = 0;                        // the queries allow 16-byte loads
+  int32_t elem = LM_BF16;
+  float scale = 1;
+  // rows that one block finishes: up to two states (m, l) and means each, [2,
+  // seqs, heads_q] and [2, seqs, heads_q, dim]
+  float *state = nullptr, *mean = nullptr;
+  float* parts = nullptr;                 // two for each block
+  unsigned int* status = nullptr;
+};
+
+struct KvJoinArgs {
+  KvSharedArgs s;
+  Rows out;
+  const float *state = nullptr, *mean = nullptr;    // of each one's own pages
+  float* lse = nullptr;
+  int32_t tile_keys = 1, tile_rows = 1, blocks = 1;
+};
+
+// The tiles of a shared-prefix kernel for rows of `dim` elements.
+LM_HD int shared_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+LM_HD int shared_keys(int dim) { return dim > 128 ? 64 : 128; }
+LM_HD int shared_rows(int dim) { return dim > 128 ? 128 : 256; }
+// Floats of a part: (m, l) of its rows, then their means.
+LM_HD int64_t shared_part(int dim) {
+  return int64_t(shared_rows(dim)) * (shared_dim(dim) + 2);
+}
+
+int launch_kv_shared(const KvSharedArgs& a, int store, void* stream);
+int launch_kv_join(const KvJoinArgs& a, void* stream);
+int launch_shared_same(const KvSharedArgs& a, void* stream);
+int launch_shared_e4m3(const KvSharedArgs& a, void* stream);
+int launch_shared_int8(const KvSharedArgs& a, void* stream);
 int launch_kv_weigh(const KvWeighArgs& a, void* stream);
 int launch_kv_bound(const KvBoundArgs& a, int elem, int store, void* stream);
 int launch_kv_select(const KvSelectArgs& a, int elem, void* stream);

@@ -1,0 +1,8 @@
+// The shared-prefix kernel over pages that hold 16-bit rows.
+#include "lm_shared.cuh"
+
+namespace lm {
+int launch_shared_same(const KvSharedArgs& a, void* stream) {
+  return launch_shared_store<LM_KV_SAME>(a, stream);
+}
+}  // namespace lm

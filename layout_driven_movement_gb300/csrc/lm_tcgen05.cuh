@@ -1,0 +1,137 @@
+// The tensor-memory instructions (tcgen05) that the library's kernels use, for
+// one block (cta_group::1): allocation, matrix products of 16-bit elements
+// with 32-bit sums, loads and stores of a warp's 32 lanes, commits.
+#pragma once
+
+#include <cstdint>
+
+namespace lm {
+
+// --- tensor memory -----------------------------------------------------------
+
+// By one whole warp: `columns` (a power of two of 32 or more) columns, their
+// address written to shared memory.
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns) {
+  asm volatile(
+      "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+          to),
+      "r"(columns)
+      : "memory");
+  asm volatile(
+      "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+  asm volatile(
+      "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(at),
+      "r"(columns));
+}
+__device__ __forceinline__ void tmem_before_sync() {
+  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_after_sync() {
+  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+
+// A warp's 32 lanes (the quarter of tensor memory that its number within four
+// warps gives) by 32 columns: lane i of the warp holds lane i's.  `at` has the
+// quarter's first lane in its upper half.  The registers are there after
+// tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]),
+        "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+      "%31, %32};\n" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};\n" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// --- products ----------------------------------------------------------------
+
+// An operand in shared memory in 128-byte rows whose 16-byte chunks are
+// exchanged by an exclusive or with the row's number within 8 (128B swizzle);
+// 8 such rows (1024 bytes) are a block.  stride: bytes between blocks of 8 rows;
+// leading: bytes between blocks of 64 elements along the rows, for an operand
+// whose rows run along M or N.
+__device__ __forceinline__ uint64_t smem_operand(uint32_t at, uint32_t leading,
+                                                 uint32_t stride) {
+  return uint64_t((at & 0x3ffff) >> 4) | uint64_t(leading >> 4) << 16 |
+         uint64_t(stride >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
+}
+// What a product is: 32-bit sums, elements bf16 or f16, M rows, N columns; the
+// second operand's rows run along N (b_rows_n) or along K.
+__device__ __forceinline__ uint32_t mma_kind(bool bf, bool b_rows_n, int m,
+                                             int n) {
+  return 1u << 4 | (bf ? 1u << 7 | 1u << 10 : 0u) |
+         (b_rows_n ? 1u << 16 : 0u) | uint32_t(n >> 3) << 17 |
+         uint32_t(m >> 4) << 24;
+}
+// One thread: D (+)= A B over 16 elements of K, A and B in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
+                                       uint32_t kind, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"(uint32_t(add))
+      : "memory");
+}
+// The same with A in tensor memory, two elements a column.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b,
+                                       uint32_t kind, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+          d),
+      "r"(a), "l"(b), "r"(kind), "r"(uint32_t(add))
+      : "memory");
+}
+// The thread's products so far arrive on `bar` when they are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+      "[%0];\n" ::"r"(bar)
+      : "memory");
+}
+// What this thread has written to shared memory is seen by the products.
+__device__ __forceinline__ void smem_to_products() {
+  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+}
+
+}  // namespace lm

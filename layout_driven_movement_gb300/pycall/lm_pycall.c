@@ -381,6 +381,57 @@ static PyObject* py_kv_attend(PyObject* self, PyObject* const* a,
   return PyLong_FromLong(rc);
 }
 
+/* kv_attend_shared(plan, cache, dim, elem, q, shared_table, shared_lens,
+ * starts, page_table, lens, out, workspace, lse, scale, stream); lse may be
+ * None */
+static PyObject* py_kv_attend_shared(PyObject* self, PyObject* const* a,
+                                     Py_ssize_t n) {
+  tensor q, o, p, l, t, sl, st;
+  lm_rows qr, orr;
+  int rc, elem;
+  void *plan, *cache, *stream;
+  int64_t dim, ws_bytes;
+  double scale;
+  char *ws, *lse;
+  (void)self;
+  if (want(n, 15, "kv_attend_shared")) return NULL;
+  plan = PTR(0);
+  cache = PTR(1);
+  dim = I64(2);
+  elem = (int)I64(3);
+  if (rows(a[4], "q", dim, elem, &q, &qr) ||
+      rows(a[10], "out", dim, elem, &o, &orr))
+    return NULL;
+  if (o.size[0] != q.size[0] || o.size[1] != q.size[1]) {
+    wrong("out", "q's shape");
+    return NULL;
+  }
+  if (look(a[6], "shared_lens", &sl) ||
+      vector(a[6], "shared_lens", sl.size[0], t_i32, &sl) ||
+      vector(a[7], "starts (one more than shared_lens)", sl.size[0] + 1, t_i32,
+             &st) ||
+      page_table(a[5], sl.size[0], &t) ||
+      vector(a[9], "lens", q.size[0], t_i32, &l) ||
+      page_table(a[8], q.size[0], &p) || space(a[11], &ws, &ws_bytes) ||
+      lse_of(a[12], &q, &lse))
+    return NULL;
+  scale = PyFloat_AsDouble(a[13]);
+  stream = PTR(14);
+  if (PyErr_Occurred()) return NULL;
+  Py_BEGIN_ALLOW_THREADS
+  rc = q.size[0] > INT32_MAX || q.size[1] > INT32_MAX ||
+               sl.size[0] > INT32_MAX
+           ? LM_E_INVALID
+           : lm_kv_attend_shared(
+                 plan, cache, &qr, &orr, (int)q.size[0], (int)q.size[1],
+                 (int32_t*)t.data, t.stride[0], (int)sl.size[0], t.size[1],
+                 (int32_t*)sl.data, (int32_t*)st.data, (int32_t*)p.data,
+                 p.stride[0], p.size[1], (int32_t*)l.data, (float)scale,
+                 (float*)lse, ws, ws_bytes, stream);
+  Py_END_ALLOW_THREADS
+  return PyLong_FromLong(rc);
+}
+
 /* bounds [pages, heads, 2, dim] int8 and scale [pages, heads] float32 */
 static int bounds_of(PyObject* bo, PyObject* so, int64_t heads, int64_t dim,
                      lm_kv_bounds* out, int64_t* pages) {
@@ -522,6 +573,8 @@ static PyMethodDef methods[] = {
     {"kv_read", (PyCFunction)(void (*)(void))py_kv_read, METH_FASTCALL, NULL},
     {"kv_attend", (PyCFunction)(void (*)(void))py_kv_attend, METH_FASTCALL,
      NULL},
+    {"kv_attend_shared", (PyCFunction)(void (*)(void))py_kv_attend_shared,
+     METH_FASTCALL, NULL},
     {"kv_bound", (PyCFunction)(void (*)(void))py_kv_bound, METH_FASTCALL,
      NULL},
     {"kv_select", (PyCFunction)(void (*)(void))py_kv_select, METH_FASTCALL,
