@@ -822,7 +822,7 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
 
 /* Bytes of lm_kv_attend_shared's workspace for seqs sequences of heads_q query
  * heads on the current device: lm_kv_attend's, some 40 MB for the parts of rows
- * that several blocks share, and 12 (dim + 2) bytes for every sequence and
+ * that several blocks share, and 12 dim + 40 bytes for every sequence and
  * query head.  Zero it once before its first use, as lm_kv_attend's, whose
  * calls it serves too.
  * Errors: LM_E_INVALID, LM_E_OVERFLOW, LM_E_CUDA. */
@@ -841,13 +841,13 @@ int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
  * (Entries are clipped to [0, seqs].  Of a sequence that several groups name
  * the outputs are not defined.)
  *
- * A weight p_j of a shared token meets its value rounded to 16 bits: to
- * bfloat16 (2^-8 of itself at most; for float16 queries of an 8-bit cache, as
- * two parts, 2^-16), or, where the cache holds float16 rows, to float16 (2^-11
- * of itself or 2^-36 of the largest weight of its row, whichever is more).
- * Otherwise precision and range are lm_kv_attend's, weights below 2^-80 of the
- * largest are lost, and scales of values any number of 32 bits, those beside
- * scales 2^60 times their own losing bits.  The same inputs give the same bits.
+ * A weight p_j of a shared token meets its value rounded to 16 bits: of a cache
+ * of bfloat16 rows to bfloat16 (off by 2^-8 of itself at most; weights below
+ * 2^-80 of the largest are lost), of any other to float16, off by 2^-11 of
+ * itself or by 2^-36 of the largest of its row, whichever is more, where a
+ * quantised value's weight counts times its scale.  Scales of values above 2^96
+ * or below 2^-96 in magnitude count as those.  Otherwise precision and range are
+ * lm_kv_attend's.  The same inputs give the same bits.
  * Errors: as lm_kv_attend. */
 int lm_kv_attend_shared(
     const lm_kv_plan* plan, const lm_kv_cache* cache, const lm_rows* q,

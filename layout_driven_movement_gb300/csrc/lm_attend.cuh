@@ -633,8 +633,10 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     }
     for (int qi = threadIdx.x; qi < a.heads_q; qi += kAttendThreads) {
       const int64_t row = int64_t(b) * a.heads_q + qi;
-      if (a.state)
+      if (a.state) {
         reinterpret_cast<float2*>(a.state)[row] = make_float2(-INFINITY, 0);
+        reinterpret_cast<int4*>(a.pieces)[row] = make_int4(0, 0, 0, 0);
+      }
       if (a.lse) a.lse[row] = -INFINITY;
       if (a.lse2) a.lse2[row] = -INFINITY;
     }
@@ -1182,8 +1184,10 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     };
     auto put_lse = [&](int i, int qi, float t, float sum) {
       const int64_t row = int64_t(done.b) * a.heads_q + row_of(i, qi);
-      if (a.state)
+      if (a.state) {
         reinterpret_cast<float2*>(a.state)[row] = make_float2(t, sum);
+        reinterpret_cast<int4*>(a.pieces)[row] = make_int4(0, 0, 0, 0);
+      }
       if (!a.lse && !a.lse2) return;
       const float lse2 = sum == 0 ? -INFINITY : t + log2f(sum);
       if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;

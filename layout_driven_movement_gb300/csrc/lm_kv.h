@@ -105,6 +105,8 @@ struct KvAttendArgs {
   // where set: the state (m, l) and the mean of each row in 32 bits, [seqs,
   // heads_q] and [seqs, heads_q, dim], in the output's place
   float *state = nullptr, *mean = nullptr;
+  // and no pieces (see KvSharedArgs) of the rows
+  int32_t* pieces = nullptr;
 };
 
 int launch_rope(const RopeArgs& a, int elem, void* stream);

@@ -28,8 +28,8 @@ WeighSpace weigh_space(int64_t plain, int64_t rows, int64_t max_tokens) {
 // each row's state over its own pages, up to two over its group's, and the
 // parts of rows that several blocks share.
 struct SharedSpace {
-  int64_t state = 0, mean = 0, shared_state = 0, shared_mean = 0, parts = 0,
-          bytes = 0;
+  int64_t state = 0, mean = 0, shared_state = 0, shared_mean = 0, pieces = 0,
+          parts = 0, bytes = 0;
 };
 SharedSpace shared_space(int64_t plain, int64_t rows, int dim, int sms) {
   const int64_t states = whole(mul_chk(rows, 8));
@@ -39,7 +39,8 @@ SharedSpace shared_space(int64_t plain, int64_t rows, int dim, int sms) {
   s.mean = add_chk(s.state, states);
   s.shared_state = add_chk(s.mean, means);
   s.shared_mean = add_chk(s.shared_state, 2 * states);
-  s.parts = add_chk(s.shared_mean, mul_chk(means, 2));
+  s.pieces = add_chk(s.shared_mean, mul_chk(means, 2));
+  s.parts = add_chk(s.pieces, 2 * states);
   s.bytes = add_chk(s.parts, 2 * int64_t(sms) * shared_part(dim) * 4);
   return s;
 }
@@ -315,19 +316,18 @@ int lm_kv_attend_shared(
     s.mean = floats(space.shared_mean);
     s.parts = floats(space.parts);
     s.status = a.status;
-    rc = lm::launch_kv_shared(s, plan->store, cuda_stream);
-    if (rc != LM_OK) return;
+    s.pieces = reinterpret_cast<int32_t*>(ws + space.pieces);
     a.state = floats(space.state);
     a.mean = floats(space.mean);
+    a.pieces = s.pieces;
+    // (this one first: it writes that rows have no pieces)
     rc = lm::launch_kv_attend(a, plan->store, cuda_stream);
+    if (rc == LM_OK) rc = lm::launch_kv_shared(s, plan->store, cuda_stream);
     if (rc != LM_OK) return;
     j.out = a.out;
     j.state = a.state;
     j.mean = a.mean;
     j.lse = lse;
-    j.tile_keys = lm::shared_keys(int(plan->dim));
-    j.tile_rows = lm::shared_rows(int(plan->dim));
-    j.blocks = sms;
     rc = lm::launch_kv_join(j, cuda_stream);
   });
   return checked != LM_OK ? checked : rc;

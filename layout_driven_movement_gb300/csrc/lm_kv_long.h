@@ -79,6 +79,11 @@ struct KvSharedArgs {
   // seqs, heads_q] and [2, seqs, heads_q, dim]
   float *state = nullptr, *mean = nullptr;
   float* parts = nullptr;                 // two for each block
+  // Where each row's pieces are, [seqs, heads_q] of 4: how many blocks have one
+  // (0: none), the part that the first of them wrote, the second's (the others'
+  // two on each), and the row's place there, + 65536 where a second state of
+  // the row lies 128 places behind.  One block: its pieces are in `state`.
+  int32_t* pieces = nullptr;
   unsigned int* status = nullptr;
 };
 
@@ -87,7 +92,6 @@ struct KvJoinArgs {
   Rows out;
   const float *state = nullptr, *mean = nullptr;    // of each one's own pages
   float* lse = nullptr;
-  int32_t tile_keys = 1, tile_rows = 1, blocks = 1;
 };
 
 // The tiles of a shared-prefix kernel for rows of `dim` elements.

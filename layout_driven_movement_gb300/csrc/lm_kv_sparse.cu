@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kScoreThreads)
   at.left -= warp;
   for (; at.left > 0; at.left -= kScoreThreads / 32) {
     while (at.in >= int64_t(tiles) * a.heads) {
+      // (never, unless the lengths change while the kernel runs)
+      if (at.b + 1 >= a.seqs) return;
       at.in -= int64_t(tiles) * a.heads;
       tiles = tiles_of(++at.b);
     }

@@ -36,6 +36,8 @@ __global__ void __launch_bounds__(kWeighThreads)
   int64_t tiles = span(at.b, &n, &first);
   for (; at.left > 0; --at.left) {
     while (at.in >= tiles * heads) {
+      // (never, unless the lengths change while the kernel runs)
+      if (at.b + 1 >= a.seqs) return;
       at.in = 0;
       tiles = span(++at.b, &n, &first);
     }

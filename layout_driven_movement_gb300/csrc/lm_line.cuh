@@ -9,9 +9,12 @@ namespace lm {
 
 // a / b of numbers that are not negative; most are small, and a 64-bit
 // division takes several times a 32-bit one's time.
+static __device__ __noinline__ int64_t large_div(int64_t a, int64_t b) {
+  return a / b;
+}
 __device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
   if ((a | b) >> 31 == 0) return uint32_t(a) / uint32_t(b);
-  return a / b;
+  return large_div(a, b);
 }
 
 struct LineShare {
@@ -22,14 +25,34 @@ struct LineShare {
   int64_t in = 0;        // and its number there
 };
 
-// Part `part` of `parts` of the line, for all T threads of the block at once:
-// every thread counts the units of a run of sequences, a scan over the block
-// does the rest.  units(b): those of sequence b, the same whenever asked.
+// Part `part` of `parts` of the line, for all T threads of the block at once.
+// units(b): those of sequence b, the same whenever asked.  Up to 32 sequences
+// are counted by every warp on its own, with no barrier and little code (a
+// kernel's first pass over its code comes from memory); else every thread
+// counts the units of a run of sequences and a scan over the block does the
+// rest.
 template <int T, class F>
 __device__ __forceinline__ LineShare line_share(int seqs, int64_t part,
                                                 int64_t parts, F&& units) {
   __shared__ int64_t sums[T / 32], found[2];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  LineShare s;
+  if (seqs <= 32) {
+    const int64_t mine = lane < seqs ? units(lane) : 0;
+    int64_t sum = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k *= 2) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, k);
+      if (lane >= k) sum += v;
+    }
+    s.total = __shfl_sync(0xffffffffu, sum, 31);
+    s.begin = small_div(part * s.total, parts);
+    s.left = small_div((part + 1) * s.total, parts) - s.begin;
+    // the first sequence whose units end behind `begin`
+    s.b = __ffs(__ballot_sync(0xffffffffu, sum > s.begin)) - 1;
+    s.in = s.begin - __shfl_sync(0xffffffffu, sum - mine, s.b & 31);
+    return s;
+  }
   const int per = (seqs + T - 1) / T;
   const int b0 = min(seqs, int(threadIdx.x) * per);
   const int b1 = min(seqs, b0 + per);
@@ -43,7 +66,6 @@ __device__ __forceinline__ LineShare line_share(int seqs, int64_t part,
   }
   if (lane == 31) sums[warp] = sum;
   __syncthreads();
-  LineShare s;
   int64_t before = sum - mine;
 #pragma unroll
   for (int w = 0; w < T / 32; ++w) {

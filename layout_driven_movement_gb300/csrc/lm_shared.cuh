@@ -14,8 +14,9 @@
 //   warps 8-11  bring keys and values from their pages into shared memory, as
 //               they are or widened from codes, in the 128-byte swizzle
 //   warp 12     one thread issues S_q = Q_q K^T and O_q += P_q V
-//   warps 0-3   and 4-7, one for each tile of queries, a row a thread: S from
-//               tensor memory, its exponentials, and P back in S's place
+//   warps 0-3   and 4-7, one for each tile of queries, a row a thread: the row
+//               of Q into shared memory, then S from tensor memory, its
+//               exponentials, and P back in S's place
 // While one tile's exponentials are taken the tensor cores have the other's
 // products.  Where there are no more than 128 queries, the two take every
 // second tile of keys instead, with states of their own that are joined later.
@@ -27,8 +28,12 @@
 //
 // Weights are one 16-bit part each (bf16's rounding of a weight costs a result
 // about as much as its own): a second part would be half as many products
-// again.  Float16 queries of 8-bit caches get the second part, since their
-// values are met by bf16 weights (of any size, as their scales are).
+// again.  Codes become f16, whose 11 bits hold them, for f16 queries (bf16 ones
+// times a power of two a row) and f16 weights.  A value's scale v_j is folded
+// into its weight's exponent, 2^(s_j + log2 v_j - m), with the reference m the
+// largest such sum: what a weight loses is relative to the largest contribution
+// of its row, whatever the scales.  The sum of the weights alone adds 1 / v_j of
+// each.
 #pragma once
 
 #include "lm_attend.cuh"
@@ -51,9 +56,12 @@ struct SharedShape {
   static constexpr int NS = D == 64 ? 3 : 2;           // stages of K, of V
   // What goes with a tile's keys (scales and which are seen) is read until
   // its weights are written.  When a tile's turn comes the values NS + 1 tiles
-  // before it are done with, so that many hold.
+  // before it are done with, so that many hold: for each key of a cache of
+  // codes its scale times log2(e) and the softmax's, its value's scale's
+  // logarithm to base 2 and the scale's inverse; then the masks, and each
+  // loading warp's least and largest logarithm.
   static constexpr int NM = NS + 1;
-  static constexpr int kMeta = NK * 8 + 32;
+  static constexpr int kMeta = NK * 12 + 48;
   static constexpr uint32_t kOut = 256;                // O's first column
   static constexpr int kBars = 4 * NS + 12;
   static constexpr int kSmem =
@@ -117,6 +125,8 @@ struct SharedWalk {
     seg->s = shared_span(a, g, NK, ROWS);
     int64_t units = int64_t(seg->s.tiles) * seg->s.row_tiles * a.c.heads;
     while (in >= units) {
+      // (never, unless the lengths change while the kernel runs)
+      if (g + 1 >= a.groups) return false;
       in -= units;
       line += units;
       seg->s = shared_span(a, ++g, NK, ROWS);
@@ -137,32 +147,59 @@ struct SharedWalk {
   }
 };
 
-// 16 codes as 16-bit floats, in order.
-template <int STORE, bool BF>
+// 16 codes as f16, in order.
+template <int STORE>
 __device__ __forceinline__ void widen16(const uint4& w, uint32_t* y) {
   const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t p[2];
     if (STORE == LM_KV_E4M3) {
-      Codes<KIND_E4M3>::keys(r[i], p);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (BF) {
-          const float2 f = unpair16<false>(p[j]);
-          p[j] = pair16<true>(f.x, f.y);
-        }
-        y[2 * i + j] = p[j];
-      }
+      Codes<KIND_E4M3>::keys(r[i], y + 2 * i);
     } else {
-      if (BF)
-        Codes<KIND_INT8>::values(r[i], p, nullptr);
-      else
-        Codes<KIND_INT8>::keys(r[i], p);
+      uint32_t p[2];
+      Codes<KIND_INT8>::keys(r[i], p);
       y[2 * i] = __byte_perm(p[0], p[1], 0x5410);
       y[2 * i + 1] = __byte_perm(p[0], p[1], 0x7632);
     }
   }
+}
+
+// Two numbers at a time: the pair forms of a multiplication, an addition and
+// both take one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long y;
+  asm("mul.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(y)
+      : "l"(reinterpret_cast<unsigned long long&>(a)),
+        "l"(reinterpret_cast<unsigned long long&>(b)));
+  return reinterpret_cast<float2&>(y);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long y;
+  asm("add.rn.f32x2 %0, %1, %2;\n"
+      : "=l"(y)
+      : "l"(reinterpret_cast<unsigned long long&>(a)),
+        "l"(reinterpret_cast<unsigned long long&>(b)));
+  return reinterpret_cast<float2&>(y);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long y;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+      : "=l"(y)
+      : "l"(reinterpret_cast<unsigned long long&>(a)),
+        "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return reinterpret_cast<float2&>(y);
+}
+
+// 8 elements of a row that allows no wide loads.  (A call: the 8 loads in every
+// place where a chunk may come this way would be most of the kernel's code.)
+static __device__ __noinline__ uint4 load8_narrow(const uint16_t* x) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = x[2 * i] | uint32_t(x[2 * i + 1]) << 16;
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 __device__ __forceinline__ void st_smem16(uint32_t to, uint32_t a, uint32_t b,
@@ -172,24 +209,23 @@ __device__ __forceinline__ void st_smem16(uint32_t to, uint32_t a, uint32_t b,
                : "memory");
 }
 
-template <int ELEM, int STORE, int D>
+// BF: the cache holds bf16 rows (and the products are bf16's).
+template <bool BF, int STORE, int D>
 __global__ void __launch_bounds__(kSharedThreads, 1)
     lm_kv_shared_kernel(const __grid_constant__ KvSharedArgs a) {
   using S = SharedShape<D>;
   constexpr int NK = S::NK, QT = S::QT, NS = S::NS, NM = S::NM;
   constexpr bool CODES = STORE != LM_KV_SAME;
-  constexpr bool QBF = ELEM == LM_BF16;         // queries and keys are bf16
-  constexpr bool VBF = QBF || CODES;            // values and weights are
-  constexpr int PARTS = CODES && !QBF ? 2 : 1;  // 16-bit parts of a weight
   // A row's reference moves when a score passes it by SLACK (in units of ln
   // 2).  f16 weights lie below 2^15, the reference's at 2^12.  bf16 values
   // reach the end of 32 bits' range, so their weights' sum stays below 1.
-  constexpr float SLACK = VBF ? 8.f : 3.f;
+  constexpr float SLACK = BF ? 8.f : 3.f;
   constexpr int KPW = NK / 4;                   // keys of a loading warp
   extern __shared__ char smem_raw[];
   __shared__ volatile int dead;
   __shared__ uint32_t tmem_at;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0);
+  const int lane = threadIdx.x % 32;
   const int dim = a.c.dim;
   const int dim16 = (dim + 15) / 16 * 16;
 
@@ -214,18 +250,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   const uint32_t q_empty = bars + 8 * (4 * NS + 9);
   const uint32_t drain = bars + 8 * (4 * NS + 10);
 
-  stream_order();
-  const LineShare share = line_share<kSharedThreads>(
-      a.groups, blockIdx.x, gridDim.x, [&](int g) {
-        const SharedSpan s = shared_span(a, g, NK, S::kRows);
-        return int64_t(s.tiles) * s.row_tiles * a.c.heads;
-      });
-  if (share.left <= 0) return;
-
+  // (none of this touches global memory)
   if (threadIdx.x == 0) {
     dead = 0;
+    // a loading thread's copies arrive by themselves, and a warp's scales and
+    // masks with one lane
+    const uint32_t come = CODES ? 128 : 132;
     for (int i = 0; i < NS; ++i) {
-      mbar_init(k_full(i), 128);
+      mbar_init(k_full(i), come);
       mbar_init(k_empty(i), 1);
       mbar_init(v_full(i), 128);
       mbar_init(v_empty(i), 1);
@@ -236,14 +268,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       mbar_init(o_full(q), 1);
       mbar_init(o_empty(q), 128);
     }
-    mbar_init(q_full, 128);
+    mbar_init(q_full, 256);
     mbar_init(q_empty, 1);
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 12)
     tmem_alloc(uint32_t(__cvta_generic_to_shared(&tmem_at)), 512);
+  stream_order();
   tmem_before_sync();
+  const LineShare share = line_share<kSharedThreads>(
+      a.groups, blockIdx.x, gridDim.x, [&](int g) {
+        const SharedSpan s = shared_span(a, g, NK, S::kRows);
+        return int64_t(s.tiles) * s.row_tiles * a.c.heads;
+      });
   __syncthreads();
   tmem_after_sync();
   const uint32_t tmem = tmem_at;
@@ -267,164 +305,160 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const int c = lane % CPR, r0 = lane / CPR;
     const bool held = c * 16 < dim * EB;
     const bool used = c * 16 < dim16 * EB;
-    int tile = 0, nth = 0;
-    int pending = 0;                            // copies not yet announced
-    uint32_t announce[2] = {0, 0};
+    int tile = 0;
     bool alive = true;
-    auto announce_all = [&] {
-      cp_wait<0>();
-      smem_to_products();
-      for (; pending > 0; --pending) {
-        mbar_arrive(announce[0]);
-        announce[0] = announce[1];
-      }
-    };
-    // waits for a stage, with nothing held back meanwhile
     auto acquire = [&](uint32_t bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, mbar_try(bar, parity))) {
-        if (!CODES) announce_all();
-        if (!warp_gate(bar, parity, &dead)) alive = false;
-      }
+      if (!warp_gate(bar, parity, &dead)) alive = false;
     };
-    const float unit = fabsf(a.scale) * 1.44269504088896341f;
+    const float unit =
+        a.scale == 0 ? 1.f : fabsf(a.scale) * 1.44269504088896341f;
+    const bool mine = KPW == 32 || lane < KPW;       // a key of this lane's
+    const uint32_t to = lw * KPW * 128;
     while (alive && walk.next(a, &seg)) {
       const int32_t* const table = a.table + seg.g * a.table_stride;
+      const int t1 = seg.t0 + seg.steps;
       auto look = [&](int t) {
         const int key = t * NK + lw * KPW + lane;
-        return (KPW == 32 || lane < KPW) && t < seg.t0 + seg.steps &&
-                       key < seg.s.len
+        return mine && t < t1 && key < seg.s.len
                    ? table[fdiv(uint32_t(key), a.c.page_div)]
                    : -1;
       };
       int page = look(seg.t0);
-      // the queries, turned round where the scale is negative
-      if (nth > 0) {
-        if (!CODES) announce_all();
-        if (!warp_gate(q_empty, (nth - 1) & 1, &dead)) break;
-      }
-      {
-        const int tiles = split_of(seg) ? 1 : (seg.rows + 127) / 128;
-        const uint16_t flip = a.scale < 0 ? 0x8000 : 0;
-        const uint32_t flip2 = flip * 0x10001u;
-        const int chunks = dim16 / 8;
-        for (int u = threadIdx.x - 256; u < tiles * 128 * chunks; u += 128) {
-          const int row = u / chunks, ch = u - row * chunks;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (row < seg.rows && ch * 8 < dim) {
-            const int rg = seg.rt * S::kRows + row;
-            const int si = rg / a.group;
-            const uint16_t* q =
-                reinterpret_cast<const uint16_t*>(a.q.p) +
-                int64_t(seg.s.start + si) * a.q.ts +
-                int64_t(seg.h * a.group + (rg - si * a.group)) * a.q.hs +
-                ch * 8;
-            if (a.q16) {
-              w = *reinterpret_cast<const uint4*>(q);
-            } else {
-              uint32_t r[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                r[i] = q[2 * i] | uint32_t(q[2 * i + 1]) << 16;
-              w = make_uint4(r[0], r[1], r[2], r[3]);
-            }
-          }
-          const uint32_t to = q_s + row / 128 * S::kQ + ch / 8 * (128 * 128) +
-                              row % 128 * 128 + ((ch ^ row) & 7) * 16;
-          st_smem16(to, w.x ^ flip2, w.y ^ flip2, w.z ^ flip2, w.w ^ flip2);
-        }
-        smem_to_products();
-        mbar_arrive(q_full);
-      }
-      ++nth;
-      for (int t = seg.t0; t < seg.t0 + seg.steps && alive; ++t, ++tile) {
+      // the lane's key of tile t, whose page has been looked up: where its row
+      // lies (-1: not seen), and the next tile's page on its way
+      int64_t from, scale_at;
+      uint32_t seen;
+      auto find = [&](int t) {
         const int key = t * NK + lw * KPW + lane;
-        const bool in = (KPW == 32 || lane < KPW) && key < seg.s.len;
+        const bool in = mine && t < t1 && key < seg.s.len;
         const bool ok = in && page >= 0 && page < a.c.pages;
         if (in && !ok && a.status) atomicOr(a.status, kStatusRange);
         const uint32_t off =
             uint32_t(key) - fdiv(uint32_t(key), a.c.page_div) * a.c.page_tokens;
-        const int64_t from =
-            ok ? int64_t(page) * a.c.page_b + int64_t(off) * a.c.token_b +
-                     int64_t(seg.h) * a.c.head_b
-               : -1;
-        float ku = 0, vs = 0;
-        if (CODES && ok) {
-          const int64_t so = (int64_t(page) * a.c.heads + seg.h) *
-                                 a.c.page_tokens + off;
-          ku = a.c.ks[so] * unit;
-          vs = a.c.vs[so];
-        }
-        const uint32_t seen = __ballot_sync(0xffffffffu, ok);
+        from = ok ? int64_t(page) * a.c.page_b + int64_t(off) * a.c.token_b +
+                        int64_t(seg.h) * a.c.head_b
+                  : -1;
+        if (CODES)
+          scale_at = ok ? (int64_t(page) * a.c.heads + seg.h) *
+                                  a.c.page_tokens +
+                              off
+                        : -1;
+        seen = __ballot_sync(0xffffffffu, ok);
         page = look(t + 1);
-        const int slot = tile % NS;
-        const uint32_t turn = tile / NS & 1;
-        const uint32_t to = lw * KPW * 128;
-        if constexpr (CODES) {
-          uint4 kr[IT], vr[IT];
+      };
+      if constexpr (CODES) {
+        // Codes pass through registers.  The next tile's keys are asked for
+        // while this one's values are widened, its values while the next one's
+        // keys are.
+        uint4 kr[IT], vr[IT];
+        float ks, vs;
+        auto ask = [&](uint4* w, const char* rows) {
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
             const int64_t o = __shfl_sync(0xffffffffu, from, i * RPI + r0);
-            kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-            if (o >= 0 && held) {
-              kr[i] = *reinterpret_cast<const uint4*>(a.c.k + o + c * 16);
-              vr[i] = *reinterpret_cast<const uint4*>(a.c.v + o + c * 16);
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (o >= 0 && held)
+              w[i] = *reinterpret_cast<const uint4*>(rows + o + c * 16);
+          }
+        };
+        auto ask_keys = [&](int t) {
+          find(t);
+          ks = vs = 0;
+          if (scale_at >= 0) {
+            ks = a.c.ks[scale_at];
+            vs = a.c.vs[scale_at];
+          }
+          ask(kr, a.c.k);
+        };
+        // widened to f16, with the sign of a row's factor (0: zeros)
+        auto widen = [&](uint32_t tile_s, const uint4* w, float factor) {
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            const int r = i * RPI + r0;
+            const float f = __shfl_sync(0xffffffffu, factor, r);
+            const uint32_t flip = f < 0 ? 0x80008000u : 0;
+            const bool zero = f == 0;
+            uint32_t y[8];
+            widen16<STORE>(w[i], y);
+            if (!held) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int ch = 2 * c + j;
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = zero ? 0 : y[4 * j + e] ^ flip;
+              st_smem16(tile_s + ch / 8 * (NK * 128) + r * 128 +
+                            ((ch ^ r) & 7) * 16,
+                        x[0], x[1], x[2], x[3]);
             }
           }
+          smem_to_products();
+        };
+        ask_keys(seg.t0);
+        ask(vr, a.c.v);
+        for (int t = seg.t0; t < t1 && alive; ++t, ++tile) {
+          const int slot = tile % NS;
+          const uint32_t turn = tile / NS & 1;
+          if (tile >= NS) acquire(k_empty(slot), turn ^ 1);
+          if (!alive) break;
+          // (see NM: nothing reads these any more)
+          char* const m = metas + tile % NM * S::kMeta;
+          // scales beyond 2^+-96 count as those; one of 0, whose values are
+          // taken as 0, as the largest about
           float top = fabsf(vs);
 #pragma unroll
           for (int k = 16; k; k /= 2)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+          const float size =
+              vs == 0 ? (top > 0 ? top : 1.f) : fabsf(vs);
+          const float held_size =
+              size < INFINITY ? fminf(fmaxf(size, 0x1p-96f), 0x1p96f) : size;
+          const float log_size = log2f(held_size);
+          float least = log_size, most = log_size;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            if (tile >= NS)
-              acquire(kv ? v_empty(slot) : k_empty(slot), turn ^ 1);
-            if (!alive) break;
-            if (kv == 0) {
-              // (see NM: nothing reads these any more)
-              char* const m = metas + tile % NM * S::kMeta;
-              if (KPW == 32 || lane < KPW) {
-                float* f = reinterpret_cast<float*>(m) + lw * KPW + lane;
-                f[0] = ku;
-                f[NK] = vs;
-              }
-              if (lane == 0) {
-                uint32_t* w = reinterpret_cast<uint32_t*>(m + NK * 8);
-                w[lw] = seen;
-                w[4 + lw] = __float_as_uint(top);
-              }
-            }
-            const uint32_t tile_s = (kv ? v_s : k_s) + slot * S::kTile + to;
-            if (held) {
-#pragma unroll
-              for (int i = 0; i < IT; ++i) {
-                const int r = i * RPI + r0;
-                uint32_t y[8];
-                if (kv)
-                  widen16<STORE, true>(vr[i], y);
-                else
-                  widen16<STORE, QBF>(kr[i], y);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const int ch = 2 * c + j;
-                  st_smem16(tile_s + ch / 8 * (NK * 128) + r * 128 +
-                                ((ch ^ r) & 7) * 16,
-                            y[4 * j], y[4 * j + 1], y[4 * j + 2],
-                            y[4 * j + 3]);
-                }
-              }
-            }
-            smem_to_products();
-            mbar_arrive(kv ? v_full(slot) : k_full(slot));
+          for (int k = 16; k; k /= 2) {
+            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, k));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
           }
-        } else {
+          if (mine) {
+            float* f = reinterpret_cast<float*>(m) + lw * KPW + lane;
+            f[0] = scale_at >= 0 ? ks * unit : 1.f;
+            f[NK] = log_size;
+            f[2 * NK] = 1.f / held_size;
+          }
+          if (lane == 0) {
+            reinterpret_cast<uint32_t*>(m + NK * 12)[lw] = seen;
+            float* f = reinterpret_cast<float*>(m + NK * 12 + 16);
+            f[lw] = least;
+            f[4 + lw] = most;
+          }
+          widen(k_s + slot * S::kTile + to, kr, 1.f);
+          mbar_arrive(k_full(slot));
+          const float factor = vs;
+          ask_keys(t + 1);
+          if (tile >= NS) acquire(v_empty(slot), turn ^ 1);
+          if (!alive) break;
+          widen(v_s + slot * S::kTile + to, vr, factor);
+          mbar_arrive(v_full(slot));
+          ask(vr, a.c.v);
+        }
+      } else {
+        for (int t = seg.t0; t < t1 && alive; ++t, ++tile) {
+          find(t);
+          const int slot = tile % NS;
+          const uint32_t turn = tile / NS & 1;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             if (tile >= NS)
               acquire(kv ? v_empty(slot) : k_empty(slot), turn ^ 1);
             if (!alive) break;
-            if (kv == 0 && lane == 0)
+            // (see NM: nothing reads the mask there any more)
+            if (kv == 0 && lane == 0) {
               reinterpret_cast<uint32_t*>(metas + tile % NM * S::kMeta +
-                                          NK * 8)[lw] = seen;
+                                          NK * 12)[lw] = seen;
+              mbar_arrive(k_full(slot));
+            }
             const uint32_t tile_s = (kv ? v_s : k_s) + slot * S::kTile + to;
             const char* const src = kv ? a.c.v : a.c.k;
 #pragma unroll
@@ -437,95 +471,114 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                          ((c ^ r) & 7) * 16,
                      src + (bytes ? o + c * 16 : 0), bytes);
             }
-            cp_commit();
-            // two copies stay in flight; the one before them has come
-            const uint32_t bar = kv ? v_full(slot) : k_full(slot);
-            if (pending == 2) {
-              cp_wait<2>();
-              smem_to_products();
-              mbar_arrive(announce[0]);
-              announce[0] = announce[1];
-              announce[1] = bar;
-            } else {
-              announce[pending++] = bar;
-            }
+            cp_async_arrive_noinc(kv ? v_full(slot) : k_full(slot));
           }
         }
       }
     }
-    if (!CODES) announce_all();
+    cp_commit();
+    cp_wait<0>();
   } else if (warp == 12) {
-    // --- products: one thread ---
-    if (lane == 0) {
-      const uint32_t kind_s = mma_kind(QBF, false, 128, NK);
-      const uint32_t kind_o = mma_kind(VBF, true, 128, dim16);
-      const int ks = dim16 / 16;
-      int tile = 0, nth = 0;
-      int n_p[2] = {0, 0}, n_o[2] = {0, 0};
-      bool alive = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (alive && !gate(bar, parity, &dead)) alive = false;
-        tmem_after_sync();
-        return alive;
+    // --- products: the warp together, one lane issues ---
+    const uint32_t kind_s = mma_kind(BF, false, 128, NK);
+    const uint32_t kind_o = mma_kind(BF, true, 128, dim16);
+    const int ks = dim16 / 16;
+    const uint64_t q_op = smem_operand(q_s, 16, 1024);
+    const uint64_t k_op = smem_operand(k_s, 16, 1024);
+    const uint64_t v_op = smem_operand(v_s, NK * 128, 1024);
+    int tile = 0, nth = 0;
+    // the phases of p_full and o_empty, a bit a tile of queries, and whether a
+    // tile's O was ever read
+    uint32_t p_phase = 0, o_phase = 0, o_read = 0;
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (alive && !warp_gate(bar, parity, &dead)) alive = false;
+      return alive;
+    };
+    while (alive && walk.next(a, &seg)) {
+      const bool split = split_of(seg);
+      const int per = split || QT == 1 ? 1 : (seg.rows + 127) / 128;
+      const int units = seg.steps * per;
+      // unit u: key tile u / per, and which half of the exponential warps has
+      // it
+      const bool two = split || per == 2;
+      const int ahead = two ? 2 : 1;
+      bool keys = false;               // unit u's keys have been waited for
+      auto look_ahead = [&](int u) {
+        if (per == 2 && (u & 1)) return;
+        const int t = tile + (per == 2 ? u / 2 : u);
+        keys = __all_sync(0xffffffffu, mbar_try(k_full(t % NS), t / NS & 1));
+        if (keys) smem_to_products();
       };
-      while (alive && walk.next(a, &seg)) {
-        const bool split = split_of(seg);
-        const int per = split || QT == 1 ? 1 : (seg.rows + 127) / 128;
-        const int units = seg.steps * per;
-        // unit u: key tile u / per, and which half of the exponential warps
-        // has it
-        auto q_of = [&](int u) {
-          return split ? u & 1 : per == 2 ? u & 1 : 0;
-        };
-        const int ahead = split || per == 2 ? 2 : 1;
-        auto score = [&](int u) {
-          const int j = u / per, t = tile + j, slot = t % NS, q = q_of(u);
-          if (u % per == 0 && !wait(k_full(slot), t / NS & 1)) return;
-          const uint32_t qa = q_s + (split ? 0 : q) * S::kQ;
-          const uint32_t ka = k_s + slot * S::kTile;
-          for (int k = 0; k < ks; ++k)
-            mma_ss(tmem + q * NK,
-                   smem_operand(qa + k / 4 * (128 * 128) + k % 4 * 32, 16, 1024),
-                   smem_operand(ka + k / 4 * (NK * 128) + k % 4 * 32, 16, 1024),
-                   kind_s, k > 0);
-          mma_commit(s_full(q));
-          if (u % per == per - 1) mma_commit(k_empty(slot));
-          if (u == units - 1) mma_commit(q_empty);
-        };
-        if (!wait(q_full, nth & 1)) break;
-        ++nth;
-        for (int u = 0; u < ahead && u < units; ++u) score(u);
-        for (int u = 0; u < units && alive; ++u) {
-          const int j = u / per, t = tile + j, slot = t % NS, q = q_of(u);
-          if (!wait(p_full(q), n_p[q]++ & 1)) break;
-          if (u % per == 0 && !wait(v_full(slot), t / NS & 1)) break;
-          const bool first = split ? u < 2 : j == 0;
-          if (first && n_o[q] > 0 && !wait(o_empty(q), (n_o[q] - 1) & 1)) break;
-          const uint32_t va = v_s + slot * S::kTile;
-          const uint32_t o = tmem + S::kOut + q * D;
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-            for (int i = 0; i < NK / 16; ++i)
-              mma_ts(o,
-                     tmem + q * NK + i / 2 * 32 + part * 16 + i % 2 * 8,
-                     smem_operand(va + i * 2048, NK * 128, 1024), kind_o,
-                     !(first && part == 0 && i == 0));
-          if (u % per == per - 1) mma_commit(v_empty(slot));
-          if (u + (split ? 2 : per) >= units) {
-            mma_commit(o_full(q));
-            ++n_o[q];
-          }
-          if (u + ahead < units) score(u + ahead);
+      auto score = [&](int u) {
+        const int j = per == 2 ? u / 2 : u, t = tile + j, slot = t % NS;
+        const int q = two ? u & 1 : 0;
+        if ((per == 1 || q == 0) && !keys) {
+          if (!wait(k_full(slot), t / NS & 1)) return;
+          smem_to_products();
         }
-        tile += seg.steps;
+        keys = false;
+        tmem_after_sync();
+        if (one_lane()) {
+          const uint64_t qa = q_op + (split ? 0 : q) * (S::kQ / 16);
+          const uint64_t ka = k_op + slot * (S::kTile / 16);
+          const uint32_t to = tmem + q * NK;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            if (k >= ks) break;
+            mma_ss(to, qa + (k / 4 * (128 * 128) + k % 4 * 32) / 16,
+                   ka + (k / 4 * (NK * 128) + k % 4 * 32) / 16, kind_s, k > 0);
+          }
+          mma_commit(s_full(q));
+          if (per == 1 || q == 1) mma_commit(k_empty(slot));
+          if (u == units - 1) mma_commit(q_empty);
+        }
+        __syncwarp();
+      };
+      if (!wait(q_full, nth & 1)) break;
+      ++nth;
+      for (int u = 0; u < ahead && u < units; ++u) score(u);
+      for (int u = 0; u < units && alive; ++u) {
+        const int j = per == 2 ? u / 2 : u, t = tile + j, slot = t % NS;
+        const int q = two ? u & 1 : 0;
+        // (the values, and the next scores' keys if they are there already,
+        // before the weights, which are waited for longest)
+        if (per == 1 || q == 0) {
+          if (!wait(v_full(slot), t / NS & 1)) break;
+          smem_to_products();
+        }
+        if (u + ahead < units) look_ahead(u + ahead);
+        if (!wait(p_full(q), p_phase >> q & 1)) break;
+        p_phase ^= 1u << q;
+        const bool first = split ? u < 2 : j == 0;
+        if (first && (o_read >> q & 1)) {
+          if (!wait(o_empty(q), o_phase >> q & 1)) break;
+          o_phase ^= 1u << q;
+        }
+        const bool last = u + (split ? 2 : per) >= units;
+        tmem_after_sync();
+        if (one_lane()) {
+          const uint64_t va = v_op + slot * (S::kTile / 16);
+          const uint32_t o = tmem + S::kOut + q * D;
+          const uint32_t p = tmem + q * NK;
+#pragma unroll
+          for (int i = 0; i < NK / 16; ++i)
+            mma_ts(o, p + i / 2 * 32 + i % 2 * 8, va + i * (2048 / 16), kind_o,
+                   !(first && i == 0));
+          if (per == 1 || q == 1) mma_commit(v_empty(slot));
+          if (last) mma_commit(o_full(q));
+        }
+        __syncwarp();
+        if (last) o_read |= 1u << q;
+        if (u + ahead < units) score(u + ahead);
       }
-      if (dead) {
-        // products may still read shared memory and write tensor memory
-        mma_commit(drain);
-        mbar_wait(drain, 0, kDrainCycles);
-      }
+      tile += seg.steps;
     }
-    __syncwarp();
+    if (dead) {
+      // products may still read shared memory and write tensor memory
+      if (one_lane()) mma_commit(drain);
+      warp_wait(drain, 0, kDrainCycles);
+    }
   } else {
     // --- exponentials: a row a thread ---
     const int q = warp / 4;
@@ -533,129 +586,278 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t quarter = uint32_t(warp % 4 * 32) << 16;
     const uint32_t s_at = tmem + q * NK + quarter;
     const uint32_t o_at = tmem + S::kOut + q * D + quarter;
-    const float unit = fabsf(a.scale) * 1.44269504088896341f;
-    int tile = 0, n_s = 0, n_o = 0;
+    // (with a scale of 0 the queries are taken as 0)
+    const float unit =
+        a.scale == 0 ? 1.f : fabsf(a.scale) * 1.44269504088896341f;
+    const uint32_t flip = a.scale < 0 ? 0x80008000u : 0;
+    int tile = 0, nth = 0, n_s = 0, n_o = 0;
     bool alive = true;
     while (alive && walk.next(a, &seg)) {
       const bool split = split_of(seg);
       const int t_first = tile;
       tile += seg.steps;
-      if (!split && q * 128 >= seg.rows) continue;
-      float m = -INFINITY, l = 0, gain = 1;
-      bool gained = false;
+      const int r = split ? row : q * 128 + row;
+      const int rg = seg.rt * S::kRows + r;
+      const int si = rg / a.group;
+      const bool valid = r < seg.rows;
+      const uint16_t* const query =
+          reinterpret_cast<const uint16_t*>(a.q.p) +
+          int64_t(seg.s.start + si) * a.q.ts +
+          int64_t(seg.h * a.group + (rg - si * a.group)) * a.q.hs;
+      const int step = split ? 2 : 1;
+      const bool active = split || q * 128 < seg.rows;
+      float m = -INFINITY, l = 0;
+      float down = 1;              // of codes: what a row's query was held times
+      float most = -INFINITY;      // and the largest logarithm of a scale so far
       // the reference's weight, as a power of two
-      const float off =
-          VBF ? -float(8 + 32 - __clz(seg.steps * NK)) : 12.f;
+      const float off = BF ? -float(8 + 32 - __clz(seg.steps * NK)) : 12.f;
       bool first = true;
-      for (int j = split ? q : 0; j < seg.steps; j += split ? 2 : 1) {
-        if (!warp_gate(s_full(q), n_s++ & 1, &dead)) {
-          alive = false;
-          break;
-        }
-        tmem_after_sync();
-        const char* const meta = metas + (t_first + j) % NM * S::kMeta;
-        const float* const ku = reinterpret_cast<const float*>(meta);
-        const uint32_t* const words =
-            reinterpret_cast<const uint32_t*>(meta + NK * 8);
-        uint32_t seen[NK / 32];
-        bool part = false;
-#pragma unroll
-        for (int i = 0; i < NK / 32; ++i) {
-          seen[i] = KPW == 32 ? words[i] : words[2 * i] | words[2 * i + 1] << 16;
-          part |= seen[i] != 0xffffffffu;
-        }
-        // the largest score
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NK / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32(r, s_at + c * 32);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float x = __uint_as_float(r[i]);
-            if (CODES) x *= ku[c * 32 + i];
-            if (part && !(seen[c] >> i & 1)) x = -INFINITY;
-            top = fmaxf(top, x);
+      // Tile -1 stands for the row's query, which goes to shared memory.  In
+      // the block's first one the weights are formed once of whatever tensor
+      // memory holds and thrown away: so that their instructions, which come
+      // from memory the first time (some 5000 cycles), are there when the first
+      // scores are.
+      for (int j = -1;;) {
+        if (j >= 0) {
+          if (!warp_gate(s_full(q), n_s & 1, &dead)) {
+            alive = false;
+            break;
           }
+          ++n_s;
+          tmem_after_sync();
         }
-        if (!CODES) top *= unit;
-        const bool move = top > m + SLACK;
-        // values' scales are met times `gain`, a power of two: the largest of
-        // the first tile lies at 1, and one that passes 2^40 sets it again
-        float scale_o = 1;
-        bool change = move;
-        if (CODES) {
-          float big = 0;
+        if (j >= 0 || nth == 0) {
+          const char* const meta = metas + (t_first + max(j, 0)) % NM * S::kMeta;
+          const float2* const ku = reinterpret_cast<const float2*>(meta);
+          const uint32_t* const words =
+              reinterpret_cast<const uint32_t*>(meta + NK * 12);
+          // which of 32 keys are seen
+          auto seen = [&](int c) {
+            return KPW == 32 ? words[c]
+                             : words[2 * c] | words[2 * c + 1] << 16;
+          };
+          // (Tile -1 takes no way that hangs on what is there: the masks of tile
+          // 0 may just be written, and a warp whose lanes read them before and
+          // after would come apart.)
+          bool part = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            big = fmaxf(big, __uint_as_float(words[4 + i]));
-          if (big > 0 && (!gained || big * gain > 0x1p40f)) {
-            const int e = min(max(127 - int(__float_as_uint(big) >> 23), -120),
-                              120);
-            const float next = __int_as_float((127 + e) << 23);
-            scale_o = next / gain;
-            gain = next;
-            gained = change = true;
-          }
-        }
-        if (__any_sync(0xffffffffu, change)) {
-          if (move) {
-            const float keep = ex2(m - top);
-            l *= keep;
-            scale_o *= keep;
-            m = top;
-          }
-          __syncwarp();
-          if (!first) {
+          for (int c = 0; c < NK / 32; ++c) part |= seen(c) != 0xffffffffu;
+          part = __any_sync(0xffffffffu, part && j >= 0);
+          // where not all keys are seen: -infinity for those that are not
+          if (part) {
 #pragma unroll 1
-            for (int c = 0; c < dim; c += 32) {
-              uint32_t r[32];
-              tmem_ld32(r, o_at + c);
+            for (int c = 0; c < NK / 32; ++c) {
+              uint32_t s[32];
+              tmem_ld32(s, s_at + c * 32);
               tmem_wait_ld();
+              const uint32_t mask = seen(c);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                r[i] = __float_as_uint(__uint_as_float(r[i]) * scale_o);
-              tmem_st32(o_at + c, r);
+                if (!(mask >> i & 1)) s[i] = 0xff800000u;
+              tmem_st16(s_at + c * 32, s);
+              tmem_st16(s_at + c * 32 + 16, s + 16);
+            }
+            tmem_wait_st();
+          }
+          // The largest exponent, in units of ln 2.  (64 columns at a time,
+          // here and below: a row's 128 at once are twice the instructions.)
+          const float2 by = make_float2(down, down);
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < NK; c += 64) {
+            uint32_t s[64];
+            tmem_ld32(s, s_at + c);
+            tmem_ld32(s + 32, s_at + c + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              float2 x = make_float2(__uint_as_float(s[i]),
+                                     __uint_as_float(s[i + 1]));
+              if (CODES)
+                x = fma2(mul2(x, ku[(c + i) / 2]), by, ku[(NK + c + i) / 2]);
+              tops[i % 4] = fmaxf(tops[i % 4], x.x);
+              tops[i % 4 + 1] = fmaxf(tops[i % 4 + 1], x.y);
             }
           }
-        }
-        first = false;
-        const float sub = (m == -INFINITY ? 0.f : m) - off;
-#pragma unroll
-        for (int c = 0; c < NK / 32; ++c) {
-          uint32_t r[32], hi[16], lo[16];
-          tmem_ld32(r, s_at + c * 32);
-          tmem_wait_ld();
-          float sum = 0;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float w[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float x = __fmaf_rn(__uint_as_float(r[i + k]),
-                                  CODES ? ku[c * 32 + i + k] : unit, -sub);
-              if (part && !(seen[c] >> (i + k) & 1)) x = -INFINITY;
-              w[k] = ex2(x);
-              sum += w[k];
-              if (CODES) w[k] *= ku[NK + c * 32 + i + k] * gain;
+          float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+          if (!CODES) top *= unit;
+          const bool move = top > m + SLACK;
+          if (__any_sync(0xffffffffu, move)) {
+            float keep = 1;
+            if (move) {
+              // (in two halves: with scales of values far apart the whole may
+              // be below 2^-126 and the sum above 2^100)
+              keep = ex2(0.5f * (m - top));
+              l = l * keep * keep;
+              keep *= keep;
+              m = top;
             }
-            hi[i / 2] = pair16<VBF>(w[0], w[1]);
-            if (PARTS == 2) {
-              const float2 f = unpair16<VBF>(hi[i / 2]);
-              lo[i / 2] = pair16<VBF>(w[0] - f.x, w[1] - f.y);
+            __syncwarp();
+            if (!first) {
+#pragma unroll 1
+              for (int c = 0; c < dim; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, o_at + c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                tmem_st16(o_at + c, o);
+                tmem_st16(o_at + c + 16, o + 16);
+              }
             }
           }
-          l += sum;
-          tmem_st16(s_at + c * 32, hi);
-          if (PARTS == 2) tmem_st16(s_at + c * 32 + 16, lo);
+          first = false;
+          const float sub = off - (m == -INFINITY ? 0.f : m);
+          const float2 sub2 = make_float2(sub, sub);
+          const float2 unit2 = make_float2(unit, unit);
+          float2 sums[2] = {make_float2(0, 0), make_float2(0, 0)};
+          // A code's weight alone is its exponential over its value's scale --
+          // unless scales lie so far apart that an exponential may be below
+          // 2^-126 where the weight is not small: then weights are summed for
+          // themselves.
+          bool apart = false;
+          if (CODES) {
+            const float* const ends =
+                reinterpret_cast<const float*>(meta + NK * 12 + 16);
+            float least = INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              least = fminf(least, ends[i]);
+              most = fmaxf(most, ends[4 + i]);
+            }
+            apart = __any_sync(0xffffffffu, most - least > 60 && j >= 0);
+            if (apart) {
+#pragma unroll 1
+              for (int c = 0; c < NK; c += 32) {
+                uint32_t s[32];
+                tmem_ld32(s, s_at + c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float2 x = make_float2(__uint_as_float(s[i]),
+                                         __uint_as_float(s[i + 1]));
+                  x = fma2(mul2(x, ku[(c + i) / 2]), by, sub2);
+                  l += ex2(x.x) + ex2(x.y);
+                }
+              }
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < NK; c += 64) {
+            uint32_t s[64];
+            tmem_ld32(s, s_at + c);
+            tmem_ld32(s + 32, s_at + c + 32);
+            tmem_wait_ld();
+#pragma unroll
+            for (int half = 0; half < 64; half += 32) {
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const int at = (c + half + i) / 2;
+                float2 x = make_float2(__uint_as_float(s[half + i]),
+                                       __uint_as_float(s[half + i + 1]));
+                if (CODES)
+                  x = fma2(mul2(x, ku[at]), by, add2(ku[NK / 2 + at], sub2));
+                else
+                  x = fma2(x, unit2, sub2);
+                x = make_float2(ex2(x.x), ex2(x.y));
+                float2& sum = sums[i / 2 % 2];
+                sum = CODES ? fma2(x, ku[NK + at], sum) : add2(x, sum);
+                p[i / 2] = pair16<BF>(x.x, x.y);
+              }
+              tmem_st16(s_at + c + half, p);
+            }
+          }
+          if (!apart) l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+          tmem_wait_st();
         }
-        tmem_wait_st();
-        tmem_before_sync();
-        mbar_arrive(p_full(q));
+        if (j >= 0) {
+          tmem_before_sync();
+          mbar_arrive(p_full(q));
+          j += step;
+        } else {
+          m = most = -INFINITY;
+          l = 0;
+          first = true;
+          // the row's query, turned round where the scale is negative
+          if (nth > 0 && !warp_gate(q_empty, (nth - 1) & 1, &dead)) {
+            alive = false;
+            break;
+          }
+          ++nth;
+          const bool row_in = valid && a.scale != 0;
+          auto load = [&](int c) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (row_in && c * 8 < dim) {
+              if (a.q16)
+                w = *reinterpret_cast<const uint4*>(query + c * 8);
+              else
+                w = load8_narrow(query + c * 8);
+            }
+            return w;
+          };
+          // Codes are met by f16 queries, scaled by a power of two so that the
+          // largest element lies in [2^14, 2^15): exact for bf16 elements down
+          // to 2^-31 of it and f16 ones down to 2^-28, below that within 2^-39
+          // of it.
+          float up = 1;
+          const bool in_bf = a.elem == LM_BF16;
+          if (CODES) {
+            float top = 0;
+#pragma unroll 4
+            for (int c = 0; c < dim16 / 8; ++c) {
+              const uint4 w = load(c);
+              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = in_bf ? unpair16<true>(x[i])
+                                       : unpair16<false>(x[i]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            }
+            int e = 14 + 127 - int(__float_as_uint(top) >> 23);
+            if (top == 0 || top == INFINITY) e = 0;
+            e = min(120, max(-120, e));
+            up = __int_as_float((127 + e) << 23);
+            down = __int_as_float((127 - e) << 23);
+          }
+          if (q * 128 < (split ? 128 : seg.rows)) {
+            const uint32_t to = q_s + q * S::kQ + row * 128;
+#pragma unroll 1
+            for (int c0 = 0; c0 < dim16 / 8; c0 += 8) {
+              uint4 w[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) w[c] = load(c0 + c);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (CODES) {
+                    const float2 f = in_bf ? unpair16<true>(x[i])
+                                           : unpair16<false>(x[i]);
+                    x[i] = pair16<false>(f.x * up, f.y * up);
+                  }
+                  x[i] ^= flip;
+                }
+                if ((c0 + c) * 8 < dim16)
+                  st_smem16(to + c0 / 8 * (128 * 128) + ((c ^ row) & 7) * 16,
+                            x[0], x[1], x[2], x[3]);
+              }
+            }
+          }
+          smem_to_products();
+          tmem_before_sync();
+          mbar_arrive(q_full);
+          if (!active) break;
+          j = split ? q : 0;
+        }
+        if (j >= seg.steps) break;
       }
       if (!alive) break;
       // --- the rows' states ---
+      if (!active) continue;
       const bool none = first;                   // no tile of keys
       if (!none) {
         if (!warp_gate(o_full(q), n_o & 1, &dead)) break;
@@ -663,10 +865,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         tmem_after_sync();
       }
       const bool whole = seg.steps == seg.s.tiles;
-      const int r = split ? row : q * 128 + row;
-      const bool valid = r < seg.rows;
-      const int rg = seg.rt * S::kRows + r;
-      const int si = rg / a.group;
       const int sub = split ? q : 0;
       const int64_t out_row =
           int64_t(sub) * a.seqs * a.heads_q +
@@ -677,19 +875,34 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           a.parts + (2 * int64_t(blockIdx.x) +
                      (share.begin < seg.item_at ? 1 : 0)) *
                         (int64_t(S::kRows) * (D + 2));
-      // weights were taken times 2^off (and the values' gain)
+      // weights were taken times 2^off
       const float f = l == 0 ? 0.f : __fdividef(1.f, l);
+      if (valid && sub == 0 && seg.t0 == 0) {
+        // where the row's pieces will be: the block of tile i of the line is
+        // ((i + 1) blocks - 1) / total
+        const int64_t c1 = small_div(
+            (seg.item_at + seg.s.tiles) * gridDim.x - 1, share.total);
+        const int n = int(c1 - blockIdx.x) + 1;
+        reinterpret_cast<int4*>(a.pieces)[out_row] = make_int4(
+            n, 2 * int(blockIdx.x) + (share.begin < seg.item_at ? 1 : 0),
+            2 * int(blockIdx.x) + 2, (q * 128 + row) | (split ? 65536 : 0));
+      }
       if (valid) {
-        const float2 ml = make_float2(none ? -INFINITY : m - off, l);
+        // (the sum's exponent goes to the reference: next to scales of values
+        // the sum may be of any size, and references far apart then say nothing
+        // about weights)
+        const int e = int(__float_as_uint(l) >> 23) - 127;
+        float2 ml = make_float2(none ? -INFINITY : m - off, l);
+        if (CODES && l > 0x1p-120f && l < INFINITY) {
+          ml.x += float(e);
+          ml.y *= __int_as_float((127 - e) << 23);
+        }
         if (whole)
           reinterpret_cast<float2*>(a.state)[out_row] = ml;
         else
           reinterpret_cast<float2*>(part)[part_row] = ml;
       }
       if (!none) {
-        const int ge = 127 - (__float_as_int(gain) >> 23);
-        const float g1 = __int_as_float((127 + ge / 2) << 23);
-        const float g2 = __int_as_float((127 + ge - ge / 2) << 23);
 #pragma unroll 1
         for (int c = 0; c < dim; c += 32) {
           uint32_t x[32];
@@ -702,10 +915,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             float4 y;
             float* const ys = &y.x;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              ys[k] = __uint_as_float(x[i + k]) * f;
-              if (CODES) ys[k] = ys[k] * g1 * g2;
-            }
+            for (int k = 0; k < 4; ++k) ys[k] = __uint_as_float(x[i + k]) * f;
             float* to = whole ? a.mean + out_row * dim + c + i
                               : part + 2 * S::kRows +
                                     (int64_t((c + i) / 4) * S::kRows +
@@ -728,13 +938,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   if (threadIdx.x == 0 && dead && a.status) atomicOr(a.status, kStatusTimeout);
 }
 
-template <int ELEM, int STORE, int D>
+template <bool BF, int STORE, int D>
 int launch_shared_d(const KvSharedArgs& a, cudaStream_t st) {
   using S = SharedShape<D>;
   int sms = 0, dev = 0;
   const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  auto* kernel = lm_kv_shared_kernel<ELEM, STORE, D>;
+  auto* kernel = lm_kv_shared_kernel<BF, STORE, D>;
   static std::atomic<uint64_t> allowed{0};    // a bit per device
   if (!(allowed.load() >> dev & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -748,17 +958,13 @@ int launch_shared_d(const KvSharedArgs& a, cudaStream_t st) {
   return launch(kernel, sms, kSharedThreads, S::kSmem, st, a);
 }
 
-template <int STORE>
+template <bool BF, int STORE>
 int launch_shared_store(const KvSharedArgs& a, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int d = shared_dim(a.c.dim);
-  if (a.elem == LM_BF16)
-    return d == 64    ? launch_shared_d<LM_BF16, STORE, 64>(a, st)
-           : d == 128 ? launch_shared_d<LM_BF16, STORE, 128>(a, st)
-                      : launch_shared_d<LM_BF16, STORE, 256>(a, st);
-  return d == 64    ? launch_shared_d<LM_F16, STORE, 64>(a, st)
-         : d == 128 ? launch_shared_d<LM_F16, STORE, 128>(a, st)
-                    : launch_shared_d<LM_F16, STORE, 256>(a, st);
+  return d == 64    ? launch_shared_d<BF, STORE, 64>(a, st)
+         : d == 128 ? launch_shared_d<BF, STORE, 128>(a, st)
+                    : launch_shared_d<BF, STORE, 256>(a, st);
 }
 
 }  // namespace lm

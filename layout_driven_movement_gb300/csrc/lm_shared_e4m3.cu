@@ -3,6 +3,6 @@
 
 namespace lm {
 int launch_shared_e4m3(const KvSharedArgs& a, void* stream) {
-  return launch_shared_store<LM_KV_E4M3>(a, stream);
+  return launch_shared_store<false, LM_KV_E4M3>(a, stream);
 }
 }  // namespace lm

@@ -3,6 +3,7 @@
 
 namespace lm {
 int launch_shared_same(const KvSharedArgs& a, void* stream) {
-  return launch_shared_store<LM_KV_SAME>(a, stream);
+  return a.elem == LM_BF16 ? launch_shared_store<true, LM_KV_SAME>(a, stream)
+                           : launch_shared_store<false, LM_KV_SAME>(a, stream);
 }
 }  // namespace lm

@@ -58,20 +58,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t* r, uint32_t at) {
       : "r"(at)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
-      "%31, %32};\n" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
-      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
-      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -103,6 +89,18 @@ __device__ __forceinline__ uint32_t mma_kind(bool bf, bool b_rows_n, int m,
          (b_rows_n ? 1u << 16 : 0u) | uint32_t(n >> 3) << 17 |
          uint32_t(m >> 4) << 24;
 }
+// One lane of a warp that has come together.  (Where the compiler can tell that
+// a whole warp takes the same way, a product's operands stay in the warp's
+// uniform registers; a branch on the lane's number costs some 130 cycles a
+// product instead.)
+__device__ __forceinline__ bool one_lane() {
+  uint32_t is;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(is));
+  return is != 0;
+}
 // One thread: D (+)= A B over 16 elements of K, A and B in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
                                        uint32_t kind, bool add) {
@@ -129,7 +127,8 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
       "[%0];\n" ::"r"(bar)
       : "memory");
 }
-// What this thread has written to shared memory is seen by the products.
+// What this thread has written to shared memory, or seen written there, is seen
+// by the products.
 __device__ __forceinline__ void smem_to_products() {
   asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
 }
