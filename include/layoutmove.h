@@ -844,7 +844,7 @@ int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
  * A weight p_j of a shared token meets its value rounded to 16 bits: of a cache
  * of bfloat16 rows to bfloat16 (off by 2^-8 of itself at most; weights below
  * 2^-80 of the largest are lost), of any other to float16, off by 2^-11 of
- * itself or by 2^-36 of the largest of its row, whichever is more, where a
+ * itself or by 2^-32 of the largest of its row, whichever is more, where a
  * quantised value's weight counts times its scale.  Scales of values above 2^96
  * or below 2^-96 in magnitude count as those.  Otherwise precision and range are
  * lm_kv_attend's.  The same inputs give the same bits.

@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         v[e] = *reinterpret_cast<const float4*>(
             where.x == 1 ? a.mean + (sub * rows + row) * dim + d
                          : part_of(p) + 2 * tile +
-                               (int64_t(d / 4) * tile + sub * 128 + r) * 4);
+                               int64_t(sub * 128 + r) * shared_dim(dim) + d);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

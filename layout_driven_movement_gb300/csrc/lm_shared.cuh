@@ -13,10 +13,14 @@
 // elements) and streams tiles of 128 (64) keys past them:
 //   warps 8-11  bring keys and values from their pages into shared memory, as
 //               they are or widened from codes, in the 128-byte swizzle
-//   warp 12     one thread issues S_q = Q_q K^T and O_q += P_q V
-//   warps 0-3   and 4-7, one for each tile of queries, a row a thread: the row
-//               of Q into shared memory, then S from tensor memory, its
-//               exponentials, and P back in S's place
+//   warp 12     one lane issues S_q = Q_q K^T and O_q += P_q V
+//   warp 13     passes on what copies have brought: a fence between the copies'
+//               writes and the products' reads, which would hold warp 12 up
+//   warps 0-3   and 4-7, one for each tile of queries: Q into shared memory, a
+//               row a thread; then S from tensor memory, 16 rows at a time and
+//               four threads a row, its exponentials, and P back in S's place.
+//               (A row a thread would be one exchange less, but every thread
+//               then reads every key's scales: 4000 of 9500 cycles a tile.)
 // While one tile's exponentials are taken the tensor cores have the other's
 // products.  Where there are no more than 128 queries, the two take every
 // second tile of keys instead, with states of their own that are joined later.
@@ -44,7 +48,7 @@
 
 namespace lm {
 
-constexpr int kSharedThreads = 13 * 32;
+constexpr int kSharedThreads = 14 * 32;
 
 template <int D>
 struct SharedShape {
@@ -63,7 +67,7 @@ struct SharedShape {
   static constexpr int NM = NS + 1;
   static constexpr int kMeta = NK * 12 + 48;
   static constexpr uint32_t kOut = 256;                // O's first column
-  static constexpr int kBars = 4 * NS + 12;
+  static constexpr int kBars = 6 * NS + 12;
   static constexpr int kSmem =
       1024 + QT * kQ + 2 * NS * kTile + NM * kMeta + kBars * 8 + 16;
 };
@@ -249,6 +253,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   const uint32_t q_full = bars + 8 * (4 * NS + 8);
   const uint32_t q_empty = bars + 8 * (4 * NS + 9);
   const uint32_t drain = bars + 8 * (4 * NS + 10);
+  // what the products wait for
+  auto k_ready = [&](int i) {
+    return CODES ? k_full(i) : bars + 8 * (4 * NS + 12 + i);
+  };
+  auto v_ready = [&](int i) {
+    return CODES ? v_full(i) : bars + 8 * (5 * NS + 12 + i);
+  };
 
   // (none of this touches global memory)
   if (threadIdx.x == 0) {
@@ -261,6 +272,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       mbar_init(k_empty(i), 1);
       mbar_init(v_full(i), 128);
       mbar_init(v_empty(i), 1);
+      if (!CODES) {
+        mbar_init(k_ready(i), 1);
+        mbar_init(v_ready(i), 1);
+      }
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(s_full(q), 1);
@@ -370,30 +385,38 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           }
           ask(kr, a.c.k);
         };
-        // widened to f16, with the sign of a row's factor (0: zeros)
-        auto widen = [&](uint32_t tile_s, const uint4* w, float factor) {
+        // widened to f16
+        auto widen = [&](uint32_t tile_s, const uint4* w) {
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
             const int r = i * RPI + r0;
-            const float f = __shfl_sync(0xffffffffu, factor, r);
-            const uint32_t flip = f < 0 ? 0x80008000u : 0;
-            const bool zero = f == 0;
             uint32_t y[8];
             widen16<STORE>(w[i], y);
             if (!held) continue;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const int ch = 2 * c + j;
-              uint32_t x[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[e] = zero ? 0 : y[4 * j + e] ^ flip;
               st_smem16(tile_s + ch / 8 * (NK * 128) + r * 128 +
                             ((ch ^ r) & 7) * 16,
-                        x[0], x[1], x[2], x[3]);
+                        y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
             }
           }
           smem_to_products();
+        };
+        // What the logarithm of a scale says nothing of, its sign and 0, goes
+        // to the codes: an int8 code's and an e4m3 code's sign alike.
+        auto signs = [&](uint4* w, float factor) {
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            const float f = __shfl_sync(0xffffffffu, factor, i * RPI + r0);
+            auto turn = [&](uint32_t x) {
+              if (f == 0) return 0u;
+              if (!(f < 0)) return x;
+              return STORE == LM_KV_E4M3 ? x ^ 0x80808080u : __vnegss4(x);
+            };
+            w[i] = make_uint4(turn(w[i].x), turn(w[i].y), turn(w[i].z),
+                              turn(w[i].w));
+          }
         };
         ask_keys(seg.t0);
         ask(vr, a.c.v);
@@ -433,13 +456,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             f[lw] = least;
             f[4 + lw] = most;
           }
-          widen(k_s + slot * S::kTile + to, kr, 1.f);
+          widen(k_s + slot * S::kTile + to, kr);
           mbar_arrive(k_full(slot));
           const float factor = vs;
           ask_keys(t + 1);
           if (tile >= NS) acquire(v_empty(slot), turn ^ 1);
           if (!alive) break;
-          widen(v_s + slot * S::kTile + to, vr, factor);
+          if (__any_sync(0xffffffffu, !(factor > 0))) signs(vr, factor);
+          widen(v_s + slot * S::kTile + to, vr);
           mbar_arrive(v_full(slot));
           ask(vr, a.c.v);
         }
@@ -478,7 +502,20 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     }
     cp_commit();
     cp_wait<0>();
-  } else if (warp == 12) {
+  } else if (warp >= 12) {
+    if (!CODES && warp == 13) {
+      // --- copies passed on ---
+      for (int64_t tile = 0; tile < share.left; ++tile) {
+        const int slot = int(tile % NS);
+        const uint32_t turn = tile / NS & 1;
+        if (!warp_gate(k_full(slot), turn, &dead)) break;
+        smem_to_products();
+        if (lane == 0) mbar_arrive(k_ready(slot));
+        if (!warp_gate(v_full(slot), turn, &dead)) break;
+        smem_to_products();
+        if (lane == 0) mbar_arrive(v_ready(slot));
+      }
+    }
     // --- products: the warp together, one lane issues ---
     const uint32_t kind_s = mma_kind(BF, false, 128, NK);
     const uint32_t kind_o = mma_kind(BF, true, 128, dim16);
@@ -490,7 +527,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     // the phases of p_full and o_empty, a bit a tile of queries, and whether a
     // tile's O was ever read
     uint32_t p_phase = 0, o_phase = 0, o_read = 0;
-    bool alive = true;
+    bool alive = warp == 12;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (alive && !warp_gate(bar, parity, &dead)) alive = false;
       return alive;
@@ -503,59 +540,52 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       // it
       const bool two = split || per == 2;
       const int ahead = two ? 2 : 1;
-      bool keys = false;               // unit u's keys have been waited for
-      auto look_ahead = [&](int u) {
-        if (per == 2 && (u & 1)) return;
-        const int t = tile + (per == 2 ? u / 2 : u);
-        keys = __all_sync(0xffffffffu, mbar_try(k_full(t % NS), t / NS & 1));
-        if (keys) smem_to_products();
-      };
-      auto score = [&](int u) {
-        const int j = per == 2 ? u / 2 : u, t = tile + j, slot = t % NS;
+      // (by one lane)
+      auto score = [&](int u, int slot) {
         const int q = two ? u & 1 : 0;
-        if ((per == 1 || q == 0) && !keys) {
-          if (!wait(k_full(slot), t / NS & 1)) return;
-          smem_to_products();
-        }
-        keys = false;
-        tmem_after_sync();
-        if (one_lane()) {
-          const uint64_t qa = q_op + (split ? 0 : q) * (S::kQ / 16);
-          const uint64_t ka = k_op + slot * (S::kTile / 16);
-          const uint32_t to = tmem + q * NK;
+        const uint64_t qa = q_op + (split ? 0 : q) * (S::kQ / 16);
+        const uint64_t ka = k_op + slot * (S::kTile / 16);
+        const uint32_t to = tmem + q * NK;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            if (k >= ks) break;
-            mma_ss(to, qa + (k / 4 * (128 * 128) + k % 4 * 32) / 16,
-                   ka + (k / 4 * (NK * 128) + k % 4 * 32) / 16, kind_s, k > 0);
-          }
-          mma_commit(s_full(q));
-          if (per == 1 || q == 1) mma_commit(k_empty(slot));
-          if (u == units - 1) mma_commit(q_empty);
+        for (int k = 0; k < D / 16; ++k) {
+          if (k >= ks) break;
+          mma_ss(to, qa + (k / 4 * (128 * 128) + k % 4 * 32) / 16,
+                 ka + (k / 4 * (NK * 128) + k % 4 * 32) / 16, kind_s, k > 0);
         }
-        __syncwarp();
+        mma_commit(s_full(q));
+        if (per == 1 || q == 1) mma_commit(k_empty(slot));
+        if (u == units - 1) mma_commit(q_empty);
       };
+      auto tile_of = [&](int u) { return tile + (per == 2 ? u / 2 : u); };
       if (!wait(q_full, nth & 1)) break;
       ++nth;
-      for (int u = 0; u < ahead && u < units; ++u) score(u);
+      for (int u = 0; u < ahead && u < units; ++u) {
+        const int t = tile_of(u), slot = t % NS;
+        if ((per == 1 || u == 0) && !wait(k_ready(slot), t / NS & 1)) break;
+        tmem_after_sync();
+        if (one_lane()) score(u, slot);
+        __syncwarp();
+      }
       for (int u = 0; u < units && alive; ++u) {
-        const int j = per == 2 ? u / 2 : u, t = tile + j, slot = t % NS;
+        const int t = tile_of(u), slot = t % NS;
         const int q = two ? u & 1 : 0;
-        // (the values, and the next scores' keys if they are there already,
-        // before the weights, which are waited for longest)
-        if (per == 1 || q == 0) {
-          if (!wait(v_full(slot), t / NS & 1)) break;
-          smem_to_products();
-        }
-        if (u + ahead < units) look_ahead(u + ahead);
-        if (!wait(p_full(q), p_phase >> q & 1)) break;
-        p_phase ^= 1u << q;
-        const bool first = split ? u < 2 : j == 0;
+        const bool opens = per == 1 || q == 0;     // a tile's first unit
+        // The values, and whether the next scores' keys are there already,
+        // before the weights, which are waited for longest.
+        if (opens && !wait(v_ready(slot), t / NS & 1)) break;
+        const bool more = u + ahead < units;
+        const int t2 = tile_of(u + ahead), slot2 = t2 % NS;
+        bool keys = more;
+        if (more && opens)
+          keys = __all_sync(0xffffffffu, mbar_try(k_ready(slot2), t2 / NS & 1));
+        const bool first = split ? u < 2 : t == tile;
         if (first && (o_read >> q & 1)) {
           if (!wait(o_empty(q), o_phase >> q & 1)) break;
           o_phase ^= 1u << q;
         }
         const bool last = u + (split ? 2 : per) >= units;
+        if (!wait(p_full(q), p_phase >> q & 1)) break;
+        p_phase ^= 1u << q;
         tmem_after_sync();
         if (one_lane()) {
           const uint64_t va = v_op + slot * (S::kTile / 16);
@@ -563,18 +593,24 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           const uint32_t p = tmem + q * NK;
 #pragma unroll
           for (int i = 0; i < NK / 16; ++i)
-            mma_ts(o, p + i / 2 * 32 + i % 2 * 8, va + i * (2048 / 16), kind_o,
+            mma_ts(o, p + i * 8, va + i * (2048 / 16), kind_o,
                    !(first && i == 0));
+          if (keys) score(u + ahead, slot2);
           if (per == 1 || q == 1) mma_commit(v_empty(slot));
           if (last) mma_commit(o_full(q));
         }
         __syncwarp();
         if (last) o_read |= 1u << q;
-        if (u + ahead < units) score(u + ahead);
+        if (more && !keys) {
+          if (!wait(k_ready(slot2), t2 / NS & 1)) break;
+          tmem_after_sync();
+          if (one_lane()) score(u + ahead, slot2);
+          __syncwarp();
+        }
       }
       tile += seg.steps;
     }
-    if (dead) {
+    if (dead && warp == 12) {
       // products may still read shared memory and write tensor memory
       if (one_lane()) mma_commit(drain);
       warp_wait(drain, 0, kDrainCycles);
@@ -606,9 +642,21 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           int64_t(seg.h * a.group + (rg - si * a.group)) * a.q.hs;
       const int step = split ? 2 : 1;
       const bool active = split || q * 128 < seg.rows;
-      float m = -INFINITY, l = 0;
-      float down = 1;              // of codes: what a row's query was held times
-      float most = -INFINITY;      // and the largest logarithm of a scale so far
+      // The thread's share of four rows: t / 4 and 8 on of a warp's first 16,
+      // then of its other 16.  The pairs change places after each 16.
+      float m[2], l[2], m2[2], l2[2];
+      // of codes: what the rows' queries were held times, and the largest
+      // logarithm of a scale so far
+      float down[2] = {1, 1}, down2[2] = {1, 1}, most = -INFINITY;
+      auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          m[i] = m2[i] = -INFINITY;
+          l[i] = l2[i] = 0;
+        }
+        most = -INFINITY;
+      };
+      clear();
       // the reference's weight, as a power of two
       const float off = BF ? -float(8 + 32 - __clz(seg.steps * NK)) : 12.f;
       bool first = true;
@@ -628,7 +676,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         }
         if (j >= 0 || nth == 0) {
           const char* const meta = metas + (t_first + max(j, 0)) % NM * S::kMeta;
-          const float2* const ku = reinterpret_cast<const float2*>(meta);
+          // (from the thread's first pair of columns on)
+          const float2* const ku =
+              reinterpret_cast<const float2*>(meta) + lane % 4;
           const uint32_t* const words =
               reinterpret_cast<const uint32_t*>(meta + NK * 12);
           // which of 32 keys are seen
@@ -643,133 +693,157 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
           for (int c = 0; c < NK / 32; ++c) part |= seen(c) != 0xffffffffu;
           part = __any_sync(0xffffffffu, part && j >= 0);
-          // where not all keys are seen: -infinity for those that are not
-          if (part) {
-#pragma unroll 1
-            for (int c = 0; c < NK / 32; ++c) {
-              uint32_t s[32];
-              tmem_ld32(s, s_at + c * 32);
-              tmem_wait_ld();
-              const uint32_t mask = seen(c);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(mask >> i & 1)) s[i] = 0xff800000u;
-              tmem_st16(s_at + c * 32, s);
-              tmem_st16(s_at + c * 32 + 16, s + 16);
-            }
-            tmem_wait_st();
-          }
-          // The largest exponent, in units of ln 2.  (64 columns at a time,
-          // here and below: a row's 128 at once are twice the instructions.)
-          const float2 by = make_float2(down, down);
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < NK; c += 64) {
-            uint32_t s[64];
-            tmem_ld32(s, s_at + c);
-            tmem_ld32(s + 32, s_at + c + 32);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              float2 x = make_float2(__uint_as_float(s[i]),
-                                     __uint_as_float(s[i + 1]));
-              if (CODES)
-                x = fma2(mul2(x, ku[(c + i) / 2]), by, ku[(NK + c + i) / 2]);
-              tops[i % 4] = fmaxf(tops[i % 4], x.x);
-              tops[i % 4 + 1] = fmaxf(tops[i % 4 + 1], x.y);
-            }
-          }
-          float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-          if (!CODES) top *= unit;
-          const bool move = top > m + SLACK;
-          if (__any_sync(0xffffffffu, move)) {
-            float keep = 1;
-            if (move) {
-              // (in two halves: with scales of values far apart the whole may
-              // be below 2^-126 and the sum above 2^100)
-              keep = ex2(0.5f * (m - top));
-              l = l * keep * keep;
-              keep *= keep;
-              m = top;
-            }
-            __syncwarp();
-            if (!first) {
-#pragma unroll 1
-              for (int c = 0; c < dim; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, o_at + c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                tmem_st16(o_at + c, o);
-                tmem_st16(o_at + c + 16, o + 16);
-              }
-            }
-          }
-          first = false;
-          const float sub = off - (m == -INFINITY ? 0.f : m);
-          const float2 sub2 = make_float2(sub, sub);
-          const float2 unit2 = make_float2(unit, unit);
-          float2 sums[2] = {make_float2(0, 0), make_float2(0, 0)};
-          // A code's weight alone is its exponential over its value's scale --
+          // Where scales of values lie within a few powers of two of each other,
+          // their largest is taken for all of them in a row's reference.  A
+          // code's weight alone is its exponential over its value's scale --
           // unless scales lie so far apart that an exponential may be below
           // 2^-126 where the weight is not small: then weights are summed for
           // themselves.
-          bool apart = false;
+          float most_of = 0;
+          bool near = true, apart = false;
           if (CODES) {
             const float* const ends =
                 reinterpret_cast<const float*>(meta + NK * 12 + 16);
             float least = INFINITY;
+            most_of = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               least = fminf(least, ends[i]);
-              most = fmaxf(most, ends[4 + i]);
+              most_of = fmaxf(most_of, ends[4 + i]);
             }
-            apart = __any_sync(0xffffffffu, most - least > 60 && j >= 0);
-            if (apart) {
+            most = fmaxf(most, most_of);
+            near = !__any_sync(0xffffffffu, !(most_of - least < 4) && j >= 0);
+            apart = __any_sync(0xffffffffu, !(most - least < 60) && j >= 0);
+          }
+          const float2 unit2 = make_float2(unit, unit);
 #pragma unroll 1
-              for (int c = 0; c < NK; c += 32) {
-                uint32_t s[32];
-                tmem_ld32(s, s_at + c);
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t lanes = uint32_t(half * 16) << 16;
+            uint32_t s[NK / 2];
+            tmem_ld<NK / 8>(s, s_at + lanes);
+            tmem_wait_ld();
+            // columns 8g + 2 (t % 4) and the next of row i
+            auto pair = [&](int g, int i) {
+              return make_float2(__uint_as_float(s[4 * g + 2 * i]),
+                                 __uint_as_float(s[4 * g + 2 * i + 1]));
+            };
+            if (part) {
+              // -infinity where a key is not seen
+#pragma unroll
+              for (int g = 0; g < NK / 8; ++g) {
+                const uint32_t mask =
+                    seen(g / 4) >> (g % 4 * 8 + lane % 4 * 2);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  if (!(mask >> k & 1))
+                    s[4 * g + k] = s[4 * g + 2 + k] = 0xff800000u;
+              }
+            }
+            // the largest exponent, in units of ln 2
+            float tops[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+#pragma unroll
+            for (int g = 0; g < NK / 8; ++g) {
+              float2 f = make_float2(1, 1);
+              if (CODES) f = ku[4 * g];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float2 x = pair(g, i);
+                if (CODES) x = mul2(x, f);
+                if (CODES && !near)
+                  x = fma2(x, make_float2(down[i], down[i]),
+                           ku[NK / 2 + 4 * g]);
+                tops[i][0] = fmaxf(tops[i][0], x.x);
+                tops[i][1] = fmaxf(tops[i][1], x.y);
+              }
+            }
+            float keep[2];
+            bool move = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float top = fmaxf(tops[i][0], tops[i][1]);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              if (!CODES) top *= unit;
+              if (CODES && near) top = __fmaf_rn(top, down[i], most_of);
+              keep[i] = 1;
+              if (top > m[i] + SLACK) {
+                // (in two halves: with scales of values far apart the whole may
+                // be below 2^-126 and the sum above 2^100)
+                keep[i] = ex2(0.5f * (m[i] - top));
+                l[i] = l[i] * keep[i] * keep[i];
+                keep[i] *= keep[i];
+                m[i] = top;
+                move = true;
+              }
+            }
+            if (__any_sync(0xffffffffu, move) && !first) {
+#pragma unroll 1
+              for (int c = 0; c < dim; c += 32) {
+                uint32_t o[16];
+                tmem_ld<4>(o, o_at + lanes + c);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                  float2 x = make_float2(__uint_as_float(s[i]),
-                                         __uint_as_float(s[i + 1]));
-                  x = fma2(mul2(x, ku[(c + i) / 2]), by, sub2);
-                  l += ex2(x.x) + ex2(x.y);
+                for (int i = 0; i < 16; ++i)
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) *
+                                         keep[i / 2 % 2]);
+                tmem_st4(o_at + lanes + c, o);
+              }
+            }
+            float2 sub[2], by[2], sums[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = off - (m[i] == -INFINITY ? 0.f : m[i]);
+              sub[i] = make_float2(x, x);
+              by[i] = make_float2(down[i], down[i]);
+              sums[i] = make_float2(0, 0);
+            }
+            if (CODES && apart) {
+#pragma unroll
+              for (int g = 0; g < NK / 8; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float2 x =
+                      fma2(mul2(pair(g, i), ku[4 * g]), by[i], sub[i]);
+                  l[i] += ex2(x.x) + ex2(x.y);
                 }
-              }
             }
-          }
-#pragma unroll 1
-          for (int c = 0; c < NK; c += 64) {
-            uint32_t s[64];
-            tmem_ld32(s, s_at + c);
-            tmem_ld32(s + 32, s_at + c + 32);
-            tmem_wait_ld();
+            uint32_t p[NK / 4];
 #pragma unroll
-            for (int half = 0; half < 64; half += 32) {
-              uint32_t p[16];
+            for (int g = 0; g < NK / 8; ++g) {
+              float2 f, lv, inv;
+              if (CODES) {
+                f = ku[4 * g];
+                lv = ku[NK / 2 + 4 * g];
+                inv = ku[NK + 4 * g];
+              }
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const int at = (c + half + i) / 2;
-                float2 x = make_float2(__uint_as_float(s[half + i]),
-                                       __uint_as_float(s[half + i + 1]));
+              for (int i = 0; i < 2; ++i) {
+                float2 x = pair(g, i);
                 if (CODES)
-                  x = fma2(mul2(x, ku[at]), by, add2(ku[NK / 2 + at], sub2));
+                  x = fma2(mul2(x, f), by[i], add2(lv, sub[i]));
                 else
-                  x = fma2(x, unit2, sub2);
+                  x = fma2(x, unit2, sub[i]);
                 x = make_float2(ex2(x.x), ex2(x.y));
-                float2& sum = sums[i / 2 % 2];
-                sum = CODES ? fma2(x, ku[NK + at], sum) : add2(x, sum);
-                p[i / 2] = pair16<BF>(x.x, x.y);
+                sums[i] = CODES ? fma2(x, inv, sums[i]) : add2(x, sums[i]);
+                p[2 * g + i] = pair16<BF>(x.x, x.y);
               }
-              tmem_st16(s_at + c + half, p);
+            }
+            tmem_st_pairs<NK / 8>(s_at + lanes, p);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (!apart) l[i] += sums[i].x + sums[i].y;
+              float t = m[i];
+              m[i] = m2[i];
+              m2[i] = t;
+              t = l[i];
+              l[i] = l2[i];
+              l2[i] = t;
+              t = down[i];
+              down[i] = down2[i];
+              down2[i] = t;
             }
           }
-          if (!apart) l += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+          first = false;
           tmem_wait_st();
         }
         if (j >= 0) {
@@ -777,8 +851,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           mbar_arrive(p_full(q));
           j += step;
         } else {
-          m = most = -INFINITY;
-          l = 0;
+          clear();
           first = true;
           // the row's query, turned round where the scale is negative
           if (nth > 0 && !warp_gate(q_empty, (nth - 1) & 1, &dead)) {
@@ -820,7 +893,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             if (top == 0 || top == INFINITY) e = 0;
             e = min(120, max(-120, e));
             up = __int_as_float((127 + e) << 23);
-            down = __int_as_float((127 - e) << 23);
+            const float back = __int_as_float((127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              down[i] = __shfl_sync(0xffffffffu, back, lane / 4 + 8 * i);
+              down2[i] = __shfl_sync(0xffffffffu, back, 16 + lane / 4 + 8 * i);
+            }
           }
           if (q * 128 < (split ? 128 : seg.rows)) {
             const uint32_t to = q_s + q * S::kQ + row * 128;
@@ -866,63 +944,95 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       }
       const bool whole = seg.steps == seg.s.tiles;
       const int sub = split ? q : 0;
-      const int64_t out_row =
-          int64_t(sub) * a.seqs * a.heads_q +
-          int64_t(seg.s.start + si) * a.heads_q + seg.h * a.group +
-          (rg - si * a.group);
-      const int part_row = q * 128 + row;
       float* const part =
           a.parts + (2 * int64_t(blockIdx.x) +
                      (share.begin < seg.item_at ? 1 : 0)) *
                         (int64_t(S::kRows) * (D + 2));
-      // weights were taken times 2^off
-      const float f = l == 0 ? 0.f : __fdividef(1.f, l);
-      if (valid && sub == 0 && seg.t0 == 0) {
-        // where the row's pieces will be: the block of tile i of the line is
-        // ((i + 1) blocks - 1) / total
-        const int64_t c1 = small_div(
-            (seg.item_at + seg.s.tiles) * gridDim.x - 1, share.total);
-        const int n = int(c1 - blockIdx.x) + 1;
-        reinterpret_cast<int4*>(a.pieces)[out_row] = make_int4(
-            n, 2 * int(blockIdx.x) + (share.begin < seg.item_at ? 1 : 0),
-            2 * int(blockIdx.x) + 2, (q * 128 + row) | (split ? 65536 : 0));
-      }
-      if (valid) {
-        // (the sum's exponent goes to the reference: next to scales of values
-        // the sum may be of any size, and references far apart then say nothing
-        // about weights)
-        const int e = int(__float_as_uint(l) >> 23) - 127;
-        float2 ml = make_float2(none ? -INFINITY : m - off, l);
-        if (CODES && l > 0x1p-120f && l < INFINITY) {
-          ml.x += float(e);
-          ml.y *= __int_as_float((127 - e) << 23);
-        }
-        if (whole)
-          reinterpret_cast<float2*>(a.state)[out_row] = ml;
-        else
-          reinterpret_cast<float2*>(part)[part_row] = ml;
-      }
-      if (!none) {
+      // where the rows' pieces will be: the block of tile i of the line is
+      // ((i + 1) blocks - 1) / total
+      const int pieces =
+          seg.t0 == 0 && sub == 0
+              ? int(small_div((seg.item_at + seg.s.tiles) * gridDim.x - 1,
+                              share.total) -
+                    blockIdx.x) +
+                    1
+              : 0;
 #pragma unroll 1
-        for (int c = 0; c < dim; c += 32) {
-          uint32_t x[32];
-          __syncwarp();
-          tmem_ld32(x, o_at + c);
-          tmem_wait_ld();
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t lanes = uint32_t(half * 16) << 16;
+        float f[2];
+        float* to[2];                // a row's mean, NULL where there is none
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            if (!valid || c + i >= dim) break;
-            float4 y;
-            float* const ys = &y.x;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) ys[k] = __uint_as_float(x[i + k]) * f;
-            float* to = whole ? a.mean + out_row * dim + c + i
-                              : part + 2 * S::kRows +
-                                    (int64_t((c + i) / 4) * S::kRows +
-                                     part_row) * 4;
-            *reinterpret_cast<float4*>(to) = y;
+        for (int i = 0; i < 2; ++i) {
+          const int in = warp % 4 * 32 + half * 16 + lane / 4 + 8 * i;
+          const int r = split ? in : q * 128 + in;
+          const int rg = seg.rt * S::kRows + r, si = rg / a.group;
+          const int64_t out_row =
+              int64_t(sub) * a.seqs * a.heads_q +
+              int64_t(seg.s.start + si) * a.heads_q + seg.h * a.group +
+              (rg - si * a.group);
+          const int part_row = q * 128 + in;
+          float sum = l[i];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          // weights were taken times 2^off
+          f[i] = sum == 0 ? 0.f : __fdividef(1.f, sum);
+          to[i] = nullptr;
+          if (r < seg.rows) {
+            to[i] = whole ? a.mean + out_row * dim
+                          : part + 2 * S::kRows + part_row * D;
+            if (lane % 4 == 0) {
+              // (the sum's exponent goes to the reference: next to scales of
+              // values the sum may be of any size, and references far apart
+              // then say nothing about weights)
+              const int e = int(__float_as_uint(sum) >> 23) - 127;
+              float2 ml = make_float2(none ? -INFINITY : m[i] - off, sum);
+              if (CODES && sum > 0x1p-120f && sum < INFINITY) {
+                ml.x += float(e);
+                ml.y *= __int_as_float((127 - e) << 23);
+              }
+              if (whole)
+                reinterpret_cast<float2*>(a.state)[out_row] = ml;
+              else
+                reinterpret_cast<float2*>(part)[part_row] = ml;
+              if (pieces > 0)
+                reinterpret_cast<int4*>(a.pieces)[out_row] = make_int4(
+                    pieces,
+                    2 * int(blockIdx.x) + (share.begin < seg.item_at ? 1 : 0),
+                    2 * int(blockIdx.x) + 2, part_row | (split ? 65536 : 0));
+            }
           }
         }
+        if (!none) {
+#pragma unroll 1
+          for (int c = 0; c < dim; c += 32) {
+            uint32_t x[16];
+            __syncwarp();
+            tmem_ld<4>(x, o_at + lanes + c);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const int d = c + g * 8 + lane % 4 * 2;
+                if (to[i] && d < dim)
+                  *reinterpret_cast<float2*>(to[i] + d) = make_float2(
+                      __uint_as_float(x[4 * g + 2 * i]) * f[i],
+                      __uint_as_float(x[4 * g + 2 * i + 1]) * f[i]);
+              }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float t = m[i];
+          m[i] = m2[i];
+          m2[i] = t;
+          t = l[i];
+          l[i] = l2[i];
+          l2[i] = t;
+        }
+      }
+      if (!none) {
         __syncwarp();
         tmem_before_sync();
         mbar_arrive(o_empty(q));
