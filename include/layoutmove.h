@@ -848,7 +848,8 @@ int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
  * quantised value's weight counts times its scale.  Scales of values above 2^96
  * or below 2^-96 in magnitude count as those.  Otherwise precision and range are
  * lm_kv_attend's.  The same inputs give the same bits.
- * Errors: as lm_kv_attend. */
+ * Errors: as lm_kv_attend, LM_E_OVERFLOW also for a quantised cache of 2^36
+ * bytes of keys or more. */
 int lm_kv_attend_shared(
     const lm_kv_plan* plan, const lm_kv_cache* cache, const lm_rows* q,
     const lm_rows* out, int seqs, int heads_q, const int32_t* shared_table,

@@ -264,6 +264,11 @@ int lm_kv_attend_shared(
       rl = lm::range_of(lse, rows * 4);
       need(!held.meet(rl) && !rl.meets(rq) && !rl.meets(ro), LM_E_OVERLAP);
     }
+    // rows of codes are counted in 16 bytes, in 32 bits
+    need(plan->store == LM_KV_SAME ||
+             lm::mul_chk(cache->pages, plan->page_stride) <
+                 (int64_t(1) << 36) - 4096,
+         LM_E_OVERFLOW);
     const int group = int(heads_q / plan->heads);
     int64_t plain = 0;
     int dev = 0, sms = 0;

@@ -7,14 +7,22 @@
 
 namespace lm {
 
-// a / b of numbers that are not negative; most are small, and a 64-bit
-// division takes several times a 32-bit one's time.
-static __device__ __noinline__ int64_t large_div(int64_t a, int64_t b) {
-  return a / b;
-}
+// a / b of numbers that are not negative and below 2^62.  Most are small, and a
+// 64-bit division takes several times a 32-bit one's time and code; the others
+// go bit by bit.
 __device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
   if ((a | b) >> 31 == 0) return uint32_t(a) / uint32_t(b);
-  return large_div(a, b);
+  int64_t q = 0, r = 0;
+#pragma unroll 1
+  for (int i = 61; i >= 0; --i) {
+    r = r * 2 + (a >> i & 1);
+    q *= 2;
+    if (r >= b) {
+      r -= b;
+      ++q;
+    }
+  }
+  return q;
 }
 
 struct LineShare {

@@ -13,7 +13,9 @@
 // elements) and streams tiles of 128 (64) keys past them:
 //   warps 8-11  bring keys and values from their pages into shared memory, as
 //               they are or widened from codes, in the 128-byte swizzle
-//   warp 12     one lane issues S_q = Q_q K^T and O_q += P_q V
+//   warps 12    and 14, one for each tile of queries: one lane issues S_q = Q_q
+//               K^T and O_q += P_q V (one warp for both left the tensor cores
+//               idle between its waits: 3.8 against 3.0 thousand cycles a tile)
 //   warp 13     passes on what copies have brought: a fence between the copies'
 //               writes and the products' reads, which would hold warp 12 up
 //   warps 0-3   and 4-7, one for each tile of queries: Q into shared memory, a
@@ -48,7 +50,12 @@
 
 namespace lm {
 
-constexpr int kSharedThreads = 14 * 32;
+// Four warpgroups, whose threads' registers are as many as their work wants;
+// together those of 512 threads of 128.
+constexpr int kSharedThreads = 512;
+constexpr int kRegsExp = 160, kRegsLoad = 136, kRegsProducts = 56;
+static_assert(128 * (2 * kRegsExp + kRegsLoad + kRegsProducts) <= 512 * 128,
+              "no more registers than the block has");
 
 template <int D>
 struct SharedShape {
@@ -196,16 +203,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return reinterpret_cast<float2&>(y);
 }
 
-// 8 elements of a row that allows no wide loads.  (A call: the 8 loads in every
-// place where a chunk may come this way would be most of the kernel's code.)
-static __device__ __noinline__ uint4 load8_narrow(const uint16_t* x) {
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = x[2 * i] | uint32_t(x[2 * i + 1]) << 16;
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-
 __device__ __forceinline__ void st_smem16(uint32_t to, uint32_t a, uint32_t b,
                                           uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(a),
@@ -269,9 +266,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t come = CODES ? 128 : 132;
     for (int i = 0; i < NS; ++i) {
       mbar_init(k_full(i), come);
-      mbar_init(k_empty(i), 1);
+      mbar_init(k_empty(i), 2);
       mbar_init(v_full(i), 128);
-      mbar_init(v_empty(i), 1);
+      mbar_init(v_empty(i), 2);
       if (!CODES) {
         mbar_init(k_ready(i), 1);
         mbar_init(v_ready(i), 1);
@@ -284,8 +281,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       mbar_init(o_empty(q), 128);
     }
     mbar_init(q_full, 256);
-    mbar_init(q_empty, 1);
-    mbar_init(drain, 1);
+    mbar_init(q_empty, 2);
+    mbar_init(drain, 2);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 12)
@@ -312,6 +309,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 
   if (warp >= 8 && warp < 12) {
     // --- keys and values ---
+    registers_up<kRegsLoad>();
     const int lw = warp - 8;
     constexpr int EB = CODES ? 1 : 2;
     constexpr int CPR = D * EB / 16;            // 16-byte chunks of a row
@@ -342,7 +340,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       // the lane's key of tile t, whose page has been looked up: where its row
       // lies (-1: not seen), and the next tile's page on its way
       int64_t from, scale_at;
-      uint32_t seen;
+      uint32_t seen, off16[IT];      // of codes: the lane's chunks, in 16 bytes
       auto find = [&](int t) {
         const int key = t * NK + lw * KPW + lane;
         const bool in = mine && t < t1 && key < seg.s.len;
@@ -353,11 +351,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         from = ok ? int64_t(page) * a.c.page_b + int64_t(off) * a.c.token_b +
                         int64_t(seg.h) * a.c.head_b
                   : -1;
-        if (CODES)
+        if (CODES) {
           scale_at = ok ? (int64_t(page) * a.c.heads + seg.h) *
                                   a.c.page_tokens +
                               off
                         : -1;
+          // (a cache of 2^36 bytes or more is refused)
+          const uint32_t row = ok ? uint32_t(from >> 4) : 0xffffffffu;
+#pragma unroll
+          for (int i = 0; i < IT; ++i) {
+            off16[i] = __shfl_sync(0xffffffffu, row, i * RPI + r0);
+            if (off16[i] != 0xffffffffu) off16[i] += c;
+          }
+        }
         seen = __ballot_sync(0xffffffffu, ok);
         page = look(t + 1);
       };
@@ -370,10 +376,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         auto ask = [&](uint4* w, const char* rows) {
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
-            const int64_t o = __shfl_sync(0xffffffffu, from, i * RPI + r0);
             w[i] = make_uint4(0, 0, 0, 0);
-            if (o >= 0 && held)
-              w[i] = *reinterpret_cast<const uint4*>(rows + o + c * 16);
+            if (off16[i] != 0xffffffffu && held)
+              w[i] = *(reinterpret_cast<const uint4*>(rows) + off16[i]);
           }
         };
         auto ask_keys = [&](int t) {
@@ -429,33 +434,27 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           char* const m = metas + tile % NM * S::kMeta;
           // scales beyond 2^+-96 count as those; one of 0, whose values are
           // taken as 0, as the largest about
-          float top = fabsf(vs);
-#pragma unroll
-          for (int k = 16; k; k /= 2)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-          const float size =
-              vs == 0 ? (top > 0 ? top : 1.f) : fabsf(vs);
+          // (magnitudes in the order of their bits)
+          const uint32_t top =
+              __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs)));
+          const float size = vs == 0 ? (top ? __uint_as_float(top) : 1.f)
+                                     : fabsf(vs);
           const float held_size =
               size < INFINITY ? fminf(fmaxf(size, 0x1p-96f), 0x1p96f) : size;
-          const float log_size = log2f(held_size);
-          float least = log_size, most = log_size;
-#pragma unroll
-          for (int k = 16; k; k /= 2) {
-            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, k));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
-          }
+          const uint32_t bits = __float_as_uint(held_size);
+          const uint32_t least = __reduce_min_sync(0xffffffffu, bits);
+          const uint32_t most = __reduce_max_sync(0xffffffffu, bits);
           if (mine) {
             float* f = reinterpret_cast<float*>(m) + lw * KPW + lane;
             f[0] = scale_at >= 0 ? ks * unit : 1.f;
-            f[NK] = log_size;
-            f[2 * NK] = 1.f / held_size;
+            f[NK] = log2f(held_size);
+            f[2 * NK] = __fdividef(1.f, held_size);
           }
-          if (lane == 0) {
+          if (lane == 0)
             reinterpret_cast<uint32_t*>(m + NK * 12)[lw] = seen;
-            float* f = reinterpret_cast<float*>(m + NK * 12 + 16);
-            f[lw] = least;
-            f[4 + lw] = most;
-          }
+          if (lane < 2)
+            reinterpret_cast<float*>(m + NK * 12 + 16)[lane * 4 + lw] =
+                log2f(__uint_as_float(lane ? most : least));
           widen(k_s + slot * S::kTile + to, kr);
           mbar_arrive(k_full(slot));
           const float factor = vs;
@@ -503,6 +502,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     cp_commit();
     cp_wait<0>();
   } else if (warp >= 12) {
+    registers_down<kRegsProducts>();
     if (!CODES && warp == 13) {
       // --- copies passed on ---
       for (int64_t tile = 0; tile < share.left; ++tile) {
@@ -523,26 +523,31 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint64_t q_op = smem_operand(q_s, 16, 1024);
     const uint64_t k_op = smem_operand(k_s, 16, 1024);
     const uint64_t v_op = smem_operand(v_s, NK * 128, 1024);
+    const int q = warp == 14;
     int tile = 0, nth = 0;
-    // the phases of p_full and o_empty, a bit a tile of queries, and whether a
-    // tile's O was ever read
-    uint32_t p_phase = 0, o_phase = 0, o_read = 0;
-    bool alive = warp == 12;
+    uint32_t p_phase = 0, o_phase = 0;
+    bool o_read = false;             // O has been read, so it is waited for
+    bool alive = warp == 12 || warp == 14;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (alive && !warp_gate(bar, parity, &dead)) alive = false;
       return alive;
     };
     while (alive && walk.next(a, &seg)) {
       const bool split = split_of(seg);
-      const int per = split || QT == 1 ? 1 : (seg.rows + 127) / 128;
-      const int units = seg.steps * per;
-      // unit u: key tile u / per, and which half of the exponential warps has
-      // it
-      const bool two = split || per == 2;
-      const int ahead = two ? 2 : 1;
+      // the key tiles of this tile of queries, or half of them; a stage that
+      // the other warp has no part in is given back twice
+      const int j0 = split ? q : 0, step = split ? 2 : 1;
+      const bool twice = split || QT == 1;
+      const bool none = j0 >= seg.steps || (QT == 1 && q == 1);
+      if (!wait(q_full, nth & 1)) break;
+      ++nth;
+      if (none) {
+        if (lane == 0) mbar_arrive(q_empty);
+        tile += seg.steps;
+        continue;
+      }
       // (by one lane)
-      auto score = [&](int u, int slot) {
-        const int q = two ? u & 1 : 0;
+      auto score = [&](int j, int slot) {
         const uint64_t qa = q_op + (split ? 0 : q) * (S::kQ / 16);
         const uint64_t ka = k_op + slot * (S::kTile / 16);
         const uint32_t to = tmem + q * NK;
@@ -553,39 +558,33 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                  ka + (k / 4 * (NK * 128) + k % 4 * 32) / 16, kind_s, k > 0);
         }
         mma_commit(s_full(q));
-        if (per == 1 || q == 1) mma_commit(k_empty(slot));
-        if (u == units - 1) mma_commit(q_empty);
+        mma_commit(k_empty(slot));
+        if (twice) mma_commit(k_empty(slot));
+        if (j + step >= seg.steps) mma_commit(q_empty);
       };
-      auto tile_of = [&](int u) { return tile + (per == 2 ? u / 2 : u); };
-      if (!wait(q_full, nth & 1)) break;
-      ++nth;
-      for (int u = 0; u < ahead && u < units; ++u) {
-        const int t = tile_of(u), slot = t % NS;
-        if ((per == 1 || u == 0) && !wait(k_ready(slot), t / NS & 1)) break;
+      {
+        const int t = tile + j0, slot = t % NS;
+        if (!wait(k_ready(slot), t / NS & 1)) break;
         tmem_after_sync();
-        if (one_lane()) score(u, slot);
+        if (one_lane()) score(j0, slot);
         __syncwarp();
       }
-      for (int u = 0; u < units && alive; ++u) {
-        const int t = tile_of(u), slot = t % NS;
-        const int q = two ? u & 1 : 0;
-        const bool opens = per == 1 || q == 0;     // a tile's first unit
+      for (int j = j0; j < seg.steps && alive; j += step) {
+        const int t = tile + j, slot = t % NS;
+        const int t2 = t + step, slot2 = t2 % NS;
+        const bool more = j + step < seg.steps;
         // The values, and whether the next scores' keys are there already,
         // before the weights, which are waited for longest.
-        if (opens && !wait(v_ready(slot), t / NS & 1)) break;
-        const bool more = u + ahead < units;
-        const int t2 = tile_of(u + ahead), slot2 = t2 % NS;
-        bool keys = more;
-        if (more && opens)
-          keys = __all_sync(0xffffffffu, mbar_try(k_ready(slot2), t2 / NS & 1));
-        const bool first = split ? u < 2 : t == tile;
-        if (first && (o_read >> q & 1)) {
-          if (!wait(o_empty(q), o_phase >> q & 1)) break;
-          o_phase ^= 1u << q;
+        if (!wait(v_ready(slot), t / NS & 1)) break;
+        const bool keys =
+            more &&
+            __all_sync(0xffffffffu, mbar_try(k_ready(slot2), t2 / NS & 1));
+        if (j == j0 && o_read) {
+          if (!wait(o_empty(q), o_phase & 1)) break;
+          ++o_phase;
         }
-        const bool last = u + (split ? 2 : per) >= units;
-        if (!wait(p_full(q), p_phase >> q & 1)) break;
-        p_phase ^= 1u << q;
+        if (!wait(p_full(q), p_phase & 1)) break;
+        ++p_phase;
         tmem_after_sync();
         if (one_lane()) {
           const uint64_t va = v_op + slot * (S::kTile / 16);
@@ -594,29 +593,31 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
           for (int i = 0; i < NK / 16; ++i)
             mma_ts(o, p + i * 8, va + i * (2048 / 16), kind_o,
-                   !(first && i == 0));
-          if (keys) score(u + ahead, slot2);
-          if (per == 1 || q == 1) mma_commit(v_empty(slot));
-          if (last) mma_commit(o_full(q));
+                   j > j0 || i > 0);
+          if (keys) score(j + step, slot2);
+          mma_commit(v_empty(slot));
+          if (twice) mma_commit(v_empty(slot));
+          if (!more) mma_commit(o_full(q));
         }
         __syncwarp();
-        if (last) o_read |= 1u << q;
         if (more && !keys) {
           if (!wait(k_ready(slot2), t2 / NS & 1)) break;
           tmem_after_sync();
-          if (one_lane()) score(u + ahead, slot2);
+          if (one_lane()) score(j + step, slot2);
           __syncwarp();
         }
       }
+      o_read = true;
       tile += seg.steps;
     }
-    if (dead && warp == 12) {
+    if (dead && (warp == 12 || warp == 14)) {
       // products may still read shared memory and write tensor memory
       if (one_lane()) mma_commit(drain);
       warp_wait(drain, 0, kDrainCycles);
     }
   } else {
-    // --- exponentials: a row a thread ---
+    // --- exponentials ---
+    registers_up<kRegsExp>();
     const int q = warp / 4;
     const int row = warp % 4 * 32 + lane;
     const uint32_t quarter = uint32_t(warp % 4 * 32) << 16;
@@ -862,13 +863,18 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           const bool row_in = valid && a.scale != 0;
           auto load = [&](int c) {
             uint4 w = make_uint4(0, 0, 0, 0);
-            if (row_in && c * 8 < dim) {
-              if (a.q16)
-                w = *reinterpret_cast<const uint4*>(query + c * 8);
-              else
-                w = load8_narrow(query + c * 8);
-            }
+            if (row_in && c * 8 < dim)
+              w = *reinterpret_cast<const uint4*>(query + c * 8);
             return w;
+          };
+          auto narrow = [&](int c) {       // of a row that allows no wide loads
+            uint32_t x[4] = {0, 0, 0, 0};
+            if (row_in && c * 8 < dim)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[i] = query[c * 8 + 2 * i] |
+                       uint32_t(query[c * 8 + 2 * i + 1]) << 16;
+            return make_uint4(x[0], x[1], x[2], x[3]);
           };
           // Codes are met by f16 queries, scaled by a power of two so that the
           // largest element lies in [2^14, 2^15): exact for bf16 elements down
@@ -878,9 +884,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           const bool in_bf = a.elem == LM_BF16;
           if (CODES) {
             float top = 0;
-#pragma unroll 4
+#pragma unroll 1
             for (int c = 0; c < dim16 / 8; ++c) {
-              const uint4 w = load(c);
+              const uint4 w = a.q16 ? load(c) : narrow(c);
               const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -902,27 +908,33 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           }
           if (q * 128 < (split ? 128 : seg.rows)) {
             const uint32_t to = q_s + q * S::kQ + row * 128;
-#pragma unroll 1
-            for (int c0 = 0; c0 < dim16 / 8; c0 += 8) {
-              uint4 w[8];
+            auto store = [&](int c, const uint4& w) {
+              uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-              for (int c = 0; c < 8; ++c) w[c] = load(c0 + c);
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (CODES) {
-                    const float2 f = in_bf ? unpair16<true>(x[i])
-                                           : unpair16<false>(x[i]);
-                    x[i] = pair16<false>(f.x * up, f.y * up);
-                  }
-                  x[i] ^= flip;
+              for (int i = 0; i < 4; ++i) {
+                if (CODES) {
+                  const float2 f = in_bf ? unpair16<true>(x[i])
+                                         : unpair16<false>(x[i]);
+                  x[i] = pair16<false>(f.x * up, f.y * up);
                 }
-                if ((c0 + c) * 8 < dim16)
-                  st_smem16(to + c0 / 8 * (128 * 128) + ((c ^ row) & 7) * 16,
-                            x[0], x[1], x[2], x[3]);
+                x[i] ^= flip;
               }
+              if (c * 8 < dim16)
+                st_smem16(to + c / 8 * (128 * 128) + ((c ^ row) & 7) * 16,
+                          x[0], x[1], x[2], x[3]);
+            };
+            if (a.q16) {
+#pragma unroll 1
+              for (int c0 = 0; c0 < dim16 / 8; c0 += 8) {
+                uint4 w[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) w[c] = load(c0 + c);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) store(c0 + c, w[c]);
+              }
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < dim16 / 8; ++c) store(c, narrow(c));
             }
           }
           smem_to_products();

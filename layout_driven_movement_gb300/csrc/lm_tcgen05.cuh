@@ -145,6 +145,19 @@ __device__ __forceinline__ void tmem_st_pairs<8>(uint32_t at, const uint32_t* r)
       : "memory");
 }
 
+// --- registers -----------------------------------------------------------------
+
+// By all four warps of a warpgroup: the registers a thread has from here on.
+// The block's shares together are no more than it was launched with.
+template <int N>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // --- products ----------------------------------------------------------------
 
 // An operand in shared memory in 128-byte rows whose 16-byte chunks are
