@@ -150,24 +150,34 @@ __device__ __forceinline__ void stream_order() {
 
 // Launches a kernel that begins with stream_order(): its launch overlaps the
 // end of the kernel before it.
+// In clusters of `cluster` blocks, which `grid` is a multiple of.
 template <class... P, class... A>
-int launch(void (*kernel)(P...), uint64_t grid, int block, int smem,
-           cudaStream_t st, const A&... args) {
+int launch_clusters(void (*kernel)(P...), int cluster, uint64_t grid, int block,
+                    int smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(block));
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   if (e == cudaSuccess) return LM_OK;
   cudaGetLastError();                      // not left for a later call
   set_cuda_error(int(e));
   return LM_E_CUDA;
+}
+
+template <class... P, class... A>
+int launch(void (*kernel)(P...), uint64_t grid, int block, int smem,
+           cudaStream_t st, const A&... args) {
+  return launch_clusters(kernel, 1, grid, block, smem, st, args...);
 }
 
 }  // namespace lm

@@ -51,34 +51,45 @@ __global__ void __launch_bounds__(T)
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnits = 8;        // 16-byte loads of a thread in flight
-constexpr int kMoveRows = 128;       // of a step at most
+constexpr int kMoveRows = 512;       // of a step at most
 
-// A block moves the keys or the values of one sequence and head.  Rows may
-// move within the same pages, but only to lower places or their own: a step's
-// rows are all read before the first of them is written, and what a later step
-// reads lies behind all that was written.
+// A cluster of C blocks moves the keys or the values of one sequence and head.
+// Rows may move within the same pages, but only to lower places or their own: a
+// step's rows are all read before the first of them is written, and what a
+// later step reads lies behind all that was written.
+template <int C>
 __global__ void __launch_bounds__(kMoveThreads)
     lm_kv_move_kernel(const __grid_constant__ KvEvictArgs a) {
-  __shared__ int64_t s_from[kMoveRows], s_to[kMoveRows];
+  __shared__ int64_t s_from[3][kMoveRows], s_to[3][kMoveRows];
   stream_order();
-  const int kv = blockIdx.x & 1;
-  const int unit = blockIdx.x >> 1;
+  const int rank = blockIdx.x % C, kv = blockIdx.x / C & 1;
+  const int unit = blockIdx.x / C >> 1;
   const int b = unit / int(a.c.heads), h = unit - b * int(a.c.heads);
   // (the same whether kept_lens, which may be lens, is written or not)
   const int count = min(evict_len(a, b), a.keep);
-  if (kv == 0 && h == 0 && threadIdx.x == 0) a.kept_lens[b] = count;
+  if (rank == 0 && kv == 0 && h == 0 && threadIdx.x == 0)
+    a.kept_lens[b] = count;
   const int32_t* list = a.list + int64_t(unit) * a.keep;
   const int32_t* table = a.table + b * a.table_stride;
   const int32_t* kept = a.kept_table + b * a.kept_stride;
   char* const rows = kv ? a.c.v : a.c.k;
   float* const scales = kv ? a.c.vs : a.c.ks;
+  constexpr int R = kMoveRows / kMoveThreads;      // rows a thread looks up
   const int step = min(kMoveRows, kMoveThreads * kMoveUnits / int(a.chunks));
-  for (int i0 = 0; i0 < count; i0 += step) {
-    const int rows_now = min(step, count - i0);
-    float scale = 0, weight = 0;
-    int64_t to = -1;
-    const int r = threadIdx.x;
-    if (r < rows_now) {
+  // Where the rows of the step at `at` lie, to buffer n of three: while one
+  // step's rows are on their way the next one's places are looked up, and the
+  // one before may still be being written.
+  float scale[R], weight[R];
+  int64_t to[R];
+  auto look = [&](int at, int n) {
+    const int i0 = at + rank * step;
+    const int rows_now = min(step, max(count - i0, 0));
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+      const int r = threadIdx.x + e * kMoveThreads;
+      to[e] = -1;
+      scale[e] = weight[e] = 0;
+      if (r >= rows_now) continue;
       const uint32_t i = uint32_t(i0 + r), j = uint32_t(list[i0 + r]);
       const uint32_t pi = fdiv(i, a.c.page_div), pj = fdiv(j, a.c.page_div);
       const uint32_t oi = i - pi * a.c.page_tokens;
@@ -87,44 +98,61 @@ __global__ void __launch_bounds__(kMoveThreads)
       const bool ok =
           src >= 0 && src < a.c.pages && dst >= 0 && dst < a.c.pages;
       if (!ok && a.status) atomicOr(a.status, kStatusRange);
-      s_from[r] = -1;
+      s_from[n][r] = -1;
       if (ok && !(src == dst && oi == oj)) {
         const int64_t hb = int64_t(h) * a.c.head_b;
-        s_from[r] = src * a.c.page_b + int64_t(oj) * a.c.token_b + hb;
-        s_to[r] = dst * a.c.page_b + int64_t(oi) * a.c.token_b + hb;
+        s_from[n][r] = src * a.c.page_b + int64_t(oj) * a.c.token_b + hb;
+        s_to[n][r] = dst * a.c.page_b + int64_t(oi) * a.c.token_b + hb;
         const int64_t from = (src * a.c.heads + h) * a.c.page_tokens + oj;
-        to = (dst * a.c.heads + h) * a.c.page_tokens + oi;
-        if (scales) scale = scales[from];
-        if (kv == 0) weight = a.weights[from];
+        to[e] = (dst * a.c.heads + h) * a.c.page_tokens + oi;
+        if (scales) scale[e] = scales[from];
+        if (kv == 0) weight[e] = a.weights[from];
       }
     }
-    __syncthreads();
-    uint4 held[kMoveUnits];
+  };
+  look(0, 0);
+  __syncthreads();
+  int n = 0;
+  for (int at = 0; at < count; at += step * C) {
+    const int rows_now = min(step, max(count - at - rank * step, 0));
     const uint32_t units = uint32_t(rows_now) * a.chunks;
+    uint4 held[kMoveUnits];
 #pragma unroll
     for (int k = 0; k < kMoveUnits; ++k) {
       const uint32_t u = threadIdx.x + k * kMoveThreads;
       if (u >= units) continue;
       const uint32_t row = fdiv(u, a.chunk_div);
-      if (s_from[row] >= 0)
+      if (s_from[n][row] >= 0)
         held[k] = *reinterpret_cast<const uint4*>(
-            rows + s_from[row] + (u - row * a.chunks) * 16);
+            rows + s_from[n][row] + (u - row * a.chunks) * 16);
     }
-    __syncthreads();
-    if (to >= 0) {
-      if (scales) scales[to] = scale;
-      if (kv == 0) a.weights[to] = weight;
+    float scale_now[R], weight_now[R];
+    int64_t to_now[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+      scale_now[e] = scale[e];
+      weight_now[e] = weight[e];
+      to_now[e] = to[e];
     }
+    const int next = n == 2 ? 0 : n + 1;
+    if (at + step * C < count) look(at + step * C, next);
+    cluster_sync<C>();
+#pragma unroll
+    for (int e = 0; e < R; ++e)
+      if (to_now[e] >= 0) {
+        if (scales) scales[to_now[e]] = scale_now[e];
+        if (kv == 0) a.weights[to_now[e]] = weight_now[e];
+      }
 #pragma unroll
     for (int k = 0; k < kMoveUnits; ++k) {
       const uint32_t u = threadIdx.x + k * kMoveThreads;
       if (u >= units) continue;
       const uint32_t row = fdiv(u, a.chunk_div);
-      if (s_from[row] >= 0)
-        *reinterpret_cast<uint4*>(rows + s_to[row] +
+      if (s_from[n][row] >= 0)
+        *reinterpret_cast<uint4*>(rows + s_to[n][row] +
                                   (u - row * a.chunks) * 16) = held[k];
     }
-    __syncthreads();
+    n = next;
   }
 }
 
@@ -133,12 +161,21 @@ __global__ void __launch_bounds__(kMoveThreads)
 int launch_kv_evict(const KvEvictArgs& a, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const uint64_t units = uint64_t(a.seqs) * a.c.heads;
-  constexpr int T = 256;
-  const int cap = int(a.max_tokens < 8192 ? a.max_tokens : 8192);
-  const int rc =
-      launch(lm_kv_keep_kernel<T, 1>, units, T, cap * 4, st, a, cap);
+  int dev = 0, sms = 0;
+  int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  return launch(lm_kv_move_kernel, units * 2, kMoveThreads, 0, st, a);
+  static std::atomic<uint64_t> allowed{0};    // a bit per device
+  rc = launch_top(lm_kv_keep_kernel<kTopThreads, 1>,
+                  lm_kv_keep_kernel<kTopMore, 1>,
+                  lm_kv_keep_kernel<kTopMore, kTopCluster>, &allowed, dev,
+                  top_plan(int64_t(units), a.max_tokens, sms), units, st, a);
+  if (rc != LM_OK) return rc;
+  // one block a list of rows where that fills the SMs, else eight
+  constexpr int C = kTopCluster;
+  return units * 2 <= uint64_t(sms)
+             ? launch_clusters(lm_kv_move_kernel<C>, C, units * 2 * C,
+                               kMoveThreads, 0, st, a)
+             : launch(lm_kv_move_kernel<1>, units * 2, kMoveThreads, 0, st, a);
 }
 
 }  // namespace lm

@@ -9,6 +9,8 @@
 // under one of its own: products and their sums are whole numbers below 2^24,
 // the same in any order and in 32-bit floats, so that ties are ties and the
 // choice depends on nothing but the inputs.
+#include <type_traits>
+
 #include "lm_kv_long.h"
 #include "lm_kv_top.cuh"
 #include "lm_line.cuh"
@@ -37,6 +39,26 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
+// Of two pairs of 16-bit elements.
+template <class T>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if (std::is_same<T, bf16>::value)
+    asm("min.NaN.bf16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+template <class T>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t y;
+  if (std::is_same<T, bf16>::value)
+    asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;\n" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+
 // --- bounds ----------------------------------------------------------------
 
 constexpr int kBoundThreads = 128;
@@ -44,7 +66,7 @@ constexpr int kBoundThreads = 128;
 // A warp has one page and head: L lanes hold a row in 16-byte chunks, 32 / L
 // of them take turns with the tokens, kAhead loads each in flight.
 template <class T, int STORE, int L>
-__global__ void __launch_bounds__(kBoundThreads)
+__global__ void __launch_bounds__(kBoundThreads, STORE == LM_KV_SAME ? 8 : 4)
     lm_kv_bound_kernel(const __grid_constant__ KvBoundArgs a) {
   constexpr int N = STORE == LM_KV_SAME ? 8 : 16;   // elements of a chunk
   constexpr int TL = 32 / L;                        // tokens at once
@@ -72,6 +94,17 @@ __global__ void __launch_bounds__(kBoundThreads)
     lo[e] = INFINITY;
     hi[e] = -INFINITY;
   }
+  // (16-bit rows two elements at a time, as they are)
+  uint32_t lo2[4], hi2[4];
+  if (STORE == LM_KV_SAME) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float inf[2] = {INFINITY, INFINITY};
+      const float minus[2] = {-INFINITY, -INFINITY};
+      lo2[e] = Word<T>::put(inf);
+      hi2[e] = Word<T>::put(minus);
+    }
+  }
   if (has)
     for (int t = t0; t < count; t += TL * kAhead) {
       uint4 w[kAhead];
@@ -87,20 +120,41 @@ __global__ void __launch_bounds__(kBoundThreads)
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         if (t + k * TL >= count) continue;
-        float x[N];
-        held_values<T, STORE>(w[k], scale[k], x);
+        if (STORE == LM_KV_SAME) {
+          const uint32_t r[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          lo[e] = min_nan(lo[e], x[e]);
-          hi[e] = max_nan(hi[e], x[e]);
+          for (int e = 0; e < 4; ++e) {
+            lo2[e] = min2_nan<T>(lo2[e], r[e]);
+            hi2[e] = max2_nan<T>(hi2[e], r[e]);
+          }
+        } else {
+          float x[N];
+          held_values<T, STORE>(w[k], scale[k], x);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            lo[e] = min_nan(lo[e], x[e]);
+            hi[e] = max_nan(hi[e], x[e]);
+          }
         }
       }
     }
+  if (STORE == LM_KV_SAME) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int k = L; k < 32; k *= 2) {
+        lo2[e] = min2_nan<T>(lo2[e], __shfl_xor_sync(0xffffffffu, lo2[e], k));
+        hi2[e] = max2_nan<T>(hi2[e], __shfl_xor_sync(0xffffffffu, hi2[e], k));
+      }
+      Word<T>::get(lo2[e], lo + 2 * e);
+      Word<T>::get(hi2[e], hi + 2 * e);
+    }
+  }
   float top = 0;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
 #pragma unroll
-    for (int k = L; k < 32; k *= 2) {
+    for (int k = STORE == LM_KV_SAME ? 32 : L; k < 32; k *= 2) {
       lo[e] = min_nan(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], k));
       hi[e] = max_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], k));
     }
@@ -152,14 +206,16 @@ constexpr int kScoreThreads = 256;
 constexpr int kScorePages = 32;      // of a warp's unit
 
 // A unit is kScorePages pages of one sequence and head.  L lanes of 8 elements
-// hold a row, 32 / L pages at a time: a query's positive and negative parts
-// meet hi and lo in four 4-way byte products, and the sums of up to 8 queries
-// over the L lanes are added up by halving: each exchange leaves a lane half
-// the queries, until each has one.
+// hold a row, 32 / L pages at a time, the loads of several rounds in flight: a
+// query's positive and negative parts meet hi and lo in four 4-way byte products.
+// The sums of up to 8 queries over the L lanes are added up by halving: each
+// exchange leaves a lane half of the queries, until it has one, whose sum is then
+// added over the lanes that have the same.
 template <class T, int L, int GQ>
-__global__ void __launch_bounds__(kScoreThreads)
+__global__ void __launch_bounds__(kScoreThreads, GQ == 8 ? 2 : 3)
     lm_kv_score_kernel(const __grid_constant__ KvSelectArgs a) {
   constexpr int PW = 32 / L;
+  constexpr int kAhead = L == 8 ? 4 : 8;    // rounds whose loads are in flight
   stream_order();
   auto pages_of = [&](int b) {
     const int64_t most = a.max_pages * a.page_tokens;
@@ -199,6 +255,11 @@ __global__ void __launch_bounds__(kScoreThreads)
     const int mine = p0 + lane < p1
                          ? a.table[at.b * a.table_stride + p0 + lane]
                          : -1;
+    const bool there = mine >= 0 && mine < a.pages;
+    // (a power of two or NaN: it multiplies the largest of the queries' as well
+    // as each)
+    const float scale =
+        there ? a.bound_scale[int64_t(mine) * a.heads + h] : 0.f;
     float best = -INFINITY;            // of page p0 + lane
     for (int g0 = 0; g0 < a.group; g0 += GQ) {
       // the queries as whole numbers
@@ -246,43 +307,71 @@ __global__ void __launch_bounds__(kScoreThreads)
           }
         }
       }
-      for (int p = 0; p < p1 - p0; p += PW) {
-        const int64_t page = __shfl_sync(0xffffffffu, mine, (p + pw) & 31);
-        const bool ok = page >= 0 && page < a.pages;
-        uint2 lo = make_uint2(0, 0), hi = lo;
-        float scale = 0;
-        if (ok) {
-          const int8_t* from = a.bounds + (page * a.heads + h) * 2 * a.dim;
-          if (has) {
-            lo = *reinterpret_cast<const uint2*>(from + c * 8);
-            hi = *reinterpret_cast<const uint2*>(from + a.dim + c * 8);
+      // the lane's query after the exchanges
+      int own_g = 0;
+      float own_scale = qs[0];
+      bool own_is = true;
+#pragma unroll
+      for (int n = GQ, k = L / 2; n > 1; n /= 2, k /= 2)
+        if (lane & k) own_g += n / 2;
+#pragma unroll
+      for (int g = 0; g < GQ; ++g)
+        if (g == own_g) own_scale = qs[g];
+      own_is = g0 + own_g < a.group;
+#pragma unroll 1
+      for (int p = 0; p < p1 - p0; p += PW * kAhead) {
+        uint2 lo[kAhead], hi[kAhead];
+        bool ok[kAhead];
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r) {
+          const int64_t page =
+              __shfl_sync(0xffffffffu, mine, (p + r * PW + pw) & 31);
+          ok[r] = page >= 0 && page < a.pages && p + r * PW + pw < p1 - p0;
+          lo[r] = hi[r] = make_uint2(0, 0);
+          if (ok[r] && has) {
+            const int8_t* from = a.bounds + (page * a.heads + h) * 2 * a.dim;
+            lo[r] = *reinterpret_cast<const uint2*>(from + c * 8);
+            hi[r] = *reinterpret_cast<const uint2*>(from + a.dim + c * 8);
           }
-          scale = a.bound_scale[page * a.heads + h];
         }
-        float score = -INFINITY;
 #pragma unroll
-        for (int g = 0; g < GQ; ++g) {
-          int s = __dp4a(int(qp[g][0]), int(hi.x), 0);
-          s = __dp4a(int(qp[g][1]), int(hi.y), s);
-          s = __dp4a(int(qn[g][0]), int(lo.x), s);
-          s = __dp4a(int(qn[g][1]), int(lo.y), s);
+        for (int r = 0; r < kAhead; ++r) {
+          int s[GQ];
 #pragma unroll
-          for (int k = 1; k < L; k *= 2)
-            s += __shfl_xor_sync(0xffffffffu, s, k);
-          if (g0 + g < a.group) score = max_nan(score, float(s) * qs[g]);
+          for (int g = 0; g < GQ; ++g) {
+            s[g] = __dp4a(int(qp[g][0]), int(hi[r].x), 0);
+            s[g] = __dp4a(int(qp[g][1]), int(hi[r].y), s[g]);
+            s[g] = __dp4a(int(qn[g][0]), int(lo[r].x), s[g]);
+            s[g] = __dp4a(int(qn[g][1]), int(lo[r].y), s[g]);
+          }
+          int k = L / 2;
+#pragma unroll
+          for (int n = GQ; n > 1; n /= 2, k /= 2)
+#pragma unroll
+            for (int g = 0; g < n / 2; ++g) {
+              const bool up = lane & k;
+              const int give = up ? s[g] : s[g + n / 2];
+              const int keep = up ? s[g + n / 2] : s[g];
+              s[g] = keep + __shfl_xor_sync(0xffffffffu, give, k);
+            }
+#pragma unroll
+          for (; k; k /= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], k);
+          float score = own_is ? float(s[0]) * own_scale : -INFINITY;
+#pragma unroll
+          for (int e = L / 2; e >= (L / GQ > 0 ? L / GQ : 1); e /= 2)
+            score = max_nan(score, __shfl_xor_sync(0xffffffffu, score, e));
+          // to the lane that has the page
+          const int first = p + r * PW;
+          const float got =
+              __shfl_sync(0xffffffffu, score, (lane - first) * L & 31);
+          if (lane >= first && lane < first + PW) best = max_nan(best, got);
         }
-        score *= scale;
-        if (!ok) score = -INFINITY;
-        // to the lane that has the page
-        const float got =
-            __shfl_sync(0xffffffffu, score, (lane - p) * L & 31);
-        if (lane >= p && lane < p + PW) best = max_nan(best, got);
       }
     }
     if (p0 + lane < p1) {
-      if ((mine < 0 || mine >= a.pages) && h == 0 && a.status)
-        atomicOr(a.status, kStatusRange);
-      a.scores[(int64_t(at.b) * a.heads + h) * a.max_pages + p0 + lane] = best;
+      if (!there && h == 0 && a.status) atomicOr(a.status, kStatusRange);
+      a.scores[(int64_t(at.b) * a.heads + h) * a.max_pages + p0 + lane] =
+          there ? best * scale : -INFINITY;
     }
   }
 }
@@ -342,7 +431,7 @@ int launch_score_l(const KvSelectArgs& a, uint64_t grid, cudaStream_t st) {
 
 template <class T>
 int launch_score(const KvSelectArgs& a, int sms, cudaStream_t st) {
-  const uint64_t grid = uint64_t(sms) * 4;
+  const uint64_t grid = uint64_t(sms) * (a.group > 4 ? 2 : 3);
   if (a.dim <= 64) return launch_score_l<T, 8>(a, grid, st);
   if (a.dim <= 128) return launch_score_l<T, 16>(a, grid, st);
   return launch_score_l<T, 32>(a, grid, st);
@@ -380,10 +469,12 @@ int launch_kv_select(const KvSelectArgs& a, int elem, void* stream) {
                          : launch_score<__half>(a, sms, st);
     if (rc != LM_OK) return rc;
   }
-  constexpr int T = 256;
-  const int cap = int(a.max_pages < 8192 ? a.max_pages : 8192);
-  return launch(lm_kv_select_kernel<T, 1>, uint64_t(a.seqs) * a.heads, T,
-                cap * 4, st, a, cap);
+  const uint64_t lists = uint64_t(a.seqs) * a.heads;
+  static std::atomic<uint64_t> allowed{0};    // a bit per device
+  return launch_top(lm_kv_select_kernel<kTopThreads, 1>,
+                    lm_kv_select_kernel<kTopMore, 1>,
+                    lm_kv_select_kernel<kTopMore, kTopCluster>, &allowed, dev,
+                    top_plan(int64_t(lists), a.max_pages, sms), lists, st, a);
 }
 
 }  // namespace lm

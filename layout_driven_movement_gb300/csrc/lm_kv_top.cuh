@@ -2,6 +2,8 @@
 // attention reads, which tokens an eviction keeps.
 #pragma once
 
+#include <atomic>
+
 #include "lm_kv_device.cuh"
 
 namespace lm {
@@ -20,8 +22,8 @@ template <int T>
 struct TopSpace {
   uint32_t bins[kTopBins];
   uint32_t warp_a[T / 32], warp_b[T / 32];
-  uint32_t found[2];                 // a bin, and how many lie above it
-  uint32_t rank_a, rank_b;           // a bin's count; then the block's own
+  uint32_t found[3];                 // a bin, how many lie above it, and in it
+  uint32_t rank_a, rank_b;           // the block's counts
 };
 
 template <int C>
@@ -52,6 +54,16 @@ __device__ __forceinline__ uint32_t cluster_word(const uint32_t* p,
   return v;
 }
 
+__device__ __forceinline__ void cluster_put(uint32_t* p, uint32_t rank,
+                                            uint32_t v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n"
+               : "=r"(at)
+               : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(at), "r"(v)
+               : "memory");
+}
+
 // Of numbers i in [0, m) the `need` (0 < need <= m) that are largest by
 // key(i), the lowest i where they are equal, to put(place, i) with places
 // rising with i, by the T threads of each of a cluster's C blocks: every block
@@ -65,14 +77,26 @@ template <int T, int C, class Key, class Put>
 __device__ __forceinline__ void take_top(int m, int need, uint32_t* cache,
                                          int cap, TopSpace<T>* sh, Key&& key,
                                          Put&& put) {
-  constexpr int W = T / 32, PER = kTopBins / T;
+  constexpr int W = T / 32;
+  // a block has kTopBins / C of the bins to add up and look through, PER a
+  // thread
+  constexpr int PER = (kTopBins / C + T - 1) / T;
+  static_assert(kTopBins / C % PER == 0, "whole threads");
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int rank = C == 1 ? 0 : int(cluster_rank());
   const int i0 = int(int64_t(m) * rank / C);
   const int n = int(int64_t(m) * (rank + 1) / C) - i0;
   const bool held = n <= cap;
   if (held)
-    for (int i = threadIdx.x; i < n; i += T) cache[i] = key(i0 + i);
+    for (int at = threadIdx.x; at < n; at += 4 * T) {
+      uint32_t k[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (at + e * T < n) k[e] = key(i0 + at + e * T);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (at + e * T < n) cache[at + e * T] = k[e];
+    }
   auto at = [&](int i) { return held ? cache[i] : key(i0 + i); };
 
   uint32_t prefix = 0;
@@ -93,20 +117,27 @@ __device__ __forceinline__ void take_top(int m, int need, uint32_t* cache,
           atomicAdd(&sh->bins[(k >> shift) & ((1u << bits) - 1)], 1u);
       }
     cluster_sync<C>();
-    // bins from the top: thread t has PER of them
+    // The bins from the top: the first block has the first of them, thread t
+    // PER of its own.
     uint32_t mine[PER], sum = 0;
+    const int first = rank * (kTopBins / C) + int(threadIdx.x) * PER;
+    const bool has = int(threadIdx.x) * PER < kTopBins / C;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int bin = kTopBins - 1 - (int(threadIdx.x) * PER + i);
-      uint32_t v = 0;
-      if (C == 1) {
-        v = sh->bins[bin];
-      } else {
+      mine[i] = 0;
+      if (has) {
+        const int bin = kTopBins - 1 - (first + i);
+        if (C == 1) {
+          mine[i] = sh->bins[bin];
+        } else {
+          uint32_t v[C];
 #pragma unroll
-        for (int r = 0; r < C; ++r) v += cluster_word(&sh->bins[bin], r);
+          for (int r = 0; r < C; ++r) v[r] = cluster_word(&sh->bins[bin], r);
+#pragma unroll
+          for (int r = 0; r < C; ++r) mine[i] += v[r];
+        }
       }
-      mine[i] = v;
-      sum += v;
+      sum += mine[i];
     }
     uint32_t upto = sum;
 #pragma unroll
@@ -116,17 +147,33 @@ __device__ __forceinline__ void take_top(int m, int need, uint32_t* cache,
     }
     if (lane == 31) sh->warp_a[warp] = upto;
     __syncthreads();
-    uint32_t above = upto - sum;
+    uint32_t above = upto - sum, all = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w)
+    for (int w = 0; w < W; ++w) {
       if (w < warp) above += sh->warp_a[w];
+      all += sh->warp_a[w];
+    }
+    if (C > 1) {
+      if (threadIdx.x == 0) sh->rank_a = all;
+      cluster_sync<C>();
+      uint32_t v = lane < rank ? cluster_word(&sh->rank_a, lane) : 0;
+      above += __reduce_add_sync(0xffffffffu, v);
+    }
     if (!whole && above < left && left <= above + sum) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (above < left && left <= above + mine[i]) {
-          sh->found[0] = kTopBins - 1 - (threadIdx.x * PER + i);
-          sh->found[1] = above;
-          sh->rank_a = mine[i];
+          const uint32_t f[3] = {uint32_t(kTopBins - 1 - (first + i)), above,
+                                 mine[i]};
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            if (C == 1) {
+              sh->found[e] = f[e];
+            } else {
+#pragma unroll
+              for (int r = 0; r < C; ++r) cluster_put(&sh->found[e], r, f[e]);
+            }
+          }
         }
         above += mine[i];
       }
@@ -136,7 +183,7 @@ __device__ __forceinline__ void take_top(int m, int need, uint32_t* cache,
     if (!whole) {
       prefix = prefix << bits | sh->found[0];
       left -= sh->found[1];
-      if (sh->rank_a == left) {      // all that agree are taken
+      if (sh->found[2] == left) {    // all that agree are taken
         whole = true;
         floor = uint64_t(prefix) << shift;
       } else if (step == 2) {
@@ -198,6 +245,53 @@ __device__ __forceinline__ void take_top(int m, int need, uint32_t* cache,
     e0 += __popc(me);
   }
   if (C > 1) cluster_sync<C>();      // nothing of this block is read from now
+}
+
+// The blocks of a list and their threads: a small block (256 lists of 1024: 9 us,
+// 18 with large ones), a large one for a list that a small one does not hold or a
+// few long ones, and eight where no block holds the list (its numbers would be
+// read again in every step: 8 lists of 100003, 703 us against 31).
+constexpr int kTopCluster = 8, kTopThreads = 256, kTopMore = 1024;
+constexpr int kTopHeld = 8192, kTopHeldMore = 40960;
+struct TopPlan {
+  bool clusters, more;
+  int held;                          // numbers that a block holds
+};
+inline TopPlan top_plan(int64_t lists, int64_t longest, int sms) {
+  TopPlan p;
+  p.more = longest > kTopHeld || (longest > 4096 && lists <= int64_t(sms));
+  p.clusters = longest > kTopHeldMore;
+  const int64_t n =
+      p.clusters ? (longest + kTopCluster - 1) / kTopCluster : longest;
+  const int most = p.more ? kTopHeldMore : kTopHeld;
+  p.held = int(n < most ? n : most);
+  return p;
+}
+// Launches the form of a kernel that a plan asks for; `small`, `large` and
+// `eight` are its forms <kTopThreads, 1>, <kTopMore, 1> and <kTopMore, 8>.
+template <class... P, class A>
+int launch_top(void (*small)(P...), void (*large)(P...), void (*eight)(P...),
+               std::atomic<uint64_t>* allowed, int dev, const TopPlan& plan,
+               uint64_t lists, cudaStream_t st, const A& a) {
+  if (!(allowed->load() >> dev & 1)) {
+    for (auto* kernel : {large, eight}) {
+      const cudaError_t e = cudaFuncSetAttribute(
+          kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          kTopHeldMore * 4);
+      if (e != cudaSuccess) {
+        set_cuda_error(int(e));
+        return LM_E_CUDA;
+      }
+    }
+    allowed->fetch_or(uint64_t(1) << dev);
+  }
+  if (plan.clusters)
+    return launch_clusters(eight, kTopCluster, lists * kTopCluster, kTopMore,
+                           plan.held * 4, st, a, plan.held);
+  return plan.more
+             ? launch(large, lists, kTopMore, plan.held * 4, st, a, plan.held)
+             : launch(small, lists, kTopThreads, plan.held * 4, st, a,
+                      plan.held);
 }
 
 }  // namespace lm

@@ -14,18 +14,23 @@ namespace lm {
 namespace {
 
 constexpr int kWeighThreads = 256;
+constexpr int kWeighKeys = 4;        // of a thread
+constexpr int kWeighUnit = kWeighThreads * kWeighKeys;
 
-// A unit is 256 keys of one head, a thread has one key.  The weights are
-// added by the memory system (one addition a key and call, so results do not
-// depend on an order, unless sequences share pages).
+// A unit is 1024 keys of one head, a thread has four, 256 apart, whose loads are
+// in flight together.  G: the queries of a key head, 0 for any number.  The
+// weights are added by the memory system (one addition a key and call, so
+// results do not depend on an order, unless sequences share pages).
+template <int G>
 __global__ void __launch_bounds__(kWeighThreads)
     lm_kv_weigh_kernel(const __grid_constant__ KvWeighArgs a) {
   stream_order();
+  const int group = G ? G : a.group;
   auto span = [&](int b, int64_t* n, int64_t* first) {
     const int64_t l = a.lens[b];
     *n = l < 0 ? 0 : l > a.max_tokens ? a.max_tokens : l;
     *first = a.window && *n > a.window ? *n - a.window : 0;
-    return (*n - *first + kWeighThreads - 1) / kWeighThreads;
+    return (*n - *first + kWeighUnit - 1) / kWeighUnit;
   };
   const int64_t heads = a.c.heads;
   int64_t n, first;
@@ -42,22 +47,65 @@ __global__ void __launch_bounds__(kWeighThreads)
       tiles = span(++at.b, &n, &first);
     }
     const uint32_t h = uint32_t(small_div(at.in, tiles));
-    const int64_t key =
-        first + (at.in - h * tiles) * kWeighThreads + threadIdx.x;
+    const int64_t key0 =
+        first + (at.in - h * tiles) * kWeighUnit + threadIdx.x;
     ++at.in;
-    if (key >= n) continue;
-    const uint32_t p = fdiv(uint32_t(key), a.c.page_div);
-    const int64_t page = a.table[at.b * a.table_stride + h * a.table_head + p];
-    if (page < 0 || page >= a.c.pages) continue;   // the attention reported it
-    const float* s =
-        a.scores + ((at.b * heads + h) * a.max_tokens + key) * a.group;
-    const float* l = a.lse2 + (at.b * heads + h) * a.group;
-    float sum = 0;
-    for (int g = 0; g < a.group; ++g)
-      sum += l[g] == -INFINITY ? 0.f : exp2f(s[g] - l[g]);
-    atomicAdd(a.weights + (page * heads + h) * a.c.page_tokens +
-                  (uint32_t(key) - p * a.c.page_tokens),
-              sum);
+    const int32_t* const table =
+        a.table + at.b * a.table_stride + h * a.table_head;
+    const int64_t row = at.b * heads + h;
+    const float* const l = a.lse2 + row * group;
+    int64_t page[kWeighKeys];
+    uint32_t off[kWeighKeys];
+    float sum[kWeighKeys];
+#pragma unroll
+    for (int k = 0; k < kWeighKeys; ++k) {
+      const int64_t key = key0 + k * kWeighThreads;
+      const uint32_t p = fdiv(uint32_t(key), a.c.page_div);
+      page[k] = key < n ? table[p] : -1;
+      off[k] = uint32_t(key) - p * a.c.page_tokens;
+      sum[k] = 0;
+    }
+    auto share_of = [&](float s, float lse) {
+      return lse == -INFINITY ? 0.f : exp2f(s - lse);
+    };
+    if constexpr (G % 4 == 0 && G > 0) {
+#pragma unroll
+      for (int g = 0; g < G; g += 4) {
+        const float l4[4] = {l[g], l[g + 1], l[g + 2], l[g + 3]};
+        float4 s[kWeighKeys];
+#pragma unroll
+        for (int k = 0; k < kWeighKeys; ++k)
+          if (page[k] >= 0)
+            s[k] = *reinterpret_cast<const float4*>(
+                a.scores +
+                (row * a.max_tokens + key0 + k * kWeighThreads) * G + g);
+#pragma unroll
+        for (int k = 0; k < kWeighKeys; ++k)
+          if (page[k] >= 0)
+            sum[k] += (share_of(s[k].x, l4[0]) + share_of(s[k].y, l4[1])) +
+                      (share_of(s[k].z, l4[2]) + share_of(s[k].w, l4[3]));
+      }
+    } else {
+      for (int g = 0; g < group; ++g) {
+        const float lse = l[g];
+        float s[kWeighKeys];
+#pragma unroll
+        for (int k = 0; k < kWeighKeys; ++k)
+          if (page[k] >= 0)
+            s[k] = a.scores[(row * a.max_tokens + key0 + k * kWeighThreads) *
+                                group +
+                            g];
+#pragma unroll
+        for (int k = 0; k < kWeighKeys; ++k)
+          if (page[k] >= 0) sum[k] += share_of(s[k], lse);
+      }
+    }
+    // (of pages out of range, which the attention has reported, nothing)
+#pragma unroll
+    for (int k = 0; k < kWeighKeys; ++k)
+      if (page[k] >= 0 && page[k] < a.c.pages)
+        atomicAdd(a.weights + (page[k] * heads + h) * a.c.page_tokens + off[k],
+                  sum[k]);
   }
 }
 
@@ -67,8 +115,14 @@ int launch_kv_weigh(const KvWeighArgs& a, void* stream) {
   int dev = 0, sms = 0;
   const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  return launch(lm_kv_weigh_kernel, uint64_t(sms) * 8, kWeighThreads, 0,
-                static_cast<cudaStream_t>(stream), a);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const uint64_t grid = uint64_t(sms) * 6;
+  auto run = [&](auto* kernel) {
+    return launch(kernel, grid, kWeighThreads, 0, st, a);
+  };
+  if (a.group == 4) return run(lm_kv_weigh_kernel<4>);
+  if (a.group == 8) return run(lm_kv_weigh_kernel<8>);
+  return run(lm_kv_weigh_kernel<0>);
 }
 
 }  // namespace lm
