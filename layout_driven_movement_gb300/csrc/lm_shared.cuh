@@ -13,9 +13,9 @@
 // elements) and streams tiles of 128 (64) keys past them:
 //   warps 8-11  bring keys and values from their pages into shared memory, as
 //               they are or widened from codes, in the 128-byte swizzle
-//   warps 12    and 14, one for each tile of queries: one lane issues S_q = Q_q
-//               K^T and O_q += P_q V (one warp for both left the tensor cores
-//               idle between its waits: 3.8 against 3.0 thousand cycles a tile)
+//   warp 12     one lane issues S_q = Q_q K^T and O_q += P_q V, in turn for the
+//               two q (a warp for each let the two fall into step, so that
+//               nothing overlapped: 4.6 against 3.8 thousand cycles a tile)
 //   warp 13     passes on what copies have brought: a fence between the copies'
 //               writes and the products' reads, which would hold warp 12 up
 //   warps 0-3   and 4-7, one for each tile of queries: Q into shared memory, a
@@ -266,9 +266,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint32_t come = CODES ? 128 : 132;
     for (int i = 0; i < NS; ++i) {
       mbar_init(k_full(i), come);
-      mbar_init(k_empty(i), 2);
+      mbar_init(k_empty(i), 1);
       mbar_init(v_full(i), 128);
-      mbar_init(v_empty(i), 2);
+      mbar_init(v_empty(i), 1);
       if (!CODES) {
         mbar_init(k_ready(i), 1);
         mbar_init(v_ready(i), 1);
@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       mbar_init(o_empty(q), 128);
     }
     mbar_init(q_full, 256);
-    mbar_init(q_empty, 2);
-    mbar_init(drain, 2);
+    mbar_init(q_empty, 1);
+    mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 12)
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 
   if (warp >= 8 && warp < 12) {
     // --- keys and values ---
-    registers_up<kRegsLoad>();
+    if (CODES) registers_up<kRegsLoad>();
     const int lw = warp - 8;
     constexpr int EB = CODES ? 1 : 2;
     constexpr int CPR = D * EB / 16;            // 16-byte chunks of a row
@@ -356,13 +356,15 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                                   a.c.page_tokens +
                               off
                         : -1;
-          // (a cache of 2^36 bytes or more is refused)
-          const uint32_t row = ok ? uint32_t(from >> 4) : 0xffffffffu;
+          // A cache of 2^36 bytes or more is refused.  A key that is not seen,
+          // and a chunk past the row's end, has any other's codes: the mask
+          // hides the key, `signs` clears its values, and the chunk stays in
+          // its registers.
+          const uint32_t row = ok ? uint32_t(from >> 4) : 0;
 #pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            off16[i] = __shfl_sync(0xffffffffu, row, i * RPI + r0);
-            if (off16[i] != 0xffffffffu) off16[i] += c;
-          }
+          for (int i = 0; i < IT; ++i)
+            off16[i] = __shfl_sync(0xffffffffu, row, i * RPI + r0) +
+                       (held ? c : 0);
         }
         seen = __ballot_sync(0xffffffffu, ok);
         page = look(t + 1);
@@ -375,11 +377,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         float ks, vs;
         auto ask = [&](uint4* w, const char* rows) {
 #pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            w[i] = make_uint4(0, 0, 0, 0);
-            if (off16[i] != 0xffffffffu && held)
-              w[i] = *(reinterpret_cast<const uint4*>(rows) + off16[i]);
-          }
+          for (int i = 0; i < IT; ++i)
+            w[i] = *(reinterpret_cast<const uint4*>(rows) + off16[i]);
         };
         auto ask_keys = [&](int t) {
           find(t);
@@ -398,12 +397,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             uint32_t y[8];
             widen16<STORE>(w[i], y);
             if (!held) continue;
+            // (four lanes begin with their first chunk and four with their
+            // second, so that eight lanes' stores lie in all banks)
+            const bool odd = c / 4 & 1;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const int ch = 2 * c + j;
+              const int ch = 2 * c + (j ^ int(odd));
+              uint32_t x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = odd ? y[4 * (1 - j) + e] : y[4 * j + e];
               st_smem16(tile_s + ch / 8 * (NK * 128) + r * 128 +
                             ((ch ^ r) & 7) * 16,
-                        y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
+                        x[0], x[1], x[2], x[3]);
             }
           }
           smem_to_products();
@@ -502,7 +508,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     cp_commit();
     cp_wait<0>();
   } else if (warp >= 12) {
-    registers_down<kRegsProducts>();
+    if (CODES) registers_down<kRegsProducts>();
     if (!CODES && warp == 13) {
       // --- copies passed on ---
       for (int64_t tile = 0; tile < share.left; ++tile) {
@@ -523,31 +529,26 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
     const uint64_t q_op = smem_operand(q_s, 16, 1024);
     const uint64_t k_op = smem_operand(k_s, 16, 1024);
     const uint64_t v_op = smem_operand(v_s, NK * 128, 1024);
-    const int q = warp == 14;
     int tile = 0, nth = 0;
-    uint32_t p_phase = 0, o_phase = 0;
-    bool o_read = false;             // O has been read, so it is waited for
-    bool alive = warp == 12 || warp == 14;
+    // the phases of p_full and o_empty, a bit a tile of queries, and whether a
+    // tile's O was ever read
+    uint32_t p_phase = 0, o_phase = 0, o_read = 0;
+    bool alive = warp == 12;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (alive && !warp_gate(bar, parity, &dead)) alive = false;
       return alive;
     };
     while (alive && walk.next(a, &seg)) {
       const bool split = split_of(seg);
-      // the key tiles of this tile of queries, or half of them; a stage that
-      // the other warp has no part in is given back twice
-      const int j0 = split ? q : 0, step = split ? 2 : 1;
-      const bool twice = split || QT == 1;
-      const bool none = j0 >= seg.steps || (QT == 1 && q == 1);
-      if (!wait(q_full, nth & 1)) break;
-      ++nth;
-      if (none) {
-        if (lane == 0) mbar_arrive(q_empty);
-        tile += seg.steps;
-        continue;
-      }
+      const int per = split || QT == 1 ? 1 : (seg.rows + 127) / 128;
+      const int units = seg.steps * per;
+      // unit u: key tile u / per, and which half of the exponential warps has
+      // it
+      const bool two = split || per == 2;
+      const int ahead = two ? 2 : 1;
       // (by one lane)
-      auto score = [&](int j, int slot) {
+      auto score = [&](int u, int slot) {
+        const int q = two ? u & 1 : 0;
         const uint64_t qa = q_op + (split ? 0 : q) * (S::kQ / 16);
         const uint64_t ka = k_op + slot * (S::kTile / 16);
         const uint32_t to = tmem + q * NK;
@@ -558,33 +559,39 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                  ka + (k / 4 * (NK * 128) + k % 4 * 32) / 16, kind_s, k > 0);
         }
         mma_commit(s_full(q));
-        mma_commit(k_empty(slot));
-        if (twice) mma_commit(k_empty(slot));
-        if (j + step >= seg.steps) mma_commit(q_empty);
+        if (per == 1 || q == 1) mma_commit(k_empty(slot));
+        if (u == units - 1) mma_commit(q_empty);
       };
-      {
-        const int t = tile + j0, slot = t % NS;
-        if (!wait(k_ready(slot), t / NS & 1)) break;
+      auto tile_of = [&](int u) { return tile + (per == 2 ? u / 2 : u); };
+      if (!wait(q_full, nth & 1)) break;
+      ++nth;
+      for (int u = 0; u < ahead && u < units; ++u) {
+        const int t = tile_of(u), slot = t % NS;
+        if ((per == 1 || u == 0) && !wait(k_ready(slot), t / NS & 1)) break;
         tmem_after_sync();
-        if (one_lane()) score(j0, slot);
+        if (one_lane()) score(u, slot);
         __syncwarp();
       }
-      for (int j = j0; j < seg.steps && alive; j += step) {
-        const int t = tile + j, slot = t % NS;
-        const int t2 = t + step, slot2 = t2 % NS;
-        const bool more = j + step < seg.steps;
+      for (int u = 0; u < units && alive; ++u) {
+        const int t = tile_of(u), slot = t % NS;
+        const int q = two ? u & 1 : 0;
+        const bool opens = per == 1 || q == 0;     // a tile's first unit
         // The values, and whether the next scores' keys are there already,
         // before the weights, which are waited for longest.
-        if (!wait(v_ready(slot), t / NS & 1)) break;
-        const bool keys =
-            more &&
-            __all_sync(0xffffffffu, mbar_try(k_ready(slot2), t2 / NS & 1));
-        if (j == j0 && o_read) {
-          if (!wait(o_empty(q), o_phase & 1)) break;
-          ++o_phase;
+        if (opens && !wait(v_ready(slot), t / NS & 1)) break;
+        const bool more = u + ahead < units;
+        const int t2 = tile_of(u + ahead), slot2 = t2 % NS;
+        bool keys = more;
+        if (more && opens)
+          keys = __all_sync(0xffffffffu, mbar_try(k_ready(slot2), t2 / NS & 1));
+        const bool first = split ? u < 2 : t == tile;
+        if (first && (o_read >> q & 1)) {
+          if (!wait(o_empty(q), o_phase >> q & 1)) break;
+          o_phase ^= 1u << q;
         }
-        if (!wait(p_full(q), p_phase & 1)) break;
-        ++p_phase;
+        const bool last = u + (split ? 2 : per) >= units;
+        if (!wait(p_full(q), p_phase >> q & 1)) break;
+        p_phase ^= 1u << q;
         tmem_after_sync();
         if (one_lane()) {
           const uint64_t va = v_op + slot * (S::kTile / 16);
@@ -593,31 +600,30 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll
           for (int i = 0; i < NK / 16; ++i)
             mma_ts(o, p + i * 8, va + i * (2048 / 16), kind_o,
-                   j > j0 || i > 0);
-          if (keys) score(j + step, slot2);
-          mma_commit(v_empty(slot));
-          if (twice) mma_commit(v_empty(slot));
-          if (!more) mma_commit(o_full(q));
+                   !(first && i == 0));
+          if (keys) score(u + ahead, slot2);
+          if (per == 1 || q == 1) mma_commit(v_empty(slot));
+          if (last) mma_commit(o_full(q));
         }
         __syncwarp();
+        if (last) o_read |= 1u << q;
         if (more && !keys) {
           if (!wait(k_ready(slot2), t2 / NS & 1)) break;
           tmem_after_sync();
-          if (one_lane()) score(j + step, slot2);
+          if (one_lane()) score(u + ahead, slot2);
           __syncwarp();
         }
       }
-      o_read = true;
       tile += seg.steps;
     }
-    if (dead && (warp == 12 || warp == 14)) {
+    if (dead && warp == 12) {
       // products may still read shared memory and write tensor memory
       if (one_lane()) mma_commit(drain);
       warp_wait(drain, 0, kDrainCycles);
     }
   } else {
     // --- exponentials ---
-    registers_up<kRegsExp>();
+    if (CODES) registers_up<kRegsExp>();
     const int q = warp / 4;
     const int row = warp % 4 * 32 + lane;
     const uint32_t quarter = uint32_t(warp % 4 * 32) << 16;
