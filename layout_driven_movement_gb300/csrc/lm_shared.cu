@@ -7,36 +7,46 @@ namespace lm {
 namespace {
 
 constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = kJoinThreads / 32;
 
-// A warp has a row.  It reads the row's states (m, l, a) -- its own pages', and
+// A block has a row.  It reads the row's states (m, l, a) -- its own pages', and
 // those of the blocks that had a piece of its group's prefix, in the order of
 // the line -- and forms sum c a / sum c with c = l 2^(m - t), t the largest m.
-// Three loads one after the other: where the pieces are, their (m, l), and
-// their means, eight of those in flight.
+// Three loads one after the other: where the pieces are, their (m, l), and their
+// means, of which each of the four warps has every fourth.
 __global__ void __launch_bounds__(kJoinThreads)
     lm_kv_join_kernel(const __grid_constant__ KvJoinArgs j) {
+  __shared__ float sums[kJoinWarps][kKvMaxDim];
   const KvSharedArgs& a = j.s;
   stream_order();
-  const int64_t rows = int64_t(a.seqs) * a.heads_q;
-  const int64_t row =
-      int64_t(blockIdx.x) * (kJoinThreads / 32) + threadIdx.x / 32;
-  if (row >= rows) return;
-  const int lane = threadIdx.x % 32, dim = a.c.dim;
+  const int64_t rows = int64_t(a.seqs) * a.heads_q, row = blockIdx.x;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, dim = a.c.dim;
   const int4 where = reinterpret_cast<const int4*>(a.pieces)[row];
   const float2 own = reinterpret_cast<const float2*>(j.state)[row];
   const int r = where.w & 0xffff, subs = where.w >> 16 ? 2 : 1;
-  const int pieces = where.x * subs, tile = shared_rows(dim);
+  const int pieces = where.x * subs;
+  // Piece k is the second state of a row where k is odd and there are two;
+  // pieces of one block lie in `state` and `mean`, those of several in their
+  // parts.
   const int64_t part = shared_part(dim);
+  const float* const parts = a.parts + int64_t(where.z) * part;
   auto part_of = [&](int c) {
-    return a.parts + int64_t(c == 0 ? where.y : where.z + 2 * (c - 1)) * part;
+    return c == 0 ? a.parts + int64_t(where.y) * part
+                  : parts + int64_t(c - 1) * 2 * part;
   };
   auto state_of = [&](int k) {
-    const int c = subs == 2 ? k / 2 : k, sub = subs == 2 ? k & 1 : 0;
+    const int c = k >> (subs - 1), sub = subs == 2 ? k & 1 : 0;
     return where.x == 1
                ? reinterpret_cast<const float2*>(a.state)[sub * rows + row]
                : reinterpret_cast<const float2*>(part_of(c))[sub * 128 + r];
   };
-  // the first 32 pieces' states stay in the lanes
+  auto mean_of = [&](int k) {
+    const int c = k >> (subs - 1), sub = subs == 2 ? k & 1 : 0;
+    return where.x == 1 ? a.mean + (sub * rows + row) * dim
+                        : part_of(c) + 2 * shared_rows(dim) +
+                              (sub * 128 + r) * shared_dim(dim);
+  };
+  // the first 32 pieces' states stay in the lanes of every warp
   float2 mine = make_float2(-INFINITY, 0);
   if (lane < pieces) mine = state_of(lane);
   float t = own.y != 0 ? own.x : -INFINITY;
@@ -51,68 +61,61 @@ __global__ void __launch_bounds__(kJoinThreads)
   auto weight_of = [&](const float2& s) {
     return s.y == 0 ? 0.f : s.y * ex2(s.x - t0);
   };
-  float sum = lane == 0 ? weight_of(own) : 0.f;
-  sum += weight_of(mine);
+  const float c_own = weight_of(own), c_mine = weight_of(mine);
+  float sum = c_mine + (lane == 0 ? c_own : 0.f);
   for (int k = lane + 32; k < pieces; k += 32) sum += weight_of(state_of(k));
 #pragma unroll
   for (int k = 16; k; k /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
   const float f = sum == 0 ? 0.f : __fdividef(1.f, sum);
-  if (lane == 0 && j.lse)
-    j.lse[row] = sum == 0 ? -INFINITY
-                          : (t + log2f(sum)) * 0.693147180559945309f;
-  const int64_t b = row / a.heads_q;
-  char* const to =
-      j.out.p + (b * j.out.ts + (row - b * a.heads_q) * j.out.hs) * 2;
-  const float own_c = weight_of(own) * f;
   for (int d0 = 0; d0 < dim; d0 += 128) {
     const int d = d0 + lane * 4;
     const bool live = d < dim;
     float y[4] = {0, 0, 0, 0};
     // (what has no weight may hold anything)
-    if (live && own.y != 0) {
-      const float4 v =
-          *reinterpret_cast<const float4*>(j.mean + row * dim + d);
-      y[0] = own_c * v.x;
-      y[1] = own_c * v.y;
-      y[2] = own_c * v.z;
-      y[3] = own_c * v.w;
-    }
-    for (int k0 = 0; k0 < pieces; k0 += 8) {
-      float4 v[8];
-      float c[8];
+    auto add = [&](float c, const float4& v) {
+      y[0] += c * v.x;
+      y[1] += c * v.y;
+      y[2] += c * v.z;
+      y[3] += c * v.w;
+    };
+    if (warp == 0 && live && own.y != 0)
+      add(c_own * f,
+          *reinterpret_cast<const float4*>(j.mean + row * dim + d));
+    for (int k0 = warp; k0 < pieces; k0 += 4 * kJoinWarps) {
+      float4 v[4];
+      float c[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int k = k0 + e;
-        float2 s = make_float2(__shfl_sync(0xffffffffu, mine.x, k & 31),
-                               __shfl_sync(0xffffffffu, mine.y, k & 31));
-        if (k >= 32 && k < pieces) s = state_of(k);
+      for (int e = 0; e < 4; ++e) {
+        const int k = k0 + e * kJoinWarps;
+        c[e] = __shfl_sync(0xffffffffu, c_mine, k & 31);
+        if (k >= 32 && k < pieces) c[e] = weight_of(state_of(k));
         v[e] = make_float4(0, 0, 0, 0);
-        c[e] = 0;
-        if (k >= pieces || s.y == 0 || !live) continue;
-        c[e] = weight_of(s) * f;
-        const int p = subs == 2 ? k / 2 : k, sub = subs == 2 ? k & 1 : 0;
-        v[e] = *reinterpret_cast<const float4*>(
-            where.x == 1 ? a.mean + (sub * rows + row) * dim + d
-                         : part_of(p) + 2 * tile +
-                               int64_t(sub * 128 + r) * shared_dim(dim) + d);
+        if (k < pieces && c[e] != 0 && live)
+          v[e] = *reinterpret_cast<const float4*>(mean_of(k) + d);
+        else
+          c[e] = 0;
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[0] += c[e] * v[e].x;
-        y[1] += c[e] * v[e].y;
-        y[2] += c[e] * v[e].z;
-        y[3] += c[e] * v[e].w;
-      }
+      for (int e = 0; e < 4; ++e) add(c[e] * f, v[e]);
     }
-    if (!live) continue;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (a.elem == LM_BF16)
-        reinterpret_cast<bf16*>(to)[d + e] = from_f32<bf16>(y[e]);
-      else
-        reinterpret_cast<__half*>(to)[d + e] = from_f32<__half>(y[e]);
-    }
+    if (live)
+      *reinterpret_cast<float4*>(&sums[warp][d]) =
+          make_float4(y[0], y[1], y[2], y[3]);
   }
+  __syncthreads();
+  const int64_t b = row / a.heads_q;
+  char* const to =
+      j.out.p + (b * j.out.ts + (row - b * a.heads_q) * j.out.hs) * 2;
+  for (int d = threadIdx.x; d < dim; d += kJoinThreads) {
+    const float y = (sums[0][d] + sums[1][d]) + (sums[2][d] + sums[3][d]);
+    if (a.elem == LM_BF16)
+      reinterpret_cast<bf16*>(to)[d] = from_f32<bf16>(y);
+    else
+      reinterpret_cast<__half*>(to)[d] = from_f32<__half>(y);
+  }
+  if (threadIdx.x == 0 && j.lse)
+    j.lse[row] = sum == 0 ? -INFINITY
+                          : (t + log2f(sum)) * 0.693147180559945309f;
 }
 
 }  // namespace
@@ -124,9 +127,7 @@ int launch_kv_shared(const KvSharedArgs& a, int store, void* stream) {
 }
 
 int launch_kv_join(const KvJoinArgs& j, void* stream) {
-  const int64_t rows = int64_t(j.s.seqs) * j.s.heads_q;
-  constexpr int per = kJoinThreads / 32;
-  return launch(lm_kv_join_kernel, uint64_t((rows + per - 1) / per),
+  return launch(lm_kv_join_kernel, uint64_t(j.s.seqs) * j.s.heads_q,
                 kJoinThreads, 0, static_cast<cudaStream_t>(stream), j);
 }
 

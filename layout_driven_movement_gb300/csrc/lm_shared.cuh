@@ -647,6 +647,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           reinterpret_cast<const uint16_t*>(a.q.p) +
           int64_t(seg.s.start + si) * a.q.ts +
           int64_t(seg.h * a.group + (rg - si * a.group)) * a.q.hs;
+      if (nth == 0 && valid)
+        for (int c = 0; c < dim; c += 64)
+          asm volatile("prefetch.global.L1 [%0];\n" ::"l"(query + c));
       const int step = split ? 2 : 1;
       const bool active = split || q * 128 < seg.rows;
       // The thread's share of four rows: t / 4 and 8 on of a warp's first 16,
@@ -931,12 +934,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             };
             if (a.q16) {
 #pragma unroll 1
-              for (int c0 = 0; c0 < dim16 / 8; c0 += 8) {
-                uint4 w[8];
+              for (int c0 = 0; c0 < dim16 / 8; c0 += 16) {
+                uint4 w[16];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) w[c] = load(c0 + c);
+                for (int c = 0; c < 16; ++c) w[c] = load(c0 + c);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) store(c0 + c, w[c]);
+                for (int c = 0; c < 16; ++c) store(c0 + c, w[c]);
               }
             } else {
 #pragma unroll 1
