@@ -328,14 +328,19 @@ __device__ __forceinline__ void attend_next(const KvAttendArgs& a, int items,
 
 // --- the kernel ----------------------------------------------------------------
 
-// SC: the scores are wanted (a form of its own: the branch alone made the 256
-// element kernel spill).
-template <int KIND, int D, int NT, int HP, bool SC>
+// FORM: the attention over one page table a sequence; over one a key head, or
+// giving the rows' states; giving the scores, over either table.  (As forms of
+// their own: branches on the arguments cost the first one 2.6% of 128 x 12288
+// tokens in e4m3, 416 against 405.5 us, and the 256 element kernel spills.)
+enum AttendForm { FORM_PLAIN, FORM_LONG, FORM_SCORES };
+
+template <int KIND, int D, int NT, int HP, int FORM>
 __global__ void
 __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     lm_kv_attend_kernel(const __grid_constant__ KvAttendArgs a,
                         const __grid_constant__ AttendGrid g) {
   using S = AttendShape<KIND, D, NT, HP>;
+  constexpr bool kStates = FORM == FORM_LONG;
   constexpr bool CODES = S::kCodes;
   constexpr bool KBF = KIND == KIND_BF16;    // bf16 keys in the products
   constexpr bool VBF = KIND != KIND_F16;     // bf16 values and weights
@@ -481,7 +486,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   auto fetch = [&](Pages* pg) {
     const int key0 = ld.tile * TK + wk * KW;
     const int32_t* table = a.table + int64_t(ld.b) * a.table_stride;
-    if (a.table_head)
+    if constexpr (FORM != FORM_PLAIN)
       table += int64_t(ld.item / g.groups * HP + sub) * a.table_head;
 #pragma unroll
     for (int i = 0; i < KL; ++i) {
@@ -625,7 +630,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     if (s.hi > s.lo) continue;
     for (int e = threadIdx.x; e < a.heads_q * dim; e += kAttendThreads) {
       const int qi = e / dim, d = e - qi * dim;
-      if (a.mean)
+      if (kStates && a.mean)
         a.mean[int64_t(b) * a.heads_q * dim + e] = 0;
       else
         reinterpret_cast<uint16_t*>(a.out.p)[int64_t(b) * a.out.ts +
@@ -633,12 +638,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     }
     for (int qi = threadIdx.x; qi < a.heads_q; qi += kAttendThreads) {
       const int64_t row = int64_t(b) * a.heads_q + qi;
-      if (a.state) {
+      if (kStates && a.state) {
         reinterpret_cast<float2*>(a.state)[row] = make_float2(-INFINITY, 0);
         reinterpret_cast<int4*>(a.pieces)[row] = make_int4(0, 0, 0, 0);
       }
       if (a.lse) a.lse[row] = -INFINITY;
-      if (a.lse2) a.lse2[row] = -INFINITY;
+      if (FORM == FORM_SCORES) a.lse2[row] = -INFINITY;
     }
   }
 
@@ -809,7 +814,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       }
       // the scores themselves, where the weights are wanted (the launch that
       // turns them into weights reads those of keys that are seen)
-      if constexpr (SC) {
+      if constexpr (FORM == FORM_SCORES) {
         const int key0 = (at.tile + step) * TK + wk * KW + row8;
         float* const to =
             a.scores + (int64_t(at.b) * a.c.heads + hp * HP + sub) *
@@ -1171,7 +1176,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       return (hp * HP + i) * a.group + q0 + qi;
     };
     auto put = [&](int i, int qi, int d, float x) {
-      if (a.mean) {
+      if (kStates && a.mean) {
         a.mean[(int64_t(done.b) * a.heads_q + row_of(i, qi)) * dim + d] = x;
         return;
       }
@@ -1184,14 +1189,14 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
     };
     auto put_lse = [&](int i, int qi, float t, float sum) {
       const int64_t row = int64_t(done.b) * a.heads_q + row_of(i, qi);
-      if (a.state) {
+      if (kStates && a.state) {
         reinterpret_cast<float2*>(a.state)[row] = make_float2(t, sum);
         reinterpret_cast<int4*>(a.pieces)[row] = make_int4(0, 0, 0, 0);
       }
-      if (!a.lse && !a.lse2) return;
+      if (FORM != FORM_SCORES && !a.lse) return;
       const float lse2 = sum == 0 ? -INFINITY : t + log2f(sum);
       if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;
-      if (a.lse2) a.lse2[row] = lse2;
+      if (FORM == FORM_SCORES) a.lse2[row] = lse2;
     };
     for (int i = 0; i < HP; ++i)
       for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {
@@ -1374,13 +1379,13 @@ inline AttendSpace attend_space(int64_t sms, int64_t blocks, int64_t floats) {
   return s;
 }
 
-template <int KIND, int D, int NT, int HP, bool SC>
-int launch_attend_sc(const KvAttendArgs& a, cudaStream_t st) {
+template <int KIND, int D, int NT, int HP, int FORM>
+int launch_attend_form(const KvAttendArgs& a, cudaStream_t st) {
   using S = AttendShape<KIND, D, NT, HP>;
   int sms = 0, dev = 0;
   const int rc = kv_device(&dev, &sms);
   if (rc != LM_OK) return rc;
-  auto* kernel = lm_kv_attend_kernel<KIND, D, NT, HP, SC>;
+  auto* kernel = lm_kv_attend_kernel<KIND, D, NT, HP, FORM>;
   static std::atomic<uint64_t> allowed{0};    // a bit per device
   if (!(allowed.load() >> dev & 1)) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -1410,8 +1415,10 @@ int launch_attend_sc(const KvAttendArgs& a, cudaStream_t st) {
 
 template <int KIND, int D, int NT, int HP>
 int launch_attend(const KvAttendArgs& a, cudaStream_t st) {
-  return a.scores ? launch_attend_sc<KIND, D, NT, HP, true>(a, st)
-                  : launch_attend_sc<KIND, D, NT, HP, false>(a, st);
+  if (a.scores) return launch_attend_form<KIND, D, NT, HP, FORM_SCORES>(a, st);
+  return a.state || a.table_head
+             ? launch_attend_form<KIND, D, NT, HP, FORM_LONG>(a, st)
+             : launch_attend_form<KIND, D, NT, HP, FORM_PLAIN>(a, st);
 }
 
 template <int KIND, int D>
