@@ -56,8 +56,8 @@ def close(out, q, k, v, group, extra=0.0):
 
 
 def test_decoding_behind_a_shared_prefix():
-    """A prefix written once, then steps that write each sequence's token to its
-    own pages and attend over both."""
+    """A prefix written once, then steps that write each sequence's token to
+    its own pages and attend over both."""
     heads, group, dim, page, seqs, steps = 2, 4, 64, 8, 5, 20
     g = torch.Generator(device="cuda").manual_seed(3)
 
