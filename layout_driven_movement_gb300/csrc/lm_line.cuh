@@ -27,14 +27,16 @@ __device__ __forceinline__ int64_t small_div(int64_t a, int64_t b) {
 
 struct LineShare {
   int64_t total = 0;     // units of the line
+  int64_t parts = 1;     // that it is cut into, none of them empty
   int64_t begin = 0;     // the part: units begin .. begin + left - 1
   int64_t left = 0;
   int b = 0;             // the sequence that unit `begin` belongs to
   int64_t in = 0;        // and its number there
 };
 
-// Part `part` of `parts` of the line, for all T threads of the block at once.
-// units(b): those of sequence b, the same whenever asked.  Up to 32 sequences
+// Part `part` of `parts` of the line, or of as many as it has units, for all T
+// threads of the block at once; a part past the last has nothing.  units(b):
+// those of sequence b, the same whenever asked.  Up to 32 sequences
 // are counted by every warp on its own, with no barrier and little code (a
 // kernel's first pass over its code comes from memory); else every thread
 // counts the units of a run of sequences and a scan over the block does the
@@ -45,6 +47,15 @@ __device__ __forceinline__ LineShare line_share(int seqs, int64_t part,
   __shared__ int64_t sums[T / 32], found[2];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   LineShare s;
+  // (the line of any cache is far below 2^63 / parts)
+  auto cut = [&] {
+    s.parts = s.total < parts ? (s.total < 1 ? 1 : s.total) : parts;
+    const int64_t at = part < s.parts ? part : s.parts;
+    s.begin = small_div(at * s.total, s.parts);
+    s.left = part < s.parts
+                 ? small_div((at + 1) * s.total, s.parts) - s.begin
+                 : 0;
+  };
   if (seqs <= 32) {
     const int64_t mine = lane < seqs ? units(lane) : 0;
     int64_t sum = mine;
@@ -54,8 +65,7 @@ __device__ __forceinline__ LineShare line_share(int seqs, int64_t part,
       if (lane >= k) sum += v;
     }
     s.total = __shfl_sync(0xffffffffu, sum, 31);
-    s.begin = small_div(part * s.total, parts);
-    s.left = small_div((part + 1) * s.total, parts) - s.begin;
+    cut();
     // the first sequence whose units end behind `begin`
     s.b = __ffs(__ballot_sync(0xffffffffu, sum > s.begin)) - 1;
     s.in = s.begin - __shfl_sync(0xffffffffu, sum - mine, s.b & 31);
@@ -80,9 +90,7 @@ __device__ __forceinline__ LineShare line_share(int seqs, int64_t part,
     if (w < warp) before += sums[w];
     s.total += sums[w];
   }
-  // (the line of any cache is far below 2^63 / parts)
-  s.begin = small_div(part * s.total, parts);
-  s.left = small_div((part + 1) * s.total, parts) - s.begin;
+  cut();
   if (s.left > 0 && s.begin >= before && s.begin < before + mine) {
     int b = b0;
     for (;; ++b) {

@@ -970,10 +970,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                      (share.begin < seg.item_at ? 1 : 0)) *
                         (int64_t(S::kRows) * (D + 2));
       // where the rows' pieces will be: the block of tile i of the line is
-      // ((i + 1) blocks - 1) / total
+      // ((i + 1) parts - 1) / total, and none of them is without any
       const int pieces =
           seg.t0 == 0 && sub == 0
-              ? int(small_div((seg.item_at + seg.s.tiles) * gridDim.x - 1,
+              ? int(small_div((seg.item_at + seg.s.tiles) * share.parts - 1,
                               share.total) -
                     blockIdx.x) +
                     1

@@ -347,6 +347,25 @@ def test_more_groups_than_a_warp_counts():
         close(out[b], q[b], *rows, 3, 2.0 ** -8)
 
 
+@pytest.mark.parametrize("keys", [1, 600, 1300])
+def test_a_short_prefix_after_a_long_one(keys):
+    """A line of fewer tiles than blocks: what blocks left in the workspace
+    that have nothing to do now is nobody's."""
+    P = lr.Held([30000, keys, 5, 3], 4, 64, 16, "nhd", BF, None, seed=3)
+    cache, plan = P.cache(lm)
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(2, 16, 64, generator=g).to(BF).cuda()
+    ws = space(lm.kv_attend_shared_workspace(plan, 2, 16))
+    t = P.table.cuda()
+    out = torch.empty_like(q)
+    for first, n in ((0, 30000), (1, keys)):
+        lm.kv_attend_shared(cache, q, t[first:first + 1], ints([n]),
+                            ints([0, 2]), t[2:], ints([5, 3]), out, ws)
+    for b in range(2):
+        rows = [torch.cat([P.seq(kv, 1), P.seq(kv, 2 + b)]) for kv in (0, 1)]
+        close(out[b], q[b], *rows, 4, 2.0 ** -8)
+
+
 @pytest.mark.parametrize("store", [None, "e4m3"])
 def test_offsets_past_32_bits(store):
     """Pages 3 GB apart: rows that lie past 2^32 elements."""
