@@ -669,6 +669,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       clear();
       // the reference's weight, as a power of two
       const float off = BF ? -float(8 + 32 - __clz(seg.steps * NK)) : 12.f;
+      // what is added to a score: `off` less the reference, but where that
+      // rounds up so far that an f16 weight might be infinite
+      auto sub_of = [&](float m) {
+        const float ref = m == -INFINITY ? 0.f : m, x = off - ref;
+        return !BF && x + ref > off + SLACK ? -ref : x;
+      };
       bool first = true;
       // Tile -1 stands for the row's query, which goes to shared memory.  In
       // the block's first one the weights are formed once of whatever tensor
@@ -712,20 +718,17 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           float most_of = 0;
           bool near = true, apart = false;
           if (CODES) {
-            const float* const ends =
-                reinterpret_cast<const float*>(meta + NK * 12 + 16);
-            float least = INFINITY;
-            most_of = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              least = fminf(least, ends[i]);
-              most_of = fmaxf(most_of, ends[4 + i]);
-            }
+            const float4 lows =
+                *reinterpret_cast<const float4*>(meta + NK * 12 + 16);
+            const float4 tops =
+                *reinterpret_cast<const float4*>(meta + NK * 12 + 32);
+            const float least =
+                fminf(fminf(lows.x, lows.y), fminf(lows.z, lows.w));
+            most_of = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
             most = fmaxf(most, most_of);
             near = !__any_sync(0xffffffffu, !(most_of - least < 4) && j >= 0);
             apart = __any_sync(0xffffffffu, !(most - least < 60) && j >= 0);
           }
-          const float2 unit2 = make_float2(unit, unit);
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
             const uint32_t lanes = uint32_t(half * 16) << 16;
@@ -802,10 +805,22 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             float2 sub[2], by[2], sums[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float x = off - (m[i] == -INFINITY ? 0.f : m[i]);
+              const float x = sub_of(m[i]);
               sub[i] = make_float2(x, x);
               by[i] = make_float2(down[i], down[i]);
               sums[i] = make_float2(0, 0);
+            }
+            // A fused multiplication would leave what a score is rounded by, 2^5
+            // of one of 2^29: large scores are rounded first.  (Codes' are, by
+            // their own factors.)
+            float2 unit2 = make_float2(unit, unit);
+            if (!CODES &&
+                __any_sync(0xffffffffu, fmaxf(fabsf(m[0]), fabsf(m[1])) >
+                                            0x1p18f)) {
+#pragma unroll
+              for (int e = 0; e < NK / 2; ++e)
+                s[e] = __float_as_uint(__fmul_rn(__uint_as_float(s[e]), unit));
+              unit2 = make_float2(1, 1);
             }
             if (CODES && apart) {
 #pragma unroll
@@ -1007,7 +1022,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               // values the sum may be of any size, and references far apart
               // then say nothing about weights)
               const int e = int(__float_as_uint(sum) >> 23) - 127;
-              float2 ml = make_float2(none ? -INFINITY : m[i] - off, sum);
+              float2 ml = make_float2(none ? -INFINITY : -sub_of(m[i]), sum);
               if (CODES && sum > 0x1p-120f && sum < INFINITY) {
                 ml.x += float(e);
                 ml.y *= __int_as_float((127 - e) << 23);

@@ -366,6 +366,39 @@ def test_a_short_prefix_after_a_long_one(keys):
         close(out[b], q[b], *rows, 4, 2.0 ** -8)
 
 
+@pytest.mark.parametrize("dtype,store", [(BF, None), (HF, None), (BF, "int8")],
+                         ids=str)
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 26, 2.0 ** 60])
+def test_scores_of_any_size(dtype, store, size):
+    """Scores up to 2^60 about (in float16 2^29): all weight lies on each row's
+    largest, whose value comes out as it is."""
+    if dtype == HF and size > 2.0 ** 29:
+        size = 2.0 ** 29
+    P = lr.Held([700, 3, 5], 1, 64, 16, "nhd", dtype, store, seed=3)
+    cache, plan = P.cache(lm)
+    g = torch.Generator().manual_seed(2)
+    q = torch.randn(2, 4, 64, generator=g) * 2.0 ** 12
+    q = q.to(dtype).cuda()
+    out = torch.empty_like(q)
+    ws = space(lm.kv_attend_shared_workspace(plan, 2, 4))
+    t = P.table.cuda()
+    # (a score is 2^12 times some 8)
+    scale = size / 2.0 ** 15
+    lm.kv_attend_shared(cache, q, t[:1], ints([700]), ints([0, 2]), t[1:],
+                        ints([3, 5]), out, ws, scale=scale)
+    for b in range(2):
+        k, v = (torch.cat([P.seq(kv, 0), P.seq(kv, 1 + b)])[:, 0]
+                for kv in (0, 1))
+        s = q[b].double() @ k.T * scale
+        top, at = s.max(-1)
+        s.scatter_(1, at[:, None], -math.inf)
+        assert (top - s.amax(-1) > 2.0 ** -14 * top).all()
+        assert (top - s.amax(-1) > 40).all()
+        want = v[at]
+        assert ((out[b].double() - want).abs() <=
+                torch.finfo(dtype).eps * want.abs()).all()
+
+
 @pytest.mark.parametrize("store", [None, "e4m3"])
 def test_offsets_past_32_bits(store):
     """Pages 3 GB apart: rows that lie past 2^32 elements."""
