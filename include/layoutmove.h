@@ -937,11 +937,12 @@ int lm_kv_evict_workspace(const lm_kv_plan* plan, int seqs, int keep,
  * their order, and kept_lens[b] is their number.  kept_table may be the page
  * table itself (the sequence goes on in its own first pages) or name other
  * pages; page i of a sequence is its own page i in page_table or one that
- * page_table does not name anywhere, and no page is named for two sequences
- * in kept_table, or written for one and read for another.  kept_lens may be
- * lens itself.  What is not written to is left as it is.  A page number
- * outside [0, pages) is out of range: a token there weighs least, and a row
- * from or to there is not moved.
+ * page_table does not name anywhere, and no page is named twice in
+ * kept_table, or written for one sequence and read for another.  kept_lens may
+ * be lens itself.  What is not written to is left as it is, so that the slots
+ * past the kept tokens hold weights of tokens that are gone: clear a slot's
+ * weight when it is written again.  A page number outside [0, pages) is out of
+ * range: a token there weighs least, and a row from or to there is not moved.
  * kept_pages: the pages of a row of kept_table, enough for min(keep, max_pages
  * * P) tokens.
  * Errors: LM_E_INVALID (NULL, counts, recent > keep, pointer alignment),
@@ -968,8 +969,8 @@ int lm_last_cuda_error(void);
 /* Synchronise cuda_stream (a cudaStream_t, NULL for the legacy stream),
  * then report in *status whether a kernel of this library on the current
  * device gave up a bounded wait since the last reset: LM_OK, or
- * LM_E_TIMEOUT (the bulk-copy STAGED kernels bound every mbarrier wait at
- * about a second; a block that gives up records it here, waits -- again
+ * LM_E_TIMEOUT (the bulk-copy STAGED kernels and lm_kv_attend_shared's bound
+ * every mbarrier wait at about a second; a block that gives up records it here, waits -- again
  * bounded, about four seconds per stage -- for its own copies still in
  * flight, and exits, leaving its part of the destination unwritten).  If
  * even that drain runs out (copies from global memory that do not complete

@@ -1144,7 +1144,8 @@ def kv_evict(cache: KVCache, weights, page_table, lens, kept_table, kept_lens,
     largest weights, float32 [pages, key heads, page_tokens].  Rows, scales and
     weights of the kept ones move up into the pages of kept_table, int32
     [sequences, pages], which may be page_table; kept_lens int32 [sequences],
-    which may be lens, gets their number (see lm_kv_evict)."""
+    which may be lens, gets their number.  The slots past them keep their
+    weights: clear a slot's when it is written again (see lm_kv_evict)."""
     p = cache.plan
     rc = _pycall().kv_evict(p._p, cache._p, weights, page_table, lens,
                             kept_table, kept_lens, keep, recent, workspace,

