@@ -207,19 +207,30 @@ __global__ void __launch_bounds__(kBoundThreads, STORE == LM_KV_SAME ? 8 : 4)
 constexpr int kScoreThreads = 256;
 constexpr int kScorePages = 32;      // of a warp's unit
 
-// A unit is kScorePages pages of one sequence and head.  L lanes of 8 elements
-// hold a row, 32 / L pages at a time, the loads of several rounds in flight: a
-// query's positive and negative parts meet hi and lo in four 4-way byte products.
-// 32 sequences x 1024 pages x 8 heads x 4 queries (67 MB of bounds): 24 us, 54%
-// of the issue slots, most of them the exchanges between lanes.
-// The sums of up to 8 queries over the L lanes are added up by halving: each
-// exchange leaves a lane half of the queries, until it has one, whose sum is then
-// added over the lanes that have the same.
-template <class T, int L, int GQ>
-__global__ void __launch_bounds__(kScoreThreads, GQ == 8 ? 2 : 3)
+// D += A B: 16 rows by 32 whole numbers of 8 bits, those by 8 columns.
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4],
+                                       uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A unit is kScorePages pages of one sequence and head, two products of 16
+// pages by 8 queries: hi meets the queries' positive parts and lo their
+// negative ones, in KS steps of 32 elements each.  A sum has no order, so that
+// of a step's elements lane t % 4 takes 8 side by side, 32 bytes of a row a
+// quad.  What bounds it are the loads, one after the other, of a unit's pages,
+// bounds and queries: 32 sequences x up to 1024 pages x 8 heads x 4 queries of
+// 128 elements (47 MB of bounds) 20 us, 13 sequences x 500 pages x 4 x 5 x 64
+// 7.8.  Three blocks an SM with one product's rows on their way, or two with
+// both: 20 against 23 us for the first, 8.4 against 7.8 for the second.  (Byte
+// products on the vector units, sums exchanged between lanes: 24 and 11.)
+template <class T, int KS>
+__global__ void __launch_bounds__(kScoreThreads, KS == 4 ? 3 : 2)
     lm_kv_score_kernel(const __grid_constant__ KvSelectArgs a) {
-  constexpr int PW = 32 / L;
-  constexpr int kAhead = L == 8 ? 4 : 8;    // rounds whose loads are in flight
+  constexpr int kRounds = KS == 2 ? 2 : 1;  // of 16 pages, loaded together
   stream_order();
   auto pages_of = [&](int b) {
     const int64_t most = a.max_pages * a.page_tokens;
@@ -236,8 +247,7 @@ __global__ void __launch_bounds__(kScoreThreads, GQ == 8 ? 2 : 3)
       a.seqs, blockIdx.x, gridDim.x,
       [&](int b) { return int64_t(tiles_of(b)) * a.heads; });
   if (at.left <= 0) return;
-  const int lane = threadIdx.x % 32, c = lane % L, pw = lane / L;
-  const bool has = c * 8 < a.dim;
+  const int lane = threadIdx.x % 32, c = lane % 4, r = lane / 4;
   const int warp = threadIdx.x / 32;
   // this warp's units: every eighth of the block's
   int tiles = tiles_of(at.b);
@@ -265,110 +275,115 @@ __global__ void __launch_bounds__(kScoreThreads, GQ == 8 ? 2 : 3)
     const float scale =
         there ? a.bound_scale[int64_t(mine) * a.heads + h] : 0.f;
     float best = -INFINITY;            // of page p0 + lane
-    for (int g0 = 0; g0 < a.group; g0 += GQ) {
-      // the queries as whole numbers
-      uint32_t qp[GQ][2], qn[GQ][2];
-      float qs[GQ];
+    for (int g0 = 0; g0 < a.group; g0 += 8) {
+      // query g0 + r as whole numbers
+      uint32_t qp[KS][2], qn[KS][2], raw[KS][4];
+      float top = 0;
+      const bool is = g0 + r < a.group;
+      const T* const q = reinterpret_cast<const T*>(a.q.p) +
+                         int64_t(at.b) * a.q.ts +
+                         int64_t(h * a.group + g0 + (is ? r : 0)) * a.q.hs;
 #pragma unroll
-      for (int g = 0; g < GQ; ++g) {
-        float x[8] = {};
-        if (has && g0 + g < a.group) {
-          const T* q = reinterpret_cast<const T*>(a.q.p) +
-                       int64_t(at.b) * a.q.ts +
-                       int64_t(h * a.group + g0 + g) * a.q.hs + c * 8;
+      for (int k = 0; k < KS; ++k) {
+        const int d = (4 * k + c) * 8;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) raw[k][e] = 0;
+        if (is && d < a.dim) {
           if (a.q16) {
-            const uint4 w = *reinterpret_cast<const uint4*>(q);
-            const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-            get_words<T, 4>(r, x);
+            const uint4 w = *reinterpret_cast<const uint4*>(q + d);
+            raw[k][0] = w.x;
+            raw[k][1] = w.y;
+            raw[k][2] = w.z;
+            raw[k][3] = w.w;
           } else {
+            const uint16_t* const y = reinterpret_cast<const uint16_t*>(q + d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = to_f32(q[e]);
+            for (int e = 0; e < 4; ++e)
+              raw[k][e] = y[2 * e] | uint32_t(y[2 * e + 1]) << 16;
           }
         }
-        float top = 0;
+        float x[8];
+        get_words<T, 4>(raw[k], x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(x[e]));
+      }
+      top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float by = 0, unit = 1;
+      if (!(top < INFINITY)) {
+        unit = __int_as_float(0x7fc00000);
+      } else if (top > 0) {
+        const int e = power_of(__float_as_uint(top));
+        unit = pow2f(e);
+        by = pow2f(-e);
+      }
 #pragma unroll
-        for (int k = 1; k < L; k *= 2)
-          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, k));
-        float by = 0;
-        qs[g] = 1;
-        if (!(top < INFINITY)) {
-          qs[g] = __int_as_float(0x7fc00000);
-        } else if (top > 0) {
-          const int e = power_of(__float_as_uint(top));
-          qs[g] = pow2f(e);
-          by = pow2f(-e);
-        }
+      for (int k = 0; k < KS; ++k) {
+        float x[8];
+        get_words<T, 4>(raw[k], x);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          qp[g][w] = qn[g][w] = 0;
+          qp[k][w] = qn[k][w] = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int v = by == 0 ? 0 : __float2int_rn(x[4 * w + k] * by);
-            qp[g][w] |= uint32_t(max(v, 0)) << (8 * k);
-            qn[g][w] |= uint32_t(min(v, 0) & 0xff) << (8 * k);
+          for (int e = 0; e < 4; ++e) {
+            const int v = by == 0 ? 0 : __float2int_rn(x[4 * w + e] * by);
+            qp[k][w] |= uint32_t(max(v, 0)) << (8 * e);
+            qn[k][w] |= uint32_t(min(v, 0) & 0xff) << (8 * e);
           }
         }
       }
-      // the lane's query after the exchanges
-      int own_g = 0;
-      float own_scale = qs[0];
-      bool own_is = true;
-#pragma unroll
-      for (int n = GQ, k = L / 2; n > 1; n /= 2, k /= 2)
-        if (lane & k) own_g += n / 2;
-#pragma unroll
-      for (int g = 0; g < GQ; ++g)
-        if (g == own_g) own_scale = qs[g];
-      own_is = g0 + own_g < a.group;
+      // those of a product's columns that this lane has
+      const bool is0 = g0 + 2 * c < a.group, is1 = g0 + 2 * c + 1 < a.group;
+      const float unit0 = __shfl_sync(0xffffffffu, unit, 8 * c);
+      const float unit1 = __shfl_sync(0xffffffffu, unit, 8 * c + 4);
 #pragma unroll 1
-      for (int p = 0; p < p1 - p0; p += PW * kAhead) {
-        uint2 lo[kAhead], hi[kAhead];
-        bool ok[kAhead];
+      for (int p = 0; p < p1 - p0; p += 16 * kRounds) {
+        uint2 lo[kRounds][2][KS], hi[kRounds][2][KS];
 #pragma unroll
-        for (int r = 0; r < kAhead; ++r) {
-          const int64_t page =
-              __shfl_sync(0xffffffffu, mine, (p + r * PW + pw) & 31);
-          ok[r] = page >= 0 && page < a.pages && p + r * PW + pw < p1 - p0;
-          lo[r] = hi[r] = make_uint2(0, 0);
-          if (ok[r] && has) {
-            const int8_t* from = a.bounds + (page * a.heads + h) * 2 * a.dim;
-            lo[r] = *reinterpret_cast<const uint2*>(from + c * 8);
-            hi[r] = *reinterpret_cast<const uint2*>(from + a.dim + c * 8);
-          }
-        }
+        for (int n = 0; n < kRounds; ++n)
 #pragma unroll
-        for (int r = 0; r < kAhead; ++r) {
-          int s[GQ];
+          for (int i = 0; i < 2; ++i) {
+            const int64_t page =
+                __shfl_sync(0xffffffffu, mine, p + 16 * n + 8 * i + r);
+            const bool ok = page >= 0 && page < a.pages;
+            const int8_t* const from =
+                a.bounds + ((ok ? page : 0) * a.heads + h) * 2 * a.dim;
 #pragma unroll
-          for (int g = 0; g < GQ; ++g) {
-            s[g] = __dp4a(int(qp[g][0]), int(hi[r].x), 0);
-            s[g] = __dp4a(int(qp[g][1]), int(hi[r].y), s[g]);
-            s[g] = __dp4a(int(qn[g][0]), int(lo[r].x), s[g]);
-            s[g] = __dp4a(int(qn[g][1]), int(lo[r].y), s[g]);
-          }
-          int k = L / 2;
-#pragma unroll
-          for (int n = GQ; n > 1; n /= 2, k /= 2)
-#pragma unroll
-            for (int g = 0; g < n / 2; ++g) {
-              const bool up = lane & k;
-              const int give = up ? s[g] : s[g + n / 2];
-              const int keep = up ? s[g + n / 2] : s[g];
-              s[g] = keep + __shfl_xor_sync(0xffffffffu, give, k);
+            for (int k = 0; k < KS; ++k) {
+              const int d = (4 * k + c) * 8;
+              lo[n][i][k] = hi[n][i][k] = make_uint2(0, 0);
+              if (ok && d < a.dim) {
+                lo[n][i][k] = *reinterpret_cast<const uint2*>(from + d);
+                hi[n][i][k] = *reinterpret_cast<const uint2*>(from + a.dim + d);
+              }
             }
+          }
 #pragma unroll
-          for (; k; k /= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], k);
-          float score = own_is ? float(s[0]) * own_scale : -INFINITY;
+        for (int n = 0; n < kRounds; ++n) {
+          int s[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int e = L / 2; e >= (L / GQ > 0 ? L / GQ : 1); e /= 2)
-            score = max_nan(score, __shfl_xor_sync(0xffffffffu, score, e));
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t up[4] = {hi[n][0][k].x, hi[n][1][k].x,
+                                    hi[n][0][k].y, hi[n][1][k].y};
+            const uint32_t down[4] = {lo[n][0][k].x, lo[n][1][k].x,
+                                      lo[n][0][k].y, lo[n][1][k].y};
+            mma_s8(s, up, qp[k][0], qp[k][1]);
+            mma_s8(s, down, qn[k][0], qn[k][1]);
+          }
+          // of rows r and r + 8 the largest over the queries
+          float y[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            y[i] = is0 ? float(s[2 * i]) * unit0 : -INFINITY;
+            if (is1) y[i] = max_nan(y[i], float(s[2 * i + 1]) * unit1);
+            y[i] = max_nan(y[i], __shfl_xor_sync(0xffffffffu, y[i], 1));
+            y[i] = max_nan(y[i], __shfl_xor_sync(0xffffffffu, y[i], 2));
+          }
           // to the lane that has the page
-          const int first = p + r * PW;
-          const float got =
-              __shfl_sync(0xffffffffu, score, (lane - first) * L & 31);
-          if (lane >= first && lane < first + PW) best = max_nan(best, got);
+          const float y0 = __shfl_sync(0xffffffffu, y[0], lane % 8 * 4);
+          const float y1 = __shfl_sync(0xffffffffu, y[1], lane % 8 * 4);
+          if (lane / 16 == p / 16 + n)
+            best = max_nan(best, lane & 8 ? y1 : y0);
         }
       }
     }
@@ -423,23 +438,14 @@ __global__ void __launch_bounds__(T)
       });
 }
 
-template <class T, int L>
-int launch_score_l(const KvSelectArgs& a, uint64_t grid, cudaStream_t st) {
-  if (a.group == 1)
-    return launch(lm_kv_score_kernel<T, L, 1>, grid, kScoreThreads, 0, st, a);
-  if (a.group == 2)
-    return launch(lm_kv_score_kernel<T, L, 2>, grid, kScoreThreads, 0, st, a);
-  if (a.group <= 4)
-    return launch(lm_kv_score_kernel<T, L, 4>, grid, kScoreThreads, 0, st, a);
-  return launch(lm_kv_score_kernel<T, L, 8>, grid, kScoreThreads, 0, st, a);
-}
-
 template <class T>
 int launch_score(const KvSelectArgs& a, int sms, cudaStream_t st) {
-  const uint64_t grid = uint64_t(sms) * (a.group > 4 ? 2 : 3);
-  if (a.dim <= 64) return launch_score_l<T, 8>(a, grid, st);
-  if (a.dim <= 128) return launch_score_l<T, 16>(a, grid, st);
-  return launch_score_l<T, 32>(a, grid, st);
+  auto run = [&](auto* kernel, int blocks) {
+    return launch(kernel, uint64_t(sms) * blocks, kScoreThreads, 0, st, a);
+  };
+  return a.dim <= 64    ? run(lm_kv_score_kernel<T, 2>, 2)
+         : a.dim <= 128 ? run(lm_kv_score_kernel<T, 4>, 3)
+                        : run(lm_kv_score_kernel<T, 8>, 2);
 }
 
 template <class T, int STORE>
