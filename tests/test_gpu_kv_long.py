@@ -347,6 +347,38 @@ def test_more_groups_than_a_warp_counts():
         close(out[b], q[b], *rows, 3, 2.0 ** -8)
 
 
+@pytest.mark.parametrize("dim,group,dtype", [(8, 1, BF), (72, 11, HF),
+                                             (128, 9, BF), (200, 3, HF),
+                                             (256, 16, BF)], ids=str)
+def test_choice_by_queries_out_of_line(dim, group, dtype):
+    """Queries whose rows allow no wide loads, more of them than a product's
+    columns, and rows that end inside a step."""
+    P = lr.Held([150, 3, 331], 2, dim, 4, "nhd", dtype, None, seed=3,
+                drift=1.0)
+    cache, plan = P.cache(lm)
+    bounds = torch.zeros(P.pool, 2, 2, dim, dtype=torch.int8, device="cuda")
+    scale = torch.ones(P.pool, 2, device="cuda")
+    ids = torch.cat([P.table[b, :-(-n // 4)] for b, n in enumerate(P.lens)])
+    counts = [min(4, n - 4 * i) for n in P.lens for i in range(-(-n // 4))]
+    lm.kv_bound(cache, ids.cuda(), ints(counts), bounds, scale)
+    g = torch.Generator().manual_seed(2)
+    wide = torch.randn(3, 2 * group, dim + 5, generator=g).to(dtype).cuda()
+    q = wide[:, :, 3:3 + dim]
+    selected = torch.empty(3, 2, 9, dtype=torch.int32, device="cuda")
+    sl = torch.empty(3, dtype=torch.int32, device="cuda")
+    lm.kv_select(cache, q, bounds, scale, P.table.cuda(), ints(P.lens),
+                 selected, sl, space(lm.kv_select_workspace(plan, 3, P.most)),
+                 first=1, last=2)
+    for b, n in enumerate(P.lens):
+        m = -(-n // 4)
+        of = P.table[b, :m].long()
+        s = lr.scores(q[b], bounds[of, :, 0].cpu(), bounds[of, :, 1].cpu(),
+                      scale[of].cpu(), group)
+        for h in range(2):
+            pages = lr.choose(s[h].tolist(), 9, 1, 2)
+            assert selected[b, h, :len(pages)].tolist() == of[pages].tolist()
+
+
 @pytest.mark.parametrize("keys", [1, 600, 1300])
 def test_a_short_prefix_after_a_long_one(keys):
     """A line of fewer tiles than blocks: what blocks left in the workspace
