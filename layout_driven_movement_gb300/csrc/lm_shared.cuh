@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                         : -1;
           // A cache of 2^36 bytes or more is refused.  A key that is not seen,
           // and a chunk past the row's end, has any other's codes: the mask
-          // hides the key, `signs` clears its values, and the chunk stays in
+          // hides the key, `widen` clears its values, and the chunk stays in
           // its registers.
           const uint32_t row = ok ? uint32_t(from >> 4) : 0;
 #pragma unroll
@@ -401,13 +401,22 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           }
           ask(kr, a.c.k);
         };
-        // widened to f16
-        auto widen = [&](uint32_t tile_s, const uint4* w) {
+        // Widened to f16.  What the logarithm of a value's scale says nothing of,
+        // its sign and 0, goes to the widened values (of the codes -128 has no
+        // opposite): `turned` where a row of the warp's is to be.
+        auto widen = [&](uint32_t tile_s, const uint4* w, auto turned,
+                         float factor) {
 #pragma unroll
           for (int i = 0; i < IT; ++i) {
             const int r = i * RPI + r0;
             uint32_t y[8];
             widen16<STORE>(w[i], y);
+            if constexpr (decltype(turned)::value) {
+              const float f = __shfl_sync(0xffffffffu, factor, r);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = f == 0 ? 0u : f < 0 ? y[e] ^ 0x80008000u : y[e];
+            }
             if (!held) continue;
             // (four lanes begin with their first chunk and four with their
             // second, so that eight lanes' stores lie in all banks)
@@ -425,21 +434,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             }
           }
           smem_to_products();
-        };
-        // What the logarithm of a scale says nothing of, its sign and 0, goes
-        // to the codes: an int8 code's and an e4m3 code's sign alike.
-        auto signs = [&](uint4* w, float factor) {
-#pragma unroll
-          for (int i = 0; i < IT; ++i) {
-            const float f = __shfl_sync(0xffffffffu, factor, i * RPI + r0);
-            auto turn = [&](uint32_t x) {
-              if (f == 0) return 0u;
-              if (!(f < 0)) return x;
-              return STORE == LM_KV_E4M3 ? x ^ 0x80808080u : __vnegss4(x);
-            };
-            w[i] = make_uint4(turn(w[i].x), turn(w[i].y), turn(w[i].z),
-                              turn(w[i].w));
-          }
         };
         ask_keys(seg.t0);
         ask(vr, a.c.v);
@@ -473,14 +467,16 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           if (lane < 2)
             reinterpret_cast<float*>(m + NK * 12 + 16)[lane * 4 + lw] =
                 log2f(__uint_as_float(lane ? most : least));
-          widen(k_s + slot * S::kTile + to, kr);
+          widen(k_s + slot * S::kTile + to, kr, std::false_type{}, 0.f);
           mbar_arrive(k_full(slot));
           const float factor = vs;
           ask_keys(t + 1);
           if (tile >= NS) acquire(v_empty(slot), turn ^ 1);
           if (!alive) break;
-          if (__any_sync(0xffffffffu, !(factor > 0))) signs(vr, factor);
-          widen(v_s + slot * S::kTile + to, vr);
+          if (__any_sync(0xffffffffu, mine && !(factor > 0)))
+            widen(v_s + slot * S::kTile + to, vr, std::true_type{}, factor);
+          else
+            widen(v_s + slot * S::kTile + to, vr, std::false_type{}, 0.f);
           mbar_arrive(v_full(slot));
           ask(vr, a.c.v);
         }
