@@ -185,8 +185,10 @@ __global__ void __launch_bounds__(kBoundThreads, STORE == LM_KV_SAME ? 8 : 4)
     uint32_t l = 0, u = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int f = zero ? 0 : __float2int_rd(lo[e + k] * by);
-      const int g = zero ? 0 : __float2int_ru(hi[e + k] * by);
+      // (outwards twice: beside a large key a small one's product lies below
+      // 2^-150, and to the nearest number of 32 bits it would be 0)
+      const int f = zero ? 0 : __float2int_rd(__fmul_rd(lo[e + k], by));
+      const int g = zero ? 0 : __float2int_ru(__fmul_ru(hi[e + k], by));
       l |= uint32_t(f & 0xff) << (8 * k);
       u |= uint32_t(g & 0xff) << (8 * k);
     }

@@ -123,6 +123,44 @@ def test_bounds_of_values_at_the_ends():
         assert got == by or (math.isnan(got) and math.isnan(by)), i
 
 
+@pytest.mark.parametrize("store,dtype", [(None, BF), ("e4m3", BF),
+                                         ("int8", HF)], ids=str)
+def test_bounds_over_a_wide_range(store, dtype):
+    """Keys far smaller than the page's largest, of either sign: a quotient
+    that 32 bits do not hold is still below or above 0."""
+    page, dim = 4, 16
+    P = lr.Held([page * 3], 1, dim, page, "nhd", dtype, store, spare=0)
+    ids = P.table[0].long().cuda()
+    x = torch.zeros(3, page, 1, dim, dtype=torch.float64)
+    big = torch.tensor([2.0 ** 100, 2.0 ** 30, 1.0])
+    small = torch.tensor([2.0 ** -60, 2.0 ** -126, 2.0 ** -126])
+    # alone in their columns, beside zeros, and beside a small one of the
+    # other sign
+    for d, s in ((1, 1), (2, -1)):
+        x[:, 2, 0, d] = s * small
+    x[:, 1, 0, 3], x[:, 2, 0, 3] = small, -small
+    x[:, :, 0, 4], x[:, :, 0, 5] = small[:, None], -small[:, None]
+    x[:, 0, 0, 0] = big
+    if store is None:
+        P.held[0][ids] = x.to(dtype).cuda()
+    else:
+        # one power of two a token: codes of 1 and -1 under its scale
+        one = {"e4m3": (0x38, 0xb8), "int8": (1, -1)}[store]
+        code = torch.zeros(x.shape, dtype=torch.int64)
+        code[x > 0], code[x < 0] = one
+        P.held[0][ids] = code.to(P.held[0].dtype).cuda()
+        scale = x.abs().amax((-2, -1))
+        scale[scale == 0] = 1
+        P.scales[0][ids, 0] = scale.float().cuda()
+        x = x.sign() * scale[..., None, None]
+    P.rows[0][ids] = x.cuda()
+    cache, plan = P.cache(lm)
+    bounds, scale = make_bounds(P, cache)
+    assert (bounds[ids, 0, :, 0] == torch.tensor([0, 64]).cuda()).all()
+    check_bounds(P, bounds, scale, *page_counts(P))
+    assert (bounds[ids[:2], 0, :, 3] == torch.tensor([-1, 1]).cuda()).all()
+
+
 def test_bounds_page_out_of_range():
     P = lr.Held([8], 1, 16, 4, "nhd", BF, None)
     cache, plan = P.cache(lm)
