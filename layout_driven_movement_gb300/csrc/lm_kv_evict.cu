@@ -26,14 +26,15 @@ __global__ void __launch_bounds__(T)
   const int b = unit / int(a.c.heads), h = unit - b * int(a.c.heads);
   const int n = evict_len(a, b);
   int32_t* list = a.list + int64_t(unit) * a.keep;
-  const int threads = T * C, me = rank * T + int(threadIdx.x);
+  // (numbers without a sign: one past a list of nearly 2^31 is still one)
+  const uint32_t threads = T * C, me = rank * T + threadIdx.x;
   if (n <= a.keep) {
-    for (int i = me; i < n; i += threads) list[i] = i;
+    for (uint32_t i = me; i < uint32_t(n); i += threads) list[i] = int32_t(i);
     return;
   }
   const int need = a.keep - a.recent;
-  for (int i = me; i < a.recent; i += threads)
-    list[need + i] = n - a.recent + i;
+  for (uint32_t i = me; i < uint32_t(a.recent); i += threads)
+    list[uint32_t(need) + i] = int32_t(uint32_t(n - a.recent) + i);
   if (need == 0) return;
   const int32_t* table = a.table + b * a.table_stride;
   take_top<T, C>(

@@ -419,15 +419,16 @@ __global__ void __launch_bounds__(T)
   if (h == 0 && rank == 0 && threadIdx.x == 0)
     a.selected_lens[b] =
         int32_t(len - int64_t(n - count) * a.page_tokens);
-  const int threads = T * C, me = rank * T + int(threadIdx.x);
-  for (int i = count + me; i < a.keep; i += threads) to[i] = -1;
+  // (numbers without a sign: one past a list of 2^31 - 1 is still one)
+  const uint32_t threads = T * C, me = rank * T + threadIdx.x;
+  for (uint32_t i = count + me; i < uint32_t(a.keep); i += threads) to[i] = -1;
   if (n <= a.keep) {
-    for (int i = me; i < n; i += threads) to[i] = table[i];
+    for (uint32_t i = me; i < uint32_t(n); i += threads) to[i] = table[i];
     return;
   }
-  for (int i = me; i < a.first; i += threads) to[i] = table[i];
-  for (int i = me; i < a.last; i += threads)
-    to[a.keep - a.last + i] = table[n - a.last + i];
+  for (uint32_t i = me; i < uint32_t(a.first); i += threads) to[i] = table[i];
+  for (uint32_t i = me; i < uint32_t(a.last); i += threads)
+    to[uint32_t(a.keep - a.last) + i] = table[uint32_t(n - a.last) + i];
   const int need = a.keep - a.first - a.last;
   if (need == 0) return;
   const float* scores =

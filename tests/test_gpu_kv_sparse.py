@@ -310,6 +310,27 @@ def test_choice_lengths_and_pages_out_of_range():
     assert selected[1].tolist() == [[int(table[1, 0]), int(table[1, 9])]] * 2
 
 
+def test_choice_into_the_longest_list():
+    """A list of 2^31 - 1 entries, 9 of them chosen: the rest is -1 to the
+    last, and nothing behind or before it is written to."""
+    P = lr.Held([9 * 16 - 3], 1, 64, 16, "nhd", BF, None, seed=3)
+    cache, plan = P.cache(lm)
+    bounds, scale = make_bounds(P, cache)
+    keep, room = 2 ** 31 - 1, 1 << 16
+    buf = torch.full((keep + 2 * room,), 5, dtype=torch.int32, device="cuda")
+    selected = buf[room:room + keep].view(1, 1, keep)
+    lens = ints([0])
+    q = torch.ones(1, 1, 64, dtype=BF, device="cuda")
+    lm.kv_select(cache, q, bounds, scale, P.table.cuda(), ints(P.lens),
+                 selected, lens, space(lm.kv_select_workspace(plan, 1, 9)))
+    torch.cuda.synchronize()
+    assert (buf[:room] == 5).all() and (buf[room + keep:] == 5).all()
+    assert lens.item() == P.lens[0]
+    assert torch.equal(selected[0, 0, :9], P.table[0].cuda())
+    assert selected[0, 0, 9:].max().item() == -1
+    assert selected[0, 0, 9:].min().item() == -1
+
+
 def test_attention_with_a_table_a_head_and_a_window():
     """Heads of different pages, their rows in pairs in one block (the 8-bit
     forms of narrow rows), strides of any size, and a window."""
