@@ -788,7 +788,7 @@ int lm_kv_attend(const lm_kv_plan* plan, const lm_kv_cache* cache,
                  int64_t workspace_bytes, void* cuda_stream);
 
 /* Bytes of the workspace of an lm_kv_attend_weigh that is given weights, over
- * tables of max_pages pages: lm_kv_attend's, and 4 (max_pages * P + 1) bytes
+ * tables of max_pages pages: lm_kv_attend's, and 4 (max_pages * P + 2) bytes
  * for every sequence and query head.  Zero it once before its first use, as
  * lm_kv_attend's, whose calls it serves too.
  * Errors: LM_E_INVALID, LM_E_OVERFLOW, LM_E_CUDA. */

@@ -643,7 +643,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
         reinterpret_cast<int4*>(a.pieces)[row] = make_int4(0, 0, 0, 0);
       }
       if (a.lse) a.lse[row] = -INFINITY;
-      if (FORM == FORM_SCORES) a.lse2[row] = -INFINITY;
+      if (FORM == FORM_SCORES)
+        reinterpret_cast<float2*>(a.norms)[row] = make_float2(0, 0);
     }
   }
 
@@ -1193,10 +1194,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
         reinterpret_cast<float2*>(a.state)[row] = make_float2(t, sum);
         reinterpret_cast<int4*>(a.pieces)[row] = make_int4(0, 0, 0, 0);
       }
-      if (FORM != FORM_SCORES && !a.lse) return;
-      const float lse2 = sum == 0 ? -INFINITY : t + log2f(sum);
-      if (a.lse) a.lse[row] = lse2 * 0.693147180559945309f;
-      if (FORM == FORM_SCORES) a.lse2[row] = lse2;
+      if (a.lse)
+        a.lse[row] = sum == 0 ? -INFINITY
+                              : (t + log2f(sum)) * 0.693147180559945309f;
+      if (FORM == FORM_SCORES)
+        reinterpret_cast<float2*>(a.norms)[row] =
+            sum == 0 ? make_float2(0, 0) : make_float2(t, 1.f / sum);
     };
     for (int i = 0; i < HP; ++i)
       for (int e = threadIdx.x; e < nq * D; e += kAttendThreads) {

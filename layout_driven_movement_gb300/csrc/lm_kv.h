@@ -99,9 +99,10 @@ struct KvAttendArgs {
   // elements of the page table from one key head's pages to the next one's
   // (0: the heads share them)
   int64_t table_head = 0;
-  // where set: the scores in units of ln 2, [seqs, key heads, max_tokens,
-  // group], and the logarithms of their sums to base 2, [seqs, heads_q]
-  float *scores = nullptr, *lse2 = nullptr;
+  // where set: the scores s in units of ln 2, [seqs, key heads, max_tokens,
+  // group], and of each row a reference t and 1 / sum 2^(s - t) (0 and 0: no
+  // weights), [seqs, heads_q, 2]
+  float *scores = nullptr, *norms = nullptr;
   // where set: the state (m, l) and the mean of each row in 32 bits, [seqs,
   // heads_q] and [seqs, heads_q, dim], in the output's place
   float *state = nullptr, *mean = nullptr;

@@ -12,14 +12,14 @@ namespace {
 int64_t whole(int64_t bytes) { return add_chk(bytes, 255) / 256 * 256; }
 
 // What an attention that weighs keeps in its workspace, behind the plain
-// attention's: log-sums of all rows, then the scores.
+// attention's: references and sums of all rows, then the scores.
 struct WeighSpace {
-  int64_t lse2 = 0, scores = 0, bytes = 0;
+  int64_t norms = 0, scores = 0, bytes = 0;
 };
 WeighSpace weigh_space(int64_t plain, int64_t rows, int64_t max_tokens) {
   WeighSpace s;
-  s.lse2 = whole(plain);
-  s.scores = add_chk(s.lse2, whole(mul_chk(rows, 4)));
+  s.norms = whole(plain);
+  s.scores = add_chk(s.norms, whole(mul_chk(rows, 8)));
   s.bytes = add_chk(s.scores, mul_chk(mul_chk(rows, max_tokens), 4));
   return s;
 }
@@ -181,7 +181,7 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
          LM_E_OVERLAP);
     if (weights) {
       char* const ws = static_cast<char*>(workspace);
-      a.lse2 = reinterpret_cast<float*>(ws + space.lse2);
+      a.norms = reinterpret_cast<float*>(ws + space.norms);
       a.scores = reinterpret_cast<float*>(ws + space.scores);
     }
     rc = lm::launch_kv_attend(a, plan->store, cuda_stream);
@@ -197,7 +197,7 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
     w.seqs = seqs;
     w.group = a.group;
     w.scores = a.scores;
-    w.lse2 = a.lse2;
+    w.norms = a.norms;
     w.weights = weights;
     rc = lm::launch_kv_weigh(w, cuda_stream);
   });

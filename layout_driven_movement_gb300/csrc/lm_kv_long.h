@@ -13,7 +13,7 @@ struct KvWeighArgs {
   int64_t table_stride = 0, table_head = 0, max_tokens = 0, window = 0;
   const int32_t* lens = nullptr;
   int32_t seqs = 0, group = 1;
-  const float *scores = nullptr, *lse2 = nullptr;
+  const float *scores = nullptr, *norms = nullptr;  // of KvAttendArgs
   float* weights = nullptr;
   unsigned int* status = nullptr;
 };

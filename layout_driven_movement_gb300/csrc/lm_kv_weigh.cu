@@ -1,6 +1,8 @@
 // The weights of an attention, from its scores: w_j += sum over the group's
-// queries g of 2^(s_gj - L_g), s in units of ln 2 and L_g the logarithm of
-// sum_j 2^s_gj to base 2.
+// queries g of 2^(s_gj - t_g) / l_g, s in units of ln 2, t_g the reference that
+// the attention ended with and l_g = sum_j 2^(s_gj - t_g).  (The difference of
+// two numbers of 32 bits that lie close is exact.  The logarithm of the sum as
+// one number is not: of 2^20 it is good to 2^-4, which is 4% of a weight.)
 //
 // The weight of a key is known only once all keys are, so the attention leaves
 // its scores (4 bytes a query and key) and this launch goes over them: 4 G + 8
@@ -55,7 +57,8 @@ __global__ void __launch_bounds__(kWeighThreads)
     const int32_t* const table =
         a.table + at.b * a.table_stride + h * a.table_head;
     const int64_t row = at.b * heads + h;
-    const float* const l = a.lse2 + row * group;
+    const float2* const l =
+        reinterpret_cast<const float2*>(a.norms) + row * group;
     int64_t page[kWeighKeys];
     uint32_t off[kWeighKeys];
     float sum[kWeighKeys];
@@ -67,13 +70,13 @@ __global__ void __launch_bounds__(kWeighThreads)
       off[k] = uint32_t(key) - p * a.c.page_tokens;
       sum[k] = 0;
     }
-    auto share_of = [&](float s, float lse) {
-      return lse == -INFINITY ? 0.f : exp2f(s - lse);
+    auto share_of = [&](float s, const float2& n) {
+      return exp2f(s - n.x) * n.y;
     };
     if constexpr (G % 4 == 0 && G > 0) {
 #pragma unroll
       for (int g = 0; g < G; g += 4) {
-        const float l4[4] = {l[g], l[g + 1], l[g + 2], l[g + 3]};
+        const float2 l4[4] = {l[g], l[g + 1], l[g + 2], l[g + 3]};
         float4 s[kWeighKeys];
 #pragma unroll
         for (int k = 0; k < kWeighKeys; ++k)
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kWeighThreads)
       }
     } else {
       for (int g = 0; g < group; ++g) {
-        const float lse = l[g];
+        const float2 n = l[g];
         float s[kWeighKeys];
 #pragma unroll
         for (int k = 0; k < kWeighKeys; ++k)
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(kWeighThreads)
                             g];
 #pragma unroll
         for (int k = 0; k < kWeighKeys; ++k)
-          if (page[k] >= 0) sum[k] += share_of(s[k], lse);
+          if (page[k] >= 0) sum[k] += share_of(s[k], n);
       }
     }
     // (of pages out of range, which the attention has reported, nothing)

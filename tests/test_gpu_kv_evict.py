@@ -164,6 +164,37 @@ def test_weights_of_scores_at_the_ends():
     assert (w[ids[2, 1].cuda()] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,store", [(BF, None), (HF, None), (BF, "e4m3"),
+                                         (HF, "int8")], ids=str)
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 16, 2.0 ** 20, 2.0 ** 24,
+                                  2.0 ** 25])
+def test_weights_of_equal_scores_of_any_size(dtype, store, size):
+    """n keys of one score, up to 2^25 about: each has a weight of 1 / n of
+    every query.  The score is one product, so equal in all bits; 2^0 is 1, the
+    sum is within n 2^-24 (of 2^10 keys at most in runs of a warp's 2^7, so
+    2^-16 covers it), and the group's four add up within 2^-22."""
+    lens = [1, 3, 40, 700]
+    P = lr.Held(lens, 2, 64, 16, "nhd", dtype, store, seed=3)
+    P.held[0].zero_()
+    P.held[0][..., 0] = {None: 1, "e4m3": 0x38, "int8": 1}[store]
+    if store is not None:
+        P.scales[0].fill_(1)
+    q = torch.zeros(4, 8, 64, dtype=dtype, device="cuda")
+    q[:, :, 0] = 1 + torch.arange(8, device="cuda") / 8
+    cache, plan = P.cache(lm)
+    for sign in (1, -1):
+        w = torch.zeros(P.pool, 2, 16, device="cuda")
+        ws = space(lm.kv_attend_workspace(plan, 4, 8,
+                                          max_pages=P.table.shape[1]))
+        lm.kv_attend(cache, q, P.table.cuda(), ints(lens),
+                     torch.empty_like(q), ws, weights=w, scale=sign * size)
+        for b, n in enumerate(lens):
+            ids = P.table[b, :-(-n // 16)].long().cuda()
+            got = w[ids].transpose(0, 1).flatten(1).double()
+            assert ((got[:, :n] - 4 / n).abs() <= 2.0 ** -15 / n).all()
+            assert (got[:, n:] == 0).all()
+
+
 # --- eviction --------------------------------------------------------------
 
 def expected(P, weights, keep, recent):
