@@ -788,10 +788,11 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       }
       // A head's reference m moves only when a score passes the largest one
       // that it was set for by SLACK, that is when a weight would pass 2^SLACK
-      // (LOW: 2^-5): one vote a step instead of the maximum over the lanes and the
-      // products' rescaling.  LOW: and when a lane's sum passes 2^-4, so that
-      // the 8 lanes' sums, with the step's 2 weights each, stay below 1 and
-      // the products below the largest value.
+      // (LOW: 2^-5): one vote a step instead of the maximum over the lanes and
+      // the products' rescaling.  (By the difference, which is exact where the
+      // two are close: m + SLACK may be rounded to more.)  LOW: and when a lane's
+      // sum passes 2^-4, so that the 8 lanes' sums, with the step's 2 weights
+      // each, stay below 1 and the products below the largest value.
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -852,7 +853,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
             t = fmaxf(t, mt ? fmaxf(s[mt][nt][j], s[mt][nt][2 + j])
                             : s[mt][nt][2 + j]);
           top[nt][j] = t;
-          above |= t > m[nt][j] + (SLACK - ROOM);
+          above |= t - m[nt][j] > SLACK - ROOM;
           if (LOW) above |= l[nt][j] > 0x1p-4f;
         }
       if (__any_sync(0xffffffffu, above)) {

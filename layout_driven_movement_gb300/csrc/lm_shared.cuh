@@ -787,7 +787,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               if (!CODES) top *= unit;
               if (CODES && near) top = __fmaf_rn(top, down[i], most_of);
               keep[i] = 1;
-              if (top > m[i] + SLACK) {
+              // (by the difference: of numbers from 2^24 on the sum may be
+              // rounded to more than the bound, and an f16 weight be infinite)
+              if (top - m[i] > SLACK) {
                 // (in two halves: with scales of values far apart the whole may
                 // be below 2^-126 and the sum above 2^100)
                 keep[i] = ex2(0.5f * (m[i] - top));

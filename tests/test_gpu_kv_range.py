@@ -319,3 +319,28 @@ def test_weights_keep_their_bits(store, dtype, rel):
     assert all(r.abs().eq(3).all() for r in P.rows[1])
     q, out, lse = run_attend(P, 1, q=q, scale=1.0)
     check(P, 1, q, out, scale=1.0, rel=rel)
+
+
+@pytest.mark.parametrize("n", [16, 700])
+def test_float16_scores_that_grow_by_little_far_from_zero(n):
+    """Scores in units of ln 2 of 2^24 to 2^26, where a number of 32 bits is 2
+    or 4 from the next, that grow by as much from step to step of a warp: every
+    result is a mean of the values, within 2^-9 for the sums and its own
+    rounding."""
+    P = kr.Pages([n] * 40, 1, 64, 16, "nhd", HF, None, seed=1)
+    for b in range(40):
+        for j in range(n):
+            at = int(P.table[b, j // 16]), j % 16
+            P.codes[0][at] = 0
+            P.codes[0][at][:, 0] = 4096
+            P.codes[0][at][:, 1] = j // 64 % 8 if n > 64 else j // 4
+    refresh(P)
+    a = 2.0 ** (24 + 2 * torch.arange(40) / 40) / 4096 * math.log(2)
+    q = torch.zeros(40, 1, 64, dtype=HF)
+    q[:, 0, 0], q[:, 0, 1] = a.to(HF), 1
+    q, out, lse = run_attend(P, 1, q=q, scale=1.0)
+    assert lse.isfinite().all()
+    for b in range(40):
+        most = P.rows[1][b].abs().amax(0)
+        assert (out[b].double() <= most * (1 + 2.0 ** -9)).all()
+        assert (out[b].double() >= -most * (1 + 2.0 ** -9)).all()

@@ -54,3 +54,53 @@ def test_value_scales_of_any_sign(store, dim, order):
                          device="cuda")
     C.check(*rescale(C, 1, lambda s: s * sign).run())
     C.check(*rescale(C, 1, lambda s: -s.abs()).run())
+
+
+def stepping(store, dtype, n, heads, seqs, wide):
+    """Held keys of two elements, the first a large constant and the second
+    larger by one in every `wide` keys of eight times as many, and queries (a,
+    1) with a such that scores in units of ln 2 run from 2^24 to 2^26."""
+    P = lr.Held([n] + [0] * seqs, heads, 64, 16, "nhd", dtype, store, seed=3)
+    x = torch.zeros(P.pool, 16, heads, 64, device="cuda")
+    ids = P.table[0, :n // 16].long().cuda()
+    step = (torch.arange(n, device="cuda") // wide % 8).view(-1, 16, 1)
+    top = 4096.0 if store is None else 64.0
+    x[ids, :, :, 0], x[ids, :, :, 1] = top, step.float()
+    P.rows[0] = x.double()
+    if store is None:
+        P.held[0] = x.to(dtype)
+    else:
+        if store == "int8":
+            P.held[0] = x.to(torch.int8)
+        else:
+            table = lr.e4m3_values().cuda()[:127]
+            P.held[0] = torch.searchsorted(table.float(), x.contiguous()).to(
+                torch.uint8)
+        P.scales[0].fill_(1)
+    a = 2.0 ** (24 + 2 * torch.arange(seqs, device="cuda") / seqs)
+    q = torch.zeros(seqs, 1, 64, dtype=dtype, device="cuda")
+    q[..., 0] = (a / top * math.log(2))[:, None].to(dtype)
+    q[..., 1] = 1
+    return P, q
+
+
+@pytest.mark.parametrize("store,dtype", [(None, HF), (None, BF),
+                                         ("e4m3", BF), ("int8", BF)], ids=str)
+def test_scores_that_grow_by_little_far_from_zero(store, dtype):
+    """Scores of 2^24 to 2^26, where a number of 32 bits is 2 or 4 from the
+    next, that grow by as much from tile to tile of a block: every result is a
+    mean of the values, within the rounding of a weight (2^-8) and its own."""
+    n, heads, seqs = 40960, 2, 40
+    P, q = stepping(store, dtype, n, heads, seqs, 128)
+    cache, plan = P.cache(lm)
+    q = q.expand(seqs, heads, 64).contiguous()
+    t = P.table.cuda()
+    out, lse = torch.empty_like(q), torch.empty(seqs, heads, device="cuda")
+    lm.kv_attend_shared(
+        cache, q, t[:1], ints([n]), ints([0, seqs]), t[1:], ints([0] * seqs),
+        out, space(lm.kv_attend_shared_workspace(plan, seqs, heads)), lse=lse,
+        scale=1.0)
+    v = P.seq(1, 0)
+    assert lse.isfinite().all()
+    most = v.abs().amax(0)
+    assert (out.double().abs() <= most * (1 + 2.0 ** -6)).all()
