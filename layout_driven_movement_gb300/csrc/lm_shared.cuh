@@ -401,9 +401,11 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           }
           ask(kr, a.c.k);
         };
-        // Widened to f16.  What the logarithm of a value's scale says nothing of,
-        // its sign and 0, goes to the widened values (of the codes -128 has no
-        // opposite): `turned` where a row of the warp's is to be.
+        // Widened to f16.  What the logarithm of a value's scale says nothing of
+        // goes to the widened values (of the codes -128 has no opposite):
+        // `turned` where a row of the warp's is to be.  Its factor is the scale
+        // for its sign, 0 or NaN, and infinite for a key that is not seen, whose
+        // values become 0 whatever they are.
         auto widen = [&](uint32_t tile_s, const uint4* w, auto turned,
                          float factor) {
 #pragma unroll
@@ -413,9 +415,14 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             widen16<STORE>(w[i], y);
             if constexpr (decltype(turned)::value) {
               const float f = __shfl_sync(0xffffffffu, factor, r);
+              const __half2 by =
+                  __float2half2_rn(f > 0 ? 1.f : f < 0 ? -1.f : f);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                y[e] = f == 0 ? 0u : f < 0 ? y[e] ^ 0x80008000u : y[e];
+              for (int e = 0; e < 8; ++e) {
+                const __half2 v =
+                    __hmul2(*reinterpret_cast<const __half2*>(&y[e]), by);
+                y[e] = f == INFINITY ? 0u : *reinterpret_cast<const uint32_t*>(&v);
+              }
             }
             if (!held) continue;
             // (four lanes begin with their first chunk and four with their
@@ -444,15 +451,17 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           if (!alive) break;
           // (see NM: nothing reads these any more)
           char* const m = metas + tile % NM * S::kMeta;
-          // scales beyond 2^+-96 count as those; one of 0, whose values are
-          // taken as 0, as the largest about
+          // scales beyond 2^+-96 count as those; one of 0, or that is no number
+          // or infinite, as the largest about: its key has a weight like any
+          // other, and its values are 0 or no numbers
           // (magnitudes in the order of their bits)
-          const uint32_t top =
-              __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(vs)));
-          const float size = vs == 0 ? (top ? __uint_as_float(top) : 1.f)
-                                     : fabsf(vs);
-          const float held_size =
-              size < INFINITY ? fminf(fmaxf(size, 0x1p-96f), 0x1p96f) : size;
+          const bool usable = fabsf(vs) > 0 && fabsf(vs) < INFINITY;
+          const uint32_t top = __reduce_max_sync(
+              0xffffffffu, usable ? __float_as_uint(fabsf(vs)) : 0u);
+          const float size = usable ? fabsf(vs)
+                             : top  ? __uint_as_float(top)
+                                    : 1.f;
+          const float held_size = fminf(fmaxf(size, 0x1p-96f), 0x1p96f);
           const uint32_t bits = __float_as_uint(held_size);
           const uint32_t least = __reduce_min_sync(0xffffffffu, bits);
           const uint32_t most = __reduce_max_sync(0xffffffffu, bits);
@@ -469,11 +478,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 log2f(__uint_as_float(lane ? most : least));
           widen(k_s + slot * S::kTile + to, kr, std::false_type{}, 0.f);
           mbar_arrive(k_full(slot));
-          const float factor = vs;
+          const float factor = scale_at < 0          ? INFINITY
+                               : usable || vs == 0 ? vs
+                                                   : NAN;
           ask_keys(t + 1);
           if (tile >= NS) acquire(v_empty(slot), turn ^ 1);
           if (!alive) break;
-          if (__any_sync(0xffffffffu, mine && !(factor > 0)))
+          if (__any_sync(0xffffffffu, mine && !(factor > 0 && factor < INFINITY)))
             widen(v_s + slot * S::kTile + to, vr, std::true_type{}, factor);
           else
             widen(v_s + slot * S::kTile + to, vr, std::false_type{}, 0.f);

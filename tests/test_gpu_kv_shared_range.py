@@ -8,6 +8,7 @@ import math
 import pytest
 
 import kv_long_reference as lr
+import kv_reference as kr
 from test_gpu_kv_shared import (BF, HF, Case, built,  # noqa: F401
                                 clean_status, ints, space)
 
@@ -54,6 +55,47 @@ def test_value_scales_of_any_sign(store, dim, order):
                          device="cuda")
     C.check(*rescale(C, 1, lambda s: s * sign).run())
     C.check(*rescale(C, 1, lambda s: -s.abs()).run())
+
+
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_value_scales_that_are_no_numbers(store, bad):
+    """One key whose value's scale is no number, as a row with one is written:
+    the results of its group are none, and the lse, which has nothing to do
+    with values, is what it is."""
+    for dim in (64, 256):
+        C = Case([300, 70], [0, 5, 9], [4, 0, 3, 1, 0, 2, 2, 9, 1], 2, 3, dim,
+                 16, "nhd", BF, store, seed=dim)
+        page = int(C.P.table[0, 200 // 16])
+        C.P.scales[1][page, :, 200 % 16] = bad
+        out, lse = C.run()
+        assert out[:5].isnan().all()
+        C.P.rows[1][page, 200 % 16] = 0
+        out[:5] = 0
+        for b in range(9):
+            k, v = C.rows(b)
+            _, wl, _, mag, dot = lr.attend(C.q[b].double(), k, v, 3, dim ** -.5)
+            bl = kr.attend_bounds(BF, dim, out[b].double(), wl, mag, dot)[1]
+            assert ((lse[b].double() - wl).abs() <= bl).all()
+        C.lens, C.q, C.starts = C.lens[5:], C.q[5:], [0, 0, 4]
+        C.groups = 2
+        table = C.P.table
+        C.P.table = torch.cat([table[:2], table[7:]])
+        C.P.lens = [300, 70] + C.lens
+        C.check(out[5:], lse[5:])
+
+
+def test_no_numbers_under_a_scale_of_0():
+    """0 times a code that is no number is none; an unseen one is not used."""
+    C = Case([300], [0, 3], [3] * 3, 1, 2, 64, 16, "nhd", BF, "e4m3")
+    page = int(C.P.table[0, 2])
+    C.P.scales[1][page, 0, 5] = 0
+    C.P.held[1][page, 5, 0, 9] = 0x7f
+    last = int(C.P.table[0, 299 // 16])
+    C.P.held[1][last, 12:] = 0x7f
+    out, lse = C.run()
+    assert out[:, :, 9].isnan().all() and not lse.isnan().any()
+    assert not out[:, :, :9].isnan().any() and not out[:, :, 10:].isnan().any()
 
 
 def stepping(store, dtype, n, heads, seqs, wide):
