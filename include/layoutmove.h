@@ -845,9 +845,9 @@ int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
  * of bfloat16 rows to bfloat16 (off by 2^-8 of itself at most; weights below
  * 2^-80 of the largest are lost), of any other to float16, off by 2^-11 of
  * itself or by 2^-32 of the largest of its row, whichever is more, where a
- * quantised value's weight counts times its scale.  Scales of values above 2^96
- * or below 2^-96 in magnitude count as those.  Otherwise precision and range are
- * lm_kv_attend's.  The same inputs give the same bits.
+ * quantised value's weight counts times its scale, which may be any number of 32
+ * bits.  Otherwise precision and range are lm_kv_attend's.  The same inputs give
+ * the same bits.
  * Errors: as lm_kv_attend, LM_E_OVERFLOW also for a quantised cache of 2^36
  * bytes of keys or more. */
 int lm_kv_attend_shared(

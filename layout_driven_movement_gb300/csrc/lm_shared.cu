@@ -12,11 +12,13 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 // A block has a row.  It reads the row's states (m, l, a) -- its own pages', and
 // those of the blocks that had a piece of its group's prefix, in the order of
 // the line -- and forms sum c a / sum c with c = l 2^(m - t), t the largest m.
+// (Next to large scales of values c may be below 2^-126 where c a counts: 2^(m -
+// t) is two factors of its root, one of which goes to a.)
 // Three loads one after the other: where the pieces are, their (m, l), and their
 // means, of which each of the four warps has every fourth.  Those loads bound it:
 // 11.6 us for 2048 rows of 128 elements in 20 pieces, 22.7 us for 8192 in 7.  (A
 // warp a row, its pieces in turn: 18 us for the first.)
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 9)
     lm_kv_join_kernel(const __grid_constant__ KvJoinArgs j) {
   __shared__ float sums[kJoinWarps][kKvMaxDim];
   const KvSharedArgs& a = j.s;
@@ -60,37 +62,48 @@ __global__ void __launch_bounds__(kJoinThreads)
 #pragma unroll
   for (int k = 16; k; k /= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
   const float t0 = t == -INFINITY ? 0.f : t;
-  auto weight_of = [&](const float2& s) {
-    return s.y == 0 ? 0.f : s.y * ex2(s.x - t0);
+  auto root_of = [&](const float2& s) {
+    return s.y == 0 ? 0.f : ex2(0.5f * (s.x - t0));
   };
-  const float c_own = weight_of(own), c_mine = weight_of(mine);
-  float sum = c_mine + (lane == 0 ? c_own : 0.f);
-  for (int k = lane + 32; k < pieces; k += 32) sum += weight_of(state_of(k));
+  const float r_own = root_of(own), r_mine = root_of(mine);
+  float sum = mine.y * r_mine * r_mine;
+  if (lane == 0) sum += own.y * r_own * r_own;
+  for (int k = lane + 32; k < pieces; k += 32) {
+    const float2 s = state_of(k);
+    const float root = root_of(s);
+    sum += s.y * root * root;
+  }
 #pragma unroll
   for (int k = 16; k; k /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, k);
   const float f = sum == 0 ? 0.f : __fdividef(1.f, sum);
+  const float c_own = own.y * r_own * f, c_mine = mine.y * r_mine * f;
   for (int d0 = 0; d0 < dim; d0 += 128) {
     const int d = d0 + lane * 4;
     const bool live = d < dim;
     float y[4] = {0, 0, 0, 0};
     // (what has no weight may hold anything)
-    auto add = [&](float c, const float4& v) {
-      y[0] += c * v.x;
-      y[1] += c * v.y;
-      y[2] += c * v.z;
-      y[3] += c * v.w;
+    auto add = [&](float c, float root, const float4& v) {
+      y[0] += c * (root * v.x);
+      y[1] += c * (root * v.y);
+      y[2] += c * (root * v.z);
+      y[3] += c * (root * v.w);
     };
     if (warp == 0 && live && own.y != 0)
-      add(c_own * f,
+      add(c_own, r_own,
           *reinterpret_cast<const float4*>(j.mean + row * dim + d));
     for (int k0 = warp; k0 < pieces; k0 += 4 * kJoinWarps) {
       float4 v[4];
-      float c[4];
+      float c[4], root[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int k = k0 + e * kJoinWarps;
         c[e] = __shfl_sync(0xffffffffu, c_mine, k & 31);
-        if (k >= 32 && k < pieces) c[e] = weight_of(state_of(k));
+        root[e] = __shfl_sync(0xffffffffu, r_mine, k & 31);
+        if (k >= 32 && k < pieces) {
+          const float2 s = state_of(k);
+          root[e] = root_of(s);
+          c[e] = s.y * root[e] * f;
+        }
         v[e] = make_float4(0, 0, 0, 0);
         if (k < pieces && c[e] != 0 && live)
           v[e] = *reinterpret_cast<const float4*>(mean_of(k) + d);
@@ -98,7 +111,7 @@ __global__ void __launch_bounds__(kJoinThreads)
           c[e] = 0;
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) add(c[e] * f, v[e]);
+      for (int e = 0; e < 4; ++e) add(c[e], root[e], v[e]);
     }
     if (live)
       *reinterpret_cast<float4*>(&sums[warp][d]) =

@@ -48,10 +48,15 @@
 // about as much as its own): a second part would be half as many products
 // again.  Codes become f16, whose 11 bits hold them, for f16 queries (bf16 ones
 // times a power of two a row) and f16 weights.  A value's scale v_j is folded
-// into its weight's exponent, 2^(s_j + log2 v_j - m), with the reference m the
-// largest such sum: what a weight loses is relative to the largest contribution
-// of its row, whatever the scales.  The sum of the weights alone adds 1 / v_j of
-// each.
+// into its weight's exponent, 2^(s_j - m + log2 v_j - L), with the row's
+// reference m the largest s_j + log2 v_j - L: what a weight loses is relative to
+// the largest contribution of its row, whatever the scales.  L, a multiple of
+// 32, is the end of the band that the logarithms of a run's scales lie in.  The
+// sum of the weights alone, relative to m too, adds 2^L / v_j of each.  Where a
+// run's scales lie in several bands (those of a model do not), a score may
+// exceed m by more than 32 bits' range has room for: from there on the weights
+// are summed for themselves, relative to a largest score of their own (see
+// SharedRare).
 #pragma once
 
 #include "lm_attend.cuh"
@@ -215,11 +220,147 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return reinterpret_cast<float2&>(y);
 }
 
+// The band that the logarithm of a scale lies in, (end - 32, end]: its end.
+__device__ __forceinline__ float scale_band(float x) {
+  return 32.f * ceilf(x * (1.f / 32));
+}
+
 __device__ __forceinline__ void st_smem16(uint32_t to, uint32_t a, uint32_t b,
                                           uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(to), "r"(a),
                "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+__device__ __forceinline__ float over_quad(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+// The means of 16 rows times keep[0] (rows t / 4 of thread t) and keep[1].
+__device__ __forceinline__ void scale_means(uint32_t at, int dim,
+                                            const float* keep) {
+#pragma unroll 1
+  for (int c = 0; c < dim; c += 32) {
+    uint32_t o[16];
+    tmem_ld<4>(o, at + c);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      o[i] = __float_as_uint(__uint_as_float(o[i]) * keep[i / 2 % 2]);
+    tmem_st4(at + c, o);
+  }
+}
+
+// What a warp of the exponentials does with a tile of keys where their values'
+// scales lie in several bands, or in another than those before, and with the
+// segment's tiles from there on.  Apart from the kernel's own way for all others,
+// and with few instructions rather than fast.
+struct SharedRare {
+  uint32_t s_at, o_at;         // the warp's scores and means in tensor memory
+  const char* meta;            // what goes with the tile's keys
+  // of rows t / 4 of thread t and 8 on, of the warp's first 16 and its others.
+  // Sums are relative to references of their own, largest scores: one may exceed
+  // m by what scales differ by.
+  float m[4], ref[4], l[4], down[4];
+  float band, off;
+  int dim;
+  bool first;
+};
+template <int NK>
+__device__ __noinline__ void shared_rare(SharedRare* const io) {
+  constexpr float SLACK = 3;
+  SharedRare r = *io;
+  const int lane = threadIdx.x % 32;
+  const float2* const ku = reinterpret_cast<const float2*>(r.meta) + lane % 4;
+  const uint32_t* const words =
+      reinterpret_cast<const uint32_t*>(r.meta + NK * 12);
+  const float4 tops = reinterpret_cast<const float4*>(words)[2];
+  const float most = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
+  const float band = fmaxf(r.band, scale_band(most));
+  if (!r.first)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.m[i] -= band - r.band;
+  r.band = band;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t lanes = uint32_t(half * 16) << 16;
+    float* const m = r.m + 2 * half;
+    float* const ref = r.ref + 2 * half;
+    float* const l = r.l + 2 * half;
+    const float* const down = r.down + 2 * half;
+    // the scores of columns 32c .. 32c + 31
+    auto scores = [&](int c, float2 (&x)[4][2]) {
+      uint32_t w[16];
+      tmem_ld<4>(w, r.s_at + lanes + c * 32);
+      tmem_wait_ld();
+      const uint32_t seen =
+          (NK == 128 ? words[c] : words[2 * c] | words[2 * c + 1] << 16) >>
+          (lane % 4 * 2);
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 y =
+              mul2(mul2(make_float2(__uint_as_float(w[4 * g + 2 * i]),
+                                    __uint_as_float(w[4 * g + 2 * i + 1])),
+                        ku[16 * c + 4 * g]),
+                   make_float2(down[i], down[i]));
+          x[g][i] = make_float2(seen >> 8 * g & 1 ? y.x : -INFINITY,
+                                seen >> (8 * g + 1) & 1 ? y.y : -INFINITY);
+        }
+    };
+    // the largest score, and with its value's scale
+    float best[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int c = 0; c < NK / 32; ++c) {
+      float2 x[4][2];
+      scores(c, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 y = x[e / 2][e % 2];
+        const float2 z = add2(y, ku[NK / 2 + 16 * c + e / 2 * 4]);
+        best[e % 2] = fmaxf(best[e % 2], fmaxf(y.x, y.y));
+        top[e % 2] = fmaxf(top[e % 2], fmaxf(z.x, z.y));
+      }
+    }
+    float keep[2] = {1, 1}, sub[2], from[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      best[i] = over_quad(best[i]);
+      top[i] = over_quad(top[i]) - band;
+      if (best[i] - ref[i] > SLACK) {
+        l[i] *= ex2(ref[i] - best[i]);
+        ref[i] = best[i];
+      }
+      from[i] = ref[i] == -INFINITY ? 0.f : ref[i];
+      if (top[i] - m[i] > SLACK) {
+        keep[i] = ex2(m[i] - top[i]);
+        m[i] = top[i];
+      }
+      sub[i] = r.off - band - (m[i] == -INFINITY ? 0.f : m[i]);
+    }
+    if (!r.first) scale_means(r.o_at + lanes, r.dim, keep);
+#pragma unroll 1
+    for (int c = 0; c < NK / 32; ++c) {
+      float2 x[4][2];
+      scores(c, x);
+      uint32_t p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int g = e / 2, i = e % 2;
+        const float2 y = x[g][i];
+        const float2 lv = ku[NK / 2 + 16 * c + 4 * g];
+        const float2 w = make_float2(ex2(y.x + (lv.x + sub[i])),
+                                     ex2(y.y + (lv.y + sub[i])));
+        l[i] += ex2(y.x - from[i]) + ex2(y.y - from[i]);
+        p[e] = pair16<false>(w.x, w.y);
+      }
+      // (over scores that have been read)
+      tmem_st_pairs<4>(r.s_at + lanes + c * 16, p);
+    }
+  }
+  r.first = false;
+  *io = r;
 }
 
 // BF: the cache holds bf16 rows (and the products are bf16's).
@@ -339,6 +480,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         a.scale == 0 ? 1.f : fabsf(a.scale) * 1.44269504088896341f;
     const bool mine = KPW == 32 || lane < KPW;       // a key of this lane's
     const uint32_t to = lw * KPW * 128;
+    float last = 1;                 // the largest scale of the tile before
     while (alive && walk.next(a, &seg)) {
       const int32_t* const table = a.table + seg.g * a.table_stride;
       const int t1 = seg.t0 + seg.steps;
@@ -451,31 +593,33 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           if (!alive) break;
           // (see NM: nothing reads these any more)
           char* const m = metas + tile % NM * S::kMeta;
-          // scales beyond 2^+-96 count as those; one of 0, or that is no number
-          // or infinite, as the largest about: its key has a weight like any
-          // other, and its values are 0 or no numbers
+          // a scale of 0, or that is no number or infinite, counts as the largest
+          // about: its key has a weight like any other, and its values are 0 or
+          // no numbers
           // (magnitudes in the order of their bits)
           const bool usable = fabsf(vs) > 0 && fabsf(vs) < INFINITY;
           const uint32_t top = __reduce_max_sync(
               0xffffffffu, usable ? __float_as_uint(fabsf(vs)) : 0u);
-          const float size = usable ? fabsf(vs)
-                             : top  ? __uint_as_float(top)
-                                    : 1.f;
-          const float held_size = fminf(fmaxf(size, 0x1p-96f), 0x1p96f);
-          const uint32_t bits = __float_as_uint(held_size);
+          if (top) last = __uint_as_float(top);
+          const float size = usable ? fabsf(vs) : last;
+          const uint32_t bits = __float_as_uint(size);
           const uint32_t least = __reduce_min_sync(0xffffffffu, bits);
           const uint32_t most = __reduce_max_sync(0xffffffffu, bits);
+          const float end = log2f(__uint_as_float(lane ? most : least));
+          const float band =
+              scale_band(__shfl_sync(0xffffffffu, end, 1));
           if (mine) {
             float* f = reinterpret_cast<float*>(m) + lw * KPW + lane;
             f[0] = scale_at >= 0 ? ks * unit : 1.f;
-            f[NK] = log2f(held_size);
-            f[2 * NK] = __fdividef(1.f, held_size);
+            const float log = log2f(size);
+            f[NK] = log;
+            // (of the rounded logarithm, so that a weight's two factors cancel)
+            f[2 * NK] = ex2(band - log);
           }
           if (lane == 0)
             reinterpret_cast<uint32_t*>(m + NK * 12)[lw] = seen;
           if (lane < 2)
-            reinterpret_cast<float*>(m + NK * 12 + 16)[lane * 4 + lw] =
-                log2f(__uint_as_float(lane ? most : least));
+            reinterpret_cast<float*>(m + NK * 12 + 16)[lane * 4 + lw] = end;
           widen(k_s + slot * S::kTile + to, kr, std::false_type{}, 0.f);
           mbar_arrive(k_full(slot));
           const float factor = scale_at < 0          ? INFINITY
@@ -674,16 +818,16 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       // The thread's share of four rows: t / 4 and 8 on of a warp's first 16,
       // then of its other 16.  The pairs change places after each 16.
       float m[2], l[2], m2[2], l2[2];
-      // of codes: what the rows' queries were held times, and the largest
-      // logarithm of a scale so far
-      float down[2] = {1, 1}, down2[2] = {1, 1}, most = -INFINITY;
+      // of codes: what the rows' queries were held times, the band that scales
+      // lie in
+      float down[2] = {1, 1}, down2[2] = {1, 1}, band = -INFINITY;
       auto clear = [&] {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           m[i] = m2[i] = -INFINITY;
           l[i] = l2[i] = 0;
         }
-        most = -INFINITY;
+        band = -INFINITY;
       };
       clear();
       // the reference's weight, as a power of two
@@ -694,13 +838,15 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         const float ref = m == -INFINITY ? 0.f : m, x = off - ref;
         return !BF && x + ref > off + SLACK ? -ref : x;
       };
-      bool first = true;
+      bool first = true, rare = false;       // (see SharedRare)
+      float ref[2], ref2[2];                 // and so what sums are relative to
+      int j = -1;
       // Tile -1 stands for the row's query, which goes to shared memory.  In
       // the block's first one the weights are formed once of whatever tensor
       // memory holds and thrown away: so that their instructions, which come
       // from memory the first time (some 5000 cycles), are there when the first
       // scores are.
-      for (int j = -1;;) {
+      for (;;) {
         if (j >= 0) {
           if (!warp_gate(s_full(q), n_s & 1, &dead)) {
             alive = false;
@@ -729,13 +875,9 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           for (int c = 0; c < NK / 32; ++c) part |= seen(c) != 0xffffffffu;
           part = __any_sync(0xffffffffu, part && j >= 0);
           // Where scales of values lie within a few powers of two of each other,
-          // their largest is taken for all of them in a row's reference.  A
-          // code's weight alone is its exponential over its value's scale --
-          // unless scales lie so far apart that an exponential may be below
-          // 2^-126 where the weight is not small: then weights are summed for
-          // themselves.
+          // their largest is taken for all of them in a row's reference.
           float most_of = 0;
-          bool near = true, apart = false;
+          bool near = true;
           if (CODES) {
             const float4 lows =
                 *reinterpret_cast<const float4*>(meta + NK * 12 + 16);
@@ -744,9 +886,19 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             const float least =
                 fminf(fminf(lows.x, lows.y), fminf(lows.z, lows.w));
             most_of = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
-            most = fmaxf(most, most_of);
             near = !__any_sync(0xffffffffu, !(most_of - least < 4) && j >= 0);
-            apart = __any_sync(0xffffffffu, !(most - least < 60) && j >= 0);
+            // (the loading warps' inverses are relative to their own keys'
+            // bands, and good to 2^64)
+            const float low =
+                fminf(fminf(tops.x, tops.y), fminf(tops.z, tops.w));
+            const float of = first ? scale_band(most_of) : band;
+            if (__any_sync(0xffffffffu, !(most_of <= of && low > of - 32 &&
+                                          least > of - 64) &&
+                                            j >= 0)) {
+              rare = true;
+              break;
+            }
+            band = of;
           }
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
@@ -797,6 +949,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
               if (!CODES) top *= unit;
               if (CODES && near) top = __fmaf_rn(top, down[i], most_of);
+              if (CODES) top -= band;
               keep[i] = 1;
               // (by the difference: of numbers from 2^24 on the sum may be
               // rounded to more than the bound, and an f16 weight be infinite)
@@ -810,23 +963,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 move = true;
               }
             }
-            if (__any_sync(0xffffffffu, move) && !first) {
-#pragma unroll 1
-              for (int c = 0; c < dim; c += 32) {
-                uint32_t o[16];
-                tmem_ld<4>(o, o_at + lanes + c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) *
-                                         keep[i / 2 % 2]);
-                tmem_st4(o_at + lanes + c, o);
-              }
-            }
+            if (__any_sync(0xffffffffu, move) && !first)
+              scale_means(o_at + lanes, dim, keep);
             float2 sub[2], by[2], sums[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float x = sub_of(m[i]);
+              const float x = CODES ? sub_of(m[i]) - band : sub_of(m[i]);
               sub[i] = make_float2(x, x);
               by[i] = make_float2(down[i], down[i]);
               sums[i] = make_float2(0, 0);
@@ -842,16 +984,6 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               for (int e = 0; e < NK / 2; ++e)
                 s[e] = __float_as_uint(__fmul_rn(__uint_as_float(s[e]), unit));
               unit2 = make_float2(1, 1);
-            }
-            if (CODES && apart) {
-#pragma unroll
-              for (int g = 0; g < NK / 8; ++g)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float2 x =
-                      fma2(mul2(pair(g, i), ku[4 * g]), by[i], sub[i]);
-                  l[i] += ex2(x.x) + ex2(x.y);
-                }
             }
             uint32_t p[NK / 4];
 #pragma unroll
@@ -877,7 +1009,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             tmem_st_pairs<NK / 8>(s_at + lanes, p);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (!apart) l[i] += sums[i].x + sums[i].y;
+              l[i] += sums[i].x + sums[i].y;
               float t = m[i];
               m[i] = m2[i];
               m2[i] = t;
@@ -990,6 +1122,51 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         }
         if (j >= seg.steps) break;
       }
+      if (CODES && rare) {
+        SharedRare r;
+        r.s_at = s_at;
+        r.o_at = o_at;
+        r.dim = dim;
+        r.off = off;
+        r.band = first ? -INFINITY : band;
+        r.first = first;
+        const float low = __int_as_float((127 - int(off)) << 23);  // 2^-off
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          r.m[i] = r.ref[i] = m[i];
+          r.m[2 + i] = r.ref[2 + i] = m2[i];
+          r.l[i] = l[i] * low;
+          r.l[2 + i] = l2[i] * low;
+          r.down[i] = down[i];
+          r.down[2 + i] = down2[i];
+        }
+        for (;;) {
+          r.meta = metas + (t_first + j) % NM * S::kMeta;
+          shared_rare<NK>(&r);
+          tmem_wait_st();
+          tmem_before_sync();
+          mbar_arrive(p_full(q));
+          j += step;
+          if (j >= seg.steps) break;
+          if (!warp_gate(s_full(q), n_s & 1, &dead)) {
+            alive = false;
+            break;
+          }
+          ++n_s;
+          tmem_after_sync();
+        }
+        first = false;
+        band = r.band;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          m[i] = r.m[i];
+          m2[i] = r.m[2 + i];
+          l[i] = r.l[i];
+          l2[i] = r.l[2 + i];
+          ref[i] = r.ref[i];
+          ref2[i] = r.ref[2 + i];
+        }
+      }
       if (!alive) break;
       // --- the rows' states ---
       if (!active) continue;
@@ -1017,7 +1194,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const uint32_t lanes = uint32_t(half * 16) << 16;
-        float f[2];
+        float f[2], f2[2] = {1, 1};
         float* to[2];                // a row's mean, NULL where there is none
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -1032,8 +1209,21 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           float sum = l[i];
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          // weights were taken times 2^off
+          // weights were taken times 2^off, and relative to m and the band; the
+          // sum is relative to m, or to a reference of its own
           f[i] = sum == 0 ? 0.f : __fdividef(1.f, sum);
+          float from = -sub_of(m[i]);
+          if (CODES) {
+            float e = band;
+            if (rare) {
+              from = ref[i];
+              e += m[i] - from;
+              f[i] *= 0x1p-12f;                  // 2^-off
+            }
+            // (in two halves: the whole may be past 32 bits' range)
+            f2[i] = ex2(0.5f * e);
+            f[i] = sum == 0 ? 0.f : f[i] * f2[i];
+          }
           to[i] = nullptr;
           if (r < seg.rows) {
             to[i] = whole ? a.mean + out_row * dim
@@ -1043,7 +1233,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               // values the sum may be of any size, and references far apart
               // then say nothing about weights)
               const int e = int(__float_as_uint(sum) >> 23) - 127;
-              float2 ml = make_float2(none ? -INFINITY : -sub_of(m[i]), sum);
+              float2 ml = make_float2(none ? -INFINITY : from, sum);
               if (CODES && sum > 0x1p-120f && sum < INFINITY) {
                 ml.x += float(e);
                 ml.y *= __int_as_float((127 - e) << 23);
@@ -1074,8 +1264,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 const int d = c + g * 8 + lane % 4 * 2;
                 if (to[i] && d < dim)
                   *reinterpret_cast<float2*>(to[i] + d) = make_float2(
-                      __uint_as_float(x[4 * g + 2 * i]) * f[i],
-                      __uint_as_float(x[4 * g + 2 * i + 1]) * f[i]);
+                      __uint_as_float(x[4 * g + 2 * i]) * f[i] * f2[i],
+                      __uint_as_float(x[4 * g + 2 * i + 1]) * f[i] * f2[i]);
               }
           }
         }
@@ -1087,6 +1277,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           t = l[i];
           l[i] = l2[i];
           l2[i] = t;
+          ref[i] = ref2[i];
         }
       }
       if (!none) {

@@ -145,6 +145,17 @@ __device__ __forceinline__ void tmem_st_pairs<8>(uint32_t at, const uint32_t* r)
       : "memory");
 }
 
+template <>
+__device__ __forceinline__ void tmem_st_pairs<4>(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8"
+      "};\n" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // --- registers -----------------------------------------------------------------
 
 // By all four warps of a warpgroup: the registers a thread has from here on.

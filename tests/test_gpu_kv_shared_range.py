@@ -98,6 +98,104 @@ def test_no_numbers_under_a_scale_of_0():
     assert not out[:, :, :9].isnan().any() and not out[:, :, 10:].isnan().any()
 
 
+def check_far(C, out, lse, scale=None):
+    """Every key's scale is its own, so that a weight's rounding counts relative
+    to the largest weight times scale of its row: besides 2^-11 of its own, off
+    by 2^-32 of that times the largest code a key."""
+    scale = C.dim ** -0.5 if scale is None else scale
+    most = {"e4m3": 448.0, "int8": 128.0}[C.store]
+    for b in {0, len(C.lens) // 2, len(C.lens) - 1}:     # (all rows are alike)
+        k, v = C.rows(b)
+        want, wl, p, mag, dot = lr.attend(C.q[b].double(), k, v, C.group, scale)
+        bo, bl = kr.attend_bounds(C.dtype, C.dim, want, wl, mag, dot)
+        bo += (2.0 ** -11 - 2.0 ** -10 + 2.0 ** -16) * mag
+        s = C.row_scales(b).abs()                # [n, heads]
+        top = (p.view(C.heads, C.group, -1) * s.T[:, None]).amax(-1)
+        bo += (len(v) * 2.0 ** -32 * most * top).reshape(-1, 1)
+        assert out[b].isfinite().all(), b
+        assert ((out[b].double() - want).abs() <= bo).all(), b
+        assert ((lse[b].double() - wl).abs() <= bl).all(), b
+
+
+class Scaled(Case):
+    """A case whose value scales, and where wanted whose scores, are given for
+    each token of a prefix (own tokens: none)."""
+
+    def __init__(self, n, seqs, heads, group, dim, store, scales, scores=None,
+                 dtype=BF):
+        super().__init__([n], [0, seqs], [0] * seqs, heads, group, dim, 16,
+                         "nhd", dtype, store, seed=dim)
+        self.at = self.P.table[0, :n // 16].long().cuda()
+        s = scales.cuda().float().view(-1, 1, 16).expand(-1, heads, -1)
+
+        def change(x):
+            x = x.clone()
+            x[self.at] = s
+            return x
+        rescale(self, 1, change)
+        if scores is not None:
+            one = {"e4m3": 0x38, "int8": 1}[store]
+            k = torch.zeros(n // 16, 16, heads, dim, device="cuda",
+                            dtype=torch.int64)
+            k[..., 0] = one
+            self.P.held[0][self.at] = k.to(self.P.held[0].dtype)
+            t = scores.cuda().float().view(-1, 1, 16).expand(-1, heads, -1)
+
+            def aim(x):
+                x = x.clone()
+                x[self.at] = t
+                return x
+            rescale(self, 0, aim)
+            self.q.zero_()
+            self.q[..., 0] = 1
+
+    def row_scales(self, b):
+        return self.P.scales[1][self.at].double().transpose(1, 2).reshape(
+            -1, self.heads)
+
+
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("power", [-140, -126, -112, -64, -33, -32, -1, 0, 1,
+                                   47, 90, 112, 118])
+def test_value_scales_of_every_size(store, power):
+    """Scales about 2^power, those of bands' ends among them; own tokens' as
+    the prefix's, so that the two parts are joined."""
+    for dim, heads, group, seqs in ((64, 2, 3, 5), (128, 1, 4, 40),
+                                    (256, 1, 2, 3)):
+        own = 3 if power > -120 else 0       # (lm_kv_attend's range)
+        C = Case([700, 130], [0, seqs - 1, seqs], [own] * seqs, heads, group,
+                 dim, 16, "nhd", BF, store, seed=dim)
+        g = torch.Generator(device="cuda").manual_seed(power)
+        by = 2.0 ** torch.randint(-1, 2, C.P.scales[1].shape, generator=g,
+                                  device="cuda")
+        shift = 2.0 ** (power + 3.0 - (3 if power > 115 else 0))
+        rescale(C, 1, lambda s: (s.double().sign() * shift * by / 8).float())
+        C.check(*C.run())
+
+
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("order", ["up", "down", "mixed", "steps"])
+@pytest.mark.parametrize("lo,hi", [(-140, 118), (-40, 30), (-8, 7)])
+def test_value_scales_over_many_bands(store, order, lo, hi):
+    """Scales over 2^lo .. 2^hi in one prefix, in tiles that one block has or
+    several; equal scores, and scores that make up for the scales, so that the
+    largest weight lies where the smallest value does."""
+    for n, seqs, dim, heads in ((640, 3, 64, 1), (20480, 3, 64, 4),
+                                (2560, 70, 256, 2)):
+        e = torch.linspace(lo, hi, n).round()
+        if order == "down":
+            e = e.flip(0)
+        elif order == "mixed":
+            e = e[torch.randperm(n, generator=torch.Generator().manual_seed(1))]
+        elif order == "steps":
+            e = torch.where(torch.arange(n) // 300 % 2 == 0, float(lo),
+                            float(hi))
+        s = torch.exp2(e.double())
+        for lean in (0.0, -0.9, -1.1):
+            C = Scaled(n, seqs, heads, 2, dim, store, s, lean * math.log(2) * e)
+            check_far(C, *C.run(scale=1.0), scale=1.0)
+
+
 def stepping(store, dtype, n, heads, seqs, wide):
     """Held keys of two elements, the first a large constant and the second
     larger by one in every `wide` keys of eight times as many, and queries (a,
