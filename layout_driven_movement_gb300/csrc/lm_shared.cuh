@@ -251,10 +251,19 @@ __device__ __forceinline__ void scale_means(uint32_t at, int dim,
   }
 }
 
+// A row's reference moves when a score passes it by SLACK (in units of ln
+// 2).  f16 weights lie below 2^15, the reference's at 2^12.  bf16 values
+// reach the end of 32 bits' range, so their weights' sum stays below 1.
+template <bool BF>
+constexpr float kSharedSlack = BF ? 8.f : 3.f;
+
 // What a warp of the exponentials does with a tile of keys where their values'
-// scales lie in several bands, or in another than those before, and with the
-// segment's tiles from there on.  Apart from the kernel's own way for all others,
-// and with few instructions rather than fast.
+// scales lie in several bands, or in another than those before, or where a
+// row's reference is large; and with the segment's tiles from there on.  Apart
+// from the kernel's own way for all others, and with few instructions rather than
+// fast.  What is rounded with a score here is its difference from a number near
+// it: beside a score of 2^20 the logarithm of a scale would lose all but four of
+// its bits.
 struct SharedRare {
   uint32_t s_at, o_at;         // the warp's scores and means in tensor memory
   const char* meta;            // what goes with the tile's keys
@@ -262,27 +271,31 @@ struct SharedRare {
   // Sums are relative to references of their own, largest scores: one may exceed
   // m by what scales differ by.
   float m[4], ref[4], l[4], down[4];
-  float band, off;
-  int dim;
+  float band, off, unit;
+  int dim, half;               // from which half of the rows on
   bool first;
 };
-template <int NK>
+template <bool BF, bool CODES, int NK>
 __device__ __noinline__ void shared_rare(SharedRare* const io) {
-  constexpr float SLACK = 3;
+  constexpr float SLACK = kSharedSlack<BF>;
   SharedRare r = *io;
   const int lane = threadIdx.x % 32;
   const float2* const ku = reinterpret_cast<const float2*>(r.meta) + lane % 4;
   const uint32_t* const words =
       reinterpret_cast<const uint32_t*>(r.meta + NK * 12);
-  const float4 tops = reinterpret_cast<const float4*>(words)[2];
-  const float most = fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w));
-  const float band = fmaxf(r.band, scale_band(most));
-  if (!r.first)
+  float band = 0;
+  if (CODES) {
+    const float4 tops = reinterpret_cast<const float4*>(words)[2];
+    band = fmaxf(r.band, scale_band(fmaxf(fmaxf(tops.x, tops.y),
+                                          fmaxf(tops.z, tops.w))));
+    if (!r.first)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r.m[i] -= band - r.band;
-  r.band = band;
+      for (int i = 0; i < 4; ++i) r.m[i] -= band - r.band;
+    r.band = band;
+  }
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    if (half < r.half) continue;
     const uint32_t lanes = uint32_t(half * 16) << 16;
     float* const m = r.m + 2 * half;
     float* const ref = r.ref + 2 * half;
@@ -300,44 +313,66 @@ __device__ __noinline__ void shared_rare(SharedRare* const io) {
       for (int g = 0; g < 4; ++g)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 y =
-              mul2(mul2(make_float2(__uint_as_float(w[4 * g + 2 * i]),
-                                    __uint_as_float(w[4 * g + 2 * i + 1])),
-                        ku[16 * c + 4 * g]),
-                   make_float2(down[i], down[i]));
+          float2 y = make_float2(__uint_as_float(w[4 * g + 2 * i]),
+                                 __uint_as_float(w[4 * g + 2 * i + 1]));
+          y = CODES ? mul2(mul2(y, ku[16 * c + 4 * g]),
+                           make_float2(down[i], down[i]))
+                    : mul2(y, make_float2(r.unit, r.unit));
           x[g][i] = make_float2(seen >> 8 * g & 1 ? y.x : -INFINITY,
                                 seen >> (8 * g + 1) & 1 ? y.y : -INFINITY);
         }
     };
-    // the largest score, and with its value's scale
-    float best[2] = {-INFINITY, -INFINITY}, top[2] = {-INFINITY, -INFINITY};
+    float best[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+    for (int c = 0; c < NK / 32; ++c) {
+      float2 x[4][2];
+      scores(c, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        best[e % 2] = fmaxf(best[e % 2],
+                            fmaxf(x[e / 2][e % 2].x, x[e / 2][e % 2].y));
+    }
+    float base[2], from[2], top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      best[i] = over_quad(best[i]);
+      if (best[i] - ref[i] > SLACK) {
+        l[i] *= ex2(ref[i] - best[i]);
+        ref[i] = best[i];
+      }
+      // (a row that has seen no key yet, or only ones of -infinity)
+      from[i] = ref[i] == -INFINITY ? 0.f : ref[i];
+      base[i] = fabsf(m[i]) < INFINITY      ? m[i]
+                : fabsf(best[i]) < INFINITY ? best[i]
+                                            : 0.f;
+    }
+    // the largest score with its value's scale, relative to the base
 #pragma unroll 1
     for (int c = 0; c < NK / 32; ++c) {
       float2 x[4][2];
       scores(c, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float2 y = x[e / 2][e % 2];
-        const float2 z = add2(y, ku[NK / 2 + 16 * c + e / 2 * 4]);
-        best[e % 2] = fmaxf(best[e % 2], fmaxf(y.x, y.y));
-        top[e % 2] = fmaxf(top[e % 2], fmaxf(z.x, z.y));
+        const int g = e / 2, i = e % 2;
+        float2 y = make_float2(x[g][i].x - base[i], x[g][i].y - base[i]);
+        if (CODES) y = add2(y, ku[NK / 2 + 16 * c + 4 * g]);
+        top[i] = fmaxf(top[i], fmaxf(y.x, y.y));
       }
     }
-    float keep[2] = {1, 1}, sub[2], from[2];
+    float keep[2] = {1, 1}, sub[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      best[i] = over_quad(best[i]);
       top[i] = over_quad(top[i]) - band;
-      if (best[i] - ref[i] > SLACK) {
-        l[i] *= ex2(ref[i] - best[i]);
-        ref[i] = best[i];
+      const float was = m[i] - base[i];
+      float to = base[i] + (top[i] - was > SLACK ? ceilf(top[i]) : was);
+      // (A sum that is rounded down.  No weight lies above the largest score's,
+      // whose scale's logarithm is no more than the band's end.)
+      if (top[i] - (to - base[i]) > SLACK) to = best[i];
+      if (to != m[i]) {
+        keep[i] = ex2(m[i] - to);
+        m[i] = to;
       }
-      from[i] = ref[i] == -INFINITY ? 0.f : ref[i];
-      if (top[i] - m[i] > SLACK) {
-        keep[i] = ex2(m[i] - top[i]);
-        m[i] = top[i];
-      }
-      sub[i] = r.off - band - (m[i] == -INFINITY ? 0.f : m[i]);
+      sub[i] = r.off - band - (to == -INFINITY ? 0.f : to - base[i]);
     }
     if (!r.first) scale_means(r.o_at + lanes, r.dim, keep);
 #pragma unroll 1
@@ -349,17 +384,18 @@ __device__ __noinline__ void shared_rare(SharedRare* const io) {
       for (int e = 0; e < 8; ++e) {
         const int g = e / 2, i = e % 2;
         const float2 y = x[g][i];
-        const float2 lv = ku[NK / 2 + 16 * c + 4 * g];
-        const float2 w = make_float2(ex2(y.x + (lv.x + sub[i])),
-                                     ex2(y.y + (lv.y + sub[i])));
+        float2 lv = make_float2(0, 0);
+        if (CODES) lv = ku[NK / 2 + 16 * c + 4 * g];
         l[i] += ex2(y.x - from[i]) + ex2(y.y - from[i]);
-        p[e] = pair16<false>(w.x, w.y);
+        p[e] = pair16<BF>(ex2((y.x - base[i]) + (lv.x + sub[i])),
+                          ex2((y.y - base[i]) + (lv.y + sub[i])));
       }
       // (over scores that have been read)
       tmem_st_pairs<4>(r.s_at + lanes + c * 16, p);
     }
   }
   r.first = false;
+  r.half = 0;
   *io = r;
 }
 
@@ -370,10 +406,12 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
   using S = SharedShape<D>;
   constexpr int NK = S::NK, QT = S::QT, NS = S::NS, NM = S::NM;
   constexpr bool CODES = STORE != LM_KV_SAME;
-  // A row's reference moves when a score passes it by SLACK (in units of ln
-  // 2).  f16 weights lie below 2^15, the reference's at 2^12.  bf16 values
-  // reach the end of 32 bits' range, so their weights' sum stays below 1.
-  constexpr float SLACK = BF ? 8.f : 3.f;
+  constexpr float SLACK = kSharedSlack<BF>;
+  // References are whole numbers: up to 2^22 they are added to and taken from
+  // scores, and move, without a rounding.  Beyond LARGE what a logarithm loses
+  // beside one (2^-15 there), or what a fused multiplication leaves of a score's
+  // rounding, would matter: see SharedRare.
+  constexpr float LARGE = CODES ? 0x1p10f : 0x1p18f;
   constexpr int KPW = NK / 4;                   // keys of a loading warp
   extern __shared__ char smem_raw[];
   __shared__ volatile int dead;
@@ -832,13 +870,8 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
       clear();
       // the reference's weight, as a power of two
       const float off = BF ? -float(8 + 32 - __clz(seg.steps * NK)) : 12.f;
-      // what is added to a score: `off` less the reference, but where that
-      // rounds up so far that an f16 weight might be infinite
-      auto sub_of = [&](float m) {
-        const float ref = m == -INFINITY ? 0.f : m, x = off - ref;
-        return !BF && x + ref > off + SLACK ? -ref : x;
-      };
       bool first = true, rare = false;       // (see SharedRare)
+      int from_half = 0;                     // of its first tile
       float ref[2], ref2[2];                 // and so what sums are relative to
       int j = -1;
       // Tile -1 stands for the row's query, which goes to shared memory.  In
@@ -940,50 +973,52 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 tops[i][1] = fmaxf(tops[i][1], x.y);
               }
             }
-            float keep[2];
-            bool move = false;
+            float to[2];
+            bool move = false, large = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float top = fmaxf(tops[i][0], tops[i][1]);
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              float top = over_quad(fmaxf(tops[i][0], tops[i][1]));
               if (!CODES) top *= unit;
               if (CODES && near) top = __fmaf_rn(top, down[i], most_of);
               if (CODES) top -= band;
-              keep[i] = 1;
               // (by the difference: of numbers from 2^24 on the sum may be
               // rounded to more than the bound, and an f16 weight be infinite)
+              to[i] = m[i];
               if (top - m[i] > SLACK) {
-                // (in two halves: with scales of values far apart the whole may
-                // be below 2^-126 and the sum above 2^100)
-                keep[i] = ex2(0.5f * (m[i] - top));
-                l[i] = l[i] * keep[i] * keep[i];
-                keep[i] *= keep[i];
-                m[i] = top;
+                to[i] = ceilf(top);
                 move = true;
+                large |= fabsf(to[i]) > LARGE && fabsf(to[i]) < INFINITY;
               }
             }
-            if (__any_sync(0xffffffffu, move) && !first)
-              scale_means(o_at + lanes, dim, keep);
+            if (__any_sync(0xffffffffu, move)) {
+              if (__any_sync(0xffffffffu, large && j >= 0)) {
+                rare = true;
+                from_half = half;
+                break;
+              }
+              float keep[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                keep[i] = 1;
+                if (to[i] != m[i]) {
+                  // (in two halves: the whole may be below 2^-126 and, with
+                  // small scales of values, the sum large)
+                  keep[i] = ex2(0.5f * (m[i] - to[i]));
+                  l[i] = l[i] * keep[i] * keep[i];
+                  keep[i] *= keep[i];
+                  m[i] = to[i];
+                }
+              }
+              if (!first) scale_means(o_at + lanes, dim, keep);
+            }
             float2 sub[2], by[2], sums[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float x = CODES ? sub_of(m[i]) - band : sub_of(m[i]);
+              const float ref = m[i] == -INFINITY ? 0.f : m[i];
+              const float x = CODES ? off - ref - band : off - ref;
               sub[i] = make_float2(x, x);
               by[i] = make_float2(down[i], down[i]);
               sums[i] = make_float2(0, 0);
-            }
-            // A fused multiplication would leave what a score is rounded by, 2^5
-            // of one of 2^29: large scores are rounded first.  (Codes' are, by
-            // their own factors.)
-            float2 unit2 = make_float2(unit, unit);
-            if (!CODES &&
-                __any_sync(0xffffffffu, fmaxf(fabsf(m[0]), fabsf(m[1])) >
-                                            0x1p18f)) {
-#pragma unroll
-              for (int e = 0; e < NK / 2; ++e)
-                s[e] = __float_as_uint(__fmul_rn(__uint_as_float(s[e]), unit));
-              unit2 = make_float2(1, 1);
             }
             uint32_t p[NK / 4];
 #pragma unroll
@@ -1000,7 +1035,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
                 if (CODES)
                   x = fma2(mul2(x, f), by[i], add2(lv, sub[i]));
                 else
-                  x = fma2(x, unit2, sub[i]);
+                  x = fma2(x, make_float2(unit, unit), sub[i]);
                 x = make_float2(ex2(x.x), ex2(x.y));
                 sums[i] = CODES ? fma2(x, inv, sums[i]) : add2(x, sums[i]);
                 p[2 * g + i] = pair16<BF>(x.x, x.y);
@@ -1021,6 +1056,7 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
               down2[i] = t;
             }
           }
+          if (rare) break;
           first = false;
           tmem_wait_st();
         }
@@ -1122,27 +1158,32 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         }
         if (j >= seg.steps) break;
       }
-      if (CODES && rare) {
+      if (rare) {
         SharedRare r;
         r.s_at = s_at;
         r.o_at = o_at;
         r.dim = dim;
         r.off = off;
-        r.band = first ? -INFINITY : band;
+        r.unit = unit;
+        r.band = band;
         r.first = first;
+        r.half = from_half;
         const float low = __int_as_float((127 - int(off)) << 23);  // 2^-off
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          r.m[i] = r.ref[i] = m[i];
-          r.m[2 + i] = r.ref[2 + i] = m2[i];
-          r.l[i] = l[i] * low;
-          r.l[2 + i] = l2[i] * low;
-          r.down[i] = down[i];
-          r.down[2 + i] = down2[i];
+          // (the pairs change places after each half)
+          r.m[i] = from_half ? m2[i] : m[i];
+          r.m[2 + i] = from_half ? m[i] : m2[i];
+          r.l[i] = (from_half ? l2[i] : l[i]) * low;
+          r.l[2 + i] = (from_half ? l[i] : l2[i]) * low;
+          r.down[i] = from_half ? down2[i] : down[i];
+          r.down[2 + i] = from_half ? down[i] : down2[i];
+          r.ref[i] = r.m[i];
+          r.ref[2 + i] = r.m[2 + i];
         }
         for (;;) {
           r.meta = metas + (t_first + j) % NM * S::kMeta;
-          shared_rare<NK>(&r);
+          shared_rare<BF, CODES, NK>(&r);
           tmem_wait_st();
           tmem_before_sync();
           mbar_arrive(p_full(q));
@@ -1210,18 +1251,17 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           // weights were taken times 2^off, and relative to m and the band; the
-          // sum is relative to m, or to a reference of its own
-          f[i] = sum == 0 ? 0.f : __fdividef(1.f, sum);
-          float from = -sub_of(m[i]);
-          if (CODES) {
-            float e = band;
-            if (rare) {
-              from = ref[i];
-              e += m[i] - from;
-              f[i] *= 0x1p-12f;                  // 2^-off
-            }
+          // sum is relative to m, or to a reference of its own and without 2^off
+          const float low = __int_as_float((127 - int(off)) << 23);
+          float from = m[i];
+          if (rare)
+            from = ref[i];
+          else
+            sum *= low;
+          f[i] = sum == 0 ? 0.f : __fdividef(low, sum);
+          if (CODES || rare) {
             // (in two halves: the whole may be past 32 bits' range)
-            f2[i] = ex2(0.5f * e);
+            f2[i] = ex2(0.5f * ((CODES ? band : 0.f) + (m[i] - from)));
             f[i] = sum == 0 ? 0.f : f[i] * f2[i];
           }
           to[i] = nullptr;
@@ -1229,12 +1269,13 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
             to[i] = whole ? a.mean + out_row * dim
                           : part + 2 * S::kRows + part_row * D;
             if (lane % 4 == 0) {
-              // (the sum's exponent goes to the reference: next to scales of
-              // values the sum may be of any size, and references far apart
-              // then say nothing about weights)
+              // (the sum's exponent goes to the reference, where that holds it:
+              // next to scales of values the sum may be of any size, and
+              // references far apart then say nothing about weights)
               const int e = int(__float_as_uint(sum) >> 23) - 127;
-              float2 ml = make_float2(none ? -INFINITY : from, sum);
-              if (CODES && sum > 0x1p-120f && sum < INFINITY) {
+              float2 ml = make_float2(from, sum);
+              if (CODES && sum > 0x1p-120f && sum < INFINITY &&
+                  fabsf(from) < 0x1p14f) {
                 ml.x += float(e);
                 ml.y *= __int_as_float((127 - e) << 23);
               }

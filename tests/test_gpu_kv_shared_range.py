@@ -244,3 +244,54 @@ def test_scores_that_grow_by_little_far_from_zero(store, dtype):
     assert lse.isfinite().all()
     most = v.abs().amax(0)
     assert (out.double().abs() <= most * (1 + 2.0 ** -6)).all()
+
+
+@pytest.mark.parametrize("store,dtype", [(None, BF), (None, HF), ("e4m3", BF),
+                                         ("int8", HF)], ids=str)
+@pytest.mark.parametrize("size", [8.0, 900.0, 2.0 ** 12, 2.0 ** 16, 2.0 ** 20,
+                                  2.0 ** 25])
+@pytest.mark.parametrize("n,heads", [(384, 1), (20480, 4)])
+def test_equal_scores_far_from_zero(store, dtype, size, n, heads):
+    """Keys of one score, `size` in units of ln 2, and of one that is lower by
+    2^-19 of it or by a half, whichever is more, in one block and in many; the
+    values' scales differ from key to key.  However far the scores lie from 0,
+    weights are what their differences say.  Those are whole numbers of steps of
+    32 bits here, and good to 2^-22 of themselves, 2^-17 of 64 at most and so a
+    weight to 2^-17.  It is rounded to 11 bits (8 of bfloat16 rows); 2^-13
+    covers that of a logarithm beside a reference of up to 2^10, 2^-15, the
+    exponentials and the sums."""
+    seqs = 3
+    C = Case([n], [0, seqs], [0] * seqs, heads, 2, 64, 16, "nhd", dtype, store,
+             seed=5)
+    ids = C.P.table[0, :n // 16].long().cuda()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    lower = torch.randint(0, 2, (n // 16, 16, heads), generator=g,
+                          device="cuda").bool()
+    x = torch.zeros(C.P.pool, 16, heads, 64, dtype=torch.float64,
+                    device="cuda")
+    x[ids, :, :, 0] = 1
+    x[ids, :, :, 1] = torch.where(lower, -1.0, 0.0).double()
+    C.P.rows[0] = x
+    one, minus = {None: (1, -1), "e4m3": (0x38, 0xb8), "int8": (1, -1)}[store]
+    held = torch.zeros(x.shape, dtype=torch.int64, device="cuda")
+    held[x > 0], held[x < 0] = one, minus
+    C.P.held[0] = held.to(C.P.held[0].dtype)
+    if store is not None:
+        C.P.scales[0].fill_(1)
+    gap = max(0.5, size * 2.0 ** -19)
+    C.q.zero_()
+    C.q[..., 0] = 2.0 ** 9
+    C.q[..., 1] = 2.0 ** round(math.log2(gap / size * 2.0 ** 9))
+    scale = torch.tensor(size * math.log(2) / 2 ** 9).item()
+    out, lse = C.run(scale=scale)
+    half = store is not None or dtype == HF
+    step = 2.0 ** -11 if half else 2.0 ** -8
+    for b in range(seqs):
+        k, v = C.rows(b)
+        want, wl, p, mag, _ = lr.attend(C.q[b].double(), k, v, 2, scale)
+        bo = (step + 2.0 ** -13) * mag + want.abs() * kr.ROUND[dtype] * 1.01
+        if half:
+            bo += len(v) * 2.0 ** -35 * v.abs().max()
+        assert ((out[b].double() - want).abs() <= bo).all()
+        assert ((lse[b].double() - wl).abs() <=
+                2.0 ** -14 + wl.abs() * 2.0 ** -22).all()
