@@ -359,9 +359,12 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
   constexpr int TOP = KIND == KIND_E4M3 ? 106 : 60;
   constexpr float MOST = KIND == KIND_E4M3 ? 0x1p118f : 0x1p76f;
   // bf16 values reach the end of 32 bits' range, so their weights' sum stays
-  // below 1: a weight's reference lies ROOM above the largest score
+  // below 1: a weight's reference lies ROOM above the largest score.  Beyond
+  // FAR, where 32 bits may not hold a score and ROOM, references are scores and
+  // weights lie a power of two of the warp's, `room`, below.
   constexpr bool LOW = KIND == KIND_BF16;
   constexpr float ROOM = LOW ? 13.f : 0.f;
+  constexpr float FAR = 0x1p20f;
   constexpr int KW = S::KW, KL = S::KL, TK = S::TK, MT = S::MT, NS = S::kS;
   constexpr int Q = S::Q;
   constexpr int KS = D / 16;                 // 16-element steps along dim
@@ -698,7 +701,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
       }
     }
 
-    float m[NT][2], l[NT][2], o[KS][NT][4], gain = 0x1p120f;
+    float m[NT][2], l[NT][2], o[KS][NT][4], gain = 0x1p120f, room = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -857,15 +860,18 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
           if (LOW) above |= l[nt][j] > 0x1p-4f;
         }
       if (__any_sync(0xffffffffu, above)) {
+        float lift[NT][2], most = 0;
+        bool far = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // over the 8 lanes that hold the column's keys
-            float t = fmaxf(top[nt][j] + ROOM, m[nt][j]);
+            float t = top[nt][j];
 #pragma unroll
             for (int k = 4; k < 32; k *= 2)
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, k));
+            top[nt][j] = t;
             if (LOW) {
               float sum = l[nt][j];
 #pragma unroll
@@ -873,9 +879,27 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
                 sum += __shfl_xor_sync(0xffffffffu, sum, k);
               // 2^e or more: down to 2^-9
               const int e = int(__float_as_uint(sum) >> 23) - 127;
-              if (sum > 0x1p-5f) t = fmaxf(t, m[nt][j] + float(e + 9));
+              lift[nt][j] = sum > 0x1p-5f ? float(e + 9) : 0.f;
+              most = fmaxf(most, lift[nt][j]);
+              t = fmaxf(t + ROOM, m[nt][j]);
+              far |= fabsf(t) > FAR && t < INFINITY;
             }
-            const float keep = ex2(m[nt][j] - (t == -INFINITY ? 0.f : t));
+          }
+        if (LOW) {
+#pragma unroll
+          for (int k = 1; k < 4; k *= 2)
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, k));
+          far = room > 0 || __any_sync(0xffffffffu, far);
+        }
+        const float now = far ? fmaxf(ROOM, room + most) : 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float t = fmaxf(far ? top[nt][j] : top[nt][j] + ROOM, m[nt][j]);
+            if (LOW && !far) t = fmaxf(t, m[nt][j] + lift[nt][j]);
+            const float by = m[nt][j] - (t == -INFINITY ? 0.f : t);
+            const float keep = ex2(LOW ? by + (room - now) : by);
             m[nt][j] = t;
             l[nt][j] *= keep;
 #pragma unroll
@@ -884,6 +908,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
               o[k][nt][2 + j] *= keep;
             }
           }
+        room = now;
         if (CODES) {
           float big = 0;
 #pragma unroll
@@ -925,6 +950,18 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           top[nt][j] = m[nt][j] == -INFINITY ? 0.f : m[nt][j];
+      if (LOW && room > 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) s[mt][nt][2 * r + j] -= top[nt][j];
+            top[nt][j] = room;
+          }
+      }
 
       // weights, and their transposes as the second operand.  A weight's 8
       // (bf16) or 11 (f16) bits alone would cost the result about as much as
@@ -1108,7 +1145,8 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
         if (row8 == 0) {
           float* st = state + (warp * Q + nt * 8 + col2 + j) * 2;
           st[0] = m[nt][j];
-          st[1] = l[nt][j];
+          st[1] = LOW ? l[nt][j] * __int_as_float((127 + int(room)) << 23)
+                      : l[nt][j];
         }
       }
 #pragma unroll

@@ -344,3 +344,38 @@ def test_float16_scores_that_grow_by_little_far_from_zero(n):
         most = P.rows[1][b].abs().amax(0)
         assert (out[b].double() <= most * (1 + 2.0 ** -9)).all()
         assert (out[b].double() >= -most * (1 + 2.0 ** -9)).all()
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 19, 2.0 ** 24, 2.0 ** 27,
+                                  2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 9), (256, 12)])
+def test_large_values_under_scores_far_from_zero(size, dim, group):
+    """Values near the top of bfloat16 under scores where 32 bits do not hold a
+    score and what lies 13 above it: equal ones, whose mean is the values', and
+    ones that grow, whose mean is one of them (off by 2^-8 for its own rounding
+    and as much for the sums)."""
+    P = kr.Pages([700, 3, 9000], 1, dim, 16, "nhd", BF, None, seed=dim)
+    top = 2.0 ** 127 * 1.5
+    P.codes[1] = torch.where(P.codes[1].isnan(), P.codes[1],
+                             P.codes[1].sign() * top)
+    used = ~P.codes[0].isnan()
+    for grow in (False, True):
+        x = torch.zeros_like(P.codes[0])
+        x[..., 0] = 1
+        if grow:
+            x[..., 1] = torch.randint(
+                0, 8, x.shape[:-1], generator=torch.Generator().manual_seed(1))
+        P.codes[0] = torch.where(used, x, math.nan)
+        refresh(P)
+        q = torch.zeros(3, group, dim, dtype=BF)
+        q[..., 0], q[..., 1] = 1, 2.0 ** -21
+        for sign in (1, -1):
+            _, out, lse = run_attend(P, group, q=q, scale=sign * size)
+            assert out.isfinite().all() and lse.isfinite().all()
+            for b in range(3):
+                if grow:
+                    assert (out[b].double().abs() <= top * (1 + 2.0 ** -7)).all()
+                    continue
+                want = P.rows[1][b].mean(0)
+                bound = top * 2.0 ** -15 + want.abs() * kr.ROUND[BF] * 1.01
+                assert ((out[b].double() - want).abs() <= bound).all()

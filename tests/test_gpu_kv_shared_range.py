@@ -295,3 +295,28 @@ def test_equal_scores_far_from_zero(store, dtype, size, n, heads):
         assert ((out[b].double() - want).abs() <= bo).all()
         assert ((lse[b].double() - wl).abs() <=
                 2.0 ** -14 + wl.abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 19, 2.0 ** 24, 2.0 ** 27,
+                                  2.0 ** 30, 2.0 ** 60])
+def test_large_values_under_scores_far_from_zero(size):
+    """Values near the top of bfloat16 behind a prefix, under equal scores of
+    any size: their mean, within 2^-8 of the values for a weight's rounding."""
+    n, seqs = 9000, 40
+    top = 2.0 ** 127 * 1.5
+    C = Case([n], [0, seqs], [3] * seqs, 1, 2, 64, 16, "nhd", BF, None)
+    live = ~C.P.held[0].isnan()
+    one = torch.zeros_like(C.P.held[0])
+    one[..., 0] = 1
+    C.P.held[0] = torch.where(live, one, math.nan)
+    C.P.held[1] = torch.where(live, C.P.held[1].sign() * top, math.nan)
+    C.P.rows = [x.double() for x in C.P.held]
+    C.q.zero_()
+    C.q[..., 0] = 1
+    for sign in (1, -1):
+        out, lse = C.run(scale=sign * size)
+        assert out.isfinite().all() and lse.isfinite().all()
+        for b in (0, 17, 39):
+            want = C.rows(b)[1].mean(0)
+            bound = top * (2.0 ** -8 + 2.0 ** -13) + want.abs() * 2.0 ** -8
+            assert ((out[b].double() - want).abs() <= bound).all()
