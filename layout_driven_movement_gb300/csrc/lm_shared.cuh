@@ -276,7 +276,7 @@ struct SharedRare {
   bool first;
 };
 template <bool BF, bool CODES, int NK>
-__device__ __noinline__ void shared_rare(SharedRare* const io) {
+__device__ __forceinline__ void shared_rare(SharedRare* const io) {
   constexpr float SLACK = kSharedSlack<BF>;
   SharedRare r = *io;
   const int lane = threadIdx.x % 32;
@@ -397,6 +397,14 @@ __device__ __noinline__ void shared_rare(SharedRare* const io) {
   r.first = false;
   r.half = 0;
   *io = r;
+}
+// As a call for 16-bit rows, in line for codes: the other way round 64 sequences
+// of bf16 behind 16384 tokens take 94.2 us for 93.2, 128 in e4m3 370 for 365.
+// (What it costs either way is registers of the loops that never come here, 346
+// and 91.4 us without.)
+template <bool BF, int NK>
+__device__ __noinline__ void shared_rare_rows(SharedRare* const io) {
+  shared_rare<BF, false, NK>(io);
 }
 
 // BF: the cache holds bf16 rows (and the products are bf16's).
@@ -1183,7 +1191,10 @@ __global__ void __launch_bounds__(kSharedThreads, 1)
         }
         for (;;) {
           r.meta = metas + (t_first + j) % NM * S::kMeta;
-          shared_rare<BF, CODES, NK>(&r);
+          if constexpr (CODES)
+            shared_rare<BF, true, NK>(&r);
+          else
+            shared_rare_rows<BF, NK>(&r);
           tmem_wait_st();
           tmem_before_sync();
           mbar_arrive(p_full(q));
