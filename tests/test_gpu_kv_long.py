@@ -431,6 +431,70 @@ def test_scores_of_any_size(dtype, store, size):
                 torch.finfo(dtype).eps * want.abs()).all()
 
 
+def test_two_streams_with_workspaces_of_their_own():
+    """The calls of two streams, each with a cache, workspaces and outputs of its
+    own, again and again and at once: what each gives alone."""
+    def make(seed, store):
+        P = lr.Held([3000, 900, 700, 1500, 40], 2, 64, 16, "nhd", BF, store,
+                    seed=seed)
+        cache, plan = P.cache(lm)
+        g = torch.Generator().manual_seed(seed)
+        q = torch.randn(4, 8, 64, generator=g).to(BF).cuda()
+        t = P.table.cuda()
+        lens = ints(P.lens[1:])
+        width = t.shape[1]
+        out = [torch.empty_like(q) for _ in range(3)]
+        bounds = torch.zeros(P.pool, 2, 2, 64, dtype=torch.int8, device="cuda")
+        bscale = torch.ones(P.pool, 2, device="cuda")
+        selected = torch.empty(4, 2, 9, dtype=torch.int32, device="cuda")
+        slens, klens = ints([0] * 4), ints([0] * 4)
+        weights = torch.zeros(P.pool, 2, 16, device="cuda")
+        spare = [x.clone() for x in P.held]
+        wide = lm.KVCache(plan, *spare,
+                          *[None if x is None else x.clone() for x in P.scales])
+        ws = [space(lm.kv_attend_shared_workspace(plan, 4, 8)),
+              space(lm.kv_attend_workspace(plan, 4, 8, max_pages=width)),
+              space(lm.kv_select_workspace(plan, 4, width)),
+              space(lm.kv_evict_workspace(plan, 4, 500))]
+        pages = ints(list(range(P.pool)))
+        counts = ints([16] * P.pool)
+
+        def run(stream=None):
+            kw = {"stream": stream}
+            lm.kv_attend_shared(cache, q, t[:1], ints3000, ints04, t[1:], lens,
+                                out[0], ws[0], **kw)
+            lm.kv_bound(cache, pages, counts, bounds, bscale, **kw)
+            lm.kv_select(cache, q, bounds, bscale, t[1:], lens, selected, slens,
+                         ws[2], first=1, last=1, **kw)
+            lm.kv_attend(cache, q, selected, slens, out[1], ws[1], **kw)
+            lm.kv_attend(cache, q, t[1:], lens, out[2], ws[1],
+                         weights=weights, **kw)
+            lm.kv_evict(wide, weights, t[1:], lens, t[1:], klens, 500, ws[3],
+                        recent=10, **kw)
+        ints3000, ints04 = ints([3000]), ints([0, 4])
+        results = [*out, bounds, bscale, selected, slens, weights, klens]
+        return run, results, weights
+    runs = [make(1, None), make(2, "int8")]
+    alone = []
+    for run, results, weights in runs:
+        weights.zero_()
+        run()
+        torch.cuda.synchronize()
+        alone.append([x.clone() for x in results])
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        for (run, results, weights), stream in zip(runs, streams):
+            with torch.cuda.stream(stream):
+                weights.zero_()
+                for x in results[:3]:
+                    x.fill_(7)
+            run(stream)
+        torch.cuda.synchronize()
+        for (_, results, _), want in zip(runs, alone):
+            for x, y in zip(results, want):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 @pytest.mark.parametrize("store", [None, "e4m3"])
 def test_offsets_past_32_bits(store):
     """Pages 3 GB apart: rows that lie past 2^32 elements."""

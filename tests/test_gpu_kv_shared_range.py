@@ -246,6 +246,49 @@ def test_scores_that_grow_by_little_far_from_zero(store, dtype):
     assert (out.double().abs() <= most * (1 + 2.0 ** -6)).all()
 
 
+def check_far_scores(C, size):
+    """Keys of C's first prefix get one score, `size` in units of ln 2, or one
+    that is lower by 2^-19 of it or by a half, whichever is more; the values'
+    scales differ from key to key.  Own tokens: none.  See
+    test_equal_scores_far_from_zero for the bound."""
+    n, store, dtype, heads = C.shared[0], C.store, C.dtype, C.heads
+    pages = -(-n // 16)
+    ids = C.P.table[0, :pages].long().cuda()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    lower = torch.randint(0, 2, (pages, 16, heads), generator=g,
+                          device="cuda").bool()
+    x = torch.zeros(C.P.pool, 16, heads, C.dim, dtype=torch.float64,
+                    device="cuda")
+    x[ids, :, :, 0] = 1
+    x[ids, :, :, 1] = torch.where(lower, -1.0, 0.0).double()
+    C.P.rows[0] = x
+    one, minus = {None: (1, -1), "e4m3": (0x38, 0xb8), "int8": (1, -1)}[store]
+    held = torch.zeros(x.shape, dtype=torch.int64, device="cuda")
+    held[x > 0], held[x < 0] = one, minus
+    if C.P.order == "hnd":
+        held = held.transpose(1, 2)
+    C.P.held[0] = held.to(C.P.held[0].dtype).contiguous()
+    if store is not None:
+        C.P.scales[0].fill_(1)
+    gap = max(0.5, abs(size) * 2.0 ** -19)
+    C.q.zero_()
+    C.q[..., 0] = 2.0 ** 9
+    C.q[..., 1] = 2.0 ** round(math.log2(gap / abs(size) * 2.0 ** 9))
+    scale = torch.tensor(size * math.log(2) / 2 ** 9).item()
+    out, lse = C.run(scale=scale)
+    half = store is not None or dtype == HF
+    step = 2.0 ** -11 if half else 2.0 ** -8
+    for b in {0, len(C.lens) // 2, len(C.lens) - 1}:
+        k, v = C.rows(b)
+        want, wl, p, mag, _ = lr.attend(C.q[b].double(), k, v, C.group, scale)
+        bo = (step + 2.0 ** -13) * mag + want.abs() * kr.ROUND[dtype] * 1.01
+        if half:
+            bo += len(v) * 2.0 ** -35 * v.abs().max()
+        assert ((out[b].double() - want).abs() <= bo).all()
+        assert ((lse[b].double() - wl).abs() <=
+                2.0 ** -14 + wl.abs() * 2.0 ** -22).all()
+
+
 @pytest.mark.parametrize("store,dtype", [(None, BF), (None, HF), ("e4m3", BF),
                                          ("int8", HF)], ids=str)
 @pytest.mark.parametrize("size", [8.0, 900.0, 2.0 ** 12, 2.0 ** 16, 2.0 ** 20,
@@ -261,40 +304,21 @@ def test_equal_scores_far_from_zero(store, dtype, size, n, heads):
     covers that of a logarithm beside a reference of up to 2^10, 2^-15, the
     exponentials and the sums."""
     seqs = 3
-    C = Case([n], [0, seqs], [0] * seqs, heads, 2, 64, 16, "nhd", dtype, store,
-             seed=5)
-    ids = C.P.table[0, :n // 16].long().cuda()
-    g = torch.Generator(device="cuda").manual_seed(9)
-    lower = torch.randint(0, 2, (n // 16, 16, heads), generator=g,
-                          device="cuda").bool()
-    x = torch.zeros(C.P.pool, 16, heads, 64, dtype=torch.float64,
-                    device="cuda")
-    x[ids, :, :, 0] = 1
-    x[ids, :, :, 1] = torch.where(lower, -1.0, 0.0).double()
-    C.P.rows[0] = x
-    one, minus = {None: (1, -1), "e4m3": (0x38, 0xb8), "int8": (1, -1)}[store]
-    held = torch.zeros(x.shape, dtype=torch.int64, device="cuda")
-    held[x > 0], held[x < 0] = one, minus
-    C.P.held[0] = held.to(C.P.held[0].dtype)
-    if store is not None:
-        C.P.scales[0].fill_(1)
-    gap = max(0.5, size * 2.0 ** -19)
-    C.q.zero_()
-    C.q[..., 0] = 2.0 ** 9
-    C.q[..., 1] = 2.0 ** round(math.log2(gap / size * 2.0 ** 9))
-    scale = torch.tensor(size * math.log(2) / 2 ** 9).item()
-    out, lse = C.run(scale=scale)
-    half = store is not None or dtype == HF
-    step = 2.0 ** -11 if half else 2.0 ** -8
-    for b in range(seqs):
-        k, v = C.rows(b)
-        want, wl, p, mag, _ = lr.attend(C.q[b].double(), k, v, 2, scale)
-        bo = (step + 2.0 ** -13) * mag + want.abs() * kr.ROUND[dtype] * 1.01
-        if half:
-            bo += len(v) * 2.0 ** -35 * v.abs().max()
-        assert ((out[b].double() - want).abs() <= bo).all()
-        assert ((lse[b].double() - wl).abs() <=
-                2.0 ** -14 + wl.abs() * 2.0 ** -22).all()
+    check_far_scores(Case([n], [0, seqs], [0] * seqs, heads, 2, 64, 16, "nhd",
+                          dtype, store, seed=5), size)
+
+
+@pytest.mark.parametrize("store,dtype", [(None, BF), (None, HF), ("e4m3", BF),
+                                         ("int8", HF)], ids=str)
+@pytest.mark.parametrize("dim", [80, 128, 256])
+@pytest.mark.parametrize("seqs,group", [(3, 5), (50, 2), (70, 4)])
+def test_scores_far_from_zero_of_every_shape(store, dtype, dim, seqs, group):
+    """The same for rows of every length, in one tile of rows, in halves of one
+    or in several, with a last tile of keys that is not full, and below 0."""
+    for n, size in ((700, 2.0 ** 20), (3001, -2.0 ** 14)):
+        check_far_scores(Case([n], [0, seqs], [0] * seqs, 2, group, dim, 16,
+                              "hnd" if dim == 128 else "nhd", dtype, store,
+                              seed=5), size)
 
 
 @pytest.mark.parametrize("size", [1.0, 2.0 ** 19, 2.0 ** 24, 2.0 ** 27,
