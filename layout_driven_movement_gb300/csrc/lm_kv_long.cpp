@@ -59,6 +59,33 @@ void check_queries(const lm_kv_plan& p, int seqs, int heads_q) {
        heads_q % p.heads == 0);
 }
 
+// The bytes that an attention's queries, outputs and lse (empty: none) span.
+struct AttendRanges {
+  Range q, out, lse;
+  bool meet(const Range& o) const {
+    return o.meets(q) || o.meets(out) || o.meets(lse);
+  }
+};
+AttendRanges check_attend(const lm_kv_plan& p, const CacheRanges& held,
+                          const lm_rows* q, const lm_rows* out, int seqs,
+                          int heads_q, const float* lse) {
+  AttendRanges r;
+  r.q = check_rows(q, seqs, heads_q, p.dim, 2, false);
+  r.out = check_rows(out, seqs, heads_q, p.dim, 2, true);
+  const bool in_place = q->data == out->data &&
+                        (seqs == 1 || q->token_stride == out->token_stride) &&
+                        (heads_q == 1 || q->head_stride == out->head_stride);
+  need(in_place || !r.q.meets(r.out), LM_E_OVERLAP);
+  need(!held.meet(r.out), LM_E_OVERLAP);
+  need(lse == nullptr || addr(lse) % 4 == 0);
+  if (lse) {
+    r.lse = range_of(lse, int64_t(seqs) * heads_q * 4);
+    need(!held.meet(r.lse) && !r.lse.meets(r.q) && !r.lse.meets(r.out),
+         LM_E_OVERLAP);
+  }
+  return r;
+}
+
 }  // namespace
 }  // namespace lm
 
@@ -123,32 +150,17 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
     a.c = lm::check_cache(*plan, cache, &held);
     if (seqs == 0) return;
     lm::check_table(*plan, page_table, table_stride, seqs, max_pages, lens);
-    const lm::Range rq =
-        lm::check_rows(q, seqs, heads_q, plan->dim, 2, false);
-    const lm::Range ro =
-        lm::check_rows(out, seqs, heads_q, plan->dim, 2, true);
-    const bool in_place =
-        q->data == out->data &&
-        (seqs == 1 || q->token_stride == out->token_stride) &&
-        (heads_q == 1 || q->head_stride == out->head_stride);
-    need(in_place || !rq.meets(ro), LM_E_OVERLAP);
-    need(!held.meet(ro), LM_E_OVERLAP);
-    need(lse == nullptr || lm::addr(lse) % 4 == 0);
     const int64_t rows = int64_t(seqs) * heads_q;
-    lm::Range rl, rw;
-    if (lse) {
-      rl = lm::range_of(lse, rows * 4);
-      need(!held.meet(rl) && !rl.meets(rq) && !rl.meets(ro), LM_E_OVERLAP);
-    }
+    const lm::AttendRanges r =
+        lm::check_attend(*plan, held, q, out, seqs, heads_q, lse);
+    lm::Range rw;
     if (weights) {
       need(lm::addr(weights) % 4 == 0);
       const int64_t n = lm::mul_chk(
           cache->pages, lm::mul_chk(plan->heads, plan->page_tokens));
       need(n <= weights_capacity, LM_E_CAPACITY);
       rw = lm::range_of(weights, lm::mul_chk(n, 4));
-      need(!held.meet(rw) && !rw.meets(rq) && !rw.meets(ro) &&
-               !rw.meets(rl),
-           LM_E_OVERLAP);
+      need(!held.meet(rw) && !r.meet(rw), LM_E_OVERLAP);
     }
     a.q = lm::rows_of(*q);
     a.out = lm::rows_of(*out);
@@ -176,9 +188,7 @@ int lm_kv_attend_weigh(const lm_kv_plan* plan, const lm_kv_cache* cache,
     }
     lm::check_workspace(workspace, workspace_bytes, want);
     const lm::Range rs = lm::range_of(workspace, want);
-    need(!held.meet(rs) && !rs.meets(rq) && !rs.meets(ro) && !rs.meets(rl) &&
-             !rs.meets(rw),
-         LM_E_OVERLAP);
+    need(!held.meet(rs) && !r.meet(rs) && !rs.meets(rw), LM_E_OVERLAP);
     if (weights) {
       char* const ws = static_cast<char*>(workspace);
       a.norms = reinterpret_cast<float*>(ws + space.norms);
@@ -248,22 +258,8 @@ int lm_kv_attend_shared(
     }
     const int64_t rows = lm::mul_chk(seqs, heads_q);
     need(rows < (int64_t(1) << 31) - 4096, LM_E_OVERFLOW);
-    const lm::Range rq =
-        lm::check_rows(q, seqs, heads_q, plan->dim, 2, false);
-    const lm::Range ro =
-        lm::check_rows(out, seqs, heads_q, plan->dim, 2, true);
-    const bool in_place =
-        q->data == out->data &&
-        (seqs == 1 || q->token_stride == out->token_stride) &&
-        (heads_q == 1 || q->head_stride == out->head_stride);
-    need(in_place || !rq.meets(ro), LM_E_OVERLAP);
-    need(!held.meet(ro), LM_E_OVERLAP);
-    need(lse == nullptr || lm::addr(lse) % 4 == 0);
-    lm::Range rl;
-    if (lse) {
-      rl = lm::range_of(lse, rows * 4);
-      need(!held.meet(rl) && !rl.meets(rq) && !rl.meets(ro), LM_E_OVERLAP);
-    }
+    const lm::AttendRanges r =
+        lm::check_attend(*plan, held, q, out, seqs, heads_q, lse);
     // rows of codes are counted in 16 bytes, in 32 bits
     need(plan->store == LM_KV_SAME ||
              lm::mul_chk(cache->pages, plan->page_stride) <
@@ -279,8 +275,7 @@ int lm_kv_attend_shared(
         lm::shared_space(plain, rows, int(plan->dim), sms);
     lm::check_workspace(workspace, workspace_bytes, space.bytes);
     const lm::Range rs = lm::range_of(workspace, space.bytes);
-    need(!held.meet(rs) && !rs.meets(rq) && !rs.meets(ro) && !rs.meets(rl),
-         LM_E_OVERLAP);
+    need(!held.meet(rs) && !r.meet(rs), LM_E_OVERLAP);
     char* const ws = static_cast<char*>(workspace);
     auto floats = [&](int64_t at) { return reinterpret_cast<float*>(ws + at); };
     a.q = lm::rows_of(*q);

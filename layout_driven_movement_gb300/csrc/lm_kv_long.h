@@ -15,7 +15,6 @@ struct KvWeighArgs {
   int32_t seqs = 0, group = 1;
   const float *scores = nullptr, *norms = nullptr;  // of KvAttendArgs
   float* weights = nullptr;
-  unsigned int* status = nullptr;
 };
 
 struct KvBoundArgs {
@@ -33,7 +32,6 @@ struct KvSelectArgs {
   int64_t pages = 0;
   uint32_t heads = 1;
   int32_t page_tokens = 1;
-  FastDiv page_div;               // division by page_tokens
   int32_t dim = 0, group = 1, seqs = 0;
   int32_t q16 = 0;                // the queries allow 16-byte loads
   const int8_t* bounds = nullptr;
