@@ -835,9 +835,11 @@ int lm_kv_attend_shared_workspace(const lm_kv_plan* plan, int seqs,
  * shared_stride + i], and each over the first lens[b] tokens of its own pages,
  * as if these followed those:
  *   out[b, h] = sum_j p_j v_j,  p_j = exp(s_j) / sum_i exp(s_i),  j and i over
- * both.  A group's prefix is read once for all of its sequences.  starts has
- * groups + 1 entries, none below the one before; a sequence that no group
- * names has its own pages alone, a group may have no sequences or no tokens.
+ * both.  A group's prefix is read once for its sequences, or once for every 256
+ * of their queries of a key head (128 of rows of more than 128 elements) where
+ * those are more.  starts has groups + 1 entries, none below the one before; a
+ * sequence that no group names has its own pages alone, a group may have no
+ * sequences or no tokens.
  * (Entries are clipped to [0, seqs].  Of a sequence that several groups name
  * the outputs are not defined.)
  *
@@ -941,7 +943,8 @@ int lm_kv_evict_workspace(const lm_kv_plan* plan, int seqs, int keep,
  * kept_table, or written for one sequence and read for another.  kept_lens may
  * be lens itself.  What is not written to is left as it is, so that the slots
  * past the kept tokens hold weights of tokens that are gone: clear a slot's
- * weight when it is written again.  A page number outside [0, pages) is out of
+ * weight when it is written again.  Bounds (lm_kv_bound) of the pages that are
+ * written to are those of the rows before: make them again.  A page number outside [0, pages) is out of
  * range: a token there weighs least, and a row from or to there is not moved.
  * kept_pages: the pages of a row of kept_table, enough for min(keep, max_pages
  * * P) tokens.

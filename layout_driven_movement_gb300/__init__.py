@@ -1078,10 +1078,11 @@ def kv_attend_shared(cache: KVCache, q, shared_table, shared_lens, starts,
                      scale: float | None = None, stream=None) -> None:
     """Enqueue kv_attend for sequences that share a prefix in groups: those
     from starts[g] up to starts[g + 1] attend over the first shared_lens[g]
-    tokens of the pages shared_table[g], read once for all of them, and each
-    over the first lens[b] tokens of its own pages behind those.  shared_table
-    int32 [groups, pages], shared_lens int32 [groups], starts int32
-    [groups + 1]; the rest as kv_attend's (see lm_kv_attend_shared)."""
+    tokens of the pages shared_table[g], read once for up to 256 of their
+    queries of a key head, and each over the first lens[b] tokens of its own
+    pages behind those.  shared_table int32 [groups, pages], shared_lens int32
+    [groups], starts int32 [groups + 1]; the rest as kv_attend's (see
+    lm_kv_attend_shared)."""
     p = cache.plan
     rc = _pycall().kv_attend_shared(
         p._p, cache._p, p.dim, p.elem, q, shared_table, shared_lens, starts,
@@ -1145,7 +1146,8 @@ def kv_evict(cache: KVCache, weights, page_table, lens, kept_table, kept_lens,
     weights of the kept ones move up into the pages of kept_table, int32
     [sequences, pages], which may be page_table; kept_lens int32 [sequences],
     which may be lens, gets their number.  The slots past them keep their
-    weights: clear a slot's when it is written again (see lm_kv_evict)."""
+    weights: clear a slot's when it is written again; and the bounds of pages
+    that were written to are out of date (see lm_kv_evict)."""
     p = cache.plan
     rc = _pycall().kv_evict(p._p, cache._p, weights, page_table, lens,
                             kept_table, kept_lens, keep, recent, workspace,
