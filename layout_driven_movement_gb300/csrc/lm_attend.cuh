@@ -882,7 +882,7 @@ __launch_bounds__(kAttendThreads, AttendShape<KIND, D, NT, HP>::kBlocks)
               lift[nt][j] = sum > 0x1p-5f ? float(e + 9) : 0.f;
               most = fmaxf(most, lift[nt][j]);
               t = fmaxf(t + ROOM, m[nt][j]);
-              far |= fabsf(t) > FAR && t < INFINITY;
+              far |= fabsf(t) > FAR && fabsf(t) < INFINITY;
             }
           }
         if (LOW) {
