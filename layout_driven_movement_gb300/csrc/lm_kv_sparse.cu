@@ -66,7 +66,9 @@ constexpr int kBoundThreads = 128;
 // A warp has one page and head: L lanes hold a row in 16-byte chunks, 32 / L
 // of them take turns with the tokens, kAhead loads each in flight.  It is one
 // pass over the keys: 8 x 8192 tokens x 8 x 128 bf16 (81 MB) 17 us, 4.8 TB/s or
-// 71% of a copy's rate, 20 us with elements widened to 32 bits one by one.
+// 71% of a copy's rate, 20 us with elements widened to 32 bits one by one.  A
+// page of 16 tokens is one batch of loads behind two that wait for each other
+// (its number and count), and the warp ends: its loads fly for a part of its life.
 template <class T, int STORE, int L>
 __global__ void __launch_bounds__(kBoundThreads, STORE == LM_KV_SAME ? 8 : 4)
     lm_kv_bound_kernel(const __grid_constant__ KvBoundArgs a) {
@@ -227,8 +229,9 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4],
 // bounds and queries: 32 sequences x up to 1024 pages x 8 heads x 4 queries of
 // 128 elements (47 MB of bounds) 20 us, 13 sequences x 500 pages x 4 x 5 x 64
 // 7.8.  Three blocks an SM with one product's rows on their way, or two with
-// both: 20 against 23 us for the first, 8.4 against 7.8 for the second.  (Byte
-// products on the vector units, sums exchanged between lanes: 24 and 11.)
+// both: 20 against 23 us for the first, 8.4 against 7.8 for the second; three
+// spill 88 bytes, the form for 256 elements at two blocks 184.  (Byte products on
+// the vector units, sums exchanged between lanes: 24 and 11.)
 template <class T, int KS>
 __global__ void __launch_bounds__(kScoreThreads, KS == 4 ? 3 : 2)
     lm_kv_score_kernel(const __grid_constant__ KvSelectArgs a) {

@@ -19,12 +19,14 @@ constexpr int kWeighThreads = 256;
 constexpr int kWeighKeys = 4;        // of a thread
 constexpr int kWeighUnit = kWeighThreads * kWeighKeys;
 
-// 32 x 8192 tokens x 8 heads x 4 queries: 13 us behind an attention of 141.
+// 32 x 8192 tokens x 8 heads x 4 queries: 15 us behind an attention of 141 to 146;
+// 5 x 30011 x 4 x 5 queries: 7.7 behind 40.
 //
 // A unit is 1024 keys of one head, a thread has four, 256 apart, whose loads are
-// in flight together.  G: the queries of a key head, 0 for any number.  The
-// weights are added by the memory system (one addition a key and call, so
-// results do not depend on an order, unless sequences share pages).
+// in flight together.  G: the queries of a key head, 4 or 8 (four scores a load)
+// or 0 for any number (one score a load).  The weights are added by the
+// memory system (one addition a key and call, so results do not depend on an
+// order, unless sequences share pages).
 template <int G>
 __global__ void __launch_bounds__(kWeighThreads)
     lm_kv_weigh_kernel(const __grid_constant__ KvWeighArgs a) {

@@ -16,7 +16,7 @@ constexpr int kJoinWarps = kJoinThreads / 32;
 // t) is two factors of its root, one of which goes to a.)
 // Three loads one after the other: where the pieces are, their (m, l), and their
 // means, of which each of the four warps has every fourth.  Those loads bound it:
-// 11.6 us for 2048 rows of 128 elements in 20 pieces, 22.7 us for 8192 in 7.  (A
+// 11.5 us for 2048 rows of 128 elements in 20 pieces, 23.4 us for 8192 in 7.  (A
 // warp a row, its pieces in turn: 18 us for the first.)
 __global__ void __launch_bounds__(kJoinThreads, 9)
     lm_kv_join_kernel(const __grid_constant__ KvJoinArgs j) {

@@ -30,14 +30,16 @@
 // What bounds it is how long one tile of queries takes: its exponentials, 2300
 // cycles (4100 for codes, whose every score meets three numbers of its key),
 // and then its two products, 1050, one after the other, while the tensor cores
-// are 24-27% busy.  Measured: 29 us for 256 queries of 8 key heads over 16384
-// tokens of 128 bf16 elements (the bytes 10, the products 9), 265 us for 128
-// sequences x 8 queries of 8 key heads in 3 groups of 32768 tokens in e4m3, 0.45
-// PFLOP/s.  Groups of 43 x 8 rows are a full tile of rows and one of 88, whose
-// blocks are done first: giving those more tiles by weight made the line's end
-// even but its time no shorter (349 us for the whole call against 344), nor did
-// three more loading warps for the values, or one pass for largest and weights
-// that is taken again when a reference moves (367).
+// are 23-26% busy.  (The way out to rare tiles, see SharedRare, came after those
+// counts and takes 5 to 8% more.)  Measured: 31 us for 256 queries of 8 key heads
+// over 16384 tokens of 128 bf16 elements (the bytes 10, the products 9), 287 us
+// for 128 sequences x 8 queries of 8 key heads in e4m3, 360, 112 and 552 rows a
+// head over 32768, 19371 and 28126 tokens, 0.42 PFLOP/s.  552 rows are two full
+// tiles and one of 40, whose empty rows take as long as full ones and which reads
+// the prefix a third time.  Giving uneven tiles of rows more tiles of keys by
+// weight made the line's end even but its time no shorter (349 us for the whole
+// call against 344 then), nor did three more loading warps for the values, or one
+// pass for largest and weights that is taken again when a reference moves (367).
 //
 // Work is one line of key tiles over all groups, key heads and tiles of rows,
 // cut evenly over the resident blocks; what one block holds of rows that others
@@ -407,7 +409,9 @@ __device__ __noinline__ void shared_rare_rows(SharedRare* const io) {
   shared_rare<BF, false, NK>(io);
 }
 
-// BF: the cache holds bf16 rows (and the products are bf16's).
+// BF: the cache holds bf16 rows (and the products are bf16's).  At 128 registers
+// a thread the forms for up to 128 elements spill: 144 bytes those for codes, up
+// to 52 the others; rows of 256 elements 24 and none.
 template <bool BF, int STORE, int D>
 __global__ void __launch_bounds__(kSharedThreads, 1)
     lm_kv_shared_kernel(const __grid_constant__ KvSharedArgs a) {
