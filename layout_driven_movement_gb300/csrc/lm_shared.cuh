@@ -285,14 +285,12 @@ __device__ __forceinline__ void shared_rare(SharedRare* const io) {
   const float2* const ku = reinterpret_cast<const float2*>(r.meta) + lane % 4;
   const uint32_t* const words =
       reinterpret_cast<const uint32_t*>(r.meta + NK * 12);
-  float band = 0;
+  float band = 0, up = 0;        // a higher band than before, by so much
   if (CODES) {
     const float4 tops = reinterpret_cast<const float4*>(words)[2];
     band = fmaxf(r.band, scale_band(fmaxf(fmaxf(tops.x, tops.y),
                                           fmaxf(tops.z, tops.w))));
-    if (!r.first)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r.m[i] -= band - r.band;
+    if (!r.first) up = band - r.band;
     r.band = band;
   }
 #pragma unroll
@@ -365,16 +363,16 @@ __device__ __forceinline__ void shared_rare(SharedRare* const io) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       top[i] = over_quad(top[i]) - band;
-      const float was = m[i] - base[i];
+      const float was = m[i] - base[i] - up;
       float to = base[i] + (top[i] - was > SLACK ? top[i] : was);
       // (A sum that is rounded down.  No weight lies above the largest score's,
       // whose scale's logarithm is no more than the band's end.)
       if (top[i] - (to - base[i]) > SLACK) to = best[i];
-      if (to != m[i]) {
-        keep[i] = ex2(m[i] - to);
-        m[i] = to;
-      }
-      sub[i] = r.off - band - (to == -INFINITY ? 0.f : to - base[i]);
+      // (nor is what a sum that is rounded differs by lost)
+      const float at = to - base[i];
+      if (at != was) keep[i] = ex2(was - at);
+      m[i] = to;
+      sub[i] = r.off - band - (at == -INFINITY ? 0.f : at);
     }
     if (!r.first) scale_means(r.o_at + lanes, r.dim, keep);
 #pragma unroll 1

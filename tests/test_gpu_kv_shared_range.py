@@ -196,6 +196,30 @@ def test_value_scales_over_many_bands(store, order, lo, hi):
             check_far(C, *C.run(scale=1.0), scale=1.0)
 
 
+@pytest.mark.parametrize("store", CODES)
+@pytest.mark.parametrize("size", [2.0 ** 20, 2.0 ** 30, 2.0 ** 60])
+def test_value_scales_over_many_bands_under_large_scores(store, size):
+    """Equal scores of any size, scales that change by 2^70 every 300 tokens: the
+    mean of the values, within 2^-11 of each for its weight and as much for the
+    rest, and 2^-32 of the largest a key."""
+    n = 20480
+    e = torch.where(torch.arange(n) // 300 % 2 == 0, -40.0, 30.0)
+    C = Scaled(n, 3, 4, 2, 64, store, torch.exp2(e.double()),
+               torch.full((n,), size))
+    # (of one sign, so that nothing averages out)
+    C.P.held[1] = C.P.held[1] & 127
+    rescale(C, 1, lambda s: s)
+    most = {"e4m3": 448.0, "int8": 128.0}[store]
+    for sign in (1.0, -1.0):
+        out, lse = C.run(scale=sign)
+        assert lse.isfinite().all()
+        v = C.rows(0)[1]
+        want, mag = (x.mean(0).repeat_interleave(2, 0) for x in (v, v.abs()))
+        bound = 2.0 ** -10 * mag + 2.0 ** -32 * most * 2.0 ** 30 \
+            + want.abs() * kr.ROUND[BF] * 1.01
+        assert ((out.double() - want).abs() <= bound).all()
+
+
 def stepping(store, dtype, n, heads, seqs, wide):
     """Held keys of two elements, the first a large constant and the second
     larger by one in every `wide` keys of eight times as many, and queries (a,
